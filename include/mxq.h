@@ -281,6 +281,147 @@ mx_status mx_gemm(const void* a_codes, const void* a_scales, const void* b_codes
                   const void* b_scales, int64_t M, int64_t N, int64_t K, int fmt, int group,
                   int layout, float alpha, void* c, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Expert layers: routing tokens to experts, 8-bit operands with one scale per block of 128, the
+ * products of such operands (dense, by expert, and for weight gradients) and the combination of
+ * the experts' outputs. The conventions at the top of this file hold; alignment is stated per
+ * call. These have no counterpart on the pages; mx_quantize_grouped takes the row_offsets of
+ * mx_route_plan too.
+ * ------------------------------------------------------------------------------------------ */
+
+/* element types of logits and of products */
+#define MX_TYPE_BF16 0
+#define MX_TYPE_FP32 1
+
+/* scores of mx_route */
+#define MX_SCORE_SOFTMAX 0
+#define MX_SCORE_SIGMOID 1
+
+/*
+ * Routing. For each of T tokens with logits l [T, E] (MX_TYPE_BF16 or MX_TYPE_FP32):
+ *   s = softmax(l) or sigmoid(l) over the E experts, in fp32;
+ *   choice c = s + bias (bias: DEVICE fp32 [E] or NULL; it takes part in the choice only); without
+ *   a bias the softmax choice is exp(l - max l), which orders the experts as s does;
+ *   an expert whose l (or c) is -inf is never chosen;
+ *   groups > 1: the E experts form `groups` equal runs, a run's score is the sum of its two
+ *   largest c (of its only one where it has one), and only the top_groups best runs stay;
+ *   experts[t, :] = the k experts of largest c, descending; ties go to the lowest index (runs
+ *   likewise), a NaN ranks below every number; -1 where none is left;
+ *   weights[t, j] = scale * s[experts[t, j]] (/ the sum of the k scores when renormalize != 0; 0
+ *   where that sum is 0), 0 where experts[t, j] = -1.
+ * A NaN logit makes its token's softmax NaN. 1 <= E <= 1024, 1 <= k <= min(E, 32), 1 <= groups
+ * <= 32, E % groups == 0, k <= top_groups * E / groups, T * k < 2^31. experts: int32 [T, k],
+ * weights: fp32 [T, k]. Alignment: that of the elements.
+ */
+mx_status mx_route(const void* logits, int logits_type, const float* bias, int64_t T, int E, int k,
+                   int score, int groups, int top_groups, int renormalize, float scale,
+                   int32_t* experts, float* weights, void* stream);
+
+/*
+ * Gradient of the logits through the weights of mx_route (the choice is taken as fixed; the bias
+ * has none). grad_weights: fp32 [T, k]; experts: as mx_route wrote them; grad_logits: [T, E] of
+ * the logits' type, written whole. With p the chosen scores, P their sum and g = grad_weights:
+ * dp_j = scale * (g_j - sum_i g_i p_i / P) / P when renormalize != 0, else scale * g_j; then
+ * s_i (1 - s_i) dp_i (sigmoid) or s_i (dp_i - sum_j dp_j s_j) (softmax).
+ */
+mx_status mx_route_backward(const float* grad_weights, const void* logits, int logits_type,
+                            const int32_t* experts, int64_t T, int E, int k, int score,
+                            int renormalize, float scale, void* grad_logits, void* stream);
+
+/*
+ * Plan of the expert rows: the T * k choices ordered by expert, and by (token, j) within one.
+ * row_offsets: int64 [E + 1], expert e owns rows [row_offsets[e], row_offsets[e + 1]);
+ * tokens: int32 [T * k], the token of each row, -1 from row_offsets[E] on; slots: int32 [T, k], the
+ * row of each choice, -1 for a choice of -1 (anything outside [0, E) counts as none). workspace:
+ * device memory of mx_route_plan_workspace() bytes (may be NULL when that is 0), 4-byte aligned.
+ */
+mx_status mx_route_plan_workspace(int64_t T, int k, int E, int64_t* bytes);
+
+mx_status mx_route_plan(const int32_t* experts, int64_t T, int k, int E, int64_t* row_offsets,
+                        int32_t* tokens, int32_t* slots, void* workspace, void* stream);
+
+/*
+ * E4M3 operands with one fp32 scale per block of 128 along the contraction. For a block with
+ * abs-max A: a = max(A, 2^-100), r = 448 / a, scale = a / 448, code_i = E4M3(x_i * r), every step
+ * one fp32 operation rounded to nearest even, codes saturating at 448; a block with a NaN or an
+ * infinity has scale NaN and codes 0x7F. x is bf16 (32-byte aligned, K % 32 == 0), codes are
+ * 32-byte and scales 4-byte aligned. A last block may be shorter than 128.
+ *
+ * rows: 1 x 128 blocks along K of R rows. index (DEVICE int32 [R]) names the row of x [M, K] that
+ * each of them is (an entry outside [0, M) gives a row of zeros); index NULL: R = M, row for row.
+ *   codes [R, K]; scales [ceil(K / 128), R].
+ * cols: 128 x 1 blocks along the rows, written transposed, for products that contract over the
+ * rows of x. Rows as above; row_offsets (DEVICE int64 [E + 1]) makes each expert's rows start a
+ * new block, filled up with zeros; NULL with E = 1: one run of R rows.
+ *   codes [K, P], scales [P / 128, K], P = mx_b128_padded_rows(R, E) = floor((R + 127 E) / 128) * 128;
+ *   expert e's columns start at the sum of its predecessors' row counts, each rounded up to 128;
+ *   what lies past the last expert's is not written.
+ * blocks: 128 x 128 squares of each of `batch` matrices [M, K] (M * K rows following one another).
+ *   codes [batch, M, K], scales [batch, ceil(M / 128), ceil(K / 128)], and unless NULL the
+ *   transposed operand: codes_t [batch, K, M], scales_t [batch, ceil(K / 128), ceil(M / 128)].
+ */
+mx_status mx_b128_padded_rows(int64_t R, int E, int64_t* rows);
+
+mx_status mx_quantize_b128_rows(const void* x, int64_t M, int64_t K, const int32_t* index, int64_t R,
+                                void* codes, float* scales, void* stream);
+
+mx_status mx_quantize_b128_cols(const void* x, int64_t M, int64_t K, const int32_t* index, int64_t R,
+                                const int64_t* row_offsets, int E, void* codes, float* scales,
+                                void* stream);
+
+mx_status mx_quantize_b128_blocks(const void* x, int64_t batch, int64_t M, int64_t K, void* codes,
+                                  float* scales, void* codes_t, float* scales_t, void* stream);
+
+/* forms of B's scales in mx_gemm_b128 */
+#define MX_B128_BLOCKS 0 /* [ceil(N / 128), ceil(K / 128)]: mx_quantize_b128_blocks */
+#define MX_B128_ROWS 1   /* [ceil(K / 128), N]: mx_quantize_b128_rows or _cols */
+
+/*
+ * Products of such operands: C[i][j] = sum over blocks b of sa[b, i] sb[b, j] times the sum over
+ * the block of a[i][k] b[j][k]; products and sums in fp32 on the tensor cores, C rounded once to
+ * c_type (MX_TYPE_BF16 or MX_TYPE_FP32). Codes [rows, K], both K-major; A's scales in the rows
+ * form. K % 32 == 0, N % 8 == 0; codes and C 16-byte aligned.
+ *
+ * mx_gemm_b128: A [M, K], B [N, K], B's scales in b_form; C [M, N]. K > 0.
+ * mx_gemm_b128_grouped: rows [row_offsets[e], row_offsets[e + 1]) of A times B[e] [N, K] (B's
+ *   scales in the blocks form, [E, ceil(N / 128), ceil(K / 128)]); rows of C [M_total, N] from
+ *   row_offsets[E] on are not written. E * N < 2^31.
+ * mx_gemm_b128_grouped_wgrad: A [M, R_padded] and B [N, R_padded] as mx_quantize_b128_cols writes
+ *   them for the same row_offsets, scales in the rows form; C [E, M, N], C[e] contracts over expert
+ *   e's rows and is 0 where it has none. R_padded % 128 == 0.
+ * row_offsets: DEVICE int64 [E + 1], 0 first, non-decreasing, 1 <= E <= 1024. Offsets that break
+ * that give unspecified values but every access stays inside the buffers.
+ */
+mx_status mx_gemm_b128(const void* a_codes, const float* a_scales, const void* b_codes,
+                       const float* b_scales, int64_t M, int64_t N, int64_t K, int b_form,
+                       int c_type, void* c, void* stream);
+
+mx_status mx_gemm_b128_grouped(const void* a_codes, const float* a_scales, const void* b_codes,
+                               const float* b_scales, const int64_t* row_offsets, int E,
+                               int64_t M_total, int64_t N, int64_t K, int c_type, void* c,
+                               void* stream);
+
+mx_status mx_gemm_b128_grouped_wgrad(const void* a_codes, const float* a_scales,
+                                     const void* b_codes, const float* b_scales,
+                                     const int64_t* row_offsets, int E, int64_t M, int64_t N,
+                                     int64_t R_padded, int c_type, void* c, void* stream);
+
+/*
+ * Combination of expert rows: out[t] = sum over j of weights[t, j] * y[slots[t, j]] (fp32, in the
+ * order of j, rounded to bf16 once); weights NULL: all ones, the gradient of gathering rows by
+ * token. A slot outside [0, R) adds nothing. y: bf16 [R, N], out: bf16 [T, N], 16-byte aligned,
+ * N % 8 == 0; slots: int32 [T, k], weights: fp32 [T, k], 1 <= k <= 64.
+ * Backward: dy[slots[t, j]] = weights[t, j] * dout[t] (rows of dy that no slot names are not
+ * written; every row may be named once), dweights[t, j] = <dout[t], y[slots[t, j]]> (fp32, 0 for a
+ * slot that is none). dweights NULL: not wanted, y is then not read.
+ */
+mx_status mx_combine(const void* y, const int32_t* slots, const float* weights, int64_t T, int k,
+                     int64_t R, int64_t N, void* out, void* stream);
+
+mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* slots,
+                              const float* weights, int64_t T, int k, int64_t R, int64_t N,
+                              void* dy, float* dweights, void* stream);
+
 /*
  * Diagnostics: the rotated values y = x_chunk * H exactly as mx_rotate_quantize computes them
  * before quantization with the same rot_kind (same device code), written as fp32 [M, K] to
@@ -334,6 +475,15 @@ mx_status mx_selftest_rotate_give_up(const void* x, int64_t M, int64_t K, const 
 mx_status mx_selftest_gemm_give_up(const void* a_codes, const void* a_scales, const void* b_codes,
                                    const void* b_scales, int64_t M, int64_t N, int64_t K, int fmt,
                                    int layout, void* c, int64_t limit_ns, void* stream);
+
+/*
+ * The same self-test of the product of operands with a scale per block of 128: mx_gemm_b128 with
+ * a bf16 C and every pipeline wait limited to limit_ns.
+ */
+mx_status mx_selftest_gemm_b128_give_up(const void* a_codes, const float* a_scales,
+                                        const void* b_codes, const float* b_scales, int64_t M,
+                                        int64_t N, int64_t K, int b_form, void* c, int64_t limit_ns,
+                                        void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,10 @@ ROT_DENSE = 0     # any H: tensor-core product
 ROT_HADAMARD = 1  # H = H[0][0] * Sylvester (stated by the caller, checked on the device)
 ROT_AUTO = 2      # the same statement; the library takes the kernel measured faster for the call
 
+SOFTMAX, SIGMOID = 0, 1          # scores of mx_route
+B128_BLOCKS, B128_ROWS = 0, 1    # forms of B's scales in mx_gemm_b128
+BLOCK128 = 128
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxq.so")
 _lib = None
@@ -36,7 +40,11 @@ EXPORTS = (
     "mx_quantize_nvfp4", "mx_qdq_nvfp4", "mx_dequantize_nvfp4", "mx_nvfp4_grouped_scales_shape",
     "mx_quantize_nvfp4_grouped", "mx_rotate_debug", "mx_device_errors",
     "mx_selftest_bounded_wait", "mx_selftest_rotate_give_up", "mx_gemm",
-    "mx_selftest_gemm_give_up",
+    "mx_selftest_gemm_give_up", "mx_route", "mx_route_backward", "mx_route_plan_workspace",
+    "mx_route_plan", "mx_b128_padded_rows", "mx_quantize_b128_rows", "mx_quantize_b128_cols",
+    "mx_quantize_b128_blocks", "mx_gemm_b128", "mx_gemm_b128_grouped",
+    "mx_gemm_b128_grouped_wgrad", "mx_combine", "mx_combine_backward",
+    "mx_selftest_gemm_b128_give_up",
 )
 
 
@@ -79,6 +87,20 @@ def lib() -> ctypes.CDLL:
         "mx_selftest_rotate_give_up": (i32, [p, i64, i64, p, i32, p, p, i64, p]),
         "mx_gemm": (i32, [p, p, p, p, i64, i64, i64, i32, i32, i32, ctypes.c_float, p, p]),
         "mx_selftest_gemm_give_up": (i32, [p, p, p, p, i64, i64, i64, i32, i32, p, i64, p]),
+        "mx_route": (i32, [p, i32, p, i64, i32, i32, i32, i32, i32, i32, ctypes.c_float, p, p, p]),
+        "mx_route_backward": (i32, [p, p, i32, p, i64, i32, i32, i32, i32, ctypes.c_float, p, p]),
+        "mx_route_plan_workspace": (i32, [i64, i32, i32, pi64]),
+        "mx_route_plan": (i32, [p, i64, i32, i32, p, p, p, p, p]),
+        "mx_b128_padded_rows": (i32, [i64, i32, pi64]),
+        "mx_quantize_b128_rows": (i32, [p, i64, i64, p, i64, p, p, p]),
+        "mx_quantize_b128_cols": (i32, [p, i64, i64, p, i64, p, i32, p, p, p]),
+        "mx_quantize_b128_blocks": (i32, [p, i64, i64, i64, p, p, p, p, p]),
+        "mx_gemm_b128": (i32, [p, p, p, p, i64, i64, i64, i32, i32, p, p]),
+        "mx_gemm_b128_grouped": (i32, [p, p, p, p, p, i32, i64, i64, i64, i32, p, p]),
+        "mx_gemm_b128_grouped_wgrad": (i32, [p, p, p, p, p, i32, i64, i64, i64, i32, p, p]),
+        "mx_combine": (i32, [p, p, p, i64, i32, i64, i64, p, p]),
+        "mx_combine_backward": (i32, [p, p, p, p, i64, i32, i64, i64, p, p, p]),
+        "mx_selftest_gemm_b128_give_up": (i32, [p, p, p, p, i64, i64, i64, i32, p, i64, p]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -413,3 +435,293 @@ def mx_gemm(a_codes, a_scales, b_codes, b_scales, K: int, fmt, layout=SWIZZLED, 
     _check(lib().mx_gemm(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N, K,
                          fmt, group, layout, alpha, _ptr(c), _stream_ptr(stream, a_codes)))
     return c
+
+
+# ---------------------------------------------------------------------------------------------
+# expert layers: routing, operands with a scale per block of 128, their products, combination
+# ---------------------------------------------------------------------------------------------
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _tensor(t, name, dtype, *, dim=None, like=None) -> torch.Tensor:
+    """A contiguous CUDA tensor of one of the dtypes (and dimensions), on like's device."""
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes):
+        raise TypeError(f"{name} must be a CUDA tensor of {' or '.join(map(str, dtypes))}")
+    if not t.is_contiguous() or (dim is not None and t.dim() not in
+                                 (dim if isinstance(dim, tuple) else (dim,))):
+        raise ValueError(f"{name} must be contiguous" +
+                         ("" if dim is None else f" with {dim} dimensions"))
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    return t
+
+
+def _output(t, name, shape, dtype, like) -> torch.Tensor:
+    """t checked against shape, or a new tensor of it on like's device."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _tensor(t, name, dtype, like=like)
+    n = 1
+    for d in shape:
+        n *= d
+    if t.numel() != n:
+        raise ValueError(f"{name} has the wrong size")
+    return t
+
+
+def mx_route(logits, k: int, score=SOFTMAX, bias=None, *, groups: int = 1, top_groups: int = 1,
+             renormalize: bool = True, scale: float = 1.0, experts=None, weights=None, stream=None):
+    """Choose k experts per token from logits [T, E] (bfloat16 or float32) -> (experts int32
+    [T, k], weights float32 [T, k]); experts of logit -inf are never chosen (-1, weight 0)."""
+    _tensor(logits, "logits", (torch.bfloat16, torch.float32), dim=2)
+    T, E = logits.shape
+    if bias is not None and _tensor(bias, "bias", torch.float32, like=logits).numel() != E:
+        raise ValueError("bias must have one value per expert")
+    experts = _output(experts, "experts", (T, k), torch.int32, logits)
+    weights = _output(weights, "weights", (T, k), torch.float32, logits)
+    _check(lib().mx_route(_ptr(logits), _TYPES[logits.dtype], _ptr(bias), T, E, k, score, groups,
+                          top_groups, int(renormalize), scale, _ptr(experts), _ptr(weights),
+                          _stream_ptr(stream, logits)))
+    return experts, weights
+
+
+def mx_route_backward(grad_weights, logits, experts, score=SOFTMAX, *, renormalize: bool = True,
+                      scale: float = 1.0, grad_logits=None, stream=None):
+    """Gradient of the logits [T, E] from that of mx_route's weights [T, k]."""
+    _tensor(logits, "logits", (torch.bfloat16, torch.float32), dim=2)
+    _tensor(experts, "experts", torch.int32, dim=2, like=logits)
+    _tensor(grad_weights, "grad_weights", torch.float32, dim=2, like=logits)
+    T, E = logits.shape
+    k = experts.shape[1]
+    if experts.shape[0] != T or grad_weights.shape != experts.shape:
+        raise ValueError("experts and grad_weights must be [T, k]")
+    grad_logits = _output(grad_logits, "grad_logits", (T, E), logits.dtype, logits)
+    _check(lib().mx_route_backward(_ptr(grad_weights), _ptr(logits), _TYPES[logits.dtype],
+                                   _ptr(experts), T, E, k, score, int(renormalize), scale,
+                                   _ptr(grad_logits), _stream_ptr(stream, logits)))
+    return grad_logits
+
+
+@functools.lru_cache(maxsize=4096)
+def mx_route_plan_workspace(T: int, k: int, E: int) -> int:
+    """Bytes of device memory mx_route_plan works in."""
+    n = ctypes.c_int64()
+    _check(lib().mx_route_plan_workspace(T, k, E, ctypes.byref(n)))
+    return n.value
+
+
+def mx_route_plan(experts, E: int, *, row_offsets=None, tokens=None, slots=None, workspace=None,
+                  stream=None):
+    """Order the choices [T, k] by expert -> (row_offsets int64 [E + 1], tokens int32 [T * k],
+    slots int32 [T, k])."""
+    _tensor(experts, "experts", torch.int32, dim=2)
+    T, k = experts.shape
+    need = mx_route_plan_workspace(T, k, E)
+    row_offsets = _output(row_offsets, "row_offsets", (E + 1,), torch.int64, experts)
+    tokens = _output(tokens, "tokens", (T * k,), torch.int32, experts)
+    slots = _output(slots, "slots", (T, k), torch.int32, experts)
+    if workspace is None:
+        # the caching allocator hands memory out per stream: allocated for the stream it is used on
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
+            if isinstance(stream, torch.cuda.Stream):
+                workspace.record_stream(stream)
+    elif workspace.device != experts.device or \
+            workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must have {need} bytes on {experts.device}")
+    _check(lib().mx_route_plan(_ptr(experts), T, k, E, _ptr(row_offsets), _ptr(tokens), _ptr(slots),
+                               _ptr(workspace), _stream_ptr(stream, experts)))
+    return row_offsets, tokens, slots
+
+
+@functools.lru_cache(maxsize=4096)
+def mx_b128_padded_rows(R: int, E: int = 1) -> int:
+    """Columns of a mx_quantize_b128_cols operand of R rows of E experts."""
+    n = ctypes.c_int64()
+    _check(lib().mx_b128_padded_rows(R, E, ctypes.byref(n)))
+    return n.value
+
+
+def _row_index(index, x, M):
+    if index is None:
+        return M
+    return _tensor(index, "index", torch.int32, dim=1, like=x).numel()
+
+
+def _offsets(row_offsets, like) -> int:
+    E = _tensor(row_offsets, "row_offsets", torch.int64, dim=1, like=like).numel() - 1
+    if E < 1:
+        raise ValueError("row_offsets must be [E + 1]")
+    return E
+
+
+def mx_quantize_b128_rows(x, index=None, *, codes=None, scales=None, stream=None):
+    """bf16 [M, K] (rows `index` of it, int32 [R]) -> (E4M3 codes uint8 [R, K], scales float32
+    [ceil(K / 128), R]), one scale per 128 elements of a row."""
+    M, K = _input(x)
+    R = _row_index(index, x, M)
+    codes = _output(codes, "codes", (R, K), torch.uint8, x)
+    scales = _output(scales, "scales", (-(-K // BLOCK128), R), torch.float32, x)
+    _check(lib().mx_quantize_b128_rows(_ptr(x), M, K, _ptr(index), R, _ptr(codes), _ptr(scales),
+                                       _stream_ptr(stream, x)))
+    return codes, scales
+
+
+def mx_quantize_b128_cols(x, index=None, row_offsets=None, *, codes=None, scales=None, stream=None):
+    """bf16 [M, K] (rows `index` of it, grouped by row_offsets) -> (codes uint8 [K, P], scales
+    float32 [P / 128, K]), transposed, one scale per 128 rows; P = mx_b128_padded_rows(R, E)."""
+    M, K = _input(x)
+    R = _row_index(index, x, M)
+    E = 1 if row_offsets is None else _offsets(row_offsets, x)
+    P = mx_b128_padded_rows(R, E)
+    codes = _output(codes, "codes", (K, P), torch.uint8, x)
+    scales = _output(scales, "scales", (P // BLOCK128, K), torch.float32, x)
+    _check(lib().mx_quantize_b128_cols(_ptr(x), M, K, _ptr(index), R, _ptr(row_offsets), E,
+                                       _ptr(codes), _ptr(scales), _stream_ptr(stream, x)))
+    return codes, scales
+
+
+def mx_quantize_b128_blocks(x, *, transpose: bool = False, codes=None, scales=None, codes_t=None,
+                            scales_t=None, stream=None):
+    """bf16 [M, K] or [batch, M, K] -> (codes uint8 like x, scales float32 [.., ceil(M / 128),
+    ceil(K / 128)]), one scale per 128 x 128 square; with transpose also the transposed operand."""
+    _tensor(x, "x", torch.bfloat16, dim=(2, 3))
+    lead, (M, K) = tuple(x.shape[:-2]), x.shape[-2:]
+    mb, kb = -(-M // BLOCK128), -(-K // BLOCK128)
+    codes = _output(codes, "codes", (*lead, M, K), torch.uint8, x)
+    scales = _output(scales, "scales", (*lead, mb, kb), torch.float32, x)
+    if transpose:
+        codes_t = _output(codes_t, "codes_t", (*lead, K, M), torch.uint8, x)
+        scales_t = _output(scales_t, "scales_t", (*lead, kb, mb), torch.float32, x)
+    else:
+        codes_t = scales_t = None
+    _check(lib().mx_quantize_b128_blocks(_ptr(x), lead[0] if lead else 1, M, K, _ptr(codes),
+                                         _ptr(scales), _ptr(codes_t), _ptr(scales_t),
+                                         _stream_ptr(stream, x)))
+    return (codes, scales, codes_t, scales_t) if transpose else (codes, scales)
+
+
+def _b128_operand(codes, scales, what, shape, like=None):
+    """Checks the codes' type and the scales' shape."""
+    _tensor(codes, f"{what}_codes", torch.uint8, dim=(2, 3), like=like)
+    _tensor(scales, f"{what}_scales", torch.float32, like=codes)
+    if tuple(scales.shape) != shape:
+        raise ValueError(f"{what}_scales must be {list(shape)}")
+
+
+def _rows_form(codes):
+    return (-(-codes.shape[-1] // BLOCK128), codes.shape[-2])
+
+
+def _blocks_form(codes):
+    return (*codes.shape[:-2], -(-codes.shape[-2] // BLOCK128), -(-codes.shape[-1] // BLOCK128))
+
+
+def _b128_dense(a_codes, a_scales, b_codes, b_scales, b_form):
+    _b128_operand(a_codes, a_scales, "a", _rows_form(a_codes))
+    _b128_operand(b_codes, b_scales, "b",
+                  _rows_form(b_codes) if b_form == B128_ROWS else _blocks_form(b_codes), a_codes)
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
+        raise ValueError("a_codes and b_codes must be [M, K] and [N, K]")
+    return a_codes.shape[0], b_codes.shape[0], a_codes.shape[1]
+
+
+def _out_type(out_dtype, c):
+    dtype = out_dtype if c is None else c.dtype
+    if dtype not in _TYPES:
+        raise TypeError("the product's type is torch.bfloat16 or torch.float32")
+    return dtype
+
+
+def mx_gemm_b128(a_codes, a_scales, b_codes, b_scales, b_form=B128_BLOCKS, *,
+                 out_dtype=torch.bfloat16, c=None, stream=None):
+    """C[M, N] = A @ B^T from E4M3 codes [M, K] and [N, K] with a scale per block of 128: A's in the
+    rows form, B's in the blocks form or (B128_ROWS) the rows form."""
+    M, N, K = _b128_dense(a_codes, a_scales, b_codes, b_scales, b_form)
+    dtype = _out_type(out_dtype, c)
+    c = _output(c, "c", (M, N), dtype, a_codes)
+    _check(lib().mx_gemm_b128(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N, K,
+                              b_form, _TYPES[dtype], _ptr(c), _stream_ptr(stream, a_codes)))
+    return c
+
+
+def mx_selftest_gemm_b128_give_up(a_codes, a_scales, b_codes, b_scales, limit_ns: int,
+                                  b_form=B128_BLOCKS, *, stream=None):
+    """mx_gemm_b128 with every pipeline wait of the kernel limited to limit_ns; returns the
+    (unspecified) C buffer. The device error word reports the give-up."""
+    M, N, K = _b128_dense(a_codes, a_scales, b_codes, b_scales, b_form)
+    c = _output(None, "c", (M, N), torch.bfloat16, a_codes)
+    _check(lib().mx_selftest_gemm_b128_give_up(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
+                                               _ptr(b_scales), M, N, K, b_form, _ptr(c), limit_ns,
+                                               _stream_ptr(stream, a_codes)))
+    return c
+
+
+def mx_gemm_b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, *,
+                         out_dtype=torch.bfloat16, c=None, stream=None):
+    """Rows of A [R, K] by expert (row_offsets int64 [E + 1]) times that expert's B [E, N, K] ->
+    C [R, N]; rows from row_offsets[E] on are not written."""
+    _b128_operand(a_codes, a_scales, "a", _rows_form(a_codes))
+    _b128_operand(b_codes, b_scales, "b", _blocks_form(b_codes), a_codes)
+    E = _offsets(row_offsets, a_codes)
+    if a_codes.dim() != 2 or b_codes.dim() != 3 or b_codes.shape[0] != E or \
+            a_codes.shape[1] != b_codes.shape[2]:
+        raise ValueError("a_codes and b_codes must be [R, K] and [E, N, K]")
+    (R, K), N = a_codes.shape, b_codes.shape[1]
+    dtype = _out_type(out_dtype, c)
+    c = _output(c, "c", (R, N), dtype, a_codes)
+    _check(lib().mx_gemm_b128_grouped(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
+                                      _ptr(row_offsets), E, R, N, K, _TYPES[dtype], _ptr(c),
+                                      _stream_ptr(stream, a_codes)))
+    return c
+
+
+def mx_gemm_b128_grouped_wgrad(a_codes, a_scales, b_codes, b_scales, row_offsets, *,
+                               out_dtype=torch.float32, c=None, stream=None):
+    """C[e] = A_e @ B_e^T over expert e's rows, from mx_quantize_b128_cols operands [M, P] and
+    [N, P] of the same row_offsets -> C [E, M, N]."""
+    _b128_operand(a_codes, a_scales, "a", _rows_form(a_codes))
+    _b128_operand(b_codes, b_scales, "b", _rows_form(b_codes), a_codes)
+    E = _offsets(row_offsets, a_codes)
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
+        raise ValueError("a_codes and b_codes must be [M, P] and [N, P]")
+    M, N, P = a_codes.shape[0], b_codes.shape[0], a_codes.shape[1]
+    dtype = _out_type(out_dtype, c)
+    c = _output(c, "c", (E, M, N), dtype, a_codes)
+    _check(lib().mx_gemm_b128_grouped_wgrad(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
+                                            _ptr(b_scales), _ptr(row_offsets), E, M, N, P,
+                                            _TYPES[dtype], _ptr(c), _stream_ptr(stream, a_codes)))
+    return c
+
+
+def _slots(y, slots, weights):
+    _input(y, "y")
+    _tensor(slots, "slots", torch.int32, dim=2, like=y)
+    if weights is not None and \
+            _tensor(weights, "weights", torch.float32, like=y).shape != slots.shape:
+        raise ValueError("weights must be [T, k] as slots")
+    return slots.shape
+
+
+def mx_combine(y, slots, weights=None, *, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * y[slots[t, j]]: bf16 rows [R, N] -> [T, N] (weights None: ones)."""
+    T, k = _slots(y, slots, weights)
+    R, N = y.shape
+    out = _output(out, "out", (T, N), torch.bfloat16, y)
+    _check(lib().mx_combine(_ptr(y), _ptr(slots), _ptr(weights), T, k, R, N, _ptr(out),
+                            _stream_ptr(stream, y)))
+    return out
+
+
+def mx_combine_backward(dout, y, slots, weights, *, dy=None, dweights=None, stream=None):
+    """Gradients of mx_combine: dout [T, N] -> (dy [R, N], dweights [T, k])."""
+    T, k = _slots(y, slots, weights)
+    R, N = y.shape
+    if _tensor(dout, "dout", torch.bfloat16, dim=2, like=y).shape != (T, N):
+        raise ValueError("dout must be [T, N]")
+    dy = _output(dy, "dy", (R, N), torch.bfloat16, y)
+    dweights = _output(dweights, "dweights", (T, k), torch.float32, y)
+    _check(lib().mx_combine_backward(_ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, R, N,
+                                     _ptr(dy), _ptr(dweights), _stream_ptr(stream, y)))
+    return dy, dweights

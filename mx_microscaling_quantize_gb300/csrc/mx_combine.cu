@@ -1,0 +1,172 @@
+// mx_combine.cu -- joining the experts' outputs: out[t] = sum_j w[t, j] y[slot[t, j]], and its
+// gradient dy[slot] = w dout[t], dw[t, j] = <dout[t], y[slot]>. A slot of -1 (no expert) takes and
+// gives nothing. Sums are in fp32 in the order of j; each output is rounded to bf16 once.
+// Without weights (all ones) the forward is the gradient of gathering rows by token.
+//
+// Bound by memory: every chosen row is read once (16-byte loads, up to eight rows in flight per
+// thread), every output row written once. The backward walks tokens, not rows, so that dout is
+// read once and not k times.
+#include "mx_device.cuh"
+#include "mx_expert.h"
+#include "mx_launch.h"
+
+namespace mxq {
+
+namespace {
+
+constexpr int kCombineThreads = 256;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ void store4(void* p, const uint32_t* r) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+
+// One item = eight columns of one token; KU choices are loaded together.
+template <int KU>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a, int64_t chunks,
+                                                                  int64_t items) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const uint16_t* y = static_cast<const uint16_t*>(a.y);
+  for (int64_t it = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x; it < items;
+       it += (int64_t)gridDim.x * kCombineThreads) {
+    const int64_t t = it / chunks, col = it % chunks * 8;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < a.k; j0 += KU) {
+      uint32_t v[KU][4];
+      float w[KU];
+      bool ok[KU];
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        const int j = j0 + u;
+        const int64_t row = j < a.k ? (int64_t)a.slots[t * a.k + j] : -1;
+        ok[u] = row >= 0 && row < a.R;
+        w[u] = 1.0f;
+        if (ok[u]) {
+          load16B(y + row * a.N + col, v[u]);
+          if (a.weights) w[u] = a.weights[t * a.k + j];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        if (!ok[u]) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[2 * i] = fmaf(w[u], bf16_lo(v[u][i]), acc[2 * i]);
+          acc[2 * i + 1] = fmaf(w[u], bf16_hi(v[u][i]), acc[2 * i + 1]);
+        }
+      }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack_bf16(acc[2 * i], acc[2 * i + 1]);
+    store4(static_cast<uint16_t*>(a.out) + t * a.N + col, o);
+  }
+}
+
+// One CTA per token; choices in groups of KU whose inner products a thread keeps in registers.
+template <int KU>
+__global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(CombineArgs a,
+                                                                           int64_t chunks) {
+  __shared__ float part[kCombineThreads / 32][KU];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t = blockIdx.x;
+  const uint16_t* y = static_cast<const uint16_t*>(a.y);
+  const uint16_t* dout = static_cast<const uint16_t*>(a.dout) + t * a.N;
+  uint16_t* dy = static_cast<uint16_t*>(a.dy);
+  for (int j0 = 0; j0 < a.k; j0 += KU) {
+    int64_t row[KU];
+    float w[KU], dot[KU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const int j = j0 + u;
+      row[u] = j < a.k ? (int64_t)a.slots[t * a.k + j] : -1;
+      if (row[u] >= a.R) row[u] = -1;
+      w[u] = row[u] >= 0 && a.weights ? a.weights[t * a.k + j] : 1.0f;
+      dot[u] = 0.0f;
+    }
+    for (int64_t c = tid; c < chunks; c += kCombineThreads) {
+      uint32_t d[4], v[KU][4];
+      load16B(dout + c * 8, d);
+      if (a.dweights) {
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+          if (row[u] >= 0) load16B(y + row[u] * a.N + c * 8, v[u]);
+        }
+      }
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(d[i]);
+        f[2 * i + 1] = bf16_hi(d[i]);
+      }
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        if (row[u] < 0) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[i] = pack_bf16(w[u] * f[2 * i], w[u] * f[2 * i + 1]);
+          if (a.dweights) {
+            dot[u] = fmaf(f[2 * i], bf16_lo(v[u][i]), dot[u]);
+            dot[u] = fmaf(f[2 * i + 1], bf16_hi(v[u][i]), dot[u]);
+          }
+        }
+        store4(dy + row[u] * a.N + c * 8, o);
+      }
+    }
+    if (!a.dweights) continue;
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+#pragma unroll
+      for (int s = 16; s; s >>= 1) dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], s);
+      if (lane == 0) part[warp][u] = dot[u];
+    }
+    __syncthreads();
+    if (tid < KU && j0 + tid < a.k) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kCombineThreads / 32; ++i) sum += part[i][tid];
+      a.dweights[t * a.k + j0 + tid] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
+  const int64_t chunks = a.N / 8, items = a.T * chunks;
+  const int64_t ctas = (items + kCombineThreads - 1) / kCombineThreads;
+  const dim3 grid((unsigned)(ctas < (1 << 20) ? ctas : (1 << 20)));
+  if (a.k <= 2) {
+    return launch_pdl(&combine_kernel<2>, grid, dim3(kCombineThreads), 0, stream, a, chunks, items);
+  }
+  if (a.k <= 4) {
+    return launch_pdl(&combine_kernel<4>, grid, dim3(kCombineThreads), 0, stream, a, chunks, items);
+  }
+  return launch_pdl(&combine_kernel<8>, grid, dim3(kCombineThreads), 0, stream, a, chunks, items);
+}
+
+cudaError_t launch_combine_backward(const CombineArgs& a, cudaStream_t stream) {
+  const int64_t chunks = a.N / 8;
+  const dim3 grid((unsigned)a.T);
+  if (a.k <= 2) {
+    return launch_pdl(&combine_backward_kernel<2>, grid, dim3(kCombineThreads), 0, stream, a, chunks);
+  }
+  if (a.k <= 4) {
+    return launch_pdl(&combine_backward_kernel<4>, grid, dim3(kCombineThreads), 0, stream, a, chunks);
+  }
+  return launch_pdl(&combine_backward_kernel<8>, grid, dim3(kCombineThreads), 0, stream, a, chunks);
+}
+
+}  // namespace mxq
