@@ -3,6 +3,39 @@
 //   C[i][j] = sum_kb sa[kb, i] sb[kb, j] sum_{k in block kb} a[i][k] b[j][k],
 // dense, by expert (rows of A by offsets, one B per expert), and by expert for weight gradients
 // (the contraction runs over each expert's own rows).
+//
+// One step is one scale block: operand P (128 tensor-memory lanes per CTA) and operand Q (up to 256
+// accumulator columns), 128 code bytes of each row, loaded by the tensor-memory accelerator into a
+// ring of 128-byte swizzled stages; four tcgen05.mma kind::f8f6f4 (K = 32) give the block's sums in
+// one of two accumulators; eight warps read it and add it, times its scales, to fp32 sums in
+// registers. The scales cannot wait until the end because they change with every block, so each
+// block costs 32768 fp32 FMAs per CTA and a trip through registers beside its MMAs (512 cycles at
+// the tensor cores' rate): that trip, not the MMAs, is what the kernel is built around.
+//   * Two accumulators fill tensor memory, so a step cannot be shorter than half of (MMA + signal +
+//     read + signal). A step's stage is full when its operands have landed AND its accumulator has
+//     been read (one barrier for both); the reads come before the sums.
+//   * The warp that multiplies runs converged and issues a step in one statement with every operand
+//     in uniform registers (issue_step): issued from a lone lane's branch it took 600 cycles.
+//   * Scales come through shared memory from a warp of their own, a group of four steps ahead.
+//   * fp32 sums are packed pairs: half the instructions beside the warp that issues the MMAs.
+//
+// Three shapes of the same kernel:
+//   rows      P = A (rows' scales), Q = B (blocks' scales), CTA pairs, 256 x 256 tiles: large dense
+//             products. A pair (cta_group::2) shares one tile, each CTA holding 128 lanes and half of
+//             Q: per step 32 KB into an SM instead of 48, which alone bound 128 x 256 tiles.
+//   columns   the same with a scale per column as well (weight gradients): the accumulator is read
+//             in fragments (4 rows x 32 columns per thread), which needs a quarter of the column
+//             scales' reads that a row per thread does (those would take 1024 cycles a step).
+//   swapped   P = B (weights), Q = A (tokens), for few tokens and for experts: a tile has as many
+//             columns as it has tokens (a multiple of 16, at run time), so a step costs its weights.
+//             Dense calls split the contraction over the CTAs of a cluster and add the parts in rank
+//             order through distributed shared memory; calls by expert run on pairs.
+//
+// Every mbarrier wait is bounded (KernelArgs::wait_limit_ns); a role whose wait ran out sets the
+// device error word and stops; loads and MMAs in flight are waited for (2 s) before the CTA frees its
+// tensor memory and exits.
+#include <mutex>
+
 #include "mx_device.cuh"
 #include "mx_expert.h"
 #include "mx_launch.h"
@@ -16,33 +49,49 @@ using namespace tc;
 
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s: drains, whatever the limit
 
-// Operand P supplies the 128 tensor-memory lanes, operand Q the BN accumulator columns.
-constexpr int kLanes = 128;
+constexpr int kLanes = 128;      // rows of P in a CTA
+constexpr int kColumns = 256;    // most columns of a tile
 constexpr int kStepBytes = 128;  // one scale block of the contraction per step
-
-// CTAS = 2: a pair of SMs shares one 256 x BN tile (cta_group::2). Each CTA loads 128 rows of P and
-// half of Q's rows, holds its 128 lanes of the accumulator and promotes them; the first CTA issues
-// the MMAs for both. Per step an SM then receives 32 KB instead of 48 and reads as much: one CTA
-// alone with 128 x 256 tiles was bound by shared memory (48 KB in, 48 KB read, about 750 of the
-// MMAs' 512 cycles).
-template <int BN, int CTAS>
-struct Shape {
-  static constexpr int kPromoWarps = BN >= 256 ? 8 : 4;
-  static constexpr int kThreads = 128 + kPromoWarps * 32;
-  static constexpr int kCols = BN / (kPromoWarps / 4);  // accumulator columns of a promoting warp
-  static constexpr int kChunk = kCols < 32 ? kCols : 32;
-  static constexpr int kQRowsLoaded = BN / CTAS;
-  static constexpr int kStageBytes = (kLanes + kQRowsLoaded) * kStepBytes;
-  static constexpr int kStages = BN >= 128 ? 6 : 8;
-  static constexpr uint32_t kTmemCols = 2 * BN;  // two accumulators: 32 .. 512 columns
-  static_assert(kStages % 2 == 0, "a stage always meets the same accumulator");
-};
+constexpr int kPromoWarps = 8;
+constexpr int kThreads = 128 + 32 * kPromoWarps;
+constexpr int kWarpCols = kColumns / 2;  // most columns of a promoting warp
+constexpr uint32_t kTmemCols = 2 * kColumns;
+constexpr int kMaxStages = 12, kMaxBufs = 8;
 // scales travel and are released by groups of steps
-constexpr int kScaleGroup = 4, kScaleGroups = 2, kScaleSlots = kScaleGroup * kScaleGroups;
-
-// tile table of the calls by expert: prefix[E + 1] (tiles or blocks before each expert), then
-// start[E + 1] (its first row) -- both int32, E <= 1024
+constexpr int kScaleGroup = 4, kScaleGroups = 4, kScaleSlots = kScaleGroup * kScaleGroups;
 constexpr int kMaxExperts = 1024;
+constexpr int kMaxSplit = 8;
+
+// CTAS: CTAs that share a tile. SWAP: P is B (weights), C is written [column][lane]. P_ROWS, Q_ROWS:
+// the operand has a scale per row (else one per block of 128 rows).
+template <int CTAS_, int MODE_, bool SWAP_, bool P_ROWS_, bool Q_ROWS_, bool F32_>
+struct Config {
+  static constexpr int CTAS = CTAS_, MODE = MODE_;
+  static constexpr bool kSwap = SWAP_, kPRows = P_ROWS_, kQRows = Q_ROWS_, kF32 = F32_;
+  static constexpr bool kFragments = Q_ROWS_;  // how the accumulator is read
+  static constexpr int kPTile = kLanes * CTAS;
+  // floats of a scale slot: one per lane / column (rows form) or one per block of 128
+  static constexpr int kPScales = P_ROWS_ ? kLanes : 4, kQScales = Q_ROWS_ ? kColumns : 4;
+  static constexpr int kSlotFloats = kPScales + kQScales;
+  // ring of stages: four of fixed size, or (swapped) as many as the call's tile size leaves room for
+  static constexpr int kFixedStageBytes = (kLanes + kColumns / CTAS_) * kStepBytes;
+  static constexpr int kRingBytes = SWAP_ ? 172 * 1024 : 4 * kFixedStageBytes;
+  // staging of the output, per promoting warp: two boxes of 32 rows x 128 bytes for tensor-map
+  // stores, or (swapped) 32 tokens x 32 bf16 in rows of 80 bytes
+  static constexpr int kStagingBytes = SWAP_ ? 32 * 80 : 2 * 4096;
+};
+
+template <typename C>
+constexpr int smem_bytes() {
+  return 1024 + C::kRingBytes + kPromoWarps * C::kStagingBytes + kScaleSlots * C::kSlotFloats * 4 +
+         (2 * kMaxStages + kMaxBufs + 2 * kScaleGroups + 1) * 8 + 16 +
+         (C::MODE != kB128Dense ? 2 * (kMaxExperts + 1) * 4 : 0);
+}
+
+struct Divisor {
+  int d;
+  uint32_t magic;
+};
 
 struct KernelArgs {
   const float* p_scales;
@@ -51,27 +100,37 @@ struct KernelArgs {
   const int64_t* offsets;
   unsigned int* err;
   unsigned long long wait_limit_ns;
-  int64_t p_rows, q_rows;      // rows of P and Q: of one expert's matrix, or of the whole of A
-  int64_t p_pitch, q_pitch;    // rows form: floats per scale row; blocks form: floats per block row
-  int64_t p_estride, q_estride;  // blocks form: floats of one expert
-  int64_t ldc;                 // floats / elements per row of C
-  int64_t c_estride;           // elements of one expert's C (wgrad)
-  int64_t rows_total;          // rows the offsets may name
-  int64_t blocks_total;        // wgrad: 128-row blocks of the padded operands
+  int64_t p_rows, q_rows;        // rows of P and Q: of one expert's matrix, or of the whole of A
+  int64_t p_pitch, q_pitch;      // rows form: floats per scale row; blocks form: per block row
+  int64_t p_estride;             // blocks form of P: floats of one expert
+  int64_t ldc;                   // elements per row of C
+  int64_t rows_total;            // rows the offsets may name
+  int64_t blocks_total;          // wgrad: 128-row blocks of the padded operands
   int E;
-  int nk;                      // steps of the contraction (dense, grouped)
-  int p_tiles, q_tiles;        // tiles of the fixed operands (grouped: of the weights only)
-  int tok_tile;                // grouped: rows of one tile of tokens
+  int nk;                        // steps of the contraction (dense, grouped)
+  int p_tiles, q_tiles;          // tiles of the operands (grouped: of P only)
+  Divisor run, per;              // eight rows of tiles; all tiles of one expert (wgrad)
+  int q_tile;                    // most columns of a tile
+  int stages, stage_bytes;       // swapped
+  int bufs_log2;                 // swapped: accumulators, of 512 >> bufs_log2 columns
+  int split;                     // swapped, dense: CTAs of a cluster along the contraction
 };
 
 struct Tile {
-  int p_row, q_row;        // first rows in the tensor maps
-  int p_valid, q_valid;    // rows of the tile that exist
-  int k0;                  // first byte along the contraction
-  int kb0, nk;             // first scale block, steps
-  int64_t p_scale, q_scale;  // first scale: rows form [kb0][row], blocks form [row / 128][kb0]
-  int64_t c;               // element of C at (lane 0, column 0)
+  int p_row, q_row;          // first rows in the tensor maps
+  int p_valid, q_valid;      // rows of the tile that exist (p_valid <= 0: none of this CTA's)
+  int n;                     // columns computed: a multiple of 16 per CTA of the tile
+  int e;
+  int k0;                    // first byte along the contraction
+  int nk;                    // steps
+  int64_t p_scale, q_scale;  // first scale: rows form [kb][row], blocks form [row / 128][kb]
+  int64_t c;                 // element of C at (lane 0, column 0) (swapped)
+  int c_row, c_col;          // the same in C's tensor map (not swapped)
 };
+
+// ------------------------------------------------------------------------------------------
+// instructions
+// ------------------------------------------------------------------------------------------
 
 // The MMAs of one step (K = 128 in four of 32, the first overwriting the accumulator) and the
 // commits that free the operands' stage and hand the accumulator over, issued by one elected lane of
@@ -113,8 +172,13 @@ __device__ __forceinline__ void issue_step(uint32_t d, uint64_t p, uint64_t q, u
         : "memory");
   }
 }
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B E4M3 (bits 7-9
+// and 10-12 = 0), both K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 
-// The pair's rank, barrier and addresses.
+// The cluster's rank, barrier and addresses.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -124,9 +188,9 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {  // the same address of CTA 0
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {  // the same address there
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
 // Box load of a pair: into this CTA, completion counted on the first CTA's barrier.
@@ -136,6 +200,13 @@ __device__ __forceinline__ void tma_load_box_pair(uint32_t dst, const void* map,
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(first_bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_box_3d(const void* map, int x, int y, int z, uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
       : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t slot_addr, uint32_t ncols) {
@@ -151,15 +222,9 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {  // to this CTA only
                : "memory");
 }
 
-// Instruction descriptor, kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B E4M3 (bits 7-9
-// and 10-12 = 0), both K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// N consecutive 32-bit columns of this thread's tensor-memory lane: the load is only issued; the
-// values are there after wait_columns, which names them so that no use moves before it.
-__device__ __forceinline__ void issue_columns(uint32_t taddr, uint32_t (&r)[32]) {
+// 32 fp32 columns of this thread's tensor-memory lane. The load is only issued; the values are there
+// after wait_columns, which names them so that no use moves before it.
+__device__ __forceinline__ void issue_row(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
@@ -171,9 +236,11 @@ __device__ __forceinline__ void issue_columns(uint32_t taddr, uint32_t (&r)[32])
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void issue_columns(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 lanes x 32 columns in fragments: r[4 g + i] of lane l is row l / 4 + 8 (i / 2), column
+// 8 g + 2 (l % 4) + i % 2.
+__device__ __forceinline__ void issue_fragment(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
@@ -189,18 +256,17 @@ __device__ __forceinline__ void wait_columns(uint32_t (&r)[32]) {
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ void wait_columns(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
 
 // Pairs of fp32 in one 64-bit register: one instruction for two (the same rate per value, half the
-// instructions, which the warp that issues the MMAs competes with for fetch and issue).
+// instructions).
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
   return ((uint64_t)hi << 32) | lo;
 }
+__device__ __forceinline__ uint64_t both(float x) {
+  return pair(__float_as_uint(x), __float_as_uint(x));
+}
+__device__ __forceinline__ float first(uint64_t p) { return __uint_as_float((uint32_t)p); }
+__device__ __forceinline__ float second(uint64_t p) { return __uint_as_float((uint32_t)(p >> 32)); }
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -211,180 +277,43 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
-
-// Scale forms of an operand and orientation of the output.
-template <int BN_, int CTAS_, int MODE_, bool SWAP_, bool P_ROWS_, bool Q_ROWS_, bool F32_>
-struct Config {
-  static constexpr int BN = BN_, CTAS = CTAS_, MODE = MODE_;
-  using S = Shape<BN_, CTAS_>;
-  static constexpr int kPRowsTile = kLanes * CTAS_;  // rows of P in a tile
-  static constexpr bool kSwap = SWAP_;    // P is B (weights), C written [column][lane]
-  static constexpr bool kPRows = P_ROWS_, kQRows = Q_ROWS_;
-  static constexpr bool kF32 = F32_;
-  // floats of a scale slot: one per lane / column (rows form) or one per block of 128
-  static constexpr int kPScales = P_ROWS_ ? kLanes : 4, kQScales = Q_ROWS_ ? BN_ : 4;
-  static constexpr int kSlotFloats = kPScales + kQScales;
-};
-
-template <typename C>
-constexpr int smem_bytes() {
-  using S = typename C::S;
-  return 1024 + S::kStages * S::kStageBytes + kScaleSlots * C::kSlotFloats * 4 +
-         (2 * S::kStages + 2 * kScaleGroups + 3) * 8 + 16 +
-         (C::MODE != kB128Dense ? 2 * (kMaxExperts + 1) * 4 : 0);
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
-
-// tiles in all; grouped and wgrad calls read the table
-template <typename C>
-__device__ __forceinline__ int tile_count(const KernelArgs& a, const int* prefix) {
-  if (C::MODE == kB128Dense) return a.p_tiles * a.q_tiles;
-  if (C::MODE == kB128Wgrad) return a.p_tiles * a.q_tiles * a.E;
-  return prefix[a.E] * (C::kSwap ? a.p_tiles : a.q_tiles);
-}
-
-// p tile and q tile of tile t of a p_tiles x q_tiles grid: runs of eight p tiles cross all q
-// tiles, so that the CTAs working at one time share operands in L2
-__device__ __forceinline__ void raster(int t, int p_tiles, int q_tiles, int* p, int* q) {
-  const int run = 8 * q_tiles, first = t / run * 8;
-  const int height = min(8, p_tiles - first);
-  const int in = t % run;
-  *p = first + in % height;
-  *q = in / height;
-}
-
-// The tile as this CTA of a pair sees it: its own 128 rows of P.
-template <typename C>
-__device__ __forceinline__ Tile own_half(const KernelArgs& a, Tile r) {
-  if constexpr (C::CTAS == 2) {
-    const int rank = (int)cluster_rank(), skip = rank * kLanes;
-    r.p_row += skip;
-    r.p_valid = min(kLanes, r.p_valid - skip);  // <= 0: nothing of it exists
-    r.p_scale += C::kPRows ? skip : rank * a.p_pitch;
-    r.c += C::kSwap ? (int64_t)skip : skip * a.ldc;
-  }
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
 }
 
-template <typename C>
-__device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* prefix,
-                                         const int* start) {
-  Tile r;
-  int e = 0, p, q;
-  if (C::MODE == kB128Grouped) {
-    const int fixed = C::kSwap ? a.p_tiles : a.q_tiles;
-    int lo = 0, hi = a.E;  // largest e with prefix[e] * fixed <= t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)prefix[mid] * fixed <= t) {
-        lo = mid;
-      } else {
-        hi = mid;
-      }
-    }
-    e = lo;
-    const int local = t - prefix[e] * fixed, n = prefix[e + 1] - prefix[e];
-    const int tok = local % n, w = local / n;  // token tiles of one weight tile run together
-    const int row = start[e] + tok * a.tok_tile;
-    const int left = start[e + 1] - row;
-    if (C::kSwap) {
-      p = w;
-      r.p_row = (int)(e * a.p_rows) + p * C::kPRowsTile;
-      r.p_valid = (int)min((int64_t)C::kPRowsTile, a.p_rows - (int64_t)p * C::kPRowsTile);
-      r.q_row = row;
-      r.q_valid = min(C::BN, left);
-      r.p_scale = e * a.p_estride + (int64_t)p * C::CTAS * a.p_pitch;
-      r.q_scale = row;
-      r.c = (int64_t)row * a.ldc + p * C::kPRowsTile;
-    } else {
-      q = w;
-      r.p_row = row;
-      r.p_valid = min(C::kPRowsTile, left);
-      r.q_row = (int)(e * a.q_rows) + q * C::BN;
-      r.q_valid = (int)min((int64_t)C::BN, a.q_rows - (int64_t)q * C::BN);
-      r.p_scale = row;
-      r.q_scale = e * a.q_estride + (int64_t)q * (C::BN / kB128) * a.q_pitch;
-      r.c = (int64_t)row * a.ldc + (int64_t)q * C::BN;
-    }
-    r.k0 = r.kb0 = 0;
-    r.nk = a.nk;
-    return own_half<C>(a, r);
-  }
-  r.kb0 = 0;
-  r.nk = a.nk;
-  if (C::MODE == kB128Wgrad) {
-    const int per = a.p_tiles * a.q_tiles;
-    e = t / per;
-    t -= e * per;
-    r.kb0 = prefix[e];
-    r.nk = prefix[e + 1] - prefix[e];
-  }
-  raster(t, a.p_tiles, a.q_tiles, &p, &q);
-  r.k0 = r.kb0 * kStepBytes;
-  r.p_row = p * C::kPRowsTile;
-  r.q_row = q * C::BN;
-  r.p_valid = (int)min((int64_t)C::kPRowsTile, a.p_rows - r.p_row);
-  r.q_valid = (int)min((int64_t)C::BN, a.q_rows - r.q_row);
-  r.p_scale = C::kPRows ? r.kb0 * a.p_pitch + r.p_row : (int64_t)p * C::CTAS * a.p_pitch + r.kb0;
-  r.q_scale = C::kQRows ? r.kb0 * a.q_pitch + r.q_row
-                        : (int64_t)q * (C::BN / kB128) * a.q_pitch + r.kb0;
-  r.c = e * a.c_estride + (C::kSwap ? (int64_t)r.q_row * a.ldc + r.p_row
-                                    : (int64_t)r.p_row * a.ldc + r.q_row);
-  return own_half<C>(a, r);
-}
-
-// Table of the calls by expert: prefix sums of ceil(n_e / unit). Offsets that break their contract
-// are clamped, so that every later access stays inside the operands.
-__device__ __forceinline__ void build_table(const KernelArgs& a, int unit, int limit, int* prefix,
-                                            int* start) {
-  if (threadIdx.x >= 32) return;
-  const int lane = threadIdx.x;
-  int before = 0;
-  if (lane == 0) prefix[0] = 0;
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
-    const int e = e0 + lane;
-    int64_t lo = 0, hi = 0;
-    if (e < a.E) {
-      lo = min(max(load_s64(a.offsets + e), (int64_t)0), a.rows_total);
-      hi = min(max(load_s64(a.offsets + e + 1), lo), a.rows_total);
-      start[e] = (int)lo;
-      if (e == a.E - 1) start[a.E] = (int)hi;
-    }
-    int sum = (int)((hi - lo + unit - 1) / unit);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-      if (lane >= d) sum += up;
-    }
-    if (e < a.E) prefix[e + 1] = min(before + sum, limit);
-    before += __shfl_sync(0xFFFFFFFFu, sum, 31);
-  }
-}
-
-struct Smem {
-  uint8_t* ring;
-  float* scales;        // [kScaleSlots][kSlotFloats]
-  uint64_t* full;
-  uint64_t* empty;
-  uint64_t* acc_full;   // [2]
-  uint64_t* scale_full;   // [kScaleGroups]
-  uint64_t* scale_empty;  // [kScaleGroups]
-  uint64_t* done;
-  uint32_t* tmem_slot;
-  int* prefix;
-  int* start;
-};
-
-// One lane of a warp that runs converged.
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
   return p != 0;
+}
+// One arrival of a converged warp.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// The same at a barrier of the cluster. The default order of one CTA is enough: what it orders are
+// reads of tensor memory, complete before it (release at cluster scope waited over 1000 cycles).
+__device__ __forceinline__ void warp_arrive_cluster(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // Whether the phase is complete. try_wait lets the hardware suspend the thread meanwhile, for longer
 // than most waits last; a call with a limit below that (the give-up self-test) asks without.
-__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity, const KernelArgs& a) {
-  if (a.wait_limit_ns >= 1000000ull) return mbar_try_wait(bar, parity);
+__device__ __forceinline__ bool phase_done_now(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred P;\n\tmbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
@@ -393,6 +322,9 @@ __device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity, const 
       : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
+}
+__device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity, const KernelArgs& a) {
+  return a.wait_limit_ns >= 1000000ull ? mbar_try_wait(bar, parity) : phase_done_now(bar, parity);
 }
 
 // A wait of the whole warp: one vote when the phase is complete; given up after the call's limit
@@ -411,38 +343,268 @@ __device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, bool* f
   }
 }
 
-// The loading and the multiplying warp run converged and issue from one elected lane: addresses
-// and descriptors then stay in uniform registers. Issued from a lone lane's own branch instead,
-// the four MMAs and two commits of a step took over 600 cycles, more than the MMAs themselves.
+// ------------------------------------------------------------------------------------------
+// tiles
+// ------------------------------------------------------------------------------------------
+
+// n / d and the remainder for 0 <= n < 2^31, d given with floor(2^32 / d) + 1: the estimate is right or
+// one too large. (Several roles find their tile at every tile's end; the compiler's divisions there
+// took half a microsecond.)
+__device__ __forceinline__ int divide(int n, Divisor d, int* rest) {
+  int q = d.d == 1 ? n : (int)__umulhi((uint32_t)n, d.magic), r = n - q * d.d;
+  if (r < 0) {
+    --q;
+    r += d.d;
+  }
+  *rest = r;
+  return q;
+}
+// The same for a divisor not known before: in fp32, exact to one below 2^23.
+__device__ __forceinline__ int divide(int n, int d, int* rest) {
+  int q = n < (1 << 23) ? (int)(__int2float_rn(n) * __frcp_rn(__int2float_rn(d))) : n / d;
+  int r = n - q * d;
+  if (r < 0) {
+    --q;
+    r += d;
+  } else if (r >= d) {
+    ++q;
+    r -= d;
+  }
+  *rest = r;
+  return q;
+}
+
+// p tile and q tile of tile t of a p_tiles x q_tiles grid: runs of eight p tiles cross all q
+// tiles, so that the CTAs working at one time share operands in L2
+__device__ __forceinline__ void raster(int t, const KernelArgs& a, int* p, int* q) {
+  int in;
+  const int first = divide(t, a.run, &in) * 8;
+  const int height = min(8, a.p_tiles - first);
+  if (height == 8) {
+    *p = first + (in & 7);
+    *q = in >> 3;
+  } else {
+    *q = divide(in, height, p);
+    *p += first;
+  }
+}
+
+template <typename C>
+__device__ __forceinline__ int tile_count(const KernelArgs& a, const int* prefix) {
+  if (C::MODE == kB128Dense) return a.p_tiles * a.q_tiles;
+  if (C::MODE == kB128Wgrad) return a.p_tiles * a.q_tiles * a.E;
+  return prefix[a.E] * a.p_tiles;
+}
+
+// `rows` rows in `tiles` tiles of nearly one size: the columns of a tile, 16 per CTA
+template <typename C>
+__device__ __forceinline__ int even_columns(int rows, int tiles) {
+  constexpr int unit = 16 * C::CTAS;
+  int rest;
+  return (divide(rows + tiles - 1, tiles, &rest) + unit - 1) / unit * unit;
+}
+
+template <typename C>
+__device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* prefix,
+                                         const int* start) {
+  Tile r;
+  int p, q, kb0 = 0;
+  r.e = 0;
+  r.nk = a.nk;
+  int64_t p_first;  // first row of the P tile in its matrix
+  if (C::MODE == kB128Grouped) {
+    // the last expert with prefix * p_tiles <= t: in two rounds, 32 at a time
+    const int lane = threadIdx.x & 31, width = (a.E + 31) >> 5;
+    const int run = __popc(__ballot_sync(
+        0xFFFFFFFFu, (int64_t)prefix[min((lane + 1) * width, a.E)] * a.p_tiles <= t));
+    const int at = run * width + 1 + lane;
+    const int lo = run * width +
+                   __popc(__ballot_sync(0xFFFFFFFFu, lane < width && at < a.E &&
+                                                         (int64_t)prefix[at] * a.p_tiles <= t));
+    const int local = t - prefix[lo] * a.p_tiles, tiles = prefix[lo + 1] - prefix[lo];
+    const int rows = start[lo + 1] - start[lo];
+    int index = 0;
+    p = local;
+    r.n = (rows + 16 * C::CTAS - 1) / (16 * C::CTAS) * (16 * C::CTAS);
+    if (tiles > 1) {  // the token tiles of one weight tile run together
+      p = divide(local, tiles, &index);
+      r.n = even_columns<C>(rows, tiles);
+    }
+    r.e = lo;
+    q = index * r.n;
+    r.q_row = start[lo] + q;
+    r.q_valid = min(r.n, rows - q);
+    p_first = (int64_t)p * C::kPTile;
+    r.p_row = (int)(lo * a.p_rows + p_first);
+  } else {
+    if (C::MODE == kB128Wgrad) {
+      r.e = divide(t, a.per, &t);
+      kb0 = prefix[r.e];
+      r.nk = prefix[r.e + 1] - kb0;
+    }
+    raster(t, a, &p, &q);
+    r.n = C::kSwap ? even_columns<C>((int)a.q_rows, a.q_tiles) : kColumns;
+    r.q_row = q * r.n;
+    r.q_valid = (int)min((int64_t)r.n, a.q_rows - r.q_row);
+    p_first = (int64_t)p * C::kPTile;
+    r.p_row = (int)p_first;
+  }
+  r.p_valid = (int)min((int64_t)C::kPTile, a.p_rows - p_first);
+  r.k0 = kb0 * kStepBytes;
+  r.p_scale = C::kPRows ? kb0 * a.p_pitch + r.p_row
+                        : r.e * a.p_estride + (int64_t)p * C::CTAS * a.p_pitch + kb0;
+  r.q_scale = C::kQRows ? kb0 * a.q_pitch + r.q_row
+                        : (int64_t)q * (kColumns / kB128) * a.q_pitch + kb0;
+  r.c = (int64_t)r.q_row * a.ldc + p_first;
+  r.c_row = (int)p_first;
+  r.c_col = r.q_row;
+  if constexpr (C::CTAS == 2) {  // this CTA's own 128 rows of P
+    const int rank = (int)cluster_rank(), skip = rank * kLanes;
+    r.p_row += skip;
+    r.p_valid = min(kLanes, r.p_valid - skip);
+    r.p_scale += C::kPRows ? skip : rank * a.p_pitch;
+    r.c += skip;
+    r.c_row += skip;
+  }
+  if (C::kSwap && C::MODE == kB128Dense && a.split > 1) {  // this CTA's share of the contraction
+    const int per = (r.nk + a.split - 1) / a.split, first = (int)cluster_rank() * per;
+    r.k0 += first * kStepBytes;
+    r.p_scale += C::kPRows ? first * a.p_pitch : first;
+    r.q_scale += C::kQRows ? first * a.q_pitch : first;
+    r.nk = max(0, min(per, r.nk - first));
+  }
+  return r;
+}
+
+// Table of the calls by expert: prefix sums of ceil(n_e / unit), and first rows. Offsets that break
+// their contract are clamped and made non-decreasing, so that every later access stays inside the
+// operands. All threads read the offsets (one trip to memory), one warp scans them.
+__device__ __forceinline__ void build_table(const KernelArgs& a, int unit, int limit, int* prefix,
+                                            int* start) {
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+    start[e] = (int)min(max(load_s64(a.offsets + e), (int64_t)0), a.rows_total);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int before = 0, reach = start[0];
+    if (lane == 0) prefix[0] = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      int end = e < a.E ? max(start[e + 1], reach) : reach;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {  // running maximum: non-decreasing ends
+        const int up = __shfl_up_sync(0xFFFFFFFFu, end, d);
+        if (lane >= d) end = max(end, up);
+      }
+      int first = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+      if (lane == 0) first = reach;
+      reach = __shfl_sync(0xFFFFFFFFu, end, 31);
+      int sum = e < a.E ? (end - first + unit - 1) / unit : 0;
+      if (e < a.E) start[e + 1] = end;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += up;
+      }
+      if (e < a.E) prefix[e + 1] = min(before + sum, limit);
+      before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      __syncwarp();
+    }
+  }
+}
+
+struct Smem {
+  uint8_t* ring;
+  uint8_t* staging;       // [kPromoWarps][kStagingBytes]
+  float* scales;          // [kScaleSlots][kSlotFloats]
+  uint64_t* full;         // [stages]: operands landed and accumulator read
+  uint64_t* empty;        // [stages]: operands read
+  uint64_t* acc_full;     // [accumulators]
+  uint64_t* scale_full;   // [kScaleGroups]
+  uint64_t* scale_empty;  // [kScaleGroups]
+  uint64_t* done;
+  uint32_t* tmem_slot;
+  int* prefix;
+  int* start;
+};
+
+template <typename C>
+__device__ __forceinline__ int stage_count(const KernelArgs& a) {
+  return C::kSwap ? a.stages : 4;
+}
+// Accumulators in tensor memory: two of 256 columns, or (swapped) up to eight narrower ones. With few
+// columns a step is short beside the way of its signals (MMA done, accumulator read, next MMA:
+// about 1700 cycles), and as many steps are under way as there are accumulators.
+template <typename C>
+__device__ __forceinline__ int bufs_log2(const KernelArgs& a) {
+  return C::kSwap ? a.bufs_log2 : 1;
+}
+template <typename C>
+__device__ __forceinline__ int stage_bytes(const KernelArgs& a) {
+  return C::kSwap ? a.stage_bytes : C::kFixedStageBytes;
+}
+
+// tiles of this CTA (or pair): t0, t0 + step, ...
+template <typename C>
+__device__ __forceinline__ void tile_range(const KernelArgs& a, int* t0, int* step) {
+  const int group = C::kSwap && C::MODE == kB128Dense ? a.split : C::CTAS;
+  *t0 = blockIdx.x / group;
+  *step = gridDim.x / group;
+}
+
+// ------------------------------------------------------------------------------------------
+// roles. The loading and the multiplying warp run converged and issue from one elected lane, so that
+// addresses and descriptors stay in uniform registers.
+// ------------------------------------------------------------------------------------------
 template <typename C>
 __device__ __forceinline__ void produce(const CUtensorMap& pmap, const CUtensorMap& qmap,
-                                        const KernelArgs& a, const Smem& s, int tiles) {
-  using S = typename C::S;
+                                        const CUtensorMap& qmap16, const KernelArgs& a,
+                                        const Smem& s, int tiles) {
+  const int stages = stage_count<C>(a);
   bool failed = false;
-  int issued = 0, st = 0;
+  int issued = 0, st = 0, t0, step;
   uint32_t parity = 1;  // a fresh barrier's preceding phase counts as complete
-  for (int t = blockIdx.x / C::CTAS; t < tiles && !failed; t += gridDim.x / C::CTAS) {
+  tile_range<C>(a, &t0, &step);
+  for (int t = t0; t < tiles && !failed; t += step) {
     const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+    // rows of Q that this CTA loads: all of the tile's columns, or its half of them
+    const int q_rows = tile.n / C::CTAS;
+    const int q_row = tile.q_row + (C::CTAS == 2 ? (int)cluster_rank() * q_rows : 0);
+    const uint32_t bytes = (uint32_t)(kLanes + q_rows) * kStepBytes;
     for (int kb = 0; kb < tile.nk; ++kb) {
       warp_wait(smem_u32(s.empty + st), parity, &failed, a);
       if (failed) break;
-      const uint32_t bar = smem_u32(s.full + st), dst = smem_u32(s.ring + st * S::kStageBytes);
+      const uint32_t bar = smem_u32(s.full + st);
+      const uint32_t dst = smem_u32(s.ring + st * stage_bytes<C>(a));
       const int x = tile.k0 + kb * kStepBytes;
       if constexpr (C::CTAS == 2) {
-        const uint32_t first = in_first_cta(bar);
-        const int q_row = tile.q_row + (int)cluster_rank() * S::kQRowsLoaded;
+        const uint32_t first = in_cta(bar, 0);
         if (elect_one()) {
-          if (cluster_rank() == 0) mbar_arrive_expect_tx(bar, 2 * S::kStageBytes);
+          if (cluster_rank() == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
           tma_load_box_pair(dst, &pmap, x, tile.p_row, first);
-          tma_load_box_pair(dst + kLanes * kStepBytes, &qmap, x, q_row, first);
+          int r = 0;
+          for (; r + 128 <= q_rows; r += 128) {
+            tma_load_box_pair(dst + (kLanes + r) * kStepBytes, &qmap, x, q_row + r, first);
+          }
+          for (; C::kSwap && r < q_rows; r += 16) {
+            tma_load_box_pair(dst + (kLanes + r) * kStepBytes, &qmap16, x, q_row + r, first);
+          }
         }
       } else if (elect_one()) {
-        mbar_arrive_expect_tx(bar, S::kStageBytes);
+        mbar_arrive_expect_tx(bar, bytes);
         tma_load_box(dst, &pmap, x, tile.p_row, bar);
-        tma_load_box(dst + kLanes * kStepBytes, &qmap, x, tile.q_row, bar);
+        int r = 0;
+        for (; r + 128 <= q_rows; r += 128) {
+          tma_load_box(dst + (kLanes + r) * kStepBytes, &qmap, x, q_row + r, bar);
+        }
+        for (; C::kSwap && r < q_rows; r += 16) {
+          tma_load_box(dst + (kLanes + r) * kStepBytes, &qmap16, x, q_row + r, bar);
+        }
       }
+      __syncwarp();
       ++issued;
-      if (++st == S::kStages) {
+      if (++st == stages) {
         st = 0;
         parity ^= 1;
       }
@@ -452,40 +614,42 @@ __device__ __forceinline__ void produce(const CUtensorMap& pmap, const CUtensorM
   // CTAs' on its barriers, and both leave together; after a give-up, in which the two may not have
   // issued the same steps, each also lets a millisecond pass, a thousand times what a load takes.
   if (C::CTAS == 2 && failed) {
-    const unsigned long long t0 = global_ns();
-    while (global_ns() - t0 < 1000000ull) {
+    const unsigned long long begin = global_ns();
+    while (global_ns() - begin < 1000000ull) {
     }
   }
   if (C::CTAS == 2 && cluster_rank() != 0) return;
   bool drain_failed = false;
-  for (int i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i) {
-    mbar_wait(smem_u32(s.full + i % S::kStages), (i / S::kStages) & 1, &drain_failed, kWaitNs, a.err);
+  for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
+    mbar_wait(smem_u32(s.full + i % stages), (i / stages) & 1, &drain_failed, kWaitNs, a.err);
   }
 }
 
 template <typename C>
 __device__ __forceinline__ void multiply(const KernelArgs& a, const Smem& s, int tiles,
                                          uint32_t tmem) {
-  using S = typename C::S;
-  constexpr uint32_t idesc = idesc_e4m3_f32(C::kPRowsTile, C::BN);
   static_assert(kStepBytes == 128, "issue_step");
+  const int stages = stage_count<C>(a);
   bool failed = false;
-  int st = 0, buf = 0;
+  int st = 0, buf = 0, t0, step;
+  const int bufs = 1 << bufs_log2<C>(a);
   uint32_t full_parity = 0;
-  for (int t = blockIdx.x / C::CTAS; t < tiles && !failed; t += gridDim.x / C::CTAS) {
-    const int nk = get_tile<C>(a, t, s.prefix, s.start).nk;
-    for (int kb = 0; kb < nk; ++kb) {
+  tile_range<C>(a, &t0, &step);
+  for (int t = t0; t < tiles && !failed; t += step) {
+    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+    const uint32_t idesc = idesc_e4m3_f32(C::kPTile, tile.n);
+    for (int kb = 0; kb < tile.nk; ++kb) {
       warp_wait(smem_u32(s.full + st), full_parity, &failed, a);
       if (failed) break;
       tc_fence_after();
-      const uint64_t p = desc_sw128(smem_u32(s.ring + st * S::kStageBytes));
-      issue_step<C::CTAS>(tmem + buf * C::BN, p, p + (kLanes * kStepBytes >> 4), idesc, smem_u32(s.empty + st),
-                 smem_u32(s.acc_full + buf));
-      if (++st == S::kStages) {
+      const uint64_t p = desc_sw128(smem_u32(s.ring + st * stage_bytes<C>(a)));
+      issue_step<C::CTAS>(tmem + buf * (kTmemCols >> bufs_log2<C>(a)), p, p + (kLanes * kStepBytes >> 4), idesc,
+                          smem_u32(s.empty + st), smem_u32(s.acc_full + buf));
+      if (++st == stages) {
         st = 0;
         full_parity ^= 1;
       }
-      buf ^= 1;
+      buf = (buf + 1) & (bufs - 1);
     }
   }
   if (elect_one()) {
@@ -515,8 +679,9 @@ template <typename C>
 __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s, int tiles) {
   const int lane = threadIdx.x & 31;
   bool failed = false;
-  int group = 0;
-  for (int t = blockIdx.x / C::CTAS; t < tiles && !failed; t += gridDim.x / C::CTAS) {
+  int group = 0, t0, step;
+  tile_range<C>(a, &t0, &step);
+  for (int t = t0; t < tiles && !failed; t += step) {
     const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
     for (int kb0 = 0; kb0 < tile.nk; kb0 += kScaleGroup, ++group) {
       const int g = group % kScaleGroups;
@@ -539,18 +704,17 @@ __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s,
         dst += C::kPScales;
         if (C::kQRows) {
           const float* src = a.q_scales + tile.q_scale + kb * a.q_pitch;
-#pragma unroll
-          for (int i = 0; i < (C::BN + 31) / 32; ++i) {
-            const int c = 32 * i + lane;
+          for (int c = lane; c < tile.n; c += 32) {
             const bool ok = c < tile.q_valid;
-            if (c < C::BN) copy_scale(dst + c, ok ? src + c : a.q_scales, ok);
+            copy_scale(dst + c, ok ? src + c : a.q_scales, ok);
           }
-        } else if (lane < C::BN / kB128) {
+        } else if (lane < kColumns / kB128) {
           const bool ok = lane * kB128 < tile.q_valid;
           copy_scale(dst + lane,
                      ok ? a.q_scales + tile.q_scale + lane * a.q_pitch + kb : a.q_scales, ok);
         }
       }
+      __syncwarp();
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                        smem_u32(s.scale_full + g))
                    : "memory");
@@ -559,195 +723,425 @@ __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s,
   asm volatile("cp.async.wait_all;" ::: "memory");  // none lands after the CTA's shared memory goes
 }
 
-// One arrival of a converged warp.
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-      "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-// The same at a barrier of the cluster. The default order of one CTA is enough: what it orders are
-// reads of tensor memory, complete before it (release at cluster scope waited over 1000 cycles).
-__device__ __forceinline__ void warp_arrive_cluster(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
-      "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-// The promoting warps: warp w holds lanes 32 (w % 4) .. and columns kCols (w / 4) .. of the tile in
-// registers, adds each step's accumulator times the step's scales, and writes the tile.
+// A promoting warp's way through the steps: the barriers of one step around its reads. (Asking the
+// next step's barrier before this step's sums, to have only the answer left, measured slower: 436
+// against 360 us at 8192^3. The answer is mostly no by then and the question costs 60 cycles.)
 template <typename C>
-__device__ __forceinline__ void promote(const KernelArgs& a, const Smem& s, int tiles,
-                                        uint32_t tmem, int pw) {
-  using S = typename C::S;
-  constexpr int kCols = S::kCols, kChunk = S::kChunk;
-  const int lane = threadIdx.x & 31;
-  const int row = (pw & 3) * 32 + lane, col0 = (pw >> 2) * kCols;
-  const uint32_t tbase = tmem + ((uint32_t)((pw & 3) * 32) << 16) + col0;
+struct Steps {
+  const KernelArgs& a;
+  const Smem& s;
+  const int stages, log2;
+  uint32_t full0;        // the barriers on which read accumulators are reported
+  int it = 0, st2;       // step, stage of the step that gets its accumulator next
+  uint32_t group = 0;
   bool failed = false;
-  int it = 0;
-  // A step's stage is full once its operands have landed and its accumulator has been read: both
-  // arrive on one barrier, so the multiplying warp waits once per step. The first two steps find
-  // their accumulators free.
-  const uint32_t full0 = C::CTAS == 2 ? in_first_cta(smem_u32(s.full)) : smem_u32(s.full);
-  auto hand_back = [&](int st) {
+
+  __device__ __forceinline__ Steps(const KernelArgs& a_, const Smem& s_)
+      : a(a_), s(s_), stages(stage_count<C>(a_)), log2(bufs_log2<C>(a_)) {
+    full0 = C::CTAS == 2 ? in_cta(smem_u32(s.full), 0) : smem_u32(s.full);
+    for (int i = 0; i < 1 << log2; ++i) hand_back(i);  // the first steps find theirs free
+    st2 = 1 << log2;
+    if (st2 == stages) st2 = 0;
+  }
+  __device__ __forceinline__ void hand_back(int st) {
     if constexpr (C::CTAS == 2) {
       warp_arrive_cluster(full0 + 8 * st);
     } else {
       warp_arrive(full0 + 8 * st);
     }
-  };
-  hand_back(0);
-  hand_back(1);
-  int st2 = 2;  // stage of the step after next
-  uint32_t group = 0;
-  for (int t = blockIdx.x / C::CTAS; t < tiles; t += gridDim.x / C::CTAS) {
-    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    const bool live = row < tile.p_valid;
-    uint64_t sums[kCols / 2];  // fp32 pairs
-#pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) sums[i] = 0u;
-    for (int kb = 0; kb < tile.nk; ++kb, ++it) {
-      const int buf = it & 1, g = group % kScaleGroups, in = kb % kScaleGroup;
-      const float* ps = s.scales + (g * kScaleGroup + in) * C::kSlotFloats;
-      const float* cs = ps + C::kPScales + (C::kQRows ? col0 : col0 / kB128);
-      if (in == 0) {
-        warp_wait(smem_u32(s.scale_full + g), (group / kScaleGroups) & 1, &failed, a);
-      }
-      const float m = ps[C::kPRows ? row : 0] * (C::kQRows ? 1.0f : cs[0]);
-      const uint64_t m2 = pair(__float_as_uint(m), __float_as_uint(m));
-      warp_wait(smem_u32(s.acc_full + buf), (it >> 1) & 1, &failed, a);
-      if (failed) break;
-      tc_fence_after();
-      // The accumulator goes back to the MMAs as soon as it is in registers: with two of them, a
-      // step cannot be shorter than half of (MMA + signal + read + signal), so the reads come first
-      // and the sums after. Three of four chunks fit beside the sums; the fourth follows the first's.
-      // With a scale per column two chunks at a time: the scales' own reads from shared memory need
-      // registers to run ahead, else each of them is waited for (1300 cycles a step).
-      constexpr int kChunks = kCols / kChunk;
-      constexpr int kFirst = kChunks > 3 ? (C::kQRows ? 2 : 3) : kChunks;
-      uint32_t v[kFirst][kChunk];
-      auto add = [&](int ch, const uint32_t (&w)[kChunk]) {
-#pragma unroll
-        for (int i = 0; i < kChunk; i += 4) {
-          uint64_t* d = sums + (ch * kChunk + i) / 2;
-          uint64_t m01 = m2, m23 = m2;
-          if (C::kQRows) {
-            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(cs + ch * kChunk + i);
-            m01 = mul2(m2, q.x);
-            m23 = mul2(m2, q.y);
-          }
-          d[0] = fma2(pair(w[i], w[i + 1]), m01, d[0]);
-          d[1] = fma2(pair(w[i + 2], w[i + 3]), m23, d[1]);
-        }
-      };
-      const uint32_t src = tbase + buf * C::BN;
-#pragma unroll
-      for (int ch = 0; ch < kFirst; ++ch) issue_columns(src + ch * kChunk, v[ch]);
-#pragma unroll
-      for (int ch = 0; ch < kFirst; ++ch) wait_columns(v[ch]);
-#pragma unroll
-      for (int ch = kFirst; ch < kChunks; ++ch) {
-        add(ch - kFirst, v[ch - kFirst]);
-        issue_columns(src + ch * kChunk, v[ch - kFirst]);
-      }
-#pragma unroll
-      for (int ch = kFirst; ch < kChunks; ++ch) wait_columns(v[ch - kFirst]);
-      tc_fence_before();
-      hand_back(st2);
-      if (++st2 == S::kStages) st2 = 0;
-#pragma unroll
-      for (int ch = kChunks - kFirst; ch < kChunks; ++ch) add(ch, v[ch % kFirst]);
-      if (in == kScaleGroup - 1 || kb == tile.nk - 1) {
-        warp_arrive(smem_u32(s.scale_empty + g));
-        ++group;
-      }
+  }
+  // scales of step kb of the tile
+  __device__ __forceinline__ const float* scales(int kb) {
+    const int g = group % kScaleGroups, in = kb % kScaleGroup;
+    if (in == 0) {
+      warp_wait(smem_u32(s.scale_full + g), (group / kScaleGroups) & 1, &failed, a);
     }
-    if (failed) {
-      // The steps that may have been loaded are handed back unread, so that the loading warp sees
-      // its copies land. Steps it and it + 1 have their arrivals already and their stages may still
-      // be in that phase, so the steps that follow on those two stages are left out: a second
-      // arrival there would complete a phase before its copies do.
-      for (int i = 0; i < S::kStages - 2; ++i) hand_back((st2 + i) % S::kStages);
-      return;
+    return s.scales + (g * kScaleGroup + in) * C::kSlotFloats;
+  }
+  __device__ __forceinline__ bool accumulator() {
+    warp_wait(smem_u32(s.acc_full + (it & ((1 << log2) - 1))), (it >> log2) & 1, &failed, a);
+    if (failed) return false;
+    tc_fence_after();
+    return true;
+  }
+  __device__ __forceinline__ uint32_t column() const {  // the step's accumulator
+    return (it & ((1 << log2) - 1)) * (kTmemCols >> log2);
+  }
+  __device__ __forceinline__ void accumulator_read() {
+    tc_fence_before();
+    hand_back(st2);
+    if (++st2 == stages) st2 = 0;
+  }
+  __device__ __forceinline__ bool group_ends(int kb, int nk) const {
+    return kb % kScaleGroup == kScaleGroup - 1 || kb == nk - 1;
+  }
+  __device__ __forceinline__ void end(int kb, int nk) {
+    if (group_ends(kb, nk)) {
+      warp_arrive(smem_u32(s.scale_empty + group % kScaleGroups));
+      ++group;
     }
-    if (!live) continue;
-    float acc[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; i += 2) {
-      acc[i] = __uint_as_float((uint32_t)sums[i / 2]);
-      acc[i + 1] = __uint_as_float((uint32_t)(sums[i / 2] >> 32));
+    ++it;
+  }
+  // The steps that may have been loaded are handed back unread, so that the loading warp sees its
+  // copies land. Of `bufs` accumulators, steps it .. it + bufs - 1 have their arrivals already and
+  // their stages may still be in that phase, so the steps that follow on those stages are left out:
+  // a second arrival there would complete a phase before its copies do.
+  __device__ __forceinline__ void give_up() {
+    for (int i = 0; i < stages - (1 << log2); ++i) hand_back((st2 + i) % stages);
+  }
+};
+
+// Staging buffers of a promoting warp's tensor-map stores: 32 rows x 128 bytes, 16-byte chunk q of
+// row r at q ^ (r % 8), two in turn.
+struct Boxes {
+  uint8_t* base;
+  int turn = 0;
+  __device__ __forceinline__ uint8_t* next() {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    turn ^= 1;
+    return base + turn * 4096;
+  }
+  __device__ __forceinline__ void store(const CUtensorMap& cmap, uint8_t* box, int x, int y, int z) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      tma_store_box_3d(&cmap, x, y, z, smem_u32(box));
+      bulk_commit_group();
     }
-    if (C::kSwap) {  // lane = column of C, a warp writes 32 neighbours of each row
+  }
+  __device__ __forceinline__ void drain() {  // read before the CTA's shared memory goes away
+    if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
+  }
+};
+
+// Swapped shape: the groups of eight columns (tokens) first, first + every, .. of a warp's fragments to
+// C [token][lane]. bf16 goes through shared memory, transposed on the way (8 tokens x 32 lanes = 64
+// bytes each), so that a lane stores 16 bytes of one token.
+template <typename C>
+__device__ __forceinline__ void store_swapped(const KernelArgs& a, const Smem& s, const Tile& tile,
+                                              int pw, const uint64_t (&sums)[kWarpCols / 2],
+                                              int first_group, int every) {
+  const int lane = threadIdx.x & 31, row0 = (pw & 3) * 32, lr = lane >> 2, lc = (lane & 3) * 2;
+  const int cols = tile.n / 2, col0 = (pw >> 2) * cols;
+  uint8_t* staging = s.staging + pw * C::kStagingBytes;
+  // what a lane stores of a group: token lane / 4, 8 lanes' worth from 8 (lane % 4) on
+  const int part = (lane & 3) * 8;
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        if (col0 + i >= tile.q_valid) break;
-        const int64_t at = tile.c + (int64_t)(col0 + i) * a.ldc + row;
-        if (C::kF32) {
-          static_cast<float*>(a.c)[at] = acc[i];
-        } else {
-          uint16_t h;
-          asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(acc[i]));
-          static_cast<uint16_t*>(a.c)[at] = h;
-        }
+  for (int gi = 0; gi < kWarpCols / 8; ++gi) {
+    if (gi * 8 >= cols || gi % every != first_group) continue;
+    if constexpr (C::kF32) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = row0 + 8 * r + lr, col = col0 + gi * 8 + lc;
+        float* o = static_cast<float*>(a.c) + tile.c + col * a.ldc + row;
+        if (row < tile.p_valid && col < tile.q_valid) o[0] = first(sums[gi * 4 + r]);
+        if (row < tile.p_valid && col + 1 < tile.q_valid) o[a.ldc] = second(sums[gi * 4 + r]);
       }
-    } else {  // lane = row of C, 16-byte pieces (columns in eights: N % 8 == 0)
-      const int64_t at = tile.c + (int64_t)row * a.ldc + col0;
+    } else {
+      uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < kCols; i += 8) {
-        if (col0 + i >= tile.q_valid) break;
-        if (C::kF32) {
-          float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.c) + at + i);
-          o[0] = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-          o[1] = make_float4(acc[i + 4], acc[i + 5], acc[i + 6], acc[i + 7]);
-        } else {
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            asm("cvt.rn.bf16x2.f32 %0, %2, %1;"
-                : "=r"(o[j])
-                : "f"(acc[i + 2 * j]), "f"(acc[i + 2 * j + 1]));
-          }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c) + at + i) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
+      for (int r = 0; r < 4; ++r) h[r] = bf16_pair(first(sums[gi * 4 + r]), second(sums[gi * 4 + r]));
+      uint8_t* slot = staging + (gi & 3) * 8 * 80;
+      asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                       smem_u32(slot + (lane & 7) * 80 + (lane >> 3) * 16)),
+                   "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                   : "memory");
+      __syncwarp();
+      const uint4 v = *reinterpret_cast<const uint4*>(slot + lr * 80 + part * 2);
+      const int col = col0 + gi * 8 + lr;
+      if (col < tile.q_valid && row0 + part < tile.p_valid) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.c) + tile.c + col * a.ldc + row0 + part) = v;
       }
     }
   }
+  __syncwarp();  // the staging is free again
+}
+
+// The promoting warps of the rows shape: warp w holds lanes 32 (w % 4) .. and columns 128 (w / 4) ..
+// of the tile, a row per thread.
+template <typename C>
+__device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const KernelArgs& a,
+                                             const Smem& s, int tiles, uint32_t tmem, int pw) {
+  const int lane = threadIdx.x & 31, row = (pw & 3) * 32 + lane, half = pw >> 2;
+  const uint32_t tbase = tmem + ((uint32_t)((pw & 3) * 32) << 16) + half * kWarpCols;
+  Steps<C> steps(a, s);
+  Boxes boxes{s.staging + pw * C::kStagingBytes};
+  int t0, step;
+  tile_range<C>(a, &t0, &step);
+  for (int t = t0; t < tiles; t += step) {
+    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+    uint64_t sums[kWarpCols / 2];
+#pragma unroll
+    for (int i = 0; i < kWarpCols / 2; ++i) sums[i] = 0u;
+    for (int kb = 0; kb < tile.nk; ++kb) {
+      const float* sc = steps.scales(kb);
+      const uint64_t m = both(sc[row] * sc[C::kPScales + half]);
+      if (!steps.accumulator()) break;
+      // The accumulator goes back as soon as it is in registers; two of its four chunks fit beside
+      // the sums, each of the others follows one that is added.
+      uint32_t v[2][32];
+      auto add = [&](int ch) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          uint64_t& d = sums[ch * 16 + i / 2];
+          d = fma2(pair(v[ch & 1][i], v[ch & 1][i + 1]), m, d);
+        }
+      };
+      const uint32_t src = tbase + steps.column();
+      issue_row(src, v[0]);
+      issue_row(src + 32, v[1]);
+      wait_columns(v[0]);
+      wait_columns(v[1]);
+      add(0);
+      issue_row(src + 64, v[0]);
+      add(1);
+      issue_row(src + 96, v[1]);
+      wait_columns(v[0]);
+      wait_columns(v[1]);
+      steps.accumulator_read();
+      add(2);
+      add(3);
+      steps.end(kb, tile.nk);
+    }
+    if (steps.failed) {
+      steps.give_up();
+      break;
+    }
+    if (tile.p_valid <= (pw & 3) * 32) continue;  // none of the warp's rows exists
+    constexpr int kBoxCols = C::kF32 ? 32 : 64;
+#pragma unroll
+    for (int b = 0; b < kWarpCols / kBoxCols; ++b) {
+      if (half * kWarpCols + b * kBoxCols >= tile.q_valid) break;
+      uint8_t* box = boxes.next();
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {  // 16 bytes: four fp32 or eight bf16
+        const uint64_t* d = sums + (b * kBoxCols + q * (kBoxCols / 8)) / 2;
+        uint4 o;
+        if constexpr (C::kF32) {
+          o = make_uint4((uint32_t)d[0], (uint32_t)(d[0] >> 32), (uint32_t)d[1], (uint32_t)(d[1] >> 32));
+        } else {
+          o = make_uint4(bf16_pair(first(d[0]), second(d[0])), bf16_pair(first(d[1]), second(d[1])),
+                         bf16_pair(first(d[2]), second(d[2])), bf16_pair(first(d[3]), second(d[3])));
+        }
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = o;
+      }
+      boxes.store(cmap, box, tile.c_col + half * kWarpCols + b * kBoxCols,
+                  tile.c_row + (pw & 3) * 32, tile.e);
+    }
+  }
+  boxes.drain();
+}
+
+// The promoting warps of the columns and swapped shapes: warp w holds lanes 32 (w % 4) .. and half
+// w / 4 of the tile's columns in fragments: sums[(ch * 4 + g) * 4 + r] of lane l are the columns
+// 32 ch + 8 g + 2 (l % 4) + {0, 1} of row 8 r + l / 4.
+template <typename C>
+__device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const KernelArgs& a,
+                                                const Smem& s, int tiles, uint32_t tmem, int pw,
+                                                uint64_t (&sums)[kWarpCols / 2], Tile* last) {
+  constexpr int kChunks = kWarpCols / 32;
+  const int lane = threadIdx.x & 31, row0 = (pw & 3) * 32, lr = lane >> 2, lc = (lane & 3) * 2;
+  Steps<C> steps(a, s);
+  Boxes boxes{s.staging + pw * C::kStagingBytes};
+  int t0, step;
+  tile_range<C>(a, &t0, &step);
+  for (int t = t0; t < tiles; t += step) {
+    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+    const int cols = tile.n / 2, col0 = (pw >> 2) * cols;  // this warp's columns
+    const int chunks = C::kSwap ? (cols + 31) / 32 : kChunks;
+    const uint32_t tbase = tmem + ((uint32_t)row0 << 16) + col0;
+#pragma unroll
+    for (int i = 0; i < kWarpCols / 2; ++i) sums[i] = 0u;
+    for (int kb = 0; kb < tile.nk; ++kb) {
+      const float* sc = steps.scales(kb);
+      const float* qs = sc + C::kPScales + col0 + lc;
+      uint64_t m[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (C::kPRows || r == 0) m[r] = both(sc[C::kPRows ? row0 + 8 * r + lr : 0]);
+      }
+      uint64_t q[4];  // of the chunk that is added next
+      auto column_scales = [&](int ch) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          q[g] = *reinterpret_cast<const uint64_t*>(qs + ch * 32 + g * 8);
+          if (!C::kPRows) q[g] = mul2(q[g], m[0]);
+        }
+      };
+      column_scales(0);
+      if (!steps.accumulator()) break;
+      uint32_t v[2][32];
+      const uint32_t src = tbase + steps.column();
+      auto issue = [&](int ch) {
+        issue_fragment(src + ch * 32, v[ch & 1]);
+        issue_fragment(src + ch * 32 + (16u << 16), v[ch & 1] + 16);
+      };
+      auto add = [&](int ch) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint64_t qg = q[g];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t* w = v[ch & 1] + (r >> 1) * 16 + g * 4 + (r & 1) * 2;
+            uint64_t& d = sums[(ch * 4 + g) * 4 + r];
+            d = fma2(pair(w[0], w[1]), C::kPRows ? mul2(qg, m[r]) : qg, d);
+          }
+        }
+      };
+      issue(0);
+      if (chunks > 1) issue(1);
+      wait_columns(v[0]);
+      wait_columns(v[1]);
+      if (chunks > 2) {
+        add(0);
+        issue(2);
+        column_scales(1);
+        if (chunks > 3) {
+          add(1);
+          issue(3);
+          column_scales(2);
+        }
+        wait_columns(v[0]);
+        wait_columns(v[1]);
+      }
+      steps.accumulator_read();
+      if (chunks <= 2) {
+        add(0);
+        if (chunks == 2) {
+          column_scales(1);
+          add(1);
+        }
+      } else if (chunks == 3) {
+        add(1);
+        column_scales(2);
+        add(2);
+      } else {
+        add(2);
+        column_scales(3);
+        add(3);
+      }
+      steps.end(kb, tile.nk);
+    }
+    if (steps.failed) {
+      steps.give_up();
+      break;
+    }
+    *last = tile;
+    if constexpr (C::kSwap) {
+      if (C::MODE == kB128Dense && a.split > 1) break;  // one tile; the cluster adds the parts
+      store_swapped<C>(a, s, tile, pw, sums, 0, 1);
+    } else {
+      if (tile.p_valid <= row0) continue;
+      constexpr int kBoxCols = C::kF32 ? 32 : 64;
+#pragma unroll
+      for (int b = 0; b < kWarpCols / kBoxCols; ++b) {
+        if (col0 + b * kBoxCols >= tile.q_valid) break;
+        uint8_t* box = boxes.next();
+#pragma unroll
+        for (int g = 0; g < kBoxCols / 8; ++g) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint64_t d = sums[(b * (kBoxCols / 8) + g) * 4 + r];
+            const int R = 8 * r + lr;
+            if constexpr (C::kF32) {
+              const int byte = (g * 8 + lc) * 4;
+              *reinterpret_cast<uint64_t*>(box + R * 128 + (((byte >> 4) ^ (R & 7)) << 4) +
+                                           (byte & 15)) = d;
+            } else {
+              const int byte = (g * 8 + lc) * 2;
+              *reinterpret_cast<uint32_t*>(box + R * 128 + (((byte >> 4) ^ (R & 7)) << 4) +
+                                           (byte & 15)) = bf16_pair(first(d), second(d));
+            }
+          }
+        }
+        boxes.store(cmap, box, tile.c_col + col0 + b * kBoxCols, tile.c_row + row0, tile.e);
+      }
+    }
+  }
+  if (!C::kSwap) boxes.drain();
+}
+
+// Adds the parts of a tile whose contraction the CTAs of a cluster shared: every CTA leaves its sums in
+// its own (now idle) ring, then each takes its share of the groups of columns, adds the parts in
+// rank order and writes them.
+template <typename C>
+__device__ __forceinline__ void add_parts(const KernelArgs& a, const Smem& s, const Tile& tile, int pw,
+                                          uint64_t (&sums)[kWarpCols / 2]) {
+  const int tid = threadIdx.x - 128, rank = (int)cluster_rank();
+  const int groups = tile.n / 2 / 8;  // of eight columns, per warp
+  uint64_t* mine = reinterpret_cast<uint64_t*>(s.ring) + tid;
+#pragma unroll
+  for (int i = 0; i < kWarpCols / 2; ++i) {
+    if (i / 4 < groups) mine[i * (kPromoWarps * 32)] = sums[i];
+  }
+  cluster_sync();
+  uint32_t from[kMaxSplit];
+#pragma unroll
+  for (int r = 0; r < kMaxSplit; ++r) from[r] = in_cta(smem_u32(mine), r < a.split ? r : 0);
+#pragma unroll
+  for (int gi = 0; gi < kWarpCols / 8; ++gi) {
+    if (gi >= groups || gi % a.split != rank) continue;
+    uint64_t v[kMaxSplit][4];  // all on their way before the first is added
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (r < a.split) {
+          asm volatile("ld.shared::cluster.b64 %0, [%1];"
+                       : "=l"(v[r][i])
+                       : "r"(from[r] + (gi * 4 + i) * (kPromoWarps * 32 * 8)));
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint64_t sum = v[0][i];
+#pragma unroll
+      for (int r = 1; r < kMaxSplit; ++r) {
+        if (r < a.split) sum = add2(sum, v[r][i]);
+      }
+      sums[gi * 4 + i] = sum;
+    }
+  }
+  store_swapped<C>(a, s, tile, pw, sums, rank, a.split);
+  cluster_sync();  // the parts are read before their CTAs leave
 }
 
 template <typename C>
-__global__ void __launch_bounds__(C::S::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     b128_gemm_kernel(const __grid_constant__ CUtensorMap pmap,
-                     const __grid_constant__ CUtensorMap qmap, KernelArgs a) {
-  using S = typename C::S;
+                     const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap qmap16,
+                     const __grid_constant__ CUtensorMap cmap, KernelArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Smem s;
   s.ring = smem;
-  s.scales = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
+  s.staging = smem + C::kRingBytes;
+  s.scales = reinterpret_cast<float*>(s.staging + kPromoWarps * C::kStagingBytes);
   s.full = reinterpret_cast<uint64_t*>(s.scales + kScaleSlots * C::kSlotFloats);
-  s.empty = s.full + S::kStages;
-  s.acc_full = s.empty + S::kStages;
-  s.scale_full = s.acc_full + 2;
+  s.empty = s.full + kMaxStages;
+  s.acc_full = s.empty + kMaxStages;
+  s.scale_full = s.acc_full + kMaxBufs;
   s.scale_empty = s.scale_full + kScaleGroups;
   s.done = s.scale_empty + kScaleGroups;
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.done + 1);
   s.prefix = reinterpret_cast<int*>(s.tmem_slot + 2);
   s.start = s.prefix + kMaxExperts + 1;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);  // uniform
+  const bool parts = C::kSwap && C::MODE == kB128Dense && a.split > 1;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(smem_u32(s.full + i), 1 + C::CTAS * S::kPromoWarps);
+    for (int i = 0; i < stage_count<C>(a); ++i) {
+      mbar_init(smem_u32(s.full + i), 1 + C::CTAS * kPromoWarps);
       mbar_init(smem_u32(s.empty + i), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(s.acc_full + i), 1);
+    for (int i = 0; i < 1 << bufs_log2<C>(a); ++i) mbar_init(smem_u32(s.acc_full + i), 1);
     for (int i = 0; i < kScaleGroups; ++i) {
       mbar_init(smem_u32(s.scale_full + i), 32);
-      mbar_init(smem_u32(s.scale_empty + i), S::kPromoWarps);
+      mbar_init(smem_u32(s.scale_empty + i), kPromoWarps);
     }
     mbar_init(smem_u32(s.done), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -755,13 +1149,13 @@ __global__ void __launch_bounds__(C::S::kThreads, 1)
   pdl_wait();
   if (warp == 1) {
     if constexpr (C::CTAS == 2) {
-      tmem_alloc_pair(smem_u32(s.tmem_slot), S::kTmemCols);
+      tmem_alloc_pair(smem_u32(s.tmem_slot), kTmemCols);
     } else {
-      tmem_alloc(smem_u32(s.tmem_slot), S::kTmemCols);
+      tmem_alloc(smem_u32(s.tmem_slot), kTmemCols);
       tmem_relinquish();
     }
   }
-  if (C::MODE == kB128Grouped) build_table(a, a.tok_tile, INT32_MAX, s.prefix, s.start);
+  if (C::MODE == kB128Grouped) build_table(a, a.q_tile, INT32_MAX, s.prefix, s.start);
   if (C::MODE == kB128Wgrad) build_table(a, kB128, (int)a.blocks_total, s.prefix, s.start);
   tc_fence_before();
   __syncthreads();
@@ -769,16 +1163,33 @@ __global__ void __launch_bounds__(C::S::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s.tmem_slot;
   const int tiles = tile_count<C>(a, s.prefix);
-  // The promoting warps hold kCols sums and two chunks in registers: of a launch with eight of them
-  // the others give theirs up (40 x 128 + 232 x 256 = 168 x 384, the launch's total).
+  // The promoting warps hold their sums and two or three chunks in registers: the others give theirs
+  // up (40 x 128 + 232 x 256 = 168 x 384, the launch's total).
   if (warp < 4) {
-    if (S::kPromoWarps == 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0) produce<C>(pmap, qmap, a, s, tiles);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) produce<C>(pmap, qmap, qmap16, a, s, tiles);
     if (warp == 1 && (C::CTAS == 1 || cluster_rank() == 0)) multiply<C>(a, s, tiles, tmem);
     if (warp == 2) fetch_scales<C>(a, s, tiles);
+    __syncwarp();
+    if (parts) {  // add_parts' two
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
-    if (S::kPromoWarps == 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    promote<C>(a, s, tiles, tmem, warp - 4);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (C::kFragments) {
+      uint64_t sums[kWarpCols / 2];
+      Tile last;
+      promote_columns<C>(cmap, a, s, tiles, tmem, warp - 4, sums, &last);
+      if constexpr (C::kSwap && C::MODE == kB128Dense) {
+        if (parts) {
+          last = get_tile<C>(a, blockIdx.x / a.split, s.prefix, s.start);
+          add_parts<C>(a, s, last, warp - 4, sums);
+        }
+      }
+    } else {
+      promote_rows<C>(cmap, a, s, tiles, tmem, warp - 4);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -786,13 +1197,16 @@ __global__ void __launch_bounds__(C::S::kThreads, 1)
   tc_fence_after();
   if (warp == 1) {
     if constexpr (C::CTAS == 2) {
-      tmem_dealloc_pair(tmem, S::kTmemCols);
+      tmem_dealloc_pair(tmem, kTmemCols);
     } else {
-      tmem_dealloc(tmem, S::kTmemCols);
+      tmem_dealloc(tmem, kTmemCols);
     }
   }
 }
 
+// ------------------------------------------------------------------------------------------
+// host
+// ------------------------------------------------------------------------------------------
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // launch_pdl with clusters of `ctas` CTAs.
@@ -818,78 +1232,130 @@ cudaError_t launch_clusters(void (*kernel)(Params...), unsigned grid, int thread
 }
 
 template <typename C>
-cudaError_t launch_config(const B128GemmArgs& g, cudaStream_t stream) {
-  using S = typename C::S;
-  auto* kernel = &b128_gemm_kernel<C>;
-  constexpr int smem = smem_bytes<C>();
-  const int slots = resident_ctas(reinterpret_cast<const void*>(kernel), S::kThreads, smem, 1);
+int slot_count() {
+  return resident_ctas(reinterpret_cast<const void*>(&b128_gemm_kernel<C>), kThreads,
+                       smem_bytes<C>(), 1);
+}
+
+// q_tile: most columns of a tile (swapped); split: CTAs along the contraction (swapped, dense)
+template <typename C>
+cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStream_t stream) {
+  const int slots = slot_count<C>();
   if (slots <= 0) return cudaErrorInvalidConfiguration;
   KernelArgs a{};
   const int64_t kblocks = ceil_div(g.K, kB128), nblocks = ceil_div(g.N, kB128);
   const bool grouped = C::MODE == kB128Grouped;
-  // rows of one matrix of each operand, and of all of its tensor map
-  const int64_t arows = g.M, brows = g.N, bmap = grouped ? g.N * g.E : g.N;
-  const int64_t apitch = g.M;
-  const int64_t bpitch = g.b_rows ? g.N : kblocks;
-  const int64_t bestride = g.b_rows ? 0 : nblocks * kblocks;
+  const int64_t bmap = grouped ? g.N * g.E : g.N;  // rows of B's tensor map
+  const int64_t apitch = g.M, bpitch = g.b_rows ? g.N : kblocks;
   a.p_scales = C::kSwap ? g.b_scales : g.a_scales;
   a.q_scales = C::kSwap ? g.a_scales : g.b_scales;
-  a.p_rows = C::kSwap ? brows : arows;
-  a.q_rows = C::kSwap ? arows : brows;
+  a.p_rows = C::kSwap ? g.N : g.M;
+  a.q_rows = C::kSwap ? g.M : g.N;
   a.p_pitch = C::kSwap ? bpitch : apitch;
   a.q_pitch = C::kSwap ? apitch : bpitch;
-  a.p_estride = C::kSwap ? bestride : 0;
-  a.q_estride = C::kSwap ? 0 : bestride;
+  a.p_estride = grouped ? nblocks * kblocks : 0;
   a.c = g.c;
   a.offsets = g.offsets;
   a.err = g.err;
   a.wait_limit_ns = g.wait_limit_ns;
   a.ldc = g.N;
-  a.c_estride = g.M * g.N;
   a.rows_total = C::MODE == kB128Wgrad ? g.rows_total : g.M;
   a.blocks_total = kblocks;
   a.E = g.E;
   a.nk = (int)kblocks;
-  a.p_tiles = (int)ceil_div(a.p_rows, C::kPRowsTile);
-  a.q_tiles = (int)ceil_div(a.q_rows, C::BN);
-  a.tok_tile = C::kSwap ? C::BN : C::kPRowsTile;
-  CUtensorMap pmap, qmap;
+  a.p_tiles = (int)ceil_div(a.p_rows, C::kPTile);
+  a.q_tiles = (int)ceil_div(a.q_rows, q_tile);
+  auto divisor = [](int64_t d) {
+    return Divisor{(int)d, (uint32_t)((uint64_t(1) << 32) / (uint64_t)d + 1)};
+  };
+  if ((int64_t)a.p_tiles * a.q_tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
+  a.run = divisor(8 * (int64_t)a.q_tiles);
+  a.per = divisor((int64_t)a.p_tiles * a.q_tiles);
+  a.q_tile = q_tile;
+  a.split = split;
+  if (C::kSwap) {
+    a.stage_bytes = (kLanes + q_tile / C::CTAS) * kStepBytes;
+    a.stages = C::kRingBytes / a.stage_bytes;
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    // as many accumulators as there is room for, and no more than stages
+    while ((2 << a.bufs_log2) <= kMaxBufs && (2 << a.bufs_log2) <= a.stages &&
+           (int)(kTmemCols >> (a.bufs_log2 + 1)) >= q_tile) {
+      ++a.bufs_log2;
+    }
+  }
   const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
-  cudaError_t err = make_tensor_map_2d(&pmap, C::kSwap ? g.b_codes : g.a_codes,
-                                       C::kSwap ? bmap : arows, g.K, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
-                                       kStepBytes, kLanes, swz);
-  if (err != cudaSuccess) return err;
-  err = make_tensor_map_2d(&qmap, C::kSwap ? g.a_codes : g.b_codes, C::kSwap ? arows : bmap, g.K,
-                           CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, kStepBytes, S::kQRowsLoaded, swz);
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const void *pcodes = C::kSwap ? g.b_codes : g.a_codes, *qcodes = C::kSwap ? g.a_codes : g.b_codes;
+  const int64_t prows = C::kSwap ? bmap : g.M, qrows = C::kSwap ? g.M : bmap;
+  CUtensorMap pmap, qmap, qmap16, cmap;
+  cudaError_t err = make_tensor_map_2d(&pmap, pcodes, prows, g.K, u8, 1, kStepBytes, kLanes, swz);
+  if (err == cudaSuccess) {
+    err = make_tensor_map_2d(&qmap, qcodes, qrows, g.K, u8, 1, kStepBytes, 128, swz);
+  }
+  if (err == cudaSuccess) {
+    err = make_tensor_map_2d(&qmap16, qcodes, qrows, g.K, u8, 1, kStepBytes, 16, swz);
+  }
+  if (err == cudaSuccess) {
+    if (C::kSwap) {
+      cmap = pmap;  // not used
+    } else {
+      err = make_tensor_map_3d(&cmap, g.c, C::MODE == kB128Wgrad ? g.E : 1, g.M, g.N,
+                               C::kF32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                               C::kF32 ? 4 : 2, C::kF32 ? 32 : 64, 32, swz);
+    }
+  }
   if (err != cudaSuccess) return err;
   int64_t tiles = (int64_t)a.p_tiles * a.q_tiles;  // at most, by expert
   if (C::MODE == kB128Wgrad) tiles *= g.E;
-  if (grouped) {
-    tiles = (g.M / a.tok_tile + (g.M < g.E ? g.M : g.E)) * (C::kSwap ? a.p_tiles : a.q_tiles);
+  if (grouped) tiles = (g.M / q_tile + (g.M < g.E ? g.M : g.E)) * (int64_t)a.p_tiles;
+  if (tiles > INT32_MAX / kMaxSplit) return cudaErrorInvalidValue;
+  const int cluster = C::kSwap && C::MODE == kB128Dense ? split : C::CTAS;
+  const int64_t groups = split > 1 ? tiles : slots / cluster;
+  return launch_clusters(&b128_gemm_kernel<C>, (unsigned)((tiles < groups ? tiles : groups) * cluster),
+                         kThreads, smem_bytes<C>(), cluster, stream, pmap, qmap, qmap16, cmap, a);
+}
+
+// Dense calls. Pairs with 256 x 256 tiles once they fill half of the SMs; below that the swapped
+// shape, whose 128-row weight tiles, times up to eight CTAs along the contraction, spread few tokens
+// over the SMs.
+template <bool B_ROWS, bool F32>
+cudaError_t launch_dense(const B128GemmArgs& g, cudaStream_t stream) {
+  using Large = Config<2, kB128Dense, false, true, B_ROWS, F32>;
+  using Small = Config<1, kB128Dense, true, B_ROWS, true, F32>;
+  const int slots = slot_count<Small>();
+  if (ceil_div(g.M, 256) * ceil_div(g.N, 256) * 4 > slots) {
+    return launch_config<Large>(g, kColumns, 1, stream);
   }
-  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  const int64_t groups = slots / C::CTAS;
-  return launch_clusters(kernel, (unsigned)((tiles < groups ? tiles : groups) * C::CTAS), S::kThreads,
-                         smem, C::CTAS, stream, pmap, qmap, a);
+  const int64_t q_tiles = ceil_div(g.M, kColumns);
+  const int q_tile = (int)ceil_div(ceil_div(g.M, q_tiles), 16) * 16;
+  const int64_t tiles = q_tiles * ceil_div(g.N, kLanes), nk = ceil_div(g.K, kB128);
+  int split = 1;
+  while (split < kMaxSplit && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
+  return launch_config<Small>(g, q_tile, split, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_b128_gemm(int mode, const B128GemmArgs& g, cudaStream_t stream) {
   if (mode == kB128Wgrad) {
-    return g.out_f32 ? launch_config<Config<256, 2, kB128Wgrad, false, true, true, true>>(g, stream)
-                     : launch_config<Config<256, 2, kB128Wgrad, false, true, true, false>>(g, stream);
+    return g.out_f32
+               ? launch_config<Config<2, kB128Wgrad, false, true, true, true>>(g, kColumns, 1, stream)
+               : launch_config<Config<2, kB128Wgrad, false, true, true, false>>(g, kColumns, 1, stream);
   }
   if (mode == kB128Grouped) {
-    return g.out_f32 ? launch_config<Config<256, 2, kB128Grouped, false, true, false, true>>(g, stream)
-                     : launch_config<Config<256, 2, kB128Grouped, false, true, false, false>>(g, stream);
+    // columns of a tile: about twice the rows of an average expert, so that most experts are one
+    // tile and the ring still holds many stages
+    const int64_t mean = g.M / g.E;
+    const int q_tile = mean <= 16 ? 64 : (mean <= 64 ? 128 : 256);
+    return g.out_f32
+               ? launch_config<Config<2, kB128Grouped, true, false, true, true>>(g, q_tile, 1, stream)
+               : launch_config<Config<2, kB128Grouped, true, false, true, false>>(g, q_tile, 1, stream);
   }
   if (g.b_rows) {
-    return g.out_f32 ? launch_config<Config<256, 2, kB128Dense, false, true, true, true>>(g, stream)
-                     : launch_config<Config<256, 2, kB128Dense, false, true, true, false>>(g, stream);
+    return g.out_f32 ? launch_dense<true, true>(g, stream) : launch_dense<true, false>(g, stream);
   }
-  return g.out_f32 ? launch_config<Config<256, 2, kB128Dense, false, true, false, true>>(g, stream)
-                   : launch_config<Config<256, 2, kB128Dense, false, true, false, false>>(g, stream);
+  return g.out_f32 ? launch_dense<false, true>(g, stream) : launch_dense<false, false>(g, stream);
 }
 
 }  // namespace mxq

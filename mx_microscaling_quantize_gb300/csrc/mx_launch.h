@@ -113,6 +113,11 @@ cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows,
                                CUtensorMapDataType type, int elem_bytes, int box_cols,
                                int box_rows, CUtensorMapSwizzle swizzle);
 
+// The same of `batch` such matrices one after another (boxes stay inside one matrix).
+cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, int64_t batch, int64_t rows,
+                               int64_t cols, CUtensorMapDataType type, int elem_bytes, int box_cols,
+                               int box_rows, CUtensorMapSwizzle swizzle);
+
 // C = alpha * dequant(A) * dequant(B)^T on the tensor cores (fmt: 1 = E2M1, 2 = E4M3).
 cudaError_t launch_gemm(int fmt, bool swizzled, const GemmArgs& a, cudaStream_t stream);
 

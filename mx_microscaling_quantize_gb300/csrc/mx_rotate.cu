@@ -821,9 +821,7 @@ cudaError_t launch_fmt(int out_kind, bool swz, int g, const RotArgs& a, cudaStre
 
 // Tensor map of a row-major [rows, cols] matrix of 1- or 2-byte elements, boxes of box_rows x
 // box_cols, the given swizzle; loads read zeros out of bounds, stores drop what falls outside.
-cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
-                               CUtensorMapDataType type, int elem_bytes, int box_cols,
-                               int box_rows, CUtensorMapSwizzle swizzle) {
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -835,6 +833,13 @@ cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows,
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
   });
+  return encode;
+}
+
+cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
+                               CUtensorMapDataType type, int elem_bytes, int box_cols,
+                               int box_rows, CUtensorMapSwizzle swizzle) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)cols * elem_bytes};
@@ -846,6 +851,20 @@ cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tensor_map_3d(CUtensorMap* map, const void* base, int64_t batch, int64_t rows,
+                               int64_t cols, CUtensorMapDataType type, int elem_bytes, int box_cols,
+                               int box_rows, CUtensorMapSwizzle swizzle) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * elem_bytes, (cuuint64_t)(rows * cols) * elem_bytes};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  const CUresult r = encode(map, type, 3, const_cast<void*>(base), dims, strides, box, elem_strides,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 cudaError_t launch_rotate(int fmt, int out_kind, bool swizzled, int g, const RotArgs& a,
                           cudaStream_t stream) {
