@@ -102,13 +102,14 @@ struct KernelArgs {
   unsigned long long wait_limit_ns;
   int64_t p_rows, q_rows;        // rows of P and Q: of one expert's matrix, or of the whole of A
   int64_t p_pitch, q_pitch;      // rows form: floats per scale row; blocks form: per block row
-  int64_t p_estride;             // blocks form of P: floats of one expert
+  int64_t b_estride;             // blocks form: floats of one expert's B
   int64_t ldc;                   // elements per row of C
   int64_t rows_total;            // rows the offsets may name
   int64_t blocks_total;          // wgrad: 128-row blocks of the padded operands
   int E;
   int nk;                        // steps of the contraction (dense, grouped)
-  int p_tiles, q_tiles;          // tiles of the operands (grouped: of P only)
+  int p_tiles, q_tiles;          // tiles of the operands (grouped: of the weights only)
+  int row_min, row_max;          // grouped: experts with this many rows are this launch's
   Divisor run, per;              // eight rows of tiles; all tiles of one expert (wgrad)
   int q_tile;                    // most columns of a tile
   int stages, stage_bytes;       // swapped
@@ -393,7 +394,7 @@ template <typename C>
 __device__ __forceinline__ int tile_count(const KernelArgs& a, const int* prefix) {
   if (C::MODE == kB128Dense) return a.p_tiles * a.q_tiles;
   if (C::MODE == kB128Wgrad) return a.p_tiles * a.q_tiles * a.E;
-  return prefix[a.E] * a.p_tiles;
+  return prefix[a.E] * (C::kSwap ? a.p_tiles : a.q_tiles);
 }
 
 // `rows` rows in `tiles` tiles of nearly one size: the columns of a tile, 16 per CTA
@@ -413,29 +414,42 @@ __device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* 
   r.nk = a.nk;
   int64_t p_first;  // first row of the P tile in its matrix
   if (C::MODE == kB128Grouped) {
-    // the last expert with prefix * p_tiles <= t: in two rounds, 32 at a time
+    const int fixed = C::kSwap ? a.p_tiles : a.q_tiles;  // tiles of the weights
+    // the last expert with prefix * fixed <= t: in two rounds, 32 at a time
     const int lane = threadIdx.x & 31, width = (a.E + 31) >> 5;
     const int run = __popc(__ballot_sync(
-        0xFFFFFFFFu, (int64_t)prefix[min((lane + 1) * width, a.E)] * a.p_tiles <= t));
+        0xFFFFFFFFu, (int64_t)prefix[min((lane + 1) * width, a.E)] * fixed <= t));
     const int at = run * width + 1 + lane;
     const int lo = run * width +
                    __popc(__ballot_sync(0xFFFFFFFFu, lane < width && at < a.E &&
-                                                         (int64_t)prefix[at] * a.p_tiles <= t));
-    const int local = t - prefix[lo] * a.p_tiles, tiles = prefix[lo + 1] - prefix[lo];
+                                                         (int64_t)prefix[at] * fixed <= t));
+    const int local = t - prefix[lo] * fixed, tiles = prefix[lo + 1] - prefix[lo];
     const int rows = start[lo + 1] - start[lo];
-    int index = 0;
-    p = local;
-    r.n = (rows + 16 * C::CTAS - 1) / (16 * C::CTAS) * (16 * C::CTAS);
-    if (tiles > 1) {  // the token tiles of one weight tile run together
-      p = divide(local, tiles, &index);
-      r.n = even_columns<C>(rows, tiles);
-    }
+    int weight = local, index = 0;  // the token tiles of one weight tile run together
+    if (tiles > 1) weight = divide(local, tiles, &index);
     r.e = lo;
-    q = index * r.n;
-    r.q_row = start[lo] + q;
-    r.q_valid = min(r.n, rows - q);
-    p_first = (int64_t)p * C::kPTile;
-    r.p_row = (int)(lo * a.p_rows + p_first);
+    if (C::kSwap) {
+      p = weight;
+      r.n = (rows + 16 * C::CTAS - 1) / (16 * C::CTAS) * (16 * C::CTAS);
+      if (tiles > 1) r.n = even_columns<C>(rows, tiles);
+      q = index * r.n;
+      r.q_row = start[lo] + q;
+      r.q_valid = min(r.n, rows - q);
+      p_first = (int64_t)p * C::kPTile;
+      r.p_row = (int)(lo * a.p_rows + p_first);
+      r.p_valid = (int)min((int64_t)C::kPTile, a.p_rows - p_first);
+      r.c_col = r.q_row;
+    } else {
+      p = index;
+      q = weight;
+      r.n = kColumns;
+      r.c_col = q * kColumns;
+      r.q_row = (int)(lo * a.q_rows) + r.c_col;
+      r.q_valid = (int)min((int64_t)kColumns, a.q_rows - r.c_col);
+      p_first = start[lo] + index * C::kPTile;
+      r.p_row = (int)p_first;
+      r.p_valid = min(C::kPTile, rows - index * C::kPTile);
+    }
   } else {
     if (C::MODE == kB128Wgrad) {
       r.e = divide(t, a.per, &t);
@@ -448,16 +462,16 @@ __device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* 
     r.q_valid = (int)min((int64_t)r.n, a.q_rows - r.q_row);
     p_first = (int64_t)p * C::kPTile;
     r.p_row = (int)p_first;
+    r.p_valid = (int)min((int64_t)C::kPTile, a.p_rows - p_first);
+    r.c_col = r.q_row;
   }
-  r.p_valid = (int)min((int64_t)C::kPTile, a.p_rows - p_first);
   r.k0 = kb0 * kStepBytes;
   r.p_scale = C::kPRows ? kb0 * a.p_pitch + r.p_row
-                        : r.e * a.p_estride + (int64_t)p * C::CTAS * a.p_pitch + kb0;
+                        : r.e * a.b_estride + (int64_t)p * C::CTAS * a.p_pitch + kb0;
   r.q_scale = C::kQRows ? kb0 * a.q_pitch + r.q_row
-                        : (int64_t)q * (kColumns / kB128) * a.q_pitch + kb0;
+                        : r.e * a.b_estride + (int64_t)q * (kColumns / kB128) * a.q_pitch + kb0;
   r.c = (int64_t)r.q_row * a.ldc + p_first;
   r.c_row = (int)p_first;
-  r.c_col = r.q_row;
   if constexpr (C::CTAS == 2) {  // this CTA's own 128 rows of P
     const int rank = (int)cluster_rank(), skip = rank * kLanes;
     r.p_row += skip;
@@ -479,6 +493,7 @@ __device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* 
 // Table of the calls by expert: prefix sums of ceil(n_e / unit), and first rows. Offsets that break
 // their contract are clamped and made non-decreasing, so that every later access stays inside the
 // operands. All threads read the offsets (one trip to memory), one warp scans them.
+template <typename C>
 __device__ __forceinline__ void build_table(const KernelArgs& a, int unit, int limit, int* prefix,
                                             int* start) {
   for (int e = threadIdx.x; e <= a.E; e += kThreads) {
@@ -500,7 +515,9 @@ __device__ __forceinline__ void build_table(const KernelArgs& a, int unit, int l
       int first = __shfl_up_sync(0xFFFFFFFFu, end, 1);
       if (lane == 0) first = reach;
       reach = __shfl_sync(0xFFFFFFFFu, end, 31);
-      int sum = e < a.E ? (end - first + unit - 1) / unit : 0;
+      int rows = e < a.E ? end - first : 0;
+      if (C::MODE == kB128Grouped && (rows < a.row_min || rows > a.row_max)) rows = 0;
+      int sum = (rows + unit - 1) / unit;
       if (e < a.E) start[e + 1] = end;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -810,6 +827,20 @@ struct Boxes {
       bulk_commit_group();
     }
   }
+  // The first `rows` rows and `cols` columns only, by ordinary stores (the box's other rows are another
+  // expert's).
+  template <typename C>
+  __device__ __forceinline__ void store_part(const KernelArgs& a, const uint8_t* box, int64_t at,
+                                             int rows, int cols) {
+    const int lane = threadIdx.x & 31, chunk = lane & 7, per = C::kF32 ? 4 : 8;
+    __syncwarp();
+    for (int r = lane >> 3; r < rows; r += 4) {
+      if (chunk * per >= cols) break;
+      const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + ((chunk ^ (r & 7)) << 4));
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c) +
+                                (at + r * a.ldc + chunk * per) * (C::kF32 ? 4 : 2)) = v;
+    }
+  }
   __device__ __forceinline__ void drain() {  // read before the CTA's shared memory goes away
     if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
   }
@@ -926,8 +957,13 @@ __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const Kern
         }
         *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = o;
       }
-      boxes.store(cmap, box, tile.c_col + half * kWarpCols + b * kBoxCols,
-                  tile.c_row + (pw & 3) * 32, tile.e);
+      const int col = half * kWarpCols + b * kBoxCols, row0 = (pw & 3) * 32;
+      if (C::MODE == kB128Grouped && tile.p_valid < row0 + 32) {
+        boxes.template store_part<C>(a, box, (int64_t)(tile.c_row + row0) * a.ldc + tile.c_col + col,
+                                     tile.p_valid - row0, tile.q_valid - col);
+      } else {
+        boxes.store(cmap, box, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0);
+      }
     }
   }
   boxes.drain();
@@ -1155,8 +1191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
-  if (C::MODE == kB128Grouped) build_table(a, a.q_tile, INT32_MAX, s.prefix, s.start);
-  if (C::MODE == kB128Wgrad) build_table(a, kB128, (int)a.blocks_total, s.prefix, s.start);
+  if (C::MODE == kB128Grouped) build_table<C>(a, C::kSwap ? a.q_tile : C::kPTile, INT32_MAX, s.prefix, s.start);
+  if (C::MODE == kB128Wgrad) build_table<C>(a, kB128, (int)a.blocks_total, s.prefix, s.start);
   tc_fence_before();
   __syncthreads();
   if constexpr (C::CTAS == 2) cluster_sync();  // the other CTA's barriers are initialised
@@ -1239,7 +1275,8 @@ int slot_count() {
 
 // q_tile: most columns of a tile (swapped); split: CTAs along the contraction (swapped, dense)
 template <typename C>
-cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStream_t stream) {
+cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStream_t stream,
+                          int row_min = 0, int row_max = INT32_MAX) {
   const int slots = slot_count<C>();
   if (slots <= 0) return cudaErrorInvalidConfiguration;
   KernelArgs a{};
@@ -1253,7 +1290,7 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
   a.q_rows = C::kSwap ? g.M : g.N;
   a.p_pitch = C::kSwap ? bpitch : apitch;
   a.q_pitch = C::kSwap ? apitch : bpitch;
-  a.p_estride = grouped ? nblocks * kblocks : 0;
+  a.b_estride = grouped ? nblocks * kblocks : 0;
   a.c = g.c;
   a.offsets = g.offsets;
   a.err = g.err;
@@ -1273,6 +1310,8 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
   a.per = divisor((int64_t)a.p_tiles * a.q_tiles);
   a.q_tile = q_tile;
   a.split = split;
+  a.row_min = row_min;
+  a.row_max = row_max;
   if (C::kSwap) {
     a.stage_bytes = (kLanes + q_tile / C::CTAS) * kStepBytes;
     a.stages = C::kRingBytes / a.stage_bytes;
@@ -1308,7 +1347,10 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
   if (err != cudaSuccess) return err;
   int64_t tiles = (int64_t)a.p_tiles * a.q_tiles;  // at most, by expert
   if (C::MODE == kB128Wgrad) tiles *= g.E;
-  if (grouped) tiles = (g.M / q_tile + (g.M < g.E ? g.M : g.E)) * (int64_t)a.p_tiles;
+  if (grouped) {
+    const int64_t unit = C::kSwap ? q_tile : C::kPTile;
+    tiles = (g.M / unit + (g.M < g.E ? g.M : g.E)) * (C::kSwap ? a.p_tiles : a.q_tiles);
+  }
   if (tiles > INT32_MAX / kMaxSplit) return cudaErrorInvalidValue;
   const int cluster = C::kSwap && C::MODE == kB128Dense ? split : C::CTAS;
   const int64_t groups = split > 1 ? tiles : slots / cluster;
@@ -1335,6 +1377,22 @@ cudaError_t launch_dense(const B128GemmArgs& g, cudaStream_t stream) {
   return launch_config<Small>(g, q_tile, split, stream);
 }
 
+// Calls by expert: experts of more than kFewRows rows in 256 x 256 tiles (0.35 us a step whatever the
+// rows), the others swapped (a step costs its weights and 0.1 us per 64 rows): two launches, each of
+// which takes its experts from the offsets. A call of few rows has no large expert.
+constexpr int kFewRows = 128;
+template <bool F32>
+cudaError_t launch_grouped(const B128GemmArgs& g, cudaStream_t stream) {
+  using Many = Config<2, kB128Grouped, false, true, false, F32>;
+  using Few = Config<2, kB128Grouped, true, false, true, F32>;
+  if (g.M > kFewRows) {
+    const cudaError_t err = launch_config<Many>(g, kColumns, 1, stream, kFewRows + 1, INT32_MAX);
+    if (err != cudaSuccess) return err;
+  }
+  // columns of a tile: a narrow tile leaves room for more stages and accumulators
+  return launch_config<Few>(g, g.M / g.E <= 16 ? 64 : kFewRows, 1, stream, 0, kFewRows);
+}
+
 }  // namespace
 
 cudaError_t launch_b128_gemm(int mode, const B128GemmArgs& g, cudaStream_t stream) {
@@ -1344,13 +1402,7 @@ cudaError_t launch_b128_gemm(int mode, const B128GemmArgs& g, cudaStream_t strea
                : launch_config<Config<2, kB128Wgrad, false, true, true, false>>(g, kColumns, 1, stream);
   }
   if (mode == kB128Grouped) {
-    // columns of a tile: about twice the rows of an average expert, so that most experts are one
-    // tile and the ring still holds many stages
-    const int64_t mean = g.M / g.E;
-    const int q_tile = mean <= 16 ? 64 : (mean <= 64 ? 128 : 256);
-    return g.out_f32
-               ? launch_config<Config<2, kB128Grouped, true, false, true, true>>(g, q_tile, 1, stream)
-               : launch_config<Config<2, kB128Grouped, true, false, true, false>>(g, q_tile, 1, stream);
+    return g.out_f32 ? launch_grouped<true>(g, stream) : launch_grouped<false>(g, stream);
   }
   if (g.b_rows) {
     return g.out_f32 ? launch_dense<true, true>(g, stream) : launch_dense<true, false>(g, stream);
