@@ -60,8 +60,9 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
   return d;
 }
 
+// Codes are written once and not read again here: evict-first.
 __device__ __forceinline__ void store16B(void* p, const uint32_t* r) {
-  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+  asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3])
                : "memory");
 }
@@ -165,7 +166,10 @@ __device__ __forceinline__ void store_transposed(const uint8_t* sm, uint8_t* dst
     if (c >= cols) continue;
     uint8_t* o = dst + c * pitch + q * 16;
     if ((pitch & 15) == 0) {
-      if (q * 16 < valid) *reinterpret_cast<uint4*>(o) = v;
+      if (q * 16 < valid) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        store16B(o, u);
+      }
     } else {  // rows that are not whole 16-byte pieces: byte by byte
       const uint32_t u[4] = {v.x, v.y, v.z, v.w};
       for (int b = 0; b < 16 && q * 16 + b < valid; ++b) o[b] = (uint8_t)(u[b >> 2] >> (8 * (b & 3)));
@@ -173,31 +177,28 @@ __device__ __forceinline__ void store_transposed(const uint8_t* sm, uint8_t* dst
   }
 }
 
-// Expert owning 128-row block b of a buffer in which every expert's rows start a new block:
-// source rows [*row0, *row_end) of the block, false when b lies past the last expert. One warp.
-__device__ __forceinline__ bool find_block(const int64_t* offsets, int E, int64_t rows, int64_t b,
-                                           int64_t* row0, int64_t* row_end) {
+// Expert owning 128-row block b of a buffer in which every expert's rows start a new block, from the
+// (clamped) offsets in shared memory: source rows [*row0, *row_end) of the block, false when b lies
+// past the last expert. One warp.
+__device__ __forceinline__ bool find_block(const int* offsets, int E, int64_t b, int* row0,
+                                           int* row_end) {
   const int lane = threadIdx.x & 31;
-  int64_t before = 0;
+  int before = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    int64_t lo = 0, hi = 0;
-    if (e < E) {
-      lo = min(max(load_s64(offsets + e), (int64_t)0), rows);
-      hi = min(max(load_s64(offsets + e + 1), lo), rows);
-    }
-    const int64_t n = (hi - lo + kB128 - 1) / kB128;
-    int64_t sum = n;
+    const int lo = e < E ? offsets[e] : 0, hi = e < E ? max(offsets[e + 1], lo) : 0;
+    const int n = (hi - lo + kB128 - 1) / kB128;
+    int sum = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      const int up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
       if (lane >= d) sum += up;
     }
     const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + sum > b);
     if (past) {
       const int who = __ffs(past) - 1;
-      const int64_t first = before + sum - n;
-      *row0 = __shfl_sync(0xFFFFFFFFu, lo + (b - first) * kB128, who);
+      const int first = before + sum - n;
+      *row0 = __shfl_sync(0xFFFFFFFFu, lo + ((int)b - first) * kB128, who);
       *row_end = __shfl_sync(0xFFFFFFFFu, hi, who);
       return true;
     }
@@ -208,19 +209,24 @@ __device__ __forceinline__ bool find_block(const int64_t* offsets, int E, int64_
 
 // 128 x 1 blocks, written transposed (codes [K, 128 * blocks], scales [blocks, K]): the operand
 // of a product that contracts over the rows of x.
-__global__ void __launch_bounds__(kTileThreads) b128_cols_kernel(B128QuantArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArgs a) {
   __shared__ __align__(16) uint8_t sm[128 * 128];
-  __shared__ uint32_t part[8][128];
-  __shared__ float factor[128];
-  __shared__ int64_t range[2];
+  __shared__ __align__(16) uint32_t part[8][64];
+  __shared__ __align__(16) float factor[128];
+  __shared__ int range[2];
+  __shared__ int offsets[1024 + 1];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4, warp = tid >> 5;
   const int64_t b = blockIdx.x;
   if (a.offsets) {
+    for (int e = tid; e <= a.E; e += kTileThreads) {  // one trip to memory
+      offsets[e] = (int)min(max(load_s64(a.offsets + e), (int64_t)0), a.R);
+    }
+    __syncthreads();
     if (warp == 0) {
-      int64_t lo = 0, hi = 0;
-      const bool found = find_block(a.offsets, a.E, a.R, b, &lo, &hi);
+      int lo = 0, hi = 0;
+      const bool found = find_block(offsets, a.E, b, &lo, &hi);
       if (tid == 0) {
         range[0] = found ? lo : -1;
         range[1] = hi;
@@ -229,8 +235,8 @@ __global__ void __launch_bounds__(kTileThreads) b128_cols_kernel(B128QuantArgs a
     __syncthreads();
     if (range[0] < 0) return;  // past the last expert: never read by the product
   } else if (tid == 0) {
-    range[0] = b * kB128;
-    range[1] = a.R;
+    range[0] = (int)(b * kB128);
+    range[1] = (int)a.R;
   }
   __syncthreads();
   const int64_t row0 = range[0], row_end = range[1];
@@ -239,30 +245,33 @@ __global__ void __launch_bounds__(kTileThreads) b128_cols_kernel(B128QuantArgs a
     uint32_t w[8][4];
     load_tile(static_cast<const uint16_t*>(a.x), a.K, a.index, a.M, row0 + rg * 8, row_end,
               c0 + cg * 8, w);
+    uint32_t m[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t m = 0u;
+      m[j] = 0u;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = amax2(m, w[i][j]);
-      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-      if ((tid & 16) == 0) {
-        part[warp][cg * 8 + 2 * j] = m << 16;
-        part[warp][cg * 8 + 2 * j + 1] = m & 0xFFFF0000u;
-      }
+      for (int i = 0; i < 8; ++i) m[j] = amax2(m[j], w[i][j]);
+      m[j] = __vmaxu2(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+    }
+    if ((tid & 16) == 0) {  // eight columns' halves, still in pairs
+      *reinterpret_cast<uint4*>(&part[warp][cg * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
     }
     __syncthreads();
     if (tid < 128) {
-      uint32_t m = part[0][tid];
+      uint32_t top = part[0][tid >> 1];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) m = max(m, part[i][tid]);
-      const Factors f = block_factors_b128(m);
+      for (int i = 1; i < 8; ++i) top = __vmaxu2(top, part[i][tid >> 1]);
+      const Factors f = block_factors_b128((tid & 1) ? top & 0xFFFF0000u : top << 16);
       factor[tid] = f.r;
       if (c0 + tid < a.K) a.scales[b * a.K + c0 + tid] = f.scale;
     }
     __syncthreads();
+    float r8[8];
+    *reinterpret_cast<float4*>(r8) = *reinterpret_cast<const float4*>(factor + cg * 8);
+    *reinterpret_cast<float4*>(r8 + 4) = *reinterpret_cast<const float4*>(factor + cg * 8 + 4);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float r = factor[cg * 8 + j];
+      const float r = r8[j];
       uint32_t v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -344,12 +353,14 @@ __global__ void __launch_bounds__(kTileThreads) b128_blocks_kernel(B128QuantArgs
 
 cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream) {
   const int64_t col_tiles = (a.K + kRowsCols - 1) / kRowsCols;
-  // eight rows per warp once that leaves every SM work; one row per warp for small calls, where
-  // the latency of a warp's own chain counts
-  if (a.R * col_tiles >= 8 * 8 * 152) {
-    const int64_t tiles = (a.R + 7) / 8 * col_tiles;
-    return launch_pdl(&b128_rows_kernel<8>, dim3((unsigned)((tiles + 7) / 8)), dim3(256), 0, stream,
-                      a, col_tiles, tiles);
+  // Four rows per warp once that leaves every SM work (x[8192, 8192]: 30.9 us; eight rows, whose 91
+  // registers halve the resident warps, 36.1); one row per warp for small calls, where the latency
+  // of a warp's own chain counts.
+  constexpr int kRows = 4;
+  if (a.R * col_tiles >= kRows * 8 * 152) {
+    const int64_t tiles = (a.R + kRows - 1) / kRows * col_tiles;
+    return launch_pdl(&b128_rows_kernel<kRows>, dim3((unsigned)((tiles + 7) / 8)), dim3(256), 0,
+                      stream, a, col_tiles, tiles);
   }
   const int64_t tiles = a.R * col_tiles;
   return launch_pdl(&b128_rows_kernel<1>, dim3((unsigned)((tiles + 3) / 4)), dim3(128), 0, stream, a,
@@ -358,8 +369,8 @@ cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_b128_cols(const B128QuantArgs& a, cudaStream_t stream) {
   const int64_t col_blocks = (a.K + kB128 - 1) / kB128;
-  // by expert, a CTA walks up to four column tiles so that finding its rows is paid once
-  const int64_t y = a.offsets ? (col_blocks + 3) / 4 : col_blocks;
+  // by expert, a CTA walks two column tiles, so that finding its rows is paid half as often
+  const int64_t y = a.offsets ? (col_blocks + 1) / 2 : col_blocks;
   return launch_pdl(&b128_cols_kernel, dim3((unsigned)a.blocks, (unsigned)(y < 65535 ? y : 65535)),
                     dim3(kTileThreads), 0, stream, a);
 }
