@@ -808,38 +808,40 @@ struct Steps {
   }
 };
 
-// Staging buffers of a promoting warp's tensor-map stores: 32 rows x 128 bytes, 16-byte chunk q of
-// row r at q ^ (r % 8), two in turn.
+// Staging of a promoting warp's output: two boxes of 32 rows x 128 bytes, 16-byte chunk q of row r at
+// q ^ (r % 8), written with tensor-map stores.
 struct Boxes {
   uint8_t* base;
-  int turn = 0;
-  __device__ __forceinline__ uint8_t* next() {
-    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  __device__ __forceinline__ void wait() {  // both are read
+    if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
     __syncwarp();
-    turn ^= 1;
-    return base + turn * 4096;
   }
-  __device__ __forceinline__ void store(const CUtensorMap& cmap, uint8_t* box, int x, int y, int z) {
+  // both boxes, `width` columns apart; the second only where it has columns
+  __device__ __forceinline__ void store(const CUtensorMap& cmap, int x, int y, int z, int width,
+                                        int cols) {
     fence_proxy_async_smem();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
-      tma_store_box_3d(&cmap, x, y, z, smem_u32(box));
+      tma_store_box_3d(&cmap, x, y, z, smem_u32(base));
+      if (cols > width) tma_store_box_3d(&cmap, x + width, y, z, smem_u32(base + 4096));
       bulk_commit_group();
     }
   }
-  // The first `rows` rows and `cols` columns only, by ordinary stores (the box's other rows are another
-  // expert's).
+  // The first `rows` rows and `cols` columns of box u only, by ordinary stores (the box's other rows
+  // are another expert's).
   template <typename C>
-  __device__ __forceinline__ void store_part(const KernelArgs& a, const uint8_t* box, int64_t at,
-                                             int rows, int cols) {
+  __device__ __forceinline__ void store_part(const KernelArgs& a, int u, int64_t at, int rows,
+                                             int cols) {
     const int lane = threadIdx.x & 31, chunk = lane & 7, per = C::kF32 ? 4 : 8;
     __syncwarp();
     for (int r = lane >> 3; r < rows; r += 4) {
       if (chunk * per >= cols) break;
-      const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + ((chunk ^ (r & 7)) << 4));
+      const uint4 v =
+          *reinterpret_cast<const uint4*>(base + u * 4096 + r * 128 + ((chunk ^ (r & 7)) << 4));
       *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.c) +
                                 (at + r * a.ldc + chunk * per) * (C::kF32 ? 4 : 2)) = v;
     }
+    __syncwarp();
   }
   __device__ __forceinline__ void drain() {  // read before the CTA's shared memory goes away
     if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
@@ -940,29 +942,39 @@ __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const Kern
       break;
     }
     if (tile.p_valid <= (pw & 3) * 32) continue;  // none of the warp's rows exists
+    // two boxes at a time: one fence and one wait for both
     constexpr int kBoxCols = C::kF32 ? 32 : 64;
+    const int row0 = (pw & 3) * 32;
 #pragma unroll
-    for (int b = 0; b < kWarpCols / kBoxCols; ++b) {
-      if (half * kWarpCols + b * kBoxCols >= tile.q_valid) break;
-      uint8_t* box = boxes.next();
+    for (int b = 0; b < kWarpCols / kBoxCols; b += 2) {
+      const int col = half * kWarpCols + b * kBoxCols;
+      if (col >= tile.q_valid) break;
+      boxes.wait();
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {  // 16 bytes: four fp32 or eight bf16
-        const uint64_t* d = sums + (b * kBoxCols + q * (kBoxCols / 8)) / 2;
-        uint4 o;
-        if constexpr (C::kF32) {
-          o = make_uint4((uint32_t)d[0], (uint32_t)(d[0] >> 32), (uint32_t)d[1], (uint32_t)(d[1] >> 32));
-        } else {
-          o = make_uint4(bf16_pair(first(d[0]), second(d[0])), bf16_pair(first(d[1]), second(d[1])),
-                         bf16_pair(first(d[2]), second(d[2])), bf16_pair(first(d[3]), second(d[3])));
+      for (int u = 0; u < 2; ++u) {
+        uint8_t* line = boxes.base + u * 4096 + lane * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {  // 16 bytes: four fp32 or eight bf16
+          const uint64_t* d = sums + ((b + u) * kBoxCols + q * (kBoxCols / 8)) / 2;
+          uint4 o;
+          if constexpr (C::kF32) {
+            o = make_uint4((uint32_t)d[0], (uint32_t)(d[0] >> 32), (uint32_t)d[1],
+                           (uint32_t)(d[1] >> 32));
+          } else {
+            o = make_uint4(bf16_pair(first(d[0]), second(d[0])), bf16_pair(first(d[1]), second(d[1])),
+                           bf16_pair(first(d[2]), second(d[2])), bf16_pair(first(d[3]), second(d[3])));
+          }
+          *reinterpret_cast<uint4*>(line + ((q ^ (lane & 7)) << 4)) = o;
         }
-        *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = o;
       }
-      const int col = half * kWarpCols + b * kBoxCols, row0 = (pw & 3) * 32;
       if (C::MODE == kB128Grouped && tile.p_valid < row0 + 32) {
-        boxes.template store_part<C>(a, box, (int64_t)(tile.c_row + row0) * a.ldc + tile.c_col + col,
-                                     tile.p_valid - row0, tile.q_valid - col);
+        const int64_t at = (int64_t)(tile.c_row + row0) * a.ldc + tile.c_col + col;
+        boxes.template store_part<C>(a, 0, at, tile.p_valid - row0, tile.q_valid - col);
+        boxes.template store_part<C>(a, 1, at + kBoxCols, tile.p_valid - row0,
+                                     tile.q_valid - col - kBoxCols);
       } else {
-        boxes.store(cmap, box, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0);
+        boxes.store(cmap, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0,
+                    kBoxCols, tile.q_valid - col);
       }
     }
   }
@@ -1071,27 +1083,31 @@ __device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const K
       if (tile.p_valid <= row0) continue;
       constexpr int kBoxCols = C::kF32 ? 32 : 64;
 #pragma unroll
-      for (int b = 0; b < kWarpCols / kBoxCols; ++b) {
-        if (col0 + b * kBoxCols >= tile.q_valid) break;
-        uint8_t* box = boxes.next();
+      for (int b = 0; b < kWarpCols / kBoxCols; b += 2) {
+        const int col = col0 + b * kBoxCols;
+        if (col >= tile.q_valid) break;
+        boxes.wait();
 #pragma unroll
-        for (int g = 0; g < kBoxCols / 8; ++g) {
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint64_t d = sums[(b * (kBoxCols / 8) + g) * 4 + r];
-            const int R = 8 * r + lr;
-            if constexpr (C::kF32) {
-              const int byte = (g * 8 + lc) * 4;
-              *reinterpret_cast<uint64_t*>(box + R * 128 + (((byte >> 4) ^ (R & 7)) << 4) +
-                                           (byte & 15)) = d;
-            } else {
-              const int byte = (g * 8 + lc) * 2;
-              *reinterpret_cast<uint32_t*>(box + R * 128 + (((byte >> 4) ^ (R & 7)) << 4) +
-                                           (byte & 15)) = bf16_pair(first(d), second(d));
+          for (int g = 0; g < kBoxCols / 8; ++g) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint64_t d = sums[((b + u) * (kBoxCols / 8) + g) * 4 + r];
+              uint8_t* line = boxes.base + u * 4096 + (8 * r + lr) * 128;
+              if constexpr (C::kF32) {
+                const int byte = (g * 8 + lc) * 4;
+                *reinterpret_cast<uint64_t*>(line + (((byte >> 4) ^ lr) << 4) + (byte & 15)) = d;
+              } else {
+                const int byte = (g * 8 + lc) * 2;
+                *reinterpret_cast<uint32_t*>(line + (((byte >> 4) ^ lr) << 4) + (byte & 15)) =
+                    bf16_pair(first(d), second(d));
+              }
             }
           }
         }
-        boxes.store(cmap, box, tile.c_col + col0 + b * kBoxCols, tile.c_row + row0, tile.e);
+        boxes.store(cmap, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0,
+                    kBoxCols, tile.q_valid - col);
       }
     }
   }
