@@ -54,9 +54,9 @@ constexpr int kColumns = 256;    // most columns of a tile
 constexpr int kStepBytes = 128;  // one scale block of the contraction per step
 constexpr int kPromoWarps = 8;
 constexpr int kThreads = 128 + 32 * kPromoWarps;
-constexpr int kWarpCols = kColumns / 2;  // most columns of a promoting warp
+constexpr int kFewRows = 128;    // most columns (tokens) of a tile of the swapped shape
 constexpr uint32_t kTmemCols = 2 * kColumns;
-constexpr int kMaxStages = 12, kMaxBufs = 8;
+constexpr int kMaxStages = 12;
 // scales travel and are released by groups of steps
 constexpr int kScaleGroup = 4, kScaleGroups = 4, kScaleSlots = kScaleGroup * kScaleGroups;
 constexpr int kMaxExperts = 1024;
@@ -68,14 +68,18 @@ template <int CTAS_, int MODE_, bool SWAP_, bool P_ROWS_, bool Q_ROWS_, bool F32
 struct Config {
   static constexpr int CTAS = CTAS_, MODE = MODE_;
   static constexpr bool kSwap = SWAP_, kPRows = P_ROWS_, kQRows = Q_ROWS_, kF32 = F32_;
-  static constexpr bool kFragments = Q_ROWS_;  // how the accumulator is read
   static constexpr int kPTile = kLanes * CTAS;
+  // most columns of a promoting warp, and the registers of the two halves of the block
+  static constexpr int kWarpCols = SWAP_ ? kFewRows / 2 : kColumns / 2;
+  static constexpr int kOtherRegs = SWAP_ ? 88 : 40, kPromoRegs = SWAP_ ? 208 : 232;
+  static_assert(kOtherRegs * 128 + kPromoRegs * 256 <= 168 * kThreads, "the launch's registers");
   // floats of a scale slot: one per lane / column (rows form) or one per block of 128
-  static constexpr int kPScales = P_ROWS_ ? kLanes : 4, kQScales = Q_ROWS_ ? kColumns : 4;
+  static constexpr int kPScales = P_ROWS_ ? kLanes : 4, kQScales = !Q_ROWS_ ? 4 : (SWAP_ ? kFewRows : kColumns);
   static constexpr int kSlotFloats = kPScales + kQScales;
   // ring of stages: four of fixed size, or (swapped) as many as the call's tile size leaves room for
   static constexpr int kFixedStageBytes = (kLanes + kColumns / CTAS_) * kStepBytes;
-  static constexpr int kRingBytes = SWAP_ ? 172 * 1024 : 4 * kFixedStageBytes;
+  static constexpr int kStages = 4;
+  static constexpr int kRingBytes = SWAP_ ? 172 * 1024 : kStages * kFixedStageBytes;
   // staging of the output, per promoting warp: two boxes of 32 rows x 128 bytes for tensor-map
   // stores, or (swapped) 32 tokens x 32 bf16 in rows of 80 bytes
   static constexpr int kStagingBytes = SWAP_ ? 32 * 80 : 2 * 4096;
@@ -84,7 +88,7 @@ struct Config {
 template <typename C>
 constexpr int smem_bytes() {
   return 1024 + C::kRingBytes + kPromoWarps * C::kStagingBytes + kScaleSlots * C::kSlotFloats * 4 +
-         (2 * kMaxStages + kMaxBufs + 2 * kScaleGroups + 1) * 8 + 16 +
+         (2 * kMaxStages + 4 + 2 * kScaleGroups + 1) * 8 + 16 +
          (C::MODE != kB128Dense ? 2 * (kMaxExperts + 1) * 4 : 0);
 }
 
@@ -113,7 +117,8 @@ struct KernelArgs {
   Divisor run, per;              // eight rows of tiles; all tiles of one expert (wgrad)
   int q_tile;                    // most columns of a tile
   int stages, stage_bytes;       // swapped
-  int bufs_log2;                 // swapped: accumulators, of 512 >> bufs_log2 columns
+  int batch, stride;             // swapped: accumulators (steps) handed over together, 2 or 4, and
+                                 // the columns from one to the next
   int split;                     // swapped, dense: CTAs of a cluster along the contraction
 };
 
@@ -134,31 +139,35 @@ struct Tile {
 // ------------------------------------------------------------------------------------------
 
 // The MMAs of one step (K = 128 in four of 32, the first overwriting the accumulator) and the
-// commits that free the operands' stage and hand the accumulator over, issued by one elected lane of
-// a converged warp. One statement with every operand computed outside: in a branch of the elected
+// commits that free the operands' stage and (if asked) hand the accumulator over, issued by one elected
+// lane of a converged warp. One statement with every operand computed outside: in a branch of the elected
 // lane the descriptors went through vector registers and a step took 400 cycles to issue.
-template <int CTAS>
+// Of a pair the commits arrive at the same barriers of both CTAs. (Every register counts in the warps
+// that gave theirs up: a few bytes of spills in the multiplying warp's loop cost half of the speed,
+// hence the forms with and without the condition.)
+template <int CTAS, bool ALWAYS>
 __device__ __forceinline__ void issue_step(uint32_t d, uint64_t p, uint64_t q, uint32_t idesc,
-                                           uint32_t empty, uint32_t acc_full) {
+                                           uint32_t empty, uint32_t acc_full, bool hand_over) {
   if constexpr (CTAS == 1) {
+    static_assert(!ALWAYS, "single CTAs run the swapped shape");
     asm volatile(
-        "{\n\t.reg .pred e, on, off;\n\t"
+        "{\n\t.reg .pred e, on, off, h;\n\t"
         "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 off, 0, 0;\n\tsetp.eq.b32 on, 0, 0;\n\t"
+        "setp.ne.and.b32 h, %12, 0, e;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %5, %9, off;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %2, %6, %9, on;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %7, %9, on;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %4, %8, %9, on;\n\t"
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t"
+        "@h tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t"
         "}" ::"r"(d),
         "l"(p), "l"(p + 2), "l"(p + 4), "l"(p + 6), "l"(q), "l"(q + 2), "l"(q + 4), "l"(q + 6),
-        "r"(idesc), "r"(empty), "r"(acc_full)
+        "r"(idesc), "r"(empty), "r"(acc_full), "r"((uint32_t)hand_over)
         : "memory");
-  } else {  // the commits arrive at the same barriers of both CTAs
+  } else if constexpr (ALWAYS) {
     asm volatile(
-        "{\n\t.reg .pred e, on, off;\n\t.reg .b16 both;\n\t"
+        "{\n\t.reg .pred e, on, off;\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
         "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 off, 0, 0;\n\tsetp.eq.b32 on, 0, 0;\n\t"
-        "mov.b16 both, 3;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %5, %9, off;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %2, %6, %9, on;\n\t"
         "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %3, %7, %9, on;\n\t"
@@ -170,6 +179,23 @@ __device__ __forceinline__ void issue_step(uint32_t d, uint64_t p, uint64_t q, u
         "}" ::"r"(d),
         "l"(p), "l"(p + 2), "l"(p + 4), "l"(p + 6), "l"(q), "l"(q + 2), "l"(q + 4), "l"(q + 6),
         "r"(idesc), "r"(empty), "r"(acc_full)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, on, off, h;\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 off, 0, 0;\n\tsetp.eq.b32 on, 0, 0;\n\t"
+        "setp.ne.and.b32 h, %12, 0, e;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %5, %9, off;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %2, %6, %9, on;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %3, %7, %9, on;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %4, %8, %9, on;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%10], both;\n\t"
+        "@h tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%11], both;\n\t"
+        "}" ::"r"(d),
+        "l"(p), "l"(p + 2), "l"(p + 4), "l"(p + 6), "l"(q), "l"(q + 2), "l"(q + 4), "l"(q + 6),
+        "r"(idesc), "r"(empty), "r"(acc_full), "r"((uint32_t)hand_over)
         : "memory");
   }
 }
@@ -223,39 +249,98 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {  // to this CTA only
                : "memory");
 }
 
-// 32 fp32 columns of this thread's tensor-memory lane. The load is only issued; the values are there
-// after wait_columns, which names them so that no use moves before it.
-__device__ __forceinline__ void issue_row(uint32_t taddr, uint32_t (&r)[32]) {
+// Reads of the accumulator: issue, wait and the joining of neighbouring columns into 64-bit pairs are
+// one statement. Written apart, ptxas was free to place the pairs' halves in registers that are no
+// pairs and to move them for every packed FMA, which it did or not depending on unrelated code (342
+// against 477 us at 8192^3).
+// 64 fp32 columns of this thread's lane.
+__device__ __forceinline__ void read_row(uint32_t taddr, uint64_t (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+      "{\n\t.reg .b32 r<64>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "r0, r1, r2, r3, r4, r5, r6, r7, r8, r9, r10, r11, r12, r13, r14, r15, "
+      "r16, r17, r18, r19, r20, r21, r22, r23, r24, r25, r26, r27, r28, r29, r30, r31, "
+      "r32, r33, r34, r35, r36, r37, r38, r39, r40, r41, r42, r43, r44, r45, r46, r47, "
+      "r48, r49, r50, r51, r52, r53, r54, r55, r56, r57, r58, r59, r60, r61, r62, r63}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {r0, r1};\n\tmov.b64 %1, {r2, r3};\n\tmov.b64 %2, {r4, r5};\n\t"
+      "mov.b64 %3, {r6, r7};\n\tmov.b64 %4, {r8, r9};\n\tmov.b64 %5, {r10, r11};\n\t"
+      "mov.b64 %6, {r12, r13};\n\tmov.b64 %7, {r14, r15};\n\tmov.b64 %8, {r16, r17};\n\t"
+      "mov.b64 %9, {r18, r19};\n\tmov.b64 %10, {r20, r21};\n\tmov.b64 %11, {r22, r23};\n\t"
+      "mov.b64 %12, {r24, r25};\n\tmov.b64 %13, {r26, r27};\n\tmov.b64 %14, {r28, r29};\n\t"
+      "mov.b64 %15, {r30, r31};\n\tmov.b64 %16, {r32, r33};\n\tmov.b64 %17, {r34, r35};\n\t"
+      "mov.b64 %18, {r36, r37};\n\tmov.b64 %19, {r38, r39};\n\tmov.b64 %20, {r40, r41};\n\t"
+      "mov.b64 %21, {r42, r43};\n\tmov.b64 %22, {r44, r45};\n\tmov.b64 %23, {r46, r47};\n\t"
+      "mov.b64 %24, {r48, r49};\n\tmov.b64 %25, {r50, r51};\n\tmov.b64 %26, {r52, r53};\n\t"
+      "mov.b64 %27, {r54, r55};\n\tmov.b64 %28, {r56, r57};\n\tmov.b64 %29, {r58, r59};\n\t"
+      "mov.b64 %30, {r60, r61};\n\tmov.b64 %31, {r62, r63};\n\t"
+      "}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]),
+        "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]),
+        "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15]), "=l"(v[16]), "=l"(v[17]),
+        "=l"(v[18]), "=l"(v[19]), "=l"(v[20]), "=l"(v[21]), "=l"(v[22]), "=l"(v[23]),
+        "=l"(v[24]), "=l"(v[25]), "=l"(v[26]), "=l"(v[27]), "=l"(v[28]), "=l"(v[29]),
+        "=l"(v[30]), "=l"(v[31])
+      : "r"(taddr)
+      : "memory");
 }
-// 16 lanes x 32 columns in fragments: r[4 g + i] of lane l is row l / 4 + 8 (i / 2), column
-// 8 g + 2 (l % 4) + i % 2.
-__device__ __forceinline__ void issue_fragment(uint32_t taddr, uint32_t* r) {
+// 32 lanes x 32 columns in fragments: v[8 h + 2 g + i] of lane l is the columns 8 g + 2 (l % 4) +
+// {0, 1} of row 16 h + 8 i + l / 4.
+__device__ __forceinline__ void read_fragments(uint32_t taddr, uint64_t (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+      "{\n\t.reg .b32 r<32>;\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {r0, r1, r2, r3, r4, r5, r6, r7, "
+      "r8, r9, r10, r11, r12, r13, r14, r15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {r16, r17, r18, r19, r20, r21, r22, r23, "
+      "r24, r25, r26, r27, r28, r29, r30, r31}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {r0, r1};\n\tmov.b64 %1, {r2, r3};\n\tmov.b64 %2, {r4, r5};\n\t"
+      "mov.b64 %3, {r6, r7};\n\tmov.b64 %4, {r8, r9};\n\tmov.b64 %5, {r10, r11};\n\t"
+      "mov.b64 %6, {r12, r13};\n\tmov.b64 %7, {r14, r15};\n\tmov.b64 %8, {r16, r17};\n\t"
+      "mov.b64 %9, {r18, r19};\n\tmov.b64 %10, {r20, r21};\n\tmov.b64 %11, {r22, r23};\n\t"
+      "mov.b64 %12, {r24, r25};\n\tmov.b64 %13, {r26, r27};\n\tmov.b64 %14, {r28, r29};\n\t"
+      "mov.b64 %15, {r30, r31};\n\t"
+      "}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]),
+        "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]),
+        "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15])
+      : "r"(taddr), "r"(taddr + (16u << 16))
+      : "memory");
 }
-__device__ __forceinline__ void wait_columns(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
+// 32 lanes x 64 columns in fragments: v[16 c + 8 h + 2 g + i] of lane l is the columns 32 c + 8 g + 2 (l % 4) +
+// {0, 1} of row 16 h + 8 i + l / 4.
+__device__ __forceinline__ void read_fragments(uint32_t taddr, uint64_t (&v)[32]) {
+  asm volatile(
+      "{\n\t.reg .b32 r<64>;\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {r0, r1, r2, r3, r4, r5, r6, r7, "
+      "r8, r9, r10, r11, r12, r13, r14, r15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {r16, r17, r18, r19, r20, r21, r22, r23, "
+      "r24, r25, r26, r27, r28, r29, r30, r31}, [%33];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {r32, r33, r34, r35, r36, r37, r38, r39, "
+      "r40, r41, r42, r43, r44, r45, r46, r47}, [%34];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {r48, r49, r50, r51, r52, r53, r54, r55, "
+      "r56, r57, r58, r59, r60, r61, r62, r63}, [%35];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {r0, r1};\n\tmov.b64 %1, {r2, r3};\n\tmov.b64 %2, {r4, r5};\n\t"
+      "mov.b64 %3, {r6, r7};\n\tmov.b64 %4, {r8, r9};\n\tmov.b64 %5, {r10, r11};\n\t"
+      "mov.b64 %6, {r12, r13};\n\tmov.b64 %7, {r14, r15};\n\tmov.b64 %8, {r16, r17};\n\t"
+      "mov.b64 %9, {r18, r19};\n\tmov.b64 %10, {r20, r21};\n\tmov.b64 %11, {r22, r23};\n\t"
+      "mov.b64 %12, {r24, r25};\n\tmov.b64 %13, {r26, r27};\n\tmov.b64 %14, {r28, r29};\n\t"
+      "mov.b64 %15, {r30, r31};\n\tmov.b64 %16, {r32, r33};\n\tmov.b64 %17, {r34, r35};\n\t"
+      "mov.b64 %18, {r36, r37};\n\tmov.b64 %19, {r38, r39};\n\tmov.b64 %20, {r40, r41};\n\t"
+      "mov.b64 %21, {r42, r43};\n\tmov.b64 %22, {r44, r45};\n\tmov.b64 %23, {r46, r47};\n\t"
+      "mov.b64 %24, {r48, r49};\n\tmov.b64 %25, {r50, r51};\n\tmov.b64 %26, {r52, r53};\n\t"
+      "mov.b64 %27, {r54, r55};\n\tmov.b64 %28, {r56, r57};\n\tmov.b64 %29, {r58, r59};\n\t"
+      "mov.b64 %30, {r60, r61};\n\tmov.b64 %31, {r62, r63};\n\t"
+      "}"
+      : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]), "=l"(v[4]), "=l"(v[5]),
+        "=l"(v[6]), "=l"(v[7]), "=l"(v[8]), "=l"(v[9]), "=l"(v[10]), "=l"(v[11]),
+        "=l"(v[12]), "=l"(v[13]), "=l"(v[14]), "=l"(v[15]), "=l"(v[16]), "=l"(v[17]),
+        "=l"(v[18]), "=l"(v[19]), "=l"(v[20]), "=l"(v[21]), "=l"(v[22]), "=l"(v[23]),
+        "=l"(v[24]), "=l"(v[25]), "=l"(v[26]), "=l"(v[27]), "=l"(v[28]), "=l"(v[29]),
+        "=l"(v[30]), "=l"(v[31])
+      : "r"(taddr), "r"(taddr + (16u << 16)), "r"(taddr + 32), "r"(taddr + 32 + (16u << 16))
+      : "memory");
 }
 
 // Pairs of fp32 in one 64-bit register: one instruction for two (the same rate per value, half the
@@ -535,9 +620,10 @@ struct Smem {
   uint8_t* ring;
   uint8_t* staging;       // [kPromoWarps][kStagingBytes]
   float* scales;          // [kScaleSlots][kSlotFloats]
-  uint64_t* full;         // [stages]: operands landed and accumulator read
+  uint64_t* full;         // [stages]: operands landed and (not swapped) accumulator read
   uint64_t* empty;        // [stages]: operands read
-  uint64_t* acc_full;     // [accumulators]
+  uint64_t* acc_full;     // [2]
+  uint64_t* acc_empty;    // [2] (swapped)
   uint64_t* scale_full;   // [kScaleGroups]
   uint64_t* scale_empty;  // [kScaleGroups]
   uint64_t* done;
@@ -548,14 +634,7 @@ struct Smem {
 
 template <typename C>
 __device__ __forceinline__ int stage_count(const KernelArgs& a) {
-  return C::kSwap ? a.stages : 4;
-}
-// Accumulators in tensor memory: two of 256 columns, or (swapped) up to eight narrower ones. With few
-// columns a step is short beside the way of its signals (MMA done, accumulator read, next MMA:
-// about 1700 cycles), and as many steps are under way as there are accumulators.
-template <typename C>
-__device__ __forceinline__ int bufs_log2(const KernelArgs& a) {
-  return C::kSwap ? a.bufs_log2 : 1;
+  return C::kSwap ? a.stages : C::kStages;
 }
 template <typename C>
 __device__ __forceinline__ int stage_bytes(const KernelArgs& a) {
@@ -648,25 +727,53 @@ __device__ __forceinline__ void multiply(const KernelArgs& a, const Smem& s, int
   static_assert(kStepBytes == 128, "issue_step");
   const int stages = stage_count<C>(a);
   bool failed = false;
-  int st = 0, buf = 0, t0, step;
-  const int bufs = 1 << bufs_log2<C>(a);
+  int st = 0, t0, step;
   uint32_t full_parity = 0;
   tile_range<C>(a, &t0, &step);
-  for (int t = t0; t < tiles && !failed; t += step) {
-    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    const uint32_t idesc = idesc_e4m3_f32(C::kPTile, tile.n);
-    for (int kb = 0; kb < tile.nk; ++kb) {
-      warp_wait(smem_u32(s.full + st), full_parity, &failed, a);
-      if (failed) break;
-      tc_fence_after();
-      const uint64_t p = desc_sw128(smem_u32(s.ring + st * stage_bytes<C>(a)));
-      issue_step<C::CTAS>(tmem + buf * (kTmemCols >> bufs_log2<C>(a)), p, p + (kLanes * kStepBytes >> 4), idesc,
-                          smem_u32(s.empty + st), smem_u32(s.acc_full + buf));
-      if (++st == stages) {
-        st = 0;
-        full_parity ^= 1;
+  if constexpr (!C::kSwap) {
+    int buf = 0;
+    for (int t = t0; t < tiles && !failed; t += step) {
+      const int nk = get_tile<C>(a, t, s.prefix, s.start).nk;
+      for (int kb = 0; kb < nk; ++kb) {
+        warp_wait(smem_u32(s.full + st), full_parity, &failed, a);
+        if (failed) break;
+        tc_fence_after();
+        const uint64_t p = desc_sw128(smem_u32(s.ring + st * C::kFixedStageBytes));
+        issue_step<C::CTAS, true>(tmem + buf * kColumns, p, p + (kLanes * kStepBytes >> 4),
+                                  idesc_e4m3_f32(C::kPTile, kColumns), smem_u32(s.empty + st),
+                                  smem_u32(s.acc_full + buf), true);
+        if (++st == stages) {
+          st = 0;
+          full_parity ^= 1;
+        }
+        buf ^= 1;
       }
-      buf = (buf + 1) & (bufs - 1);
+    }
+  } else {
+    uint32_t batch = 0;
+    for (int t = t0; t < tiles && !failed; t += step) {
+      const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+      const int nk = tile.nk;
+      const uint32_t idesc = idesc_e4m3_f32(C::kPTile, tile.n);
+      for (int kb = 0; kb < nk; ++batch) {
+        const uint32_t half = batch & 1;
+        warp_wait(smem_u32(s.acc_empty + half), ((batch >> 1) & 1) ^ 1, &failed, a);
+        uint32_t column = tmem + half * kColumns;
+        for (int left = min(a.batch, nk - kb); left > 0; --left, ++kb) {
+          warp_wait(smem_u32(s.full + st), full_parity, &failed, a);
+          if (failed) break;
+          tc_fence_after();
+          const uint64_t p = desc_sw128(smem_u32(s.ring + st * stage_bytes<C>(a)));
+          issue_step<C::CTAS, false>(column, p, p + (kLanes * kStepBytes >> 4), idesc,
+                                     smem_u32(s.empty + st), smem_u32(s.acc_full + half), left == 1);
+          column += a.stride;
+          if (++st == stages) {
+            st = 0;
+            full_parity ^= 1;
+          }
+        }
+        if (failed) break;
+      }
     }
   }
   if (elect_one()) {
@@ -682,10 +789,12 @@ __device__ __forceinline__ void multiply(const KernelArgs& a, const Smem& s, int
   mbar_wait(smem_u32(s.done), 0, &drain_failed, kWaitNs, a.err);
 }
 
-// 4-byte asynchronous copy to shared memory; zero where !ok (nothing is read then).
-__device__ __forceinline__ void copy_scale(float* dst, const float* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(ok ? 4 : 0)
+// 4-byte asynchronous copy to shared memory, `at` floats on from dst and src; zero where !ok (nothing is
+// read then).
+template <int AT>
+__device__ __forceinline__ void copy_scale(uint32_t dst, const float* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0 + %3], [%1 + %3], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 4 : 0), "n"(AT * 4)
                : "memory");
 }
 
@@ -700,36 +809,46 @@ __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s,
   tile_range<C>(a, &t0, &step);
   for (int t = t0; t < tiles && !failed; t += step) {
     const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    for (int kb0 = 0; kb0 < tile.nk; kb0 += kScaleGroup, ++group) {
+    const int nk = tile.nk, p_valid = tile.p_valid, q_valid = tile.q_valid;
+    // this lane's scales of the current step: its rows of P (or P's block), its columns (or blocks) of Q
+    const float* p = a.p_scales + tile.p_scale + (C::kPRows ? lane : 0);
+    const float* q = a.q_scales + tile.q_scale + (C::kQRows ? (int64_t)lane : lane * a.q_pitch);
+    for (int kb0 = 0; kb0 < nk; kb0 += kScaleGroup, ++group) {
       const int g = group % kScaleGroups;
       warp_wait(smem_u32(s.scale_empty + g), ((group / kScaleGroups) & 1) ^ 1, &failed, a);
       if (failed) break;
-      for (int kb = kb0; kb < min(kb0 + kScaleGroup, tile.nk); ++kb) {
-        float* dst = s.scales + (g * kScaleGroup + kb - kb0) * C::kSlotFloats;
-        if (C::kPRows) {
-          const float* src = a.p_scales + tile.p_scale + kb * a.p_pitch;
-#pragma unroll
-          for (int i = 0; i < kLanes / 32; ++i) {
-            const int r = 32 * i + lane;
-            const bool ok = r < tile.p_valid;
-            copy_scale(dst + r, ok ? src + r : a.p_scales, ok);
-          }
-        } else if (lane == 0) {
-          const bool ok = tile.p_valid > 0;
-          copy_scale(dst, ok ? a.p_scales + tile.p_scale + kb : a.p_scales, ok);
+      uint32_t dst = smem_u32(s.scales + g * kScaleGroup * C::kSlotFloats + lane);
+      for (int left = min(kScaleGroup, nk - kb0); left > 0; --left) {
+        if constexpr (C::kPRows) {
+          copy_scale<0>(dst, p, lane < p_valid);
+          copy_scale<32>(dst, p, 32 + lane < p_valid);
+          copy_scale<64>(dst, p, 64 + lane < p_valid);
+          copy_scale<96>(dst, p, 96 + lane < p_valid);
+          p += a.p_pitch;
+        } else {
+          if (lane == 0) copy_scale<0>(dst, p, p_valid > 0);
+          ++p;
         }
-        dst += C::kPScales;
-        if (C::kQRows) {
-          const float* src = a.q_scales + tile.q_scale + kb * a.q_pitch;
-          for (int c = lane; c < tile.n; c += 32) {
-            const bool ok = c < tile.q_valid;
-            copy_scale(dst + c, ok ? src + c : a.q_scales, ok);
+        if constexpr (C::kQRows) {
+#define MXQ_COLUMNS(at) \
+  if (!C::kSwap || (at) < tile.n) copy_scale<at>(dst + C::kPScales * 4, q, (at) + lane < q_valid)
+          MXQ_COLUMNS(0);
+          MXQ_COLUMNS(32);
+          MXQ_COLUMNS(64);
+          MXQ_COLUMNS(96);
+          if constexpr (!C::kSwap) MXQ_COLUMNS(128);
+          if constexpr (!C::kSwap) MXQ_COLUMNS(160);
+          if constexpr (!C::kSwap) MXQ_COLUMNS(192);
+          if constexpr (!C::kSwap) MXQ_COLUMNS(224);
+#undef MXQ_COLUMNS
+          q += a.q_pitch;
+        } else {
+          if (lane < kColumns / kB128) {
+            copy_scale<0>(dst + C::kPScales * 4, q, lane * kB128 < q_valid);
           }
-        } else if (lane < kColumns / kB128) {
-          const bool ok = lane * kB128 < tile.q_valid;
-          copy_scale(dst + lane,
-                     ok ? a.q_scales + tile.q_scale + lane * a.q_pitch + kb : a.q_scales, ok);
+          ++q;
         }
+        dst += C::kSlotFloats * 4;
       }
       __syncwarp();
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
@@ -740,25 +859,23 @@ __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s,
   asm volatile("cp.async.wait_all;" ::: "memory");  // none lands after the CTA's shared memory goes
 }
 
-// A promoting warp's way through the steps: the barriers of one step around its reads. (Asking the
-// next step's barrier before this step's sums, to have only the answer left, measured slower: 436
-// against 360 us at 8192^3. The answer is mostly no by then and the question costs 60 cycles.)
+// A promoting warp's way through the steps of the shapes with two accumulators: the barriers of one
+// step around its reads. (Asking the next step's barrier before this step's sums, to have only the
+// answer left, measured slower: 436 against 360 us at 8192^3; so did fetching its scales there, 392
+// against 340.)
 template <typename C>
 struct Steps {
   const KernelArgs& a;
   const Smem& s;
-  const int stages, log2;
   uint32_t full0;        // the barriers on which read accumulators are reported
-  int it = 0, st2;       // step, stage of the step that gets its accumulator next
+  int it = 0, st2 = 2;   // step, stage of the step after next
   uint32_t group = 0;
   bool failed = false;
 
-  __device__ __forceinline__ Steps(const KernelArgs& a_, const Smem& s_)
-      : a(a_), s(s_), stages(stage_count<C>(a_)), log2(bufs_log2<C>(a_)) {
+  __device__ __forceinline__ Steps(const KernelArgs& a_, const Smem& s_) : a(a_), s(s_) {
     full0 = C::CTAS == 2 ? in_cta(smem_u32(s.full), 0) : smem_u32(s.full);
-    for (int i = 0; i < 1 << log2; ++i) hand_back(i);  // the first steps find theirs free
-    st2 = 1 << log2;
-    if (st2 == stages) st2 = 0;
+    hand_back(0);  // the first two steps find theirs free
+    hand_back(1);
   }
   __device__ __forceinline__ void hand_back(int st) {
     if constexpr (C::CTAS == 2) {
@@ -776,35 +893,78 @@ struct Steps {
     return s.scales + (g * kScaleGroup + in) * C::kSlotFloats;
   }
   __device__ __forceinline__ bool accumulator() {
-    warp_wait(smem_u32(s.acc_full + (it & ((1 << log2) - 1))), (it >> log2) & 1, &failed, a);
+    warp_wait(smem_u32(s.acc_full + (it & 1)), (it >> 1) & 1, &failed, a);
     if (failed) return false;
     tc_fence_after();
     return true;
   }
-  __device__ __forceinline__ uint32_t column() const {  // the step's accumulator
-    return (it & ((1 << log2) - 1)) * (kTmemCols >> log2);
-  }
+  __device__ __forceinline__ uint32_t column() const { return (it & 1) * kColumns; }
   __device__ __forceinline__ void accumulator_read() {
     tc_fence_before();
     hand_back(st2);
-    if (++st2 == stages) st2 = 0;
-  }
-  __device__ __forceinline__ bool group_ends(int kb, int nk) const {
-    return kb % kScaleGroup == kScaleGroup - 1 || kb == nk - 1;
+    if (++st2 == C::kStages) st2 = 0;
   }
   __device__ __forceinline__ void end(int kb, int nk) {
-    if (group_ends(kb, nk)) {
+    if (kb % kScaleGroup == kScaleGroup - 1 || kb == nk - 1) {
       warp_arrive(smem_u32(s.scale_empty + group % kScaleGroups));
       ++group;
     }
     ++it;
   }
   // The steps that may have been loaded are handed back unread, so that the loading warp sees its
-  // copies land. Of `bufs` accumulators, steps it .. it + bufs - 1 have their arrivals already and
-  // their stages may still be in that phase, so the steps that follow on those stages are left out:
-  // a second arrival there would complete a phase before its copies do.
+  // copies land. Steps it and it + 1 have their arrivals already and their stages may still be in
+  // that phase, so the steps that follow on those two stages are left out: a second arrival there
+  // would complete a phase before its copies do.
   __device__ __forceinline__ void give_up() {
-    for (int i = 0; i < stages - (1 << log2); ++i) hand_back((st2 + i) % stages);
+    for (int i = 0; i < C::kStages - 2; ++i) hand_back((st2 + i) % C::kStages);
+  }
+};
+
+// The same of the swapped shape, whose steps are short beside the way of their signals (about 650 cycles
+// of barriers and reads a step, whatever its columns): tensor memory holds two batches of up to four
+// accumulators, and a batch is handed over, read and handed back as one.
+template <typename C>
+struct Batches {
+  const KernelArgs& a;
+  const Smem& s;
+  uint32_t empty0;
+  uint32_t batch = 0, group = 0;
+  bool failed = false;
+
+  __device__ __forceinline__ Batches(const KernelArgs& a_, const Smem& s_) : a(a_), s(s_) {
+    empty0 = C::CTAS == 2 ? in_cta(smem_u32(s.acc_empty), 0) : smem_u32(s.acc_empty);
+  }
+  // scales of the batch that begins with step kb of the tile (a batch lies in one group)
+  __device__ __forceinline__ const float* scales(int kb) {
+    const int g = group % kScaleGroups, in = kb % kScaleGroup;
+    if (in == 0) {
+      warp_wait(smem_u32(s.scale_full + g), (group / kScaleGroups) & 1, &failed, a);
+    }
+    return s.scales + (g * kScaleGroup + in) * C::kSlotFloats;
+  }
+  __device__ __forceinline__ bool accumulators() {
+    warp_wait(smem_u32(s.acc_full + (batch & 1)), (batch >> 1) & 1, &failed, a);
+    if (failed) return false;
+    tc_fence_after();
+    return true;
+  }
+  __device__ __forceinline__ uint32_t column(int in) const {
+    return (batch & 1) * kColumns + in * a.stride;
+  }
+  __device__ __forceinline__ void accumulators_read() {
+    tc_fence_before();
+    if constexpr (C::CTAS == 2) {
+      warp_arrive_cluster(empty0 + 8 * (batch & 1));
+    } else {
+      warp_arrive(empty0 + 8 * (batch & 1));
+    }
+  }
+  __device__ __forceinline__ void end(int kb, int nk) {  // kb: the step after the batch
+    if (kb % kScaleGroup == 0 || kb == nk) {
+      warp_arrive(smem_u32(s.scale_empty + group % kScaleGroups));
+      ++group;
+    }
+    ++batch;
   }
 };
 
@@ -853,7 +1013,7 @@ struct Boxes {
 // bytes each), so that a lane stores 16 bytes of one token.
 template <typename C>
 __device__ __forceinline__ void store_swapped(const KernelArgs& a, const Smem& s, const Tile& tile,
-                                              int pw, const uint64_t (&sums)[kWarpCols / 2],
+                                              int pw, const uint64_t (&sums)[C::kWarpCols / 2],
                                               int first_group, int every) {
   const int lane = threadIdx.x & 31, row0 = (pw & 3) * 32, lr = lane >> 2, lc = (lane & 3) * 2;
   const int cols = tile.n / 2, col0 = (pw >> 2) * cols;
@@ -861,7 +1021,7 @@ __device__ __forceinline__ void store_swapped(const KernelArgs& a, const Smem& s
   // what a lane stores of a group: token lane / 4, 8 lanes' worth from 8 (lane % 4) on
   const int part = (lane & 3) * 8;
 #pragma unroll
-  for (int gi = 0; gi < kWarpCols / 8; ++gi) {
+  for (int gi = 0; gi < C::kWarpCols / 8; ++gi) {
     if (gi * 8 >= cols || gi % every != first_group) continue;
     if constexpr (C::kF32) {
 #pragma unroll
@@ -897,57 +1057,47 @@ template <typename C>
 __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const KernelArgs& a,
                                              const Smem& s, int tiles, uint32_t tmem, int pw) {
   const int lane = threadIdx.x & 31, row = (pw & 3) * 32 + lane, half = pw >> 2;
-  const uint32_t tbase = tmem + ((uint32_t)((pw & 3) * 32) << 16) + half * kWarpCols;
+  const uint32_t tbase = tmem + ((uint32_t)((pw & 3) * 32) << 16) + half * C::kWarpCols;
   Steps<C> steps(a, s);
   Boxes boxes{s.staging + pw * C::kStagingBytes};
   int t0, step;
   tile_range<C>(a, &t0, &step);
   for (int t = t0; t < tiles; t += step) {
-    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    uint64_t sums[kWarpCols / 2];
+    const int nk = get_tile<C>(a, t, s.prefix, s.start).nk;
+    uint64_t sums[C::kWarpCols / 2];
 #pragma unroll
-    for (int i = 0; i < kWarpCols / 2; ++i) sums[i] = 0u;
-    for (int kb = 0; kb < tile.nk; ++kb) {
+    for (int i = 0; i < C::kWarpCols / 2; ++i) sums[i] = 0u;
+    for (int kb = 0; kb < nk; ++kb) {
       const float* sc = steps.scales(kb);
       const uint64_t m = both(sc[row] * sc[C::kPScales + half]);
       if (!steps.accumulator()) break;
-      // The accumulator goes back as soon as it is in registers; two of its four chunks fit beside
-      // the sums, each of the others follows one that is added.
-      uint32_t v[2][32];
-      auto add = [&](int ch) {
+      // The accumulator goes back as soon as it is in registers; half of it fits beside the sums.
+      uint64_t v[32];
+      auto add = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          uint64_t& d = sums[ch * 16 + i / 2];
-          d = fma2(pair(v[ch & 1][i], v[ch & 1][i + 1]), m, d);
-        }
+        for (int i = 0; i < 32; ++i) sums[h * 32 + i] = fma2(v[i], m, sums[h * 32 + i]);
       };
       const uint32_t src = tbase + steps.column();
-      issue_row(src, v[0]);
-      issue_row(src + 32, v[1]);
-      wait_columns(v[0]);
-      wait_columns(v[1]);
+      read_row(src, v);
       add(0);
-      issue_row(src + 64, v[0]);
-      add(1);
-      issue_row(src + 96, v[1]);
-      wait_columns(v[0]);
-      wait_columns(v[1]);
+      read_row(src + 64, v);
       steps.accumulator_read();
-      add(2);
-      add(3);
-      steps.end(kb, tile.nk);
+      add(1);
+      steps.end(kb, nk);
     }
     if (steps.failed) {
       steps.give_up();
       break;
     }
+    // found again: kept through the steps, its fields would take the sums' registers
+    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
     if (tile.p_valid <= (pw & 3) * 32) continue;  // none of the warp's rows exists
     // two boxes at a time: one fence and one wait for both
     constexpr int kBoxCols = C::kF32 ? 32 : 64;
     const int row0 = (pw & 3) * 32;
 #pragma unroll
-    for (int b = 0; b < kWarpCols / kBoxCols; b += 2) {
-      const int col = half * kWarpCols + b * kBoxCols;
+    for (int b = 0; b < C::kWarpCols / kBoxCols; b += 2) {
+      const int col = half * C::kWarpCols + b * kBoxCols;
       if (col >= tile.q_valid) break;
       boxes.wait();
 #pragma unroll
@@ -981,137 +1131,166 @@ __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const Kern
   boxes.drain();
 }
 
-// The promoting warps of the columns and swapped shapes: warp w holds lanes 32 (w % 4) .. and half
-// w / 4 of the tile's columns in fragments: sums[(ch * 4 + g) * 4 + r] of lane l are the columns
-// 32 ch + 8 g + 2 (l % 4) + {0, 1} of row 8 r + l / 4.
+// The promoting warps of the columns and swapped shapes read the accumulator in fragments: warp w holds
+// lanes 32 (w % 4) .. and half w / 4 of the tile's columns, and sums[(ch * 4 + g) * 4 + r] of lane l are
+// the columns 32 ch + 8 g + 2 (l % 4) + {0, 1} of row 8 r + l / 4.
+// Fragments reads one accumulator and adds it, `chunks` chunks of 32 columns, two at a time in registers:
+// read(): the reads, with the first two chunks' sums between them; rest(): the sums that are left.
+template <typename C>
+struct Fragments {
+  uint64_t (&sums)[C::kWarpCols / 2];
+  uint64_t m[4], q[4];  // row scales; column scales of the chunk that is added next
+  uint64_t v[32];
+  const float* qs;
+
+  __device__ __forceinline__ void column_scales(int ch) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      q[g] = *reinterpret_cast<const uint64_t*>(qs + ch * 32 + g * 8);
+      if (!C::kPRows) q[g] = mul2(q[g], m[0]);
+    }
+  }
+  // ps: scales of P's rows (at this warp's first and lane / 4) or of its block; qs_: of the columns
+  __device__ __forceinline__ void scales(const float* ps, const float* qs_) {
+    qs = qs_;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (C::kPRows || r == 0) m[r] = both(ps[C::kPRows ? 8 * r : 0]);
+    }
+    column_scales(0);
+  }
+  // ch is known at compile time wherever this is called; w: the chunk's sixteen pairs
+  __device__ __forceinline__ void add(int ch, const uint64_t* w) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint64_t& d = sums[(ch * 4 + g) * 4 + r];
+        d = fma2(w[8 * (r >> 1) + 2 * g + (r & 1)], C::kPRows ? mul2(q[g], m[r]) : q[g], d);
+      }
+    }
+  }
+  __device__ __forceinline__ void add_two(int ch, bool second) {
+    add(ch, v);
+    if (second) {
+      column_scales(ch + 1);
+      add(ch + 1, v + 16);
+    }
+  }
+  __device__ __forceinline__ void read(uint32_t src, int chunks) {  // chunks <= kWarpCols / 32
+    if constexpr (C::kWarpCols > 64) {  // all four chunks
+      read_fragments(src, v);
+      add_two(0, true);
+      column_scales(2);
+      read_fragments(src + 64, v);
+    } else if (chunks > 1) {
+      read_fragments(src, v);
+    } else {
+      read_fragments(src, *reinterpret_cast<uint64_t(*)[16]>(v));
+    }
+  }
+  __device__ __forceinline__ void rest(int chunks) {
+    add_two(C::kWarpCols > 64 ? 2 : 0, chunks > 1);
+  }
+};
+
+// The columns shape.
 template <typename C>
 __device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const KernelArgs& a,
-                                                const Smem& s, int tiles, uint32_t tmem, int pw,
-                                                uint64_t (&sums)[kWarpCols / 2], Tile* last) {
-  constexpr int kChunks = kWarpCols / 32;
+                                                const Smem& s, int tiles, uint32_t tmem, int pw) {
+  constexpr int kChunks = C::kWarpCols / 32;
   const int lane = threadIdx.x & 31, row0 = (pw & 3) * 32, lr = lane >> 2, lc = (lane & 3) * 2;
+  const int col0 = (pw >> 2) * C::kWarpCols;
+  const uint32_t tbase = tmem + ((uint32_t)row0 << 16) + col0;
   Steps<C> steps(a, s);
   Boxes boxes{s.staging + pw * C::kStagingBytes};
   int t0, step;
   tile_range<C>(a, &t0, &step);
   for (int t = t0; t < tiles; t += step) {
     const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    const int cols = tile.n / 2, col0 = (pw >> 2) * cols;  // this warp's columns
-    const int chunks = C::kSwap ? (cols + 31) / 32 : kChunks;
-    const uint32_t tbase = tmem + ((uint32_t)row0 << 16) + col0;
+    uint64_t sums[C::kWarpCols / 2];
 #pragma unroll
-    for (int i = 0; i < kWarpCols / 2; ++i) sums[i] = 0u;
+    for (int i = 0; i < C::kWarpCols / 2; ++i) sums[i] = 0u;
+    Fragments<C> f{sums};
     for (int kb = 0; kb < tile.nk; ++kb) {
       const float* sc = steps.scales(kb);
-      const float* qs = sc + C::kPScales + col0 + lc;
-      uint64_t m[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (C::kPRows || r == 0) m[r] = both(sc[C::kPRows ? row0 + 8 * r + lr : 0]);
-      }
-      uint64_t q[4];  // of the chunk that is added next
-      auto column_scales = [&](int ch) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          q[g] = *reinterpret_cast<const uint64_t*>(qs + ch * 32 + g * 8);
-          if (!C::kPRows) q[g] = mul2(q[g], m[0]);
-        }
-      };
-      column_scales(0);
+      f.scales(sc + row0 + lr, sc + C::kPScales + col0 + lc);
       if (!steps.accumulator()) break;
-      uint32_t v[2][32];
-      const uint32_t src = tbase + steps.column();
-      auto issue = [&](int ch) {
-        issue_fragment(src + ch * 32, v[ch & 1]);
-        issue_fragment(src + ch * 32 + (16u << 16), v[ch & 1] + 16);
-      };
-      auto add = [&](int ch) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint64_t qg = q[g];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t* w = v[ch & 1] + (r >> 1) * 16 + g * 4 + (r & 1) * 2;
-            uint64_t& d = sums[(ch * 4 + g) * 4 + r];
-            d = fma2(pair(w[0], w[1]), C::kPRows ? mul2(qg, m[r]) : qg, d);
-          }
-        }
-      };
-      issue(0);
-      if (chunks > 1) issue(1);
-      wait_columns(v[0]);
-      wait_columns(v[1]);
-      if (chunks > 2) {
-        add(0);
-        issue(2);
-        column_scales(1);
-        if (chunks > 3) {
-          add(1);
-          issue(3);
-          column_scales(2);
-        }
-        wait_columns(v[0]);
-        wait_columns(v[1]);
-      }
+      f.read(tbase + steps.column(), kChunks);
       steps.accumulator_read();
-      if (chunks <= 2) {
-        add(0);
-        if (chunks == 2) {
-          column_scales(1);
-          add(1);
-        }
-      } else if (chunks == 3) {
-        add(1);
-        column_scales(2);
-        add(2);
-      } else {
-        add(2);
-        column_scales(3);
-        add(3);
-      }
+      f.rest(kChunks);
       steps.end(kb, tile.nk);
     }
     if (steps.failed) {
       steps.give_up();
       break;
     }
-    *last = tile;
-    if constexpr (C::kSwap) {
-      if (C::MODE == kB128Dense && a.split > 1) break;  // one tile; the cluster adds the parts
-      store_swapped<C>(a, s, tile, pw, sums, 0, 1);
-    } else {
-      if (tile.p_valid <= row0) continue;
-      constexpr int kBoxCols = C::kF32 ? 32 : 64;
+    if (tile.p_valid <= row0) continue;
+    constexpr int kBoxCols = C::kF32 ? 32 : 64;
 #pragma unroll
-      for (int b = 0; b < kWarpCols / kBoxCols; b += 2) {
-        const int col = col0 + b * kBoxCols;
-        if (col >= tile.q_valid) break;
-        boxes.wait();
+    for (int b = 0; b < C::kWarpCols / kBoxCols; b += 2) {
+      const int col = col0 + b * kBoxCols;
+      if (col >= tile.q_valid) break;
+      boxes.wait();
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
-          for (int g = 0; g < kBoxCols / 8; ++g) {
+        for (int g = 0; g < kBoxCols / 8; ++g) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint64_t d = sums[((b + u) * (kBoxCols / 8) + g) * 4 + r];
-              uint8_t* line = boxes.base + u * 4096 + (8 * r + lr) * 128;
-              if constexpr (C::kF32) {
-                const int byte = (g * 8 + lc) * 4;
-                *reinterpret_cast<uint64_t*>(line + (((byte >> 4) ^ lr) << 4) + (byte & 15)) = d;
-              } else {
-                const int byte = (g * 8 + lc) * 2;
-                *reinterpret_cast<uint32_t*>(line + (((byte >> 4) ^ lr) << 4) + (byte & 15)) =
-                    bf16_pair(first(d), second(d));
-              }
+          for (int r = 0; r < 4; ++r) {
+            const uint64_t d = sums[((b + u) * (kBoxCols / 8) + g) * 4 + r];
+            uint8_t* line = boxes.base + u * 4096 + (8 * r + lr) * 128;
+            if constexpr (C::kF32) {
+              const int byte = (g * 8 + lc) * 4;
+              *reinterpret_cast<uint64_t*>(line + (((byte >> 4) ^ lr) << 4) + (byte & 15)) = d;
+            } else {
+              const int byte = (g * 8 + lc) * 2;
+              *reinterpret_cast<uint32_t*>(line + (((byte >> 4) ^ lr) << 4) + (byte & 15)) =
+                  bf16_pair(first(d), second(d));
             }
           }
         }
-        boxes.store(cmap, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0,
-                    kBoxCols, tile.q_valid - col);
       }
+      boxes.store(cmap, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0,
+                  kBoxCols, tile.q_valid - col);
     }
   }
-  if (!C::kSwap) boxes.drain();
+  boxes.drain();
+}
+
+// The swapped shape. A call that splits the contraction has one tile, whose sums are left for add_parts.
+template <typename C>
+__device__ __forceinline__ void promote_swapped(const KernelArgs& a, const Smem& s, int tiles,
+                                                uint32_t tmem, int pw,
+                                                uint64_t (&sums)[C::kWarpCols / 2]) {
+  const int lane = threadIdx.x & 31, row0 = (pw & 3) * 32, lr = lane >> 2, lc = (lane & 3) * 2;
+  Batches<C> batches(a, s);
+  int t0, step;
+  tile_range<C>(a, &t0, &step);
+  for (int t = t0; t < tiles; t += step) {
+    const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+    const int cols = tile.n / 2, col0 = (pw >> 2) * cols;  // this warp's columns
+    const int chunks = (cols + 31) / 32;
+    const uint32_t tbase = tmem + ((uint32_t)row0 << 16) + col0;
+#pragma unroll
+    for (int i = 0; i < C::kWarpCols / 2; ++i) sums[i] = 0u;
+    Fragments<C> f{sums};
+    for (int kb = 0; kb < tile.nk; kb += a.batch) {
+      const int n = min(a.batch, tile.nk - kb);
+      const float* sc = batches.scales(kb);
+      if (!batches.accumulators()) break;
+      for (int in = 0; in < n; ++in, sc += C::kSlotFloats) {
+        f.scales(sc + (C::kPRows ? row0 + lr : 0), sc + C::kPScales + col0 + lc);
+        f.read(tbase + batches.column(in), chunks);
+        if (in == n - 1) batches.accumulators_read();
+        f.rest(chunks);
+      }
+      batches.end(kb + n, tile.nk);
+    }
+    if (batches.failed) break;
+    if (C::MODE == kB128Dense && a.split > 1) break;
+    store_swapped<C>(a, s, tile, pw, sums, 0, 1);
+  }
 }
 
 // Adds the parts of a tile whose contraction the CTAs of a cluster shared: every CTA leaves its sums in
@@ -1119,12 +1298,12 @@ __device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const K
 // rank order and writes them.
 template <typename C>
 __device__ __forceinline__ void add_parts(const KernelArgs& a, const Smem& s, const Tile& tile, int pw,
-                                          uint64_t (&sums)[kWarpCols / 2]) {
+                                          uint64_t (&sums)[C::kWarpCols / 2]) {
   const int tid = threadIdx.x - 128, rank = (int)cluster_rank();
   const int groups = tile.n / 2 / 8;  // of eight columns, per warp
   uint64_t* mine = reinterpret_cast<uint64_t*>(s.ring) + tid;
 #pragma unroll
-  for (int i = 0; i < kWarpCols / 2; ++i) {
+  for (int i = 0; i < C::kWarpCols / 2; ++i) {
     if (i / 4 < groups) mine[i * (kPromoWarps * 32)] = sums[i];
   }
   cluster_sync();
@@ -1132,7 +1311,7 @@ __device__ __forceinline__ void add_parts(const KernelArgs& a, const Smem& s, co
 #pragma unroll
   for (int r = 0; r < kMaxSplit; ++r) from[r] = in_cta(smem_u32(mine), r < a.split ? r : 0);
 #pragma unroll
-  for (int gi = 0; gi < kWarpCols / 8; ++gi) {
+  for (int gi = 0; gi < C::kWarpCols / 8; ++gi) {
     if (gi >= groups || gi % a.split != rank) continue;
     uint64_t v[kMaxSplit][4];  // all on their way before the first is added
 #pragma unroll
@@ -1175,7 +1354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   s.full = reinterpret_cast<uint64_t*>(s.scales + kScaleSlots * C::kSlotFloats);
   s.empty = s.full + kMaxStages;
   s.acc_full = s.empty + kMaxStages;
-  s.scale_full = s.acc_full + kMaxBufs;
+  s.acc_empty = s.acc_full + 2;
+  s.scale_full = s.acc_empty + 2;
   s.scale_empty = s.scale_full + kScaleGroups;
   s.done = s.scale_empty + kScaleGroups;
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.done + 1);
@@ -1187,10 +1367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < stage_count<C>(a); ++i) {
-      mbar_init(smem_u32(s.full + i), 1 + C::CTAS * kPromoWarps);
+      mbar_init(smem_u32(s.full + i), C::kSwap ? 1 : 1 + C::CTAS * kPromoWarps);
       mbar_init(smem_u32(s.empty + i), 1);
     }
-    for (int i = 0; i < 1 << bufs_log2<C>(a); ++i) mbar_init(smem_u32(s.acc_full + i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(s.acc_full + i), 1);
+      mbar_init(smem_u32(s.acc_empty + i), C::CTAS * kPromoWarps);
+    }
     for (int i = 0; i < kScaleGroups; ++i) {
       mbar_init(smem_u32(s.scale_full + i), 32);
       mbar_init(smem_u32(s.scale_empty + i), kPromoWarps);
@@ -1216,9 +1399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s.tmem_slot;
   const int tiles = tile_count<C>(a, s.prefix);
   // The promoting warps hold their sums and two or three chunks in registers: the others give theirs
-  // up (40 x 128 + 232 x 256 = 168 x 384, the launch's total).
+  // up.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 0) produce<C>(pmap, qmap, qmap16, a, s, tiles);
     if (warp == 1 && (C::CTAS == 1 || cluster_rank() == 0)) multiply<C>(a, s, tiles, tmem);
     if (warp == 2) fetch_scales<C>(a, s, tiles);
@@ -1228,17 +1411,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_sync();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    if constexpr (C::kFragments) {
-      uint64_t sums[kWarpCols / 2];
-      Tile last;
-      promote_columns<C>(cmap, a, s, tiles, tmem, warp - 4, sums, &last);
-      if constexpr (C::kSwap && C::MODE == kB128Dense) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kPromoRegs));
+    if constexpr (C::kSwap) {
+      uint64_t sums[C::kWarpCols / 2];
+      promote_swapped<C>(a, s, tiles, tmem, warp - 4, sums);
+      if constexpr (C::MODE == kB128Dense) {
         if (parts) {
-          last = get_tile<C>(a, blockIdx.x / a.split, s.prefix, s.start);
-          add_parts<C>(a, s, last, warp - 4, sums);
+          const Tile tile = get_tile<C>(a, blockIdx.x / a.split, s.prefix, s.start);
+          add_parts<C>(a, s, tile, warp - 4, sums);
         }
       }
+    } else if constexpr (C::kQRows) {
+      promote_columns<C>(cmap, a, s, tiles, tmem, warp - 4);
     } else {
       promote_rows<C>(cmap, a, s, tiles, tmem, warp - 4);
     }
@@ -1332,11 +1516,8 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
     a.stage_bytes = (kLanes + q_tile / C::CTAS) * kStepBytes;
     a.stages = C::kRingBytes / a.stage_bytes;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    // as many accumulators as there is room for, and no more than stages
-    while ((2 << a.bufs_log2) <= kMaxBufs && (2 << a.bufs_log2) <= a.stages &&
-           (int)(kTmemCols >> (a.bufs_log2 + 1)) >= q_tile) {
-      ++a.bufs_log2;
-    }
+    a.batch = q_tile <= 64 ? 4 : 2;  // two batches fill tensor memory
+    a.stride = kColumns / a.batch;
   }
   const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -1374,29 +1555,33 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
                          kThreads, smem_bytes<C>(), cluster, stream, pmap, qmap, qmap16, cmap, a);
 }
 
-// Dense calls. Pairs with 256 x 256 tiles once they fill half of the SMs; below that the swapped
-// shape, whose 128-row weight tiles, times up to eight CTAs along the contraction, spread few tokens
-// over the SMs.
+// Dense calls: 256 x 256 tiles on pairs, or the swapped shape, whose 128-row weight tiles, times up to
+// eight CTAs along the contraction, spread few tokens over the SMs. The rule compares what each costs
+// by its waves (us, measured: 0.40 a step and 3 a tile of the pairs, whatever the rows; 0.25 a step
+// and 2 us more with 128 tokens than with 16, and 5 a tile with the joining of the parts).
 template <bool B_ROWS, bool F32>
 cudaError_t launch_dense(const B128GemmArgs& g, cudaStream_t stream) {
   using Large = Config<2, kB128Dense, false, true, B_ROWS, F32>;
   using Small = Config<1, kB128Dense, true, B_ROWS, true, F32>;
   const int slots = slot_count<Small>();
-  if (ceil_div(g.M, 256) * ceil_div(g.N, 256) * 4 > slots) {
-    return launch_config<Large>(g, kColumns, 1, stream);
-  }
-  const int64_t q_tiles = ceil_div(g.M, kColumns);
+  if (slots <= 1) return cudaErrorInvalidConfiguration;
+  const int64_t nk = ceil_div(g.K, kB128);
+  const int64_t q_tiles = ceil_div(g.M, kFewRows);
   const int q_tile = (int)ceil_div(ceil_div(g.M, q_tiles), 16) * 16;
-  const int64_t tiles = q_tiles * ceil_div(g.N, kLanes), nk = ceil_div(g.K, kB128);
+  const int64_t tiles = q_tiles * ceil_div(g.N, kLanes);
   int split = 1;
   while (split < kMaxSplit && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
-  return launch_config<Small>(g, q_tile, split, stream);
+  const double few = (double)ceil_div(tiles * split, slots) *
+                     ((double)ceil_div(nk, split) * (0.25 + 0.0015 * q_tile) + (split > 1 ? 5 : 3));
+  const double many =
+      (double)ceil_div(ceil_div(g.M, 256) * ceil_div(g.N, 256), slots / 2) * ((double)nk * 0.40 + 3);
+  return many <= few ? launch_config<Large>(g, kColumns, 1, stream)
+                     : launch_config<Small>(g, q_tile, split, stream);
 }
 
 // Calls by expert: experts of more than kFewRows rows in 256 x 256 tiles (0.35 us a step whatever the
 // rows), the others swapped (a step costs its weights and 0.1 us per 64 rows): two launches, each of
 // which takes its experts from the offsets. A call of few rows has no large expert.
-constexpr int kFewRows = 128;
 template <bool F32>
 cudaError_t launch_grouped(const B128GemmArgs& g, cudaStream_t stream) {
   using Many = Config<2, kB128Grouped, false, true, false, F32>;
