@@ -7,29 +7,34 @@
 // One step is one scale block: operand P (128 tensor-memory lanes per CTA) and operand Q (up to 256
 // accumulator columns), 128 code bytes of each row, loaded by the tensor-memory accelerator into a
 // ring of 128-byte swizzled stages; four tcgen05.mma kind::f8f6f4 (K = 32) give the block's sums in
-// one of two accumulators; eight warps read it and add it, times its scales, to fp32 sums in
-// registers. The scales cannot wait until the end because they change with every block, so each
-// block costs 32768 fp32 FMAs per CTA and a trip through registers beside its MMAs (512 cycles at
-// the tensor cores' rate): that trip, not the MMAs, is what the kernel is built around.
-//   * Two accumulators fill tensor memory, so a step cannot be shorter than half of (MMA + signal +
-//     read + signal). A step's stage is full when its operands have landed AND its accumulator has
-//     been read (one barrier for both); the reads come before the sums.
+// an accumulator; eight warps read it and add it, times its scales, to fp32 sums in registers. The
+// scales cannot wait until the end because they change with every block, so each block of a 128 x 256
+// tile costs 32768 fp32 FMAs and a trip through registers beside its MMAs (512 cycles at the tensor
+// cores' rate): that trip, not the MMAs, is what the kernel is built around.
+//   * Two accumulators of 256 columns fill tensor memory, so a step cannot be shorter than half of
+//     (MMA + signal + read + signal). A step's stage is full when its operands have landed AND its
+//     accumulator has been read (one barrier for both); the reads come before the sums.
 //   * The warp that multiplies runs converged and issues a step in one statement with every operand
 //     in uniform registers (issue_step): issued from a lone lane's branch it took 600 cycles.
 //   * Scales come through shared memory from a warp of their own, a group of four steps ahead.
 //   * fp32 sums are packed pairs: half the instructions beside the warp that issues the MMAs.
 //
-// Three shapes of the same kernel:
+// Four shapes of the same kernel:
 //   rows      P = A (rows' scales), Q = B (blocks' scales), CTA pairs, 256 x 256 tiles: large dense
-//             products. A pair (cta_group::2) shares one tile, each CTA holding 128 lanes and half of
-//             Q: per step 32 KB into an SM instead of 48, which alone bound 128 x 256 tiles.
+//             products and experts with many rows. A pair (cta_group::2) shares one tile, each CTA
+//             holding 128 lanes and half of Q: per step 32 KB into an SM instead of 48, which alone
+//             bound 128 x 256 tiles.
 //   columns   the same with a scale per column as well (weight gradients): the accumulator is read
 //             in fragments (4 rows x 32 columns per thread), which needs a quarter of the column
 //             scales' reads that a row per thread does (those would take 1024 cycles a step).
-//   swapped   P = B (weights), Q = A (tokens), for few tokens and for experts: a tile has as many
+//   narrow    the rows shape in 128 x 128 tiles on single CTAs, with four accumulators: experts with
+//             few rows, whose weights bound the product. Of A only the sixteens of rows that exist are
+//             loaded, and only the warps that hold some read the accumulator. A row for each of 128
+//             experts of 1024 x 2048 takes 46 us (5.8 TB/s of weights), 128 for each of 152 68 us.
+//   swapped   P = B (weights), Q = A (tokens), for few tokens in dense products: a tile has as many
 //             columns as it has tokens (a multiple of 16, at run time), so a step costs its weights.
-//             Dense calls split the contraction over the CTAs of a cluster and add the parts in rank
-//             order through distributed shared memory; calls by expert run on pairs.
+//             The contraction is split over the CTAs of a cluster, whose parts are added in rank
+//             order through distributed shared memory.
 //
 // Every mbarrier wait is bounded (KernelArgs::wait_limit_ns); a role whose wait ran out sets the
 // device error word and stops; loads and MMAs in flight are waited for (2 s) before the CTA frees its
@@ -50,11 +55,10 @@ using namespace tc;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // 2 s: drains, whatever the limit
 
 constexpr int kLanes = 128;      // rows of P in a CTA
-constexpr int kColumns = 256;    // most columns of a tile
+constexpr int kColumns = 256;    // columns of half of tensor memory: of an accumulator, or of a batch
 constexpr int kStepBytes = 128;  // one scale block of the contraction per step
 constexpr int kPromoWarps = 8;
 constexpr int kThreads = 128 + 32 * kPromoWarps;
-constexpr int kFewRows = 128;    // most columns (tokens) of a tile of the swapped shape
 constexpr uint32_t kTmemCols = 2 * kColumns;
 constexpr int kMaxStages = 12;
 // scales travel and are released by groups of steps
@@ -68,27 +72,35 @@ template <int CTAS_, int MODE_, bool SWAP_, bool P_ROWS_, bool Q_ROWS_, bool F32
 struct Config {
   static constexpr int CTAS = CTAS_, MODE = MODE_;
   static constexpr bool kSwap = SWAP_, kPRows = P_ROWS_, kQRows = Q_ROWS_, kF32 = F32_;
+  static constexpr bool kNarrow = CTAS_ == 1 && !SWAP_;
   static constexpr int kPTile = kLanes * CTAS;
+  // columns of a tile (swapped: at most), accumulators of that many in tensor memory (swapped: two
+  // batches)
+  static constexpr int kTileCols = SWAP_ || kNarrow ? 128 : 256;
+  static constexpr int kBufs = kNarrow ? 4 : 2;
   // most columns of a promoting warp, and the registers of the two halves of the block
-  static constexpr int kWarpCols = SWAP_ ? kFewRows / 2 : kColumns / 2;
-  static constexpr int kOtherRegs = SWAP_ ? 88 : 40, kPromoRegs = SWAP_ ? 208 : 232;
+  static constexpr int kWarpCols = kTileCols / 2;
+  static constexpr int kOtherRegs = kWarpCols == 64 ? 88 : 40;
+  static constexpr int kPromoRegs = kWarpCols == 64 ? 208 : 232;
   static_assert(kOtherRegs * 128 + kPromoRegs * 256 <= 168 * kThreads, "the launch's registers");
   // floats of a scale slot: one per lane / column (rows form) or one per block of 128
-  static constexpr int kPScales = P_ROWS_ ? kLanes : 4, kQScales = !Q_ROWS_ ? 4 : (SWAP_ ? kFewRows : kColumns);
+  static constexpr int kPScales = P_ROWS_ ? kLanes : 4, kQScales = Q_ROWS_ ? kTileCols : 4;
   static constexpr int kSlotFloats = kPScales + kQScales;
-  // ring of stages: four of fixed size, or (swapped) as many as the call's tile size leaves room for
-  static constexpr int kFixedStageBytes = (kLanes + kColumns / CTAS_) * kStepBytes;
-  static constexpr int kStages = 4;
+  // ring of stages: four or five of fixed size, or (swapped) as many as the call's tile size leaves
+  // room for
+  static constexpr int kFixedStageBytes = (kLanes + kTileCols / CTAS_) * kStepBytes;
+  static constexpr int kStages = kNarrow ? 5 : 4;
   static constexpr int kRingBytes = SWAP_ ? 172 * 1024 : kStages * kFixedStageBytes;
-  // staging of the output, per promoting warp: two boxes of 32 rows x 128 bytes for tensor-map
+  // staging of the output, per promoting warp: one or two boxes of 32 rows x 128 bytes for tensor-map
   // stores, or (swapped) 32 tokens x 32 bf16 in rows of 80 bytes
-  static constexpr int kStagingBytes = SWAP_ ? 32 * 80 : 2 * 4096;
+  static constexpr int kBoxes = kNarrow ? 1 : 2;
+  static constexpr int kStagingBytes = SWAP_ ? 32 * 80 : kBoxes * 4096;
 };
 
 template <typename C>
 constexpr int smem_bytes() {
   return 1024 + C::kRingBytes + kPromoWarps * C::kStagingBytes + kScaleSlots * C::kSlotFloats * 4 +
-         (2 * kMaxStages + 4 + 2 * kScaleGroups + 1) * 8 + 16 +
+         (2 * kMaxStages + 6 + 2 * kScaleGroups + 1) * 8 + 16 +
          (C::MODE != kB128Dense ? 2 * (kMaxExperts + 1) * 4 : 0);
 }
 
@@ -115,7 +127,7 @@ struct KernelArgs {
   int p_tiles, q_tiles;          // tiles of the operands (grouped: of the weights only)
   int row_min, row_max;          // grouped: experts with this many rows are this launch's
   Divisor run, per;              // eight rows of tiles; all tiles of one expert (wgrad)
-  int q_tile;                    // most columns of a tile
+  int q_even;                    // swapped: columns of a tile, the tokens spread evenly
   int stages, stage_bytes;       // swapped
   int batch, stride;             // swapped: accumulators (steps) handed over together, 2 or 4, and
                                  // the columns from one to the next
@@ -125,7 +137,7 @@ struct KernelArgs {
 struct Tile {
   int p_row, q_row;          // first rows in the tensor maps
   int p_valid, q_valid;      // rows of the tile that exist (p_valid <= 0: none of this CTA's)
-  int n;                     // columns computed: a multiple of 16 per CTA of the tile
+  int n;                     // columns computed (swapped: a multiple of 16)
   int e;
   int k0;                    // first byte along the contraction
   int nk;                    // steps
@@ -144,12 +156,11 @@ struct Tile {
 // lane the descriptors went through vector registers and a step took 400 cycles to issue.
 // Of a pair the commits arrive at the same barriers of both CTAs. (Every register counts in the warps
 // that gave theirs up: a few bytes of spills in the multiplying warp's loop cost half of the speed,
-// hence the forms with and without the condition.)
-template <int CTAS, bool ALWAYS>
+// hence no condition where none is needed.)
+template <int CTAS>
 __device__ __forceinline__ void issue_step(uint32_t d, uint64_t p, uint64_t q, uint32_t idesc,
                                            uint32_t empty, uint32_t acc_full, bool hand_over) {
   if constexpr (CTAS == 1) {
-    static_assert(!ALWAYS, "single CTAs run the swapped shape");
     asm volatile(
         "{\n\t.reg .pred e, on, off, h;\n\t"
         "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 off, 0, 0;\n\tsetp.eq.b32 on, 0, 0;\n\t"
@@ -164,7 +175,7 @@ __device__ __forceinline__ void issue_step(uint32_t d, uint64_t p, uint64_t q, u
         "l"(p), "l"(p + 2), "l"(p + 4), "l"(p + 6), "l"(q), "l"(q + 2), "l"(q + 4), "l"(q + 6),
         "r"(idesc), "r"(empty), "r"(acc_full), "r"((uint32_t)hand_over)
         : "memory");
-  } else if constexpr (ALWAYS) {
+  } else {  // always hands over
     asm volatile(
         "{\n\t.reg .pred e, on, off;\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
         "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 off, 0, 0;\n\tsetp.eq.b32 on, 0, 0;\n\t"
@@ -179,23 +190,6 @@ __device__ __forceinline__ void issue_step(uint32_t d, uint64_t p, uint64_t q, u
         "}" ::"r"(d),
         "l"(p), "l"(p + 2), "l"(p + 4), "l"(p + 6), "l"(q), "l"(q + 2), "l"(q + 4), "l"(q + 6),
         "r"(idesc), "r"(empty), "r"(acc_full)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred e, on, off, h;\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
-        "elect.sync _|e, 0xFFFFFFFF;\n\tsetp.ne.b32 off, 0, 0;\n\tsetp.eq.b32 on, 0, 0;\n\t"
-        "setp.ne.and.b32 h, %12, 0, e;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %5, %9, off;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %2, %6, %9, on;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %3, %7, %9, on;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %4, %8, %9, on;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%10], both;\n\t"
-        "@h tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%11], both;\n\t"
-        "}" ::"r"(d),
-        "l"(p), "l"(p + 2), "l"(p + 4), "l"(p + 6), "l"(q), "l"(q + 2), "l"(q + 4), "l"(q + 6),
-        "r"(idesc), "r"(empty), "r"(acc_full), "r"((uint32_t)hand_over)
         : "memory");
   }
 }
@@ -413,6 +407,11 @@ __device__ __forceinline__ bool phase_done(uint32_t bar, uint32_t parity, const 
   return a.wait_limit_ns >= 1000000ull ? mbar_try_wait(bar, parity) : phase_done_now(bar, parity);
 }
 
+// A value that is the same in all lanes, as the hardware's reduction gives it: in a uniform register.
+__device__ __forceinline__ int uniform(int x) {
+  return (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)x);
+}
+
 // A wait of the whole warp: one vote when the phase is complete; given up after the call's limit
 // (then at once, and the device error word says so).
 __device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, bool* failed,
@@ -479,15 +478,7 @@ template <typename C>
 __device__ __forceinline__ int tile_count(const KernelArgs& a, const int* prefix) {
   if (C::MODE == kB128Dense) return a.p_tiles * a.q_tiles;
   if (C::MODE == kB128Wgrad) return a.p_tiles * a.q_tiles * a.E;
-  return prefix[a.E] * (C::kSwap ? a.p_tiles : a.q_tiles);
-}
-
-// `rows` rows in `tiles` tiles of nearly one size: the columns of a tile, 16 per CTA
-template <typename C>
-__device__ __forceinline__ int even_columns(int rows, int tiles) {
-  constexpr int unit = 16 * C::CTAS;
-  int rest;
-  return (divide(rows + tiles - 1, tiles, &rest) + unit - 1) / unit * unit;
+  return prefix[a.E] * a.q_tiles;
 }
 
 template <typename C>
@@ -498,43 +489,27 @@ __device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* 
   r.e = 0;
   r.nk = a.nk;
   int64_t p_first;  // first row of the P tile in its matrix
-  if (C::MODE == kB128Grouped) {
-    const int fixed = C::kSwap ? a.p_tiles : a.q_tiles;  // tiles of the weights
-    // the last expert with prefix * fixed <= t: in two rounds, 32 at a time
+  if (C::MODE == kB128Grouped) {  // P: tokens, Q: weights
+    // the last expert with prefix * q_tiles <= t: in two rounds, 32 at a time
     const int lane = threadIdx.x & 31, width = (a.E + 31) >> 5;
     const int run = __popc(__ballot_sync(
-        0xFFFFFFFFu, (int64_t)prefix[min((lane + 1) * width, a.E)] * fixed <= t));
+        0xFFFFFFFFu, (int64_t)prefix[min((lane + 1) * width, a.E)] * a.q_tiles <= t));
     const int at = run * width + 1 + lane;
     const int lo = run * width +
                    __popc(__ballot_sync(0xFFFFFFFFu, lane < width && at < a.E &&
-                                                         (int64_t)prefix[at] * fixed <= t));
-    const int local = t - prefix[lo] * fixed, tiles = prefix[lo + 1] - prefix[lo];
-    const int rows = start[lo + 1] - start[lo];
-    int weight = local, index = 0;  // the token tiles of one weight tile run together
-    if (tiles > 1) weight = divide(local, tiles, &index);
+                                                         (int64_t)prefix[at] * a.q_tiles <= t));
+    const int local = t - prefix[lo] * a.q_tiles, row_tiles = prefix[lo + 1] - prefix[lo];
+    q = local;
+    p = 0;
+    if (row_tiles > 1) q = divide(local, row_tiles, &p);  // one weight tile's token tiles together
     r.e = lo;
-    if (C::kSwap) {
-      p = weight;
-      r.n = (rows + 16 * C::CTAS - 1) / (16 * C::CTAS) * (16 * C::CTAS);
-      if (tiles > 1) r.n = even_columns<C>(rows, tiles);
-      q = index * r.n;
-      r.q_row = start[lo] + q;
-      r.q_valid = min(r.n, rows - q);
-      p_first = (int64_t)p * C::kPTile;
-      r.p_row = (int)(lo * a.p_rows + p_first);
-      r.p_valid = (int)min((int64_t)C::kPTile, a.p_rows - p_first);
-      r.c_col = r.q_row;
-    } else {
-      p = index;
-      q = weight;
-      r.n = kColumns;
-      r.c_col = q * kColumns;
-      r.q_row = (int)(lo * a.q_rows) + r.c_col;
-      r.q_valid = (int)min((int64_t)kColumns, a.q_rows - r.c_col);
-      p_first = start[lo] + index * C::kPTile;
-      r.p_row = (int)p_first;
-      r.p_valid = min(C::kPTile, rows - index * C::kPTile);
-    }
+    r.n = C::kTileCols;
+    r.c_col = q * C::kTileCols;
+    r.q_row = (int)(lo * a.q_rows) + r.c_col;
+    r.q_valid = (int)min((int64_t)C::kTileCols, a.q_rows - r.c_col);
+    p_first = start[lo] + p * C::kPTile;
+    r.p_row = (int)p_first;
+    r.p_valid = min(C::kPTile, start[lo + 1] - r.p_row);
   } else {
     if (C::MODE == kB128Wgrad) {
       r.e = divide(t, a.per, &t);
@@ -542,7 +517,7 @@ __device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* 
       r.nk = prefix[r.e + 1] - kb0;
     }
     raster(t, a, &p, &q);
-    r.n = C::kSwap ? even_columns<C>((int)a.q_rows, a.q_tiles) : kColumns;
+    r.n = C::kSwap ? a.q_even : C::kTileCols;
     r.q_row = q * r.n;
     r.q_valid = (int)min((int64_t)r.n, a.q_rows - r.q_row);
     p_first = (int64_t)p * C::kPTile;
@@ -552,9 +527,9 @@ __device__ __forceinline__ Tile get_tile(const KernelArgs& a, int t, const int* 
   }
   r.k0 = kb0 * kStepBytes;
   r.p_scale = C::kPRows ? kb0 * a.p_pitch + r.p_row
-                        : r.e * a.b_estride + (int64_t)p * C::CTAS * a.p_pitch + kb0;
+                        : (int64_t)p * C::CTAS * a.p_pitch + kb0;
   r.q_scale = C::kQRows ? kb0 * a.q_pitch + r.q_row
-                        : r.e * a.b_estride + (int64_t)q * (kColumns / kB128) * a.q_pitch + kb0;
+                        : r.e * a.b_estride + (int64_t)q * (C::kTileCols / kB128) * a.q_pitch + kb0;
   r.c = (int64_t)r.q_row * a.ldc + p_first;
   r.c_row = (int)p_first;
   if constexpr (C::CTAS == 2) {  // this CTA's own 128 rows of P
@@ -622,7 +597,7 @@ struct Smem {
   float* scales;          // [kScaleSlots][kSlotFloats]
   uint64_t* full;         // [stages]: operands landed and (not swapped) accumulator read
   uint64_t* empty;        // [stages]: operands read
-  uint64_t* acc_full;     // [2]
+  uint64_t* acc_full;     // [accumulators or batches, at most 4]
   uint64_t* acc_empty;    // [2] (swapped)
   uint64_t* scale_full;   // [kScaleGroups]
   uint64_t* scale_empty;  // [kScaleGroups]
@@ -655,7 +630,7 @@ __device__ __forceinline__ void tile_range(const KernelArgs& a, int* t0, int* st
 // ------------------------------------------------------------------------------------------
 template <typename C>
 __device__ __forceinline__ void produce(const CUtensorMap& pmap, const CUtensorMap& qmap,
-                                        const CUtensorMap& qmap16, const KernelArgs& a,
+                                        const CUtensorMap& map16, const KernelArgs& a,
                                         const Smem& s, int tiles) {
   const int stages = stage_count<C>(a);
   bool failed = false;
@@ -664,38 +639,41 @@ __device__ __forceinline__ void produce(const CUtensorMap& pmap, const CUtensorM
   tile_range<C>(a, &t0, &step);
   for (int t = t0; t < tiles && !failed; t += step) {
     const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    // rows of Q that this CTA loads: all of the tile's columns, or its half of them
+    // rows this CTA loads: of Q all of the tile's columns, or its half of them; of P 128, or (narrow) the
+    // sixteens that hold rows of the expert (what is left in the others reaches lanes that are not
+    // written)
     const int q_rows = tile.n / C::CTAS;
     const int q_row = tile.q_row + (C::CTAS == 2 ? (int)cluster_rank() * q_rows : 0);
-    const uint32_t bytes = (uint32_t)(kLanes + q_rows) * kStepBytes;
+    const int p_rows = C::kNarrow ? min(kLanes, (tile.p_valid + 15) & ~15) : kLanes;
+    const uint32_t bytes = (uint32_t)(p_rows + q_rows) * kStepBytes;
     for (int kb = 0; kb < tile.nk; ++kb) {
       warp_wait(smem_u32(s.empty + st), parity, &failed, a);
       if (failed) break;
       const uint32_t bar = smem_u32(s.full + st);
-      const uint32_t dst = smem_u32(s.ring + st * stage_bytes<C>(a));
+      const uint32_t dst = smem_u32(s.ring + st * stage_bytes<C>(a)), q_dst = dst + kLanes * kStepBytes;
       const int x = tile.k0 + kb * kStepBytes;
       if constexpr (C::CTAS == 2) {
         const uint32_t first = in_cta(bar, 0);
         if (elect_one()) {
           if (cluster_rank() == 0) mbar_arrive_expect_tx(bar, 2 * bytes);
           tma_load_box_pair(dst, &pmap, x, tile.p_row, first);
-          int r = 0;
-          for (; r + 128 <= q_rows; r += 128) {
-            tma_load_box_pair(dst + (kLanes + r) * kStepBytes, &qmap, x, q_row + r, first);
-          }
-          for (; C::kSwap && r < q_rows; r += 16) {
-            tma_load_box_pair(dst + (kLanes + r) * kStepBytes, &qmap16, x, q_row + r, first);
-          }
+          tma_load_box_pair(q_dst, &qmap, x, q_row, first);
         }
       } else if (elect_one()) {
         mbar_arrive_expect_tx(bar, bytes);
-        tma_load_box(dst, &pmap, x, tile.p_row, bar);
-        int r = 0;
-        for (; r + 128 <= q_rows; r += 128) {
-          tma_load_box(dst + (kLanes + r) * kStepBytes, &qmap, x, q_row + r, bar);
+        if (p_rows == kLanes) {
+          tma_load_box(dst, &pmap, x, tile.p_row, bar);
+        } else {
+          for (int r = 0; r < p_rows; r += 16) {
+            tma_load_box(dst + r * kStepBytes, &map16, x, tile.p_row + r, bar);
+          }
         }
-        for (; C::kSwap && r < q_rows; r += 16) {
-          tma_load_box(dst + (kLanes + r) * kStepBytes, &qmap16, x, q_row + r, bar);
+        if (!C::kSwap || q_rows == 128) {
+          tma_load_box(q_dst, &qmap, x, q_row, bar);
+        } else {
+          for (int r = 0; r < q_rows; r += 16) {
+            tma_load_box(q_dst + r * kStepBytes, &map16, x, q_row + r, bar);
+          }
         }
       }
       __syncwarp();
@@ -733,28 +711,28 @@ __device__ __forceinline__ void multiply(const KernelArgs& a, const Smem& s, int
   if constexpr (!C::kSwap) {
     int buf = 0;
     for (int t = t0; t < tiles && !failed; t += step) {
-      const int nk = get_tile<C>(a, t, s.prefix, s.start).nk;
+      const int nk = uniform(get_tile<C>(a, t, s.prefix, s.start).nk);
       for (int kb = 0; kb < nk; ++kb) {
         warp_wait(smem_u32(s.full + st), full_parity, &failed, a);
         if (failed) break;
         tc_fence_after();
         const uint64_t p = desc_sw128(smem_u32(s.ring + st * C::kFixedStageBytes));
-        issue_step<C::CTAS, true>(tmem + buf * kColumns, p, p + (kLanes * kStepBytes >> 4),
-                                  idesc_e4m3_f32(C::kPTile, kColumns), smem_u32(s.empty + st),
-                                  smem_u32(s.acc_full + buf), true);
+        issue_step<C::CTAS>(tmem + buf * C::kTileCols, p, p + (kLanes * kStepBytes >> 4),
+                            idesc_e4m3_f32(C::kPTile, C::kTileCols), smem_u32(s.empty + st),
+                            smem_u32(s.acc_full + buf), true);
         if (++st == stages) {
           st = 0;
           full_parity ^= 1;
         }
-        buf ^= 1;
+        buf = (buf + 1) & (C::kBufs - 1);
       }
     }
   } else {
     uint32_t batch = 0;
     for (int t = t0; t < tiles && !failed; t += step) {
       const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-      const int nk = tile.nk;
-      const uint32_t idesc = idesc_e4m3_f32(C::kPTile, tile.n);
+      const int nk = uniform(tile.nk);
+      const uint32_t idesc = idesc_e4m3_f32(C::kPTile, uniform(tile.n));
       for (int kb = 0; kb < nk; ++batch) {
         const uint32_t half = batch & 1;
         warp_wait(smem_u32(s.acc_empty + half), ((batch >> 1) & 1) ^ 1, &failed, a);
@@ -764,8 +742,8 @@ __device__ __forceinline__ void multiply(const KernelArgs& a, const Smem& s, int
           if (failed) break;
           tc_fence_after();
           const uint64_t p = desc_sw128(smem_u32(s.ring + st * stage_bytes<C>(a)));
-          issue_step<C::CTAS, false>(column, p, p + (kLanes * kStepBytes >> 4), idesc,
-                                     smem_u32(s.empty + st), smem_u32(s.acc_full + half), left == 1);
+          issue_step<C::CTAS>(column, p, p + (kLanes * kStepBytes >> 4), idesc,
+                              smem_u32(s.empty + st), smem_u32(s.acc_full + half), left == 1);
           column += a.stride;
           if (++st == stages) {
             st = 0;
@@ -843,7 +821,7 @@ __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s,
 #undef MXQ_COLUMNS
           q += a.q_pitch;
         } else {
-          if (lane < kColumns / kB128) {
+          if (lane < C::kTileCols / kB128) {
             copy_scale<0>(dst + C::kPScales * 4, q, lane * kB128 < q_valid);
           }
           ++q;
@@ -859,23 +837,22 @@ __device__ __forceinline__ void fetch_scales(const KernelArgs& a, const Smem& s,
   asm volatile("cp.async.wait_all;" ::: "memory");  // none lands after the CTA's shared memory goes
 }
 
-// A promoting warp's way through the steps of the shapes with two accumulators: the barriers of one
-// step around its reads. (Asking the next step's barrier before this step's sums, to have only the
-// answer left, measured slower: 436 against 360 us at 8192^3; so did fetching its scales there, 392
-// against 340.)
+// A promoting warp's way through the steps (not swapped): the barriers of one step around its reads.
+// (Asking the next step's barrier before this step's sums, to have only the answer left, measured
+// slower: 436 against 360 us at 8192^3; so did fetching its scales there, 392 against 340.)
 template <typename C>
 struct Steps {
   const KernelArgs& a;
   const Smem& s;
   uint32_t full0;        // the barriers on which read accumulators are reported
-  int it = 0, st2 = 2;   // step, stage of the step after next
+  int it = 0, st2 = C::kBufs % C::kStages;  // step, stage of the step that gets its accumulator next
   uint32_t group = 0;
   bool failed = false;
 
   __device__ __forceinline__ Steps(const KernelArgs& a_, const Smem& s_) : a(a_), s(s_) {
+    static_assert(C::kBufs <= C::kStages, "a stage has one accumulator's arrivals under way");
     full0 = C::CTAS == 2 ? in_cta(smem_u32(s.full), 0) : smem_u32(s.full);
-    hand_back(0);  // the first two steps find theirs free
-    hand_back(1);
+    for (int i = 0; i < C::kBufs; ++i) hand_back(i);  // the first steps find theirs free
   }
   __device__ __forceinline__ void hand_back(int st) {
     if constexpr (C::CTAS == 2) {
@@ -893,12 +870,12 @@ struct Steps {
     return s.scales + (g * kScaleGroup + in) * C::kSlotFloats;
   }
   __device__ __forceinline__ bool accumulator() {
-    warp_wait(smem_u32(s.acc_full + (it & 1)), (it >> 1) & 1, &failed, a);
+    warp_wait(smem_u32(s.acc_full + it % C::kBufs), (it / C::kBufs) & 1, &failed, a);
     if (failed) return false;
     tc_fence_after();
     return true;
   }
-  __device__ __forceinline__ uint32_t column() const { return (it & 1) * kColumns; }
+  __device__ __forceinline__ uint32_t column() const { return it % C::kBufs * C::kTileCols; }
   __device__ __forceinline__ void accumulator_read() {
     tc_fence_before();
     hand_back(st2);
@@ -912,11 +889,11 @@ struct Steps {
     ++it;
   }
   // The steps that may have been loaded are handed back unread, so that the loading warp sees its
-  // copies land. Steps it and it + 1 have their arrivals already and their stages may still be in
-  // that phase, so the steps that follow on those two stages are left out: a second arrival there
-  // would complete a phase before its copies do.
+  // copies land. Steps it .. it + kBufs - 1 have their arrivals already and their stages may still be
+  // in that phase, so the steps that follow on those stages are left out: a second arrival there would
+  // complete a phase before its copies do.
   __device__ __forceinline__ void give_up() {
-    for (int i = 0; i < C::kStages - 2; ++i) hand_back((st2 + i) % C::kStages);
+    for (int i = 0; i < C::kStages - C::kBufs; ++i) hand_back((st2 + i) % C::kStages);
   }
 };
 
@@ -927,12 +904,11 @@ template <typename C>
 struct Batches {
   const KernelArgs& a;
   const Smem& s;
-  uint32_t empty0;
   uint32_t batch = 0, group = 0;
   bool failed = false;
 
   __device__ __forceinline__ Batches(const KernelArgs& a_, const Smem& s_) : a(a_), s(s_) {
-    empty0 = C::CTAS == 2 ? in_cta(smem_u32(s.acc_empty), 0) : smem_u32(s.acc_empty);
+    static_assert(C::CTAS == 1, "the swapped shape runs on single CTAs");
   }
   // scales of the batch that begins with step kb of the tile (a batch lies in one group)
   __device__ __forceinline__ const float* scales(int kb) {
@@ -953,11 +929,7 @@ struct Batches {
   }
   __device__ __forceinline__ void accumulators_read() {
     tc_fence_before();
-    if constexpr (C::CTAS == 2) {
-      warp_arrive_cluster(empty0 + 8 * (batch & 1));
-    } else {
-      warp_arrive(empty0 + 8 * (batch & 1));
-    }
+    warp_arrive(smem_u32(s.acc_empty + (batch & 1)));
   }
   __device__ __forceinline__ void end(int kb, int nk) {  // kb: the step after the batch
     if (kb % kScaleGroup == 0 || kb == nk) {
@@ -968,28 +940,30 @@ struct Batches {
   }
 };
 
-// Staging of a promoting warp's output: two boxes of 32 rows x 128 bytes, 16-byte chunk q of row r at
-// q ^ (r % 8), written with tensor-map stores.
+// Staging of a promoting warp's output: one or two boxes of 32 rows x 128 bytes, 16-byte chunk q of row
+// r at q ^ (r % 8), written with tensor-map stores.
+template <typename C>
 struct Boxes {
+  static constexpr int kCols = C::kF32 ? 32 : 64;  // columns of a box
   uint8_t* base;
-  __device__ __forceinline__ void wait() {  // both are read
+  __device__ __forceinline__ void wait() {  // all are read
     if ((threadIdx.x & 31) == 0) bulk_wait_read_all();
     __syncwarp();
   }
-  // both boxes, `width` columns apart; the second only where it has columns
-  __device__ __forceinline__ void store(const CUtensorMap& cmap, int x, int y, int z, int width,
-                                        int cols) {
+  // the boxes, side by side; the second only where it has columns
+  __device__ __forceinline__ void store(const CUtensorMap& cmap, int x, int y, int z, int cols) {
     fence_proxy_async_smem();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
       tma_store_box_3d(&cmap, x, y, z, smem_u32(base));
-      if (cols > width) tma_store_box_3d(&cmap, x + width, y, z, smem_u32(base + 4096));
+      if (C::kBoxes > 1 && cols > kCols) {
+        tma_store_box_3d(&cmap, x + kCols, y, z, smem_u32(base + 4096));
+      }
       bulk_commit_group();
     }
   }
   // The first `rows` rows and `cols` columns of box u only, by ordinary stores (the box's other rows
   // are another expert's).
-  template <typename C>
   __device__ __forceinline__ void store_part(const KernelArgs& a, int u, int64_t at, int rows,
                                              int cols) {
     const int lane = threadIdx.x & 31, chunk = lane & 7, per = C::kF32 ? 4 : 8;
@@ -1051,38 +1025,48 @@ __device__ __forceinline__ void store_swapped(const KernelArgs& a, const Smem& s
   __syncwarp();  // the staging is free again
 }
 
-// The promoting warps of the rows shape: warp w holds lanes 32 (w % 4) .. and columns 128 (w / 4) ..
-// of the tile, a row per thread.
+// The promoting warps of the rows and narrow shapes: warp w holds lanes 32 (w % 4) .. and half w / 4 of
+// the tile's columns, a row per thread.
 template <typename C>
 __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const KernelArgs& a,
                                              const Smem& s, int tiles, uint32_t tmem, int pw) {
-  const int lane = threadIdx.x & 31, row = (pw & 3) * 32 + lane, half = pw >> 2;
-  const uint32_t tbase = tmem + ((uint32_t)((pw & 3) * 32) << 16) + half * C::kWarpCols;
+  const int lane = threadIdx.x & 31, row0 = (pw & 3) * 32, row = row0 + lane, half = pw >> 2;
+  const uint32_t tbase = tmem + ((uint32_t)row0 << 16) + half * C::kWarpCols;
   Steps<C> steps(a, s);
-  Boxes boxes{s.staging + pw * C::kStagingBytes};
+  Boxes<C> boxes{s.staging + pw * C::kStagingBytes};
   int t0, step;
   tile_range<C>(a, &t0, &step);
   for (int t = t0; t < tiles; t += step) {
-    const int nk = get_tile<C>(a, t, s.prefix, s.start).nk;
+    int nk;
+    bool live;  // narrow: some of the warp's rows exist, of an expert's few
+    {
+      const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
+      nk = tile.nk;
+      live = !C::kNarrow || tile.p_valid > row0;
+    }
     uint64_t sums[C::kWarpCols / 2];
 #pragma unroll
     for (int i = 0; i < C::kWarpCols / 2; ++i) sums[i] = 0u;
     for (int kb = 0; kb < nk; ++kb) {
       const float* sc = steps.scales(kb);
-      const uint64_t m = both(sc[row] * sc[C::kPScales + half]);
+      const uint64_t m = both(sc[row] * sc[C::kPScales + half * C::kWarpCols / kB128]);
       if (!steps.accumulator()) break;
-      // The accumulator goes back as soon as it is in registers; half of it fits beside the sums.
+      // The accumulator goes back as soon as it is in registers; 64 columns of it fit beside the sums.
       uint64_t v[32];
       auto add = [&](int h) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) sums[h * 32 + i] = fma2(v[i], m, sums[h * 32 + i]);
       };
       const uint32_t src = tbase + steps.column();
-      read_row(src, v);
-      add(0);
-      read_row(src + 64, v);
+      if (live) {
+        read_row(src, v);
+        if constexpr (C::kWarpCols == 128) {
+          add(0);
+          read_row(src + 64, v);
+        }
+      }
       steps.accumulator_read();
-      add(1);
+      if (live) add(C::kWarpCols / 64 - 1);
       steps.end(kb, nk);
     }
     if (steps.failed) {
@@ -1091,21 +1075,19 @@ __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const Kern
     }
     // found again: kept through the steps, its fields would take the sums' registers
     const Tile tile = get_tile<C>(a, t, s.prefix, s.start);
-    if (tile.p_valid <= (pw & 3) * 32) continue;  // none of the warp's rows exists
-    // two boxes at a time: one fence and one wait for both
-    constexpr int kBoxCols = C::kF32 ? 32 : 64;
-    const int row0 = (pw & 3) * 32;
+    if (tile.p_valid <= row0) continue;  // none of the warp's rows exists
+    // all boxes of the staging at a time: one fence and one wait
 #pragma unroll
-    for (int b = 0; b < C::kWarpCols / kBoxCols; b += 2) {
-      const int col = half * C::kWarpCols + b * kBoxCols;
+    for (int b = 0; b < C::kWarpCols / Boxes<C>::kCols; b += C::kBoxes) {
+      const int col = half * C::kWarpCols + b * Boxes<C>::kCols;
       if (col >= tile.q_valid) break;
       boxes.wait();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < C::kBoxes; ++u) {
         uint8_t* line = boxes.base + u * 4096 + lane * 128;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {  // 16 bytes: four fp32 or eight bf16
-          const uint64_t* d = sums + ((b + u) * kBoxCols + q * (kBoxCols / 8)) / 2;
+          const uint64_t* d = sums + ((b + u) * Boxes<C>::kCols + q * (Boxes<C>::kCols / 8)) / 2;
           uint4 o;
           if constexpr (C::kF32) {
             o = make_uint4((uint32_t)d[0], (uint32_t)(d[0] >> 32), (uint32_t)d[1],
@@ -1119,12 +1101,14 @@ __device__ __forceinline__ void promote_rows(const CUtensorMap& cmap, const Kern
       }
       if (C::MODE == kB128Grouped && tile.p_valid < row0 + 32) {
         const int64_t at = (int64_t)(tile.c_row + row0) * a.ldc + tile.c_col + col;
-        boxes.template store_part<C>(a, 0, at, tile.p_valid - row0, tile.q_valid - col);
-        boxes.template store_part<C>(a, 1, at + kBoxCols, tile.p_valid - row0,
-                                     tile.q_valid - col - kBoxCols);
+#pragma unroll
+        for (int u = 0; u < C::kBoxes; ++u) {
+          boxes.store_part(a, u, at + u * Boxes<C>::kCols, tile.p_valid - row0,
+                           tile.q_valid - col - u * Boxes<C>::kCols);
+        }
       } else {
         boxes.store(cmap, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0,
-                    kBoxCols, tile.q_valid - col);
+                    tile.q_valid - col);
       }
     }
   }
@@ -1203,7 +1187,7 @@ __device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const K
   const int col0 = (pw >> 2) * C::kWarpCols;
   const uint32_t tbase = tmem + ((uint32_t)row0 << 16) + col0;
   Steps<C> steps(a, s);
-  Boxes boxes{s.staging + pw * C::kStagingBytes};
+  Boxes<C> boxes{s.staging + pw * C::kStagingBytes};
   int t0, step;
   tile_range<C>(a, &t0, &step);
   for (int t = t0; t < tiles; t += step) {
@@ -1226,7 +1210,7 @@ __device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const K
       break;
     }
     if (tile.p_valid <= row0) continue;
-    constexpr int kBoxCols = C::kF32 ? 32 : 64;
+    constexpr int kBoxCols = Boxes<C>::kCols;
 #pragma unroll
     for (int b = 0; b < C::kWarpCols / kBoxCols; b += 2) {
       const int col = col0 + b * kBoxCols;
@@ -1252,7 +1236,7 @@ __device__ __forceinline__ void promote_columns(const CUtensorMap& cmap, const K
         }
       }
       boxes.store(cmap, tile.c_col + col, tile.c_row + row0, C::MODE == kB128Wgrad ? tile.e : 0,
-                  kBoxCols, tile.q_valid - col);
+                  tile.q_valid - col);
     }
   }
   boxes.drain();
@@ -1343,7 +1327,7 @@ template <typename C>
 __global__ void __launch_bounds__(kThreads, 1)
     b128_gemm_kernel(const __grid_constant__ CUtensorMap pmap,
                      const __grid_constant__ CUtensorMap qmap,
-                     const __grid_constant__ CUtensorMap qmap16,
+                     const __grid_constant__ CUtensorMap map16,
                      const __grid_constant__ CUtensorMap cmap, KernelArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -1354,7 +1338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   s.full = reinterpret_cast<uint64_t*>(s.scales + kScaleSlots * C::kSlotFloats);
   s.empty = s.full + kMaxStages;
   s.acc_full = s.empty + kMaxStages;
-  s.acc_empty = s.acc_full + 2;
+  s.acc_empty = s.acc_full + 4;
   s.scale_full = s.acc_empty + 2;
   s.scale_empty = s.scale_full + kScaleGroups;
   s.done = s.scale_empty + kScaleGroups;
@@ -1370,10 +1354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(s.full + i), C::kSwap ? 1 : 1 + C::CTAS * kPromoWarps);
       mbar_init(smem_u32(s.empty + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(s.acc_full + i), 1);
-      mbar_init(smem_u32(s.acc_empty + i), C::CTAS * kPromoWarps);
-    }
+    for (int i = 0; i < C::kBufs; ++i) mbar_init(smem_u32(s.acc_full + i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(s.acc_empty + i), kPromoWarps);
     for (int i = 0; i < kScaleGroups; ++i) {
       mbar_init(smem_u32(s.scale_full + i), 32);
       mbar_init(smem_u32(s.scale_empty + i), kPromoWarps);
@@ -1390,7 +1372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_relinquish();
     }
   }
-  if (C::MODE == kB128Grouped) build_table<C>(a, C::kSwap ? a.q_tile : C::kPTile, INT32_MAX, s.prefix, s.start);
+  if (C::MODE == kB128Grouped) build_table<C>(a, C::kPTile, INT32_MAX, s.prefix, s.start);
   if (C::MODE == kB128Wgrad) build_table<C>(a, kB128, (int)a.blocks_total, s.prefix, s.start);
   tc_fence_before();
   __syncthreads();
@@ -1402,7 +1384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // up.
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (warp == 0) produce<C>(pmap, qmap, qmap16, a, s, tiles);
+    if (warp == 0) produce<C>(pmap, qmap, map16, a, s, tiles);
     if (warp == 1 && (C::CTAS == 1 || cluster_rank() == 0)) multiply<C>(a, s, tiles, tmem);
     if (warp == 2) fetch_scales<C>(a, s, tiles);
     __syncwarp();
@@ -1473,9 +1455,10 @@ int slot_count() {
                        smem_bytes<C>(), 1);
 }
 
-// q_tile: most columns of a tile (swapped); split: CTAs along the contraction (swapped, dense)
+// q_even, split (swapped): columns of a tile and CTAs along the contraction; row_min, row_max (by
+// expert): the experts of this launch
 template <typename C>
-cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStream_t stream,
+cudaError_t launch_config(const B128GemmArgs& g, cudaStream_t stream, int q_even = 0, int split = 1,
                           int row_min = 0, int row_max = INT32_MAX) {
   const int slots = slot_count<C>();
   if (slots <= 0) return cudaErrorInvalidConfiguration;
@@ -1501,35 +1484,35 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
   a.E = g.E;
   a.nk = (int)kblocks;
   a.p_tiles = (int)ceil_div(a.p_rows, C::kPTile);
-  a.q_tiles = (int)ceil_div(a.q_rows, q_tile);
+  a.q_tiles = (int)ceil_div(a.q_rows, C::kSwap ? q_even : C::kTileCols);
   auto divisor = [](int64_t d) {
     return Divisor{(int)d, (uint32_t)((uint64_t(1) << 32) / (uint64_t)d + 1)};
   };
   if ((int64_t)a.p_tiles * a.q_tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
   a.run = divisor(8 * (int64_t)a.q_tiles);
   a.per = divisor((int64_t)a.p_tiles * a.q_tiles);
-  a.q_tile = q_tile;
+  a.q_even = q_even;
   a.split = split;
   a.row_min = row_min;
   a.row_max = row_max;
   if (C::kSwap) {
-    a.stage_bytes = (kLanes + q_tile / C::CTAS) * kStepBytes;
+    a.stage_bytes = (kLanes + q_even) * kStepBytes;
     a.stages = C::kRingBytes / a.stage_bytes;
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    a.batch = q_tile <= 64 ? 4 : 2;  // two batches fill tensor memory
+    a.batch = q_even <= 64 ? 4 : 2;  // two batches fill tensor memory
     a.stride = kColumns / a.batch;
   }
   const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const void *pcodes = C::kSwap ? g.b_codes : g.a_codes, *qcodes = C::kSwap ? g.a_codes : g.b_codes;
   const int64_t prows = C::kSwap ? bmap : g.M, qrows = C::kSwap ? g.M : bmap;
-  CUtensorMap pmap, qmap, qmap16, cmap;
+  CUtensorMap pmap, qmap, map16, cmap;  // map16: boxes of 16 rows of the tokens
   cudaError_t err = make_tensor_map_2d(&pmap, pcodes, prows, g.K, u8, 1, kStepBytes, kLanes, swz);
   if (err == cudaSuccess) {
     err = make_tensor_map_2d(&qmap, qcodes, qrows, g.K, u8, 1, kStepBytes, 128, swz);
   }
   if (err == cudaSuccess) {
-    err = make_tensor_map_2d(&qmap16, qcodes, qrows, g.K, u8, 1, kStepBytes, 16, swz);
+    err = make_tensor_map_2d(&map16, g.a_codes, g.M, g.K, u8, 1, kStepBytes, 16, swz);
   }
   if (err == cudaSuccess) {
     if (C::kSwap) {
@@ -1544,15 +1527,12 @@ cudaError_t launch_config(const B128GemmArgs& g, int q_tile, int split, cudaStre
   if (err != cudaSuccess) return err;
   int64_t tiles = (int64_t)a.p_tiles * a.q_tiles;  // at most, by expert
   if (C::MODE == kB128Wgrad) tiles *= g.E;
-  if (grouped) {
-    const int64_t unit = C::kSwap ? q_tile : C::kPTile;
-    tiles = (g.M / unit + (g.M < g.E ? g.M : g.E)) * (C::kSwap ? a.p_tiles : a.q_tiles);
-  }
+  if (grouped) tiles = (g.M / C::kPTile + (g.M < g.E ? g.M : g.E)) * a.q_tiles;
   if (tiles > INT32_MAX / kMaxSplit) return cudaErrorInvalidValue;
   const int cluster = C::kSwap && C::MODE == kB128Dense ? split : C::CTAS;
   const int64_t groups = split > 1 ? tiles : slots / cluster;
   return launch_clusters(&b128_gemm_kernel<C>, (unsigned)((tiles < groups ? tiles : groups) * cluster),
-                         kThreads, smem_bytes<C>(), cluster, stream, pmap, qmap, qmap16, cmap, a);
+                         kThreads, smem_bytes<C>(), cluster, stream, pmap, qmap, map16, cmap, a);
 }
 
 // Dense calls: 256 x 256 tiles on pairs, or the swapped shape, whose 128-row weight tiles, times up to
@@ -1566,32 +1546,33 @@ cudaError_t launch_dense(const B128GemmArgs& g, cudaStream_t stream) {
   const int slots = slot_count<Small>();
   if (slots <= 1) return cudaErrorInvalidConfiguration;
   const int64_t nk = ceil_div(g.K, kB128);
-  const int64_t q_tiles = ceil_div(g.M, kFewRows);
-  const int q_tile = (int)ceil_div(ceil_div(g.M, q_tiles), 16) * 16;
-  const int64_t tiles = q_tiles * ceil_div(g.N, kLanes);
+  const int64_t q_tiles = ceil_div(g.M, Small::kTileCols);
+  const int q_even = (int)ceil_div(ceil_div(g.M, q_tiles), 16) * 16;
+  const int64_t tiles = ceil_div(g.M, q_even) * ceil_div(g.N, kLanes);
   int split = 1;
   while (split < kMaxSplit && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
   const double few = (double)ceil_div(tiles * split, slots) *
-                     ((double)ceil_div(nk, split) * (0.25 + 0.0015 * q_tile) + (split > 1 ? 5 : 3));
+                     ((double)ceil_div(nk, split) * (0.25 + 0.0015 * q_even) + (split > 1 ? 5 : 3));
   const double many =
       (double)ceil_div(ceil_div(g.M, 256) * ceil_div(g.N, 256), slots / 2) * ((double)nk * 0.40 + 3);
-  return many <= few ? launch_config<Large>(g, kColumns, 1, stream)
-                     : launch_config<Small>(g, q_tile, split, stream);
+  return many <= few ? launch_config<Large>(g, stream)
+                     : launch_config<Small>(g, stream, q_even, split);
 }
 
-// Calls by expert: experts of more than kFewRows rows in 256 x 256 tiles (0.35 us a step whatever the
-// rows), the others swapped (a step costs its weights and 0.1 us per 64 rows): two launches, each of
-// which takes its experts from the offsets. A call of few rows has no large expert.
+// Calls by expert: experts of more than kFewRows rows in 256 x 256 tiles on pairs, the others in tiles of
+// 128 x 128: two launches, each of which takes its experts from the offsets. A call of few rows has
+// no large expert. Weights of 1024 x 2048, us: 76 experts of 128 rows 39 narrow, of 130 rows 44 and of
+// 256 rows 47 in pairs; 128 experts that share 16384 rows unevenly 76, of which the narrow shape was
+// taken in place of the swapped one for 86 (128 choices among them: 34.5 for 39).
+constexpr int kFewRows = 128;
 template <bool F32>
 cudaError_t launch_grouped(const B128GemmArgs& g, cudaStream_t stream) {
-  using Many = Config<2, kB128Grouped, false, true, false, F32>;
-  using Few = Config<2, kB128Grouped, true, false, true, F32>;
   if (g.M > kFewRows) {
-    const cudaError_t err = launch_config<Many>(g, kColumns, 1, stream, kFewRows + 1, INT32_MAX);
+    const cudaError_t err = launch_config<Config<2, kB128Grouped, false, true, false, F32>>(
+        g, stream, 0, 1, kFewRows + 1, INT32_MAX);
     if (err != cudaSuccess) return err;
   }
-  // columns of a tile: a narrow tile leaves room for more stages and accumulators
-  return launch_config<Few>(g, g.M / g.E <= 16 ? 64 : kFewRows, 1, stream, 0, kFewRows);
+  return launch_config<Config<1, kB128Grouped, false, true, false, F32>>(g, stream, 0, 1, 0, kFewRows);
 }
 
 }  // namespace
@@ -1599,8 +1580,8 @@ cudaError_t launch_grouped(const B128GemmArgs& g, cudaStream_t stream) {
 cudaError_t launch_b128_gemm(int mode, const B128GemmArgs& g, cudaStream_t stream) {
   if (mode == kB128Wgrad) {
     return g.out_f32
-               ? launch_config<Config<2, kB128Wgrad, false, true, true, true>>(g, kColumns, 1, stream)
-               : launch_config<Config<2, kB128Wgrad, false, true, true, false>>(g, kColumns, 1, stream);
+               ? launch_config<Config<2, kB128Wgrad, false, true, true, true>>(g, stream)
+               : launch_config<Config<2, kB128Wgrad, false, true, true, false>>(g, stream);
   }
   if (mode == kB128Grouped) {
     return g.out_f32 ? launch_grouped<true>(g, stream) : launch_grouped<false>(g, stream);

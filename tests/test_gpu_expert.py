@@ -451,6 +451,22 @@ def test_gemm_grouped_wgrad(counts, M, N, dtype):
         check_product(C[e], u, v, R.up(n), e)
 
 
+@pytest.mark.parametrize("E,most,N,K", [(96, 40, 520, 2016), (40, 300, 264, 1568), (1024, 3, 128, 160)])
+def test_gemm_grouped_many_tiles_and_steps(E, most, N, K):
+    """More tiles than CTAs and more steps than stages, in both sizes of tiles."""
+    rng = np.random.default_rng(E)
+    counts = rng.integers(0, most + 1, E)
+    (ac, asc), a = operand(rng, int(counts.sum()), K, "rows")
+    bs = [operand(rng, N, K, "blocks") for _ in range(E)]
+    bc, bsc = torch.stack([b[0][0] for b in bs]), torch.stack([b[0][1] for b in bs])
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    c = mxq.mx_gemm_b128_grouped(ac, asc, bc, bsc, torch.from_numpy(offsets).cuda())
+    for e in range(E):
+        part = slice(offsets[e], offsets[e + 1])
+        if counts[e]:
+            check_product(c[part], a[part], bs[e][1], K, e)
+
+
 def test_gemm_grouped_contract_breaking_offsets_stay_inside():
     rng = np.random.default_rng(4)
     (ac, asc), _ = operand(rng, 100, 128, "rows")
