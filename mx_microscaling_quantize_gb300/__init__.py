@@ -445,7 +445,12 @@ _TYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 def _tensor(t, name, dtype, *, dim=None, like=None) -> torch.Tensor:
     """A contiguous CUDA tensor of one of the dtypes (and dimensions), on like's device."""
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    # The usual case first: the small calls take longer in Python than on the device.
+    if type(t) is torch.Tensor and t.is_cuda and t.is_contiguous() and \
+            (t.dtype is dtype or (dtype is _TYPES and t.dtype in dtype)) and \
+            (dim is None or t.ndim == dim) and (like is None or t.get_device() == like.get_device()):
+        return t
+    dtypes = dtype if isinstance(dtype, (tuple, dict)) else (dtype,)
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes):
         raise TypeError(f"{name} must be a CUDA tensor of {' or '.join(map(str, dtypes))}")
     if not t.is_contiguous() or (dim is not None and t.dim() not in
@@ -474,7 +479,7 @@ def mx_route(logits, k: int, score=SOFTMAX, bias=None, *, groups: int = 1, top_g
              renormalize: bool = True, scale: float = 1.0, experts=None, weights=None, stream=None):
     """Choose k experts per token from logits [T, E] (bfloat16 or float32) -> (experts int32
     [T, k], weights float32 [T, k]); experts of logit -inf are never chosen (-1, weight 0)."""
-    _tensor(logits, "logits", (torch.bfloat16, torch.float32), dim=2)
+    _tensor(logits, "logits", _TYPES, dim=2)
     T, E = logits.shape
     if bias is not None and _tensor(bias, "bias", torch.float32, like=logits).numel() != E:
         raise ValueError("bias must have one value per expert")
@@ -489,7 +494,7 @@ def mx_route(logits, k: int, score=SOFTMAX, bias=None, *, groups: int = 1, top_g
 def mx_route_backward(grad_weights, logits, experts, score=SOFTMAX, *, renormalize: bool = True,
                       scale: float = 1.0, grad_logits=None, stream=None):
     """Gradient of the logits [T, E] from that of mx_route's weights [T, k]."""
-    _tensor(logits, "logits", (torch.bfloat16, torch.float32), dim=2)
+    _tensor(logits, "logits", _TYPES, dim=2)
     _tensor(experts, "experts", torch.int32, dim=2, like=logits)
     _tensor(grad_weights, "grad_weights", torch.float32, dim=2, like=logits)
     T, E = logits.shape
@@ -602,29 +607,25 @@ def mx_quantize_b128_blocks(x, *, transpose: bool = False, codes=None, scales=No
     return (codes, scales, codes_t, scales_t) if transpose else (codes, scales)
 
 
-def _b128_operand(codes, scales, what, shape, like=None):
-    """Checks the codes' type and the scales' shape."""
-    _tensor(codes, f"{what}_codes", torch.uint8, dim=(2, 3), like=like)
+def _b128_operand(codes, scales, what, rows, dim=2, like=None):
+    """Checks an operand whose scales are in the rows or the blocks form; returns the codes' shape."""
+    _tensor(codes, f"{what}_codes", torch.uint8, dim=dim, like=like)
     _tensor(scales, f"{what}_scales", torch.float32, like=codes)
-    if tuple(scales.shape) != shape:
-        raise ValueError(f"{what}_scales must be {list(shape)}")
-
-
-def _rows_form(codes):
-    return (-(-codes.shape[-1] // BLOCK128), codes.shape[-2])
-
-
-def _blocks_form(codes):
-    return (*codes.shape[:-2], -(-codes.shape[-2] // BLOCK128), -(-codes.shape[-1] // BLOCK128))
+    shape = codes.shape
+    R, K = shape[-2:] if dim == 3 else shape
+    kb = -(-K // BLOCK128)
+    want = (kb, R) if rows else (-(-R // BLOCK128), kb)
+    if scales.shape != ((shape[0], *want) if dim == 3 else want):
+        raise ValueError(f"{what}_scales must be {[*shape[:-2], *want]}")
+    return shape
 
 
 def _b128_dense(a_codes, a_scales, b_codes, b_scales, b_form):
-    _b128_operand(a_codes, a_scales, "a", _rows_form(a_codes))
-    _b128_operand(b_codes, b_scales, "b",
-                  _rows_form(b_codes) if b_form == B128_ROWS else _blocks_form(b_codes), a_codes)
-    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
+    M, K = _b128_operand(a_codes, a_scales, "a", True)
+    N, Kb = _b128_operand(b_codes, b_scales, "b", b_form == B128_ROWS, like=a_codes)
+    if K != Kb:
         raise ValueError("a_codes and b_codes must be [M, K] and [N, K]")
-    return a_codes.shape[0], b_codes.shape[0], a_codes.shape[1]
+    return M, N, K
 
 
 def _out_type(out_dtype, c):
@@ -662,13 +663,11 @@ def mx_gemm_b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, *,
                          out_dtype=torch.bfloat16, c=None, stream=None):
     """Rows of A [R, K] by expert (row_offsets int64 [E + 1]) times that expert's B [E, N, K] ->
     C [R, N]; rows from row_offsets[E] on are not written."""
-    _b128_operand(a_codes, a_scales, "a", _rows_form(a_codes))
-    _b128_operand(b_codes, b_scales, "b", _blocks_form(b_codes), a_codes)
+    R, K = _b128_operand(a_codes, a_scales, "a", True)
+    experts, N, Kb = _b128_operand(b_codes, b_scales, "b", False, 3, a_codes)
     E = _offsets(row_offsets, a_codes)
-    if a_codes.dim() != 2 or b_codes.dim() != 3 or b_codes.shape[0] != E or \
-            a_codes.shape[1] != b_codes.shape[2]:
+    if experts != E or K != Kb:
         raise ValueError("a_codes and b_codes must be [R, K] and [E, N, K]")
-    (R, K), N = a_codes.shape, b_codes.shape[1]
     dtype = _out_type(out_dtype, c)
     c = _output(c, "c", (R, N), dtype, a_codes)
     _check(lib().mx_gemm_b128_grouped(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
@@ -681,12 +680,11 @@ def mx_gemm_b128_grouped_wgrad(a_codes, a_scales, b_codes, b_scales, row_offsets
                                out_dtype=torch.float32, c=None, stream=None):
     """C[e] = A_e @ B_e^T over expert e's rows, from mx_quantize_b128_cols operands [M, P] and
     [N, P] of the same row_offsets -> C [E, M, N]."""
-    _b128_operand(a_codes, a_scales, "a", _rows_form(a_codes))
-    _b128_operand(b_codes, b_scales, "b", _rows_form(b_codes), a_codes)
+    M, P = _b128_operand(a_codes, a_scales, "a", True)
+    N, Pb = _b128_operand(b_codes, b_scales, "b", True, like=a_codes)
     E = _offsets(row_offsets, a_codes)
-    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
+    if P != Pb:
         raise ValueError("a_codes and b_codes must be [M, P] and [N, P]")
-    M, N, P = a_codes.shape[0], b_codes.shape[0], a_codes.shape[1]
     dtype = _out_type(out_dtype, c)
     c = _output(c, "c", (E, M, N), dtype, a_codes)
     _check(lib().mx_gemm_b128_grouped_wgrad(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes),

@@ -1511,7 +1511,8 @@ cudaError_t launch_config(const B128GemmArgs& g, cudaStream_t stream, int q_even
   if (err == cudaSuccess) {
     err = make_tensor_map_2d(&qmap, qcodes, qrows, g.K, u8, 1, kStepBytes, 128, swz);
   }
-  if (err == cudaSuccess) {
+  map16 = pmap;  // where it is not used
+  if (err == cudaSuccess && (C::kSwap || C::kNarrow)) {
     err = make_tensor_map_2d(&map16, g.a_codes, g.M, g.K, u8, 1, kStepBytes, 16, swz);
   }
   if (err == cudaSuccess) {
