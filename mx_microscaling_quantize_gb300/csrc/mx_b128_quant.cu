@@ -9,7 +9,9 @@
 // multiplication and differ only next to a rounding midpoint.
 //
 // All three kernels are bound by memory: 2 bytes read and 1 written per element (2 written when
-// the square kernel writes both orders), scales 1/32 of a byte.
+// the square kernel writes both orders), scales 1/32 of a byte. x[8192, 8192], where a plain copy of
+// as many bytes takes 30 us: rows 31 us (6.6 TB/s), columns 37 (5.5), squares 30 (6.7), squares in both
+// orders 42 (6.4).
 #include "mx_device.cuh"
 #include "mx_expert.h"
 #include "mx_launch.h"
@@ -208,7 +210,9 @@ __device__ __forceinline__ bool find_block(const int* offsets, int E, int64_t b,
 }
 
 // 128 x 1 blocks, written transposed (codes [K, 128 * blocks], scales [blocks, K]): the operand
-// of a product that contracts over the rows of x.
+// of a product that contracts over the rows of x. The transposition goes through shared memory, a CTA's
+// tile of 128 rows being one block: it is loaded, reduced and written before the CTA's next, and other
+// CTAs of the SM fill the gaps (0.81 of a copy's rate).
 __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArgs a) {
   __shared__ __align__(16) uint8_t sm[128 * 128];
   __shared__ __align__(16) uint32_t part[8][64];

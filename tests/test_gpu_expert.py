@@ -240,7 +240,8 @@ def test_route_backward_of_no_choice_is_nothing():
 
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 8, 128), (5, 3, 7), (300, 8, 64),
-                                   (511, 8, 1024), (513, 8, 256), (4096, 1, 3), (9001, 7, 130),
+                                   (128, 4, 9), (128, 8, 40), (205, 5, 40), (511, 8, 1024), (513, 8, 256),
+                                   (4096, 1, 3), (9001, 7, 130),
                                    (70000, 4, 17)])
 def test_plan(T, k, E):
     rng = np.random.default_rng(T + E)
