@@ -10,7 +10,7 @@
 //
 // All three kernels are bound by memory: 2 bytes read and 1 written per element (2 written when
 // the square kernel writes both orders), scales 1/32 of a byte. x[8192, 8192], where a plain copy of
-// as many bytes takes 30 us: rows 31 us (6.6 TB/s), columns 37 (5.5), squares 30 (6.7), squares in both
+// as many bytes takes 30 us: rows 31 us (6.6 TB/s), columns 31 (6.5), squares 30 (6.7), squares in both
 // orders 42 (6.4).
 #include "mx_device.cuh"
 #include "mx_expert.h"
@@ -150,6 +150,13 @@ __device__ __forceinline__ void load_tile(const uint16_t* x, int64_t K, const in
   }
 }
 
+__device__ __forceinline__ void copy16B_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+
 __device__ __forceinline__ void stage_transposed(uint8_t* sm, int rg, int cg, int j,
                                                  const uint32_t (&v)[2]) {
   *reinterpret_cast<uint2*>(sm + (cg * 8 + j) * 128 + ((rg ^ cg) << 3)) = make_uint2(v[0], v[1]);
@@ -209,46 +216,94 @@ __device__ __forceinline__ bool find_block(const int* offsets, int E, int64_t b,
   return false;
 }
 
+// Blocks of 128 rows of the buffer above that belong to experts. One warp.
+__device__ __forceinline__ int64_t count_blocks(const int* offsets, int E) {
+  int n = 0;
+  for (int e = threadIdx.x & 31; e < E; e += 32) {
+    n += (max(offsets[e + 1] - offsets[e], 0) + kB128 - 1) / kB128;
+  }
+  return (int64_t)__reduce_add_sync(0xFFFFFFFFu, (unsigned)n);
+}
+
 // 128 x 1 blocks, written transposed (codes [K, 128 * blocks], scales [blocks, K]): the operand
-// of a product that contracts over the rows of x. The transposition goes through shared memory, a CTA's
-// tile of 128 rows being one block: it is loaded, reduced and written before the CTA's next, and other
-// CTAs of the SM fill the gaps (0.81 of a copy's rate).
+// of a product that contracts over the rows of x. The transposition goes through shared memory, a tile
+// of 128 rows being one block. A CTA walks a run of tiles along x's rows, and while it reduces, converts
+// and writes one, the next is on its way into shared memory, every thread's pieces to places of its
+// own: four CTAs keep 128 KB of an SM's loads in flight (x[8192, 8192] 31.3 us; a tile's own loads in
+// registers, nothing on its way meanwhile, 36.6).
+struct ColsShared {
+  uint4 next[8][kTileThreads];  // the tile on its way
+  uint8_t out[128 * 128];
+  uint32_t part[8][64];
+  float factor[128];
+  int64_t blocks;
+  int offsets[1024 + 1];
+};
 __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArgs a) {
-  __shared__ __align__(16) uint8_t sm[128 * 128];
-  __shared__ __align__(16) uint32_t part[8][64];
-  __shared__ __align__(16) float factor[128];
-  __shared__ int range[2];
-  __shared__ int offsets[1024 + 1];
+  extern __shared__ __align__(128) uint8_t cols_shared[];
+  ColsShared& s = *reinterpret_cast<ColsShared*>(cols_shared);
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4, warp = tid >> 5;
-  const int64_t b = blockIdx.x;
+  int64_t blocks = a.blocks;
   if (a.offsets) {
     for (int e = tid; e <= a.E; e += kTileThreads) {  // one trip to memory
-      offsets[e] = (int)min(max(load_s64(a.offsets + e), (int64_t)0), a.R);
+      s.offsets[e] = (int)min(max(load_s64(a.offsets + e), (int64_t)0), a.R);
     }
     __syncthreads();
     if (warp == 0) {
-      int lo = 0, hi = 0;
-      const bool found = find_block(offsets, a.E, b, &lo, &hi);
-      if (tid == 0) {
-        range[0] = found ? lo : -1;
-        range[1] = hi;
-      }
+      const int64_t n = count_blocks(s.offsets, a.E);
+      if (tid == 0) s.blocks = min(n, a.blocks);
     }
     __syncthreads();
-    if (range[0] < 0) return;  // past the last expert: never read by the product
-  } else if (tid == 0) {
-    range[0] = (int)(b * kB128);
-    range[1] = (int)a.R;
+    blocks = s.blocks;  // those past the last expert's are never read by the product
   }
-  __syncthreads();
-  const int64_t row0 = range[0], row_end = range[1];
+  const int64_t cols = (a.K + kB128 - 1) / kB128, tiles = blocks * cols;
+  const int64_t t0 = tiles * blockIdx.x / gridDim.x, t1 = tiles * (blockIdx.x + 1) / gridDim.x;
+  if (t0 == t1) return;
   const int64_t pitch = a.blocks * kB128;
-  for (int64_t c0 = (int64_t)blockIdx.y * kB128; c0 < a.K; c0 += (int64_t)gridDim.y * kB128) {
+  int64_t b = t0 / cols, c = t0 - b * cols;
+  int row0 = 0, row_end = 0;  // source rows of block b
+  auto find = [&] {
+    if (a.offsets) {
+      find_block(s.offsets, a.E, b, &row0, &row_end);
+    } else {
+      row0 = (int)(b * kB128);
+      row_end = (int)a.R;
+    }
+  };
+  auto load = [&] {  // tile (b, c)
+    const int64_t col = c * kB128 + cg * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = (int64_t)row0 + rg * 8 + i;
+      int64_t src = row;
+      bool ok = row < row_end && col < a.K;
+      if (ok && a.index) {
+        src = a.index[row];
+        ok = src >= 0 && src < a.M;
+      }
+      if (ok) {
+        copy16B_async(&s.next[i][tid], static_cast<const uint16_t*>(a.x) + src * a.K + col);
+      } else {
+        s.next[i][tid] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  find();
+  load();
+  for (int64_t t = t0; t < t1; ++t) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");  // a thread reads only what it copied
     uint32_t w[8][4];
-    load_tile(static_cast<const uint16_t*>(a.x), a.K, a.index, a.M, row0 + rg * 8, row_end,
-              c0 + cg * 8, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 v = s.next[i][tid];
+      w[i][0] = v.x;
+      w[i][1] = v.y;
+      w[i][2] = v.z;
+      w[i][3] = v.w;
+    }
     uint32_t m[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -258,41 +313,50 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArg
       m[j] = __vmaxu2(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
     }
     if ((tid & 16) == 0) {  // eight columns' halves, still in pairs
-      *reinterpret_cast<uint4*>(&part[warp][cg * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
+      *reinterpret_cast<uint4*>(&s.part[warp][cg * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
     }
     __syncthreads();
+    const int64_t at = b, c0 = c * kB128;
+    if (t + 1 < t1) {
+      if (++c == cols) {
+        c = 0;
+        ++b;
+        find();
+      }
+      load();
+    }
     if (tid < 128) {
-      uint32_t top = part[0][tid >> 1];
+      uint32_t top = s.part[0][tid >> 1];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) top = __vmaxu2(top, part[i][tid >> 1]);
+      for (int i = 1; i < 8; ++i) top = __vmaxu2(top, s.part[i][tid >> 1]);
       const Factors f = block_factors_b128((tid & 1) ? top & 0xFFFF0000u : top << 16);
-      factor[tid] = f.r;
-      if (c0 + tid < a.K) a.scales[b * a.K + c0 + tid] = f.scale;
+      s.factor[tid] = f.r;
+      if (c0 + tid < a.K) a.scales[at * a.K + c0 + tid] = f.scale;
     }
     __syncthreads();
     float r8[8];
-    *reinterpret_cast<float4*>(r8) = *reinterpret_cast<const float4*>(factor + cg * 8);
-    *reinterpret_cast<float4*>(r8 + 4) = *reinterpret_cast<const float4*>(factor + cg * 8 + 4);
+    *reinterpret_cast<float4*>(r8) = *reinterpret_cast<const float4*>(s.factor + cg * 8);
+    *reinterpret_cast<float4*>(r8 + 4) = *reinterpret_cast<const float4*>(s.factor + cg * 8 + 4);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float r = r8[j];
       uint32_t v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float t[4];
+        float f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t u = w[4 * h + i][j >> 1];
-          t[i] = __fmul_rn((j & 1) ? bf16_hi(u) : bf16_lo(u), r);
+          f[i] = __fmul_rn((j & 1) ? bf16_hi(u) : bf16_lo(u), r);
         }
-        v[h] = codes2(t[0], t[1]) | codes2(t[2], t[3]) << 16;
+        v[h] = codes2(f[0], f[1]) | codes2(f[2], f[3]) << 16;
       }
-      stage_transposed(sm, rg, cg, j, v);
+      stage_transposed(s.out, rg, cg, j, v);
     }
     __syncthreads();
-    store_transposed(sm, a.codes + c0 * pitch + b * kB128, pitch, kB128,
+    // (the next tile's first barriers keep its codes from overtaking these reads)
+    store_transposed(s.out, a.codes + c0 * pitch + at * kB128, pitch, kB128,
                      (int)min((int64_t)kB128, a.K - c0));
-    __syncthreads();
   }
 }
 
@@ -372,11 +436,12 @@ cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_b128_cols(const B128QuantArgs& a, cudaStream_t stream) {
-  const int64_t col_blocks = (a.K + kB128 - 1) / kB128;
-  // by expert, a CTA walks two column tiles, so that finding its rows is paid half as often
-  const int64_t y = a.offsets ? (col_blocks + 1) / 2 : col_blocks;
-  return launch_pdl(&b128_cols_kernel, dim3((unsigned)a.blocks, (unsigned)(y < 65535 ? y : 65535)),
-                    dim3(kTileThreads), 0, stream, a);
+  const int64_t tiles = a.blocks * ((a.K + kB128 - 1) / kB128);  // by expert: at most
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(&b128_cols_kernel), kTileThreads,
+                                      sizeof(ColsShared), 0);
+  if (slots <= 0) return cudaErrorInvalidConfiguration;
+  return launch_pdl(&b128_cols_kernel, dim3((unsigned)(tiles < slots ? tiles : slots)),
+                    dim3(kTileThreads), sizeof(ColsShared), stream, a);
 }
 
 cudaError_t launch_b128_blocks(const B128QuantArgs& a, cudaStream_t stream) {
