@@ -530,8 +530,9 @@ def mx_route_plan(experts, E: int, *, row_offsets=None, tokens=None, slots=None,
         # the caching allocator hands memory out per stream: allocated for the stream it is used on
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
-            if isinstance(stream, torch.cuda.Stream):
-                workspace.record_stream(stream)
+            if stream is not None:
+                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                        torch.cuda.ExternalStream(stream, experts.device))
     elif workspace.device != experts.device or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must have {need} bytes on {experts.device}")

@@ -597,6 +597,37 @@ def test_on_a_side_stream_and_in_a_graph():
     assert torch.equal(captured, layer())
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_stream_argument(raw):
+    """Every call on a stream passed as an object or as a handle."""
+    rng = np.random.default_rng(14)
+    T, E, k, N, K = 700, 6, 2, 128, 256
+    x, dout = bf16_inputs(rng, T, K, False), bf16_inputs(rng, T, N, False)
+    logits = spaced_logits(rng, T, E, torch.float32)
+    weight = torch.stack([bf16_inputs(rng, N, K, False) for _ in range(E)])
+
+    def layer(**at):
+        experts, weights = mxq.mx_route(logits, k, **at)
+        offsets, tokens, slots = mxq.mx_route_plan(experts, E, **at)
+        wc, ws, wct, wst = mxq.mx_quantize_b128_blocks(weight, transpose=True, **at)
+        y = mxq.mx_gemm_b128_grouped(*mxq.mx_quantize_b128_rows(x, tokens, **at), wc, ws, offsets, **at)
+        out = mxq.mx_combine(y, slots, weights, **at)
+        dy, dweights = mxq.mx_combine_backward(dout, y, slots, weights, **at)
+        dw = mxq.mx_gemm_b128_grouped_wgrad(*mxq.mx_quantize_b128_cols(dy, None, offsets, **at),
+                                            *mxq.mx_quantize_b128_cols(x, tokens, offsets, **at),
+                                            offsets, **at)
+        one = mxq.mx_gemm_b128(*mxq.mx_quantize_b128_rows(x, **at), wc[0], ws[0], **at)
+        return out, dy, dw, one, mxq.mx_route_backward(dweights, logits, experts, **at)
+
+    want = layer()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = layer(stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+
+
 def test_repeated_calls_give_the_same_bits():
     rng = np.random.default_rng(12)
     (ac, asc), _ = operand(rng, 70, 2048, "rows")
