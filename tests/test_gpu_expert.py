@@ -291,6 +291,35 @@ def test_quantize_cols(M, K):
     assert (cpu(codes) == want_c).all() and (cpu(scales) == want_s).all()
 
 
+@pytest.mark.parametrize("M,K,E", [(2500, 4128, 0), (9000, 1056, 40)])
+def test_quantize_cols_many_tiles(M, K, E):
+    """More tiles than resident CTAs: every one walks several, over ends of blocks and of experts."""
+    rng = np.random.default_rng(M)
+    x = bf16_inputs(rng, M, K)
+    offsets = None
+    if E:
+        offsets = np.concatenate([[0], np.sort(rng.integers(0, M, E - 1)), [M]]).astype(np.int64)
+        offsets[5] = offsets[4]  # an expert without rows
+    codes, scales = mxq.mx_quantize_b128_cols(
+        x, None, None if offsets is None else torch.from_numpy(offsets).cuda())
+    want_c, want_s = R.cols(x, None, offsets)
+    n = want_s.shape[0]  # blocks that belong to experts
+    assert (cpu(codes)[:, :n * 128] == want_c[:, :n * 128]).all() and (cpu(scales)[:n] == want_s).all()
+
+
+def test_quantize_cols_contract_breaking_offsets_stay_inside():
+    x = bf16_inputs(np.random.default_rng(1), 100, 128)
+    P = mxq.mx_b128_padded_rows(100, 3)
+    codes = torch.full((130, P), 5, device="cuda", dtype=torch.uint8)
+    scales = torch.full((P // 128 + 2, 128), 5.0, device="cuda")
+    for off in ([0, 90, 40, 1000], [-5, 10, 2 ** 40, 7], [50, 20, 10, 0], [0, 100, 0, 100]):
+        mxq.mx_quantize_b128_cols(x, None, torch.tensor(off, device="cuda"), codes=codes[1:129],
+                                  scales=scales[1:-1])
+    torch.cuda.synchronize()
+    assert (codes[0] == 5).all() and (codes[129] == 5).all()
+    assert (scales[0] == 5).all() and (scales[-1] == 5).all()
+
+
 @pytest.mark.parametrize("counts", [[0, 5, 0, 300, 128], [1], [0, 0], [129, 1, 127, 0, 64, 256]])
 @pytest.mark.parametrize("gather", [False, True])
 def test_quantize_cols_by_expert(counts, gather):
