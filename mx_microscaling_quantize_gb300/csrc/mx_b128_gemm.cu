@@ -39,7 +39,9 @@
 // Every mbarrier wait is bounded (KernelArgs::wait_limit_ns); a role whose wait ran out sets the
 // device error word and stops; loads and MMAs in flight are waited for (2 s) before the CTA frees its
 // tensor memory and exits.
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "mx_device.cuh"
 #include "mx_expert.h"
@@ -1536,10 +1538,42 @@ cudaError_t launch_config(const B128GemmArgs& g, cudaStream_t stream, int q_even
                          kThreads, smem_bytes<C>(), cluster, stream, pmap, qmap, map16, cmap, a);
 }
 
+// CTAs of the swapped shape that run at once in clusters of 1, 2, 4 or 8: the parts of the chip that a
+// cluster cannot cross leave SMs over. Asked once per device.
+template <typename C>
+int cluster_slots(int ctas) {
+  static std::mutex mu;
+  static std::map<std::pair<int, int>, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& known = cache[{dev, ctas}];
+  if (known == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<C>();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, &b128_gemm_kernel<C>, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return 0;
+    }
+    known = clusters * ctas;
+  }
+  return known;
+}
+
 // Dense calls: 256 x 256 tiles on pairs, or the swapped shape, whose 128-row weight tiles, times up to
-// eight CTAs along the contraction, spread few tokens over the SMs. The rule compares what each costs
-// by its waves (us, measured: 0.40 a step and 3 a tile of the pairs, whatever the rows; 0.25 a step
-// and 2 us more with 128 tokens than with 16, and 5 a tile with the joining of the parts).
+// eight CTAs along the contraction as long as all run at once, spread few tokens over the SMs. The rule
+// compares what each costs by its waves, from measured steps (us): 0.32 and 2.3 a tile of the pairs,
+// whatever the rows; 0.25 to 0.29 up to 64 columns, 0.44 beyond (batches of two), and 4 for joining
+// the parts. 8192 x 8192, swapped / pairs: 1 token 14 / 34, 128 21 / 26, 192 31 / 26, 512 59 / 27.
 template <bool B_ROWS, bool F32>
 cudaError_t launch_dense(const B128GemmArgs& g, cudaStream_t stream) {
   using Large = Config<2, kB128Dense, false, true, B_ROWS, F32>;
@@ -1551,11 +1585,16 @@ cudaError_t launch_dense(const B128GemmArgs& g, cudaStream_t stream) {
   const int q_even = (int)ceil_div(ceil_div(g.M, q_tiles), 16) * 16;
   const int64_t tiles = ceil_div(g.M, q_even) * ceil_div(g.N, kLanes);
   int split = 1;
-  while (split < kMaxSplit && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
-  const double few = (double)ceil_div(tiles * split, slots) *
-                     ((double)ceil_div(nk, split) * (0.25 + 0.0015 * q_even) + (split > 1 ? 5 : 3));
+  while (split < kMaxSplit && nk >= 4 * split && tiles * split * 2 <= slots &&
+         tiles * split * 2 <= cluster_slots<Small>(split * 2)) {
+    split *= 2;
+  }
+  const double step = q_even <= 64 ? 0.25 + 0.0007 * q_even : 0.44;
+  const double few = (double)ceil_div(tiles * split, slots) * ((double)ceil_div(nk, split) * step + 1.2) +
+                     (split > 1 ? 5.8 : 2.0);
   const double many =
-      (double)ceil_div(ceil_div(g.M, 256) * ceil_div(g.N, 256), slots / 2) * ((double)nk * 0.40 + 3);
+      (double)ceil_div(ceil_div(g.M, 256) * ceil_div(g.N, 256), slots / 2) * ((double)nk * 0.32 + 2.3) +
+      2.9;
   return many <= few ? launch_config<Large>(g, stream)
                      : launch_config<Small>(g, stream, q_even, split);
 }
