@@ -79,16 +79,13 @@ __device__ __forceinline__ void load_logits(const void* logits, int64_t t, int E
   }
 }
 
-// Scores of one token: sigmoid, or exp(l - max) with the sum in *total.
-template <int V, bool SIGMOID>
-__device__ __forceinline__ void token_scores(const float (&l)[V], float (&s)[V], float* total) {
-  if (SIGMOID) {
-    // the reciprocal rounded to nearest is the quotient 1 / (1 + exp(-l)) rounded to nearest
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = __frcp_rn(__fadd_rn(1.0f, expf(-l[i])));
-    *total = 1.0f;
-    return;
-  }
+// The reciprocal rounded to nearest is the quotient 1 / (1 + exp(-l)) rounded to nearest.
+__device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(__fadd_rn(1.0f, expf(-l))); }
+
+// Scores of one token before the division: exp(l - max) with the sum in *total and the maximum in *top.
+template <int V>
+__device__ __forceinline__ void softmax_scores(const float (&l)[V], float (&s)[V], float* total,
+                                               float* top) {
   float m = -INFINITY;
   bool nan = false;
 #pragma unroll
@@ -106,6 +103,7 @@ __device__ __forceinline__ void token_scores(const float (&l)[V], float (&s)[V],
     sum += s[i];
   }
   *total = warp_sum(sum);
+  *top = m;
 }
 
 // The two largest keys of two pairs.
@@ -142,7 +140,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, in
   if (t >= a.T) return;
   float l[V], s[V], total;
   load_logits<V, BF16>(a.logits, t, a.E, wide, l);
-  token_scores<V, SIGMOID>(l, s, &total);
+  if (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = sigmoid(l[i]);
+    total = 1.0f;
+  } else {
+    float top;
+    softmax_scores(l, s, &total, &top);
+  }
   if constexpr (V >= 4) {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
@@ -282,35 +287,48 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, in
 //   sigmoid: dl = dp s (1 - s), nothing for the others;
 //   softmax: dl_i = s_i (dp_i - sum_j dp_j s_j), every logit.
 // A choice of -1 (no expert) takes and gives nothing. The scores are computed again from the
-// logits: reading them back would cost what the logits cost.
+// logits: reading them back would cost what the logits cost. The row is written as if nothing had been
+// chosen (d = 0), then lane j its choice's element over it, whose score it has from its own logit: no
+// row of scores or gradients is kept beside the registers (4096 tokens of 512 experts, 8 chosen: 5.9 us,
+// with such rows in shared memory 14.3; 4097 of 64 3.1 either way).
+template <bool BF16>
+__device__ __forceinline__ void store_grad(void* p, int64_t at, float v) {
+  if (BF16) {
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(v));
+    static_cast<uint16_t*>(p)[at] = h;
+  } else {
+    static_cast<float*>(p)[at] = v;
+  }
+}
 template <int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteArgs a, bool wide) {
-  __shared__ __align__(16) float score_row[kRouteWarps][V * 32];
-  __shared__ __align__(16) float grad_row[kRouteWarps][V * 32];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = lane * V;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
   if (t >= a.T) return;
-  float l[V], s[V], total;
-  load_logits<V, BF16>(a.logits, t, a.E, wide, l);
-  token_scores<V, SIGMOID>(l, s, &total);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (!SIGMOID) s[i] = total == 0.0f ? 0.0f : __fdiv_rn(s[i], total);
-    score_row[warp][e0 + i] = s[i];
-    grad_row[warp][e0 + i] = 0.0f;
-  }
-  __syncwarp();
+  float l[V];
+  if (!SIGMOID) load_logits<V, BF16>(a.logits, t, a.E, wide, l);  // asked for before the choice's
   int32_t expert = -1;
-  float g = 0.0f, p = 0.0f;
+  float g = 0.0f, p = 0.0f, chosen = 0.0f;  // gradient, score and logit of the lane's choice
   if (lane < a.k) {
     expert = a.chosen[t * a.k + lane];
-    if (expert >= a.E) expert = -1;
+    if (expert >= a.E || expert < 0) expert = -1;
   }
   if (expert >= 0) {
     g = a.scale * a.grad_weights[t * a.k + lane];
-    p = score_row[warp][expert];
+    chosen = load_logit<BF16>(a.logits, t * a.E + expert);
+  }
+  float dl[V];
+  if (SIGMOID) {
+    if (expert >= 0) p = sigmoid(chosen);
+  } else {
+    float total, m;
+    softmax_scores(l, dl, &total, &m);
+#pragma unroll
+    for (int i = 0; i < V; ++i) dl[i] = total == 0.0f ? 0.0f : __fdiv_rn(dl[i], total);
+    if (expert >= 0) p = total == 0.0f ? 0.0f : __fdiv_rn(expf(__fsub_rn(chosen, m)), total);
   }
   if (a.renormalize) {
     const float P = warp_sum(p);
@@ -318,17 +336,24 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
     g = P == 0.0f ? 0.0f : (g - along / P) / P;
   }
   const float through = warp_sum(expert >= 0 ? g * p : 0.0f);
-  // an expert named twice (no call of the router does that) adds both
-  if (expert >= 0) atomicAdd(&grad_row[warp][expert], g);
-  __syncwarp();
-  float dl[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float d = grad_row[warp][e0 + i];
-    dl[i] = SIGMOID ? d * s[i] * (1.0f - s[i]) : s[i] * (d - through);
+  // an expert named twice (no call of the router does that) adds both, in order; its first lane writes
+  float d = g;
+  bool first = expert >= 0;
+  const uint32_t same = __match_any_sync(0xFFFFFFFFu, expert);
+  if (__any_sync(0xFFFFFFFFu, first && (same & (same - 1u)))) {
+    d = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+      const float other = __shfl_sync(0xFFFFFFFFu, g, j);
+      if ((same >> j) & 1u) d += other;
+    }
+    first = first && lane == __ffs(same) - 1;
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) dl[i] = SIGMOID ? 0.0f : dl[i] * (0.0f - through);
+  bool whole = false;
   if constexpr (V >= 4) {
-    if (wide && e0 + V <= a.E) {
+    whole = wide && e0 + V <= a.E;
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < V; i += 4) {
         if constexpr (BF16) {
@@ -342,19 +367,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
               make_float4(dl[i], dl[i + 1], dl[i + 2], dl[i + 3]);
         }
       }
-      return;
     }
   }
+  if (!whole) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (e0 + i >= a.E) continue;
-    if (BF16) {
-      uint16_t h;
-      asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(dl[i]));
-      static_cast<uint16_t*>(a.grad_logits)[t * a.E + e0 + i] = h;
-    } else {
-      static_cast<float*>(a.grad_logits)[t * a.E + e0 + i] = dl[i];
+    for (int i = 0; i < V; ++i) {
+      if (e0 + i < a.E) store_grad<BF16>(a.grad_logits, t * a.E + e0 + i, dl[i]);
     }
+  }
+  __syncwarp();  // the row comes before its choices
+  if (first) {
+    store_grad<BF16>(a.grad_logits, t * a.E + expert,
+                     SIGMOID ? d * p * (1.0f - p) : p * (d - through));
   }
 }
 

@@ -239,6 +239,36 @@ def test_route_backward_of_no_choice_is_nothing():
             assert (d[0] == 0).all() and np.isfinite(d).all()
 
 
+@pytest.mark.parametrize("score", [mxq.SOFTMAX, mxq.SIGMOID])
+@pytest.mark.parametrize("E", [6, 40, 600])
+def test_route_backward_of_choices_named_twice(score, E):
+    """No call of the router names an expert twice; the gradient of such weights is the sum."""
+    rng = np.random.default_rng(E)
+    experts = np.array([[2, 2, 5], [1, 1, 1], [-1, 0, 0], [3, -1, 4]], dtype=np.int32)
+    l = rng.standard_normal((4, E)).astype(np.float32)
+    g = rng.standard_normal((4, 3)).astype(np.float32)
+    got = cpu(mxq.mx_route_backward(torch.from_numpy(g).cuda(), torch.from_numpy(l).cuda(),
+                                    torch.from_numpy(experts).cuda(), score, renormalize=False))
+    x = l.astype(np.float64)
+    if score == mxq.SOFTMAX:
+        s = np.exp(x - x.max(1, keepdims=True))
+        s /= s.sum(1, keepdims=True)
+    else:
+        s = 1 / (1 + np.exp(-x))
+    for t in range(4):
+        d, size = np.zeros(E), np.zeros(E)
+        for j, e in enumerate(experts[t]):
+            if e >= 0:
+                d[e] += g[t, j]
+                size[e] += abs(float(g[t, j]))
+        if score == mxq.SOFTMAX:
+            want, size = s[t] * (d - d @ s[t]), s[t] * (size + size @ s[t])
+        else:
+            want, size = d * s[t] * (1 - s[t]), size * s[t]
+        # exponentials, sums of E and of the choices, divisions and products: under 256 units in all
+        assert (np.abs(got[t] - want) <= 256 * R.U * size + 1e-38).all()
+
+
 @pytest.mark.parametrize("T,k,E", [(0, 2, 4), (1, 1, 1), (1, 8, 128), (5, 3, 7), (300, 8, 64),
                                    (128, 4, 9), (128, 8, 40), (205, 5, 40), (511, 8, 1024), (513, 8, 256),
                                    (4096, 1, 3), (9001, 7, 130),
