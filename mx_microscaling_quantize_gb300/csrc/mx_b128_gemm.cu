@@ -1384,7 +1384,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = tile_count<C>(a, s.prefix);
   // The promoting warps hold their sums and two or three chunks in registers: the others give theirs
   // up.
-  if (warp < 4) {
+  if (C::MODE == kB128Grouped && tiles == 0) {
+    // none of this launch's experts has rows (3.2 us a launch in all, 2.6 so)
+  } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 0) produce<C>(pmap, qmap, map16, a, s, tiles);
     if (warp == 1 && (C::CTAS == 1 || cluster_rank() == 0)) multiply<C>(a, s, tiles, tmem);
