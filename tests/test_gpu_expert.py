@@ -757,3 +757,109 @@ def test_refusals():
         mxq.mx_combine(x, torch.zeros(2, 2, **i32), torch.zeros(2, 3, device="cuda"))
     with pytest.raises(ValueError):
         mxq.mx_combine_backward(x, x, torch.zeros(2, 2, **i32), torch.zeros(2, 2, device="cuda"))
+
+
+# ---------------------------------------------------------------------------------------------
+# tensors of more than 2^31 elements: the far end against a small call on a copy of it
+# ---------------------------------------------------------------------------------------------
+FAR, WIDE = 1_100_000, 2048
+
+
+def far_rows(n):
+    x = torch.zeros(FAR, WIDE, device="cuda", dtype=torch.bfloat16)
+    x[-n:] = bf16_inputs(np.random.default_rng(n), n, WIDE, False)
+    return x
+
+
+def test_far_end_of_quantised_rows_and_columns():
+    x = far_rows(300)
+    near = x[-300:].clone()
+    want_c, want_s = mxq.mx_quantize_b128_rows(near)
+    codes, scales = mxq.mx_quantize_b128_rows(x)
+    assert torch.equal(codes[-300:], want_c) and torch.equal(scales[:, -300:], want_s)
+    del codes, scales
+    index = torch.arange(FAR - 300, FAR, device="cuda", dtype=torch.int32)
+    codes, scales = mxq.mx_quantize_b128_rows(x, index)
+    assert torch.equal(codes, want_c) and torch.equal(scales, want_s)
+    del codes, scales
+    offsets = torch.tensor([0, FAR - 300, FAR], device="cuda")
+    codes, scales = mxq.mx_quantize_b128_cols(x, None, offsets)
+    want_c, want_s = mxq.mx_quantize_b128_cols(near)
+    at = -(-(FAR - 300) // 128)
+    assert torch.equal(codes[:, at * 128:at * 128 + 384], want_c)
+    assert torch.equal(scales[at:at + 3], want_s)
+
+
+def test_far_end_of_squares():
+    x = far_rows(256).view(FAR // 16, 16 * WIDE)
+    codes, scales, codes_t, scales_t = mxq.mx_quantize_b128_blocks(x, transpose=True)
+    start = (x.shape[0] - 1) // 128 * 128
+    want = mxq.mx_quantize_b128_blocks(x[start:].clone(), transpose=True)
+    assert torch.equal(codes[start:], want[0]) and torch.equal(scales[-1:], want[1])
+    assert torch.equal(codes_t[:, start:], want[2]) and torch.equal(scales_t[:, -1:], want[3])
+
+
+def test_far_end_of_products():
+    rng = np.random.default_rng(5)
+    (bc, bsc), b = operand(rng, WIDE, 128, "blocks")
+    (ac, asc), a = operand(rng, 300, 128, "rows")
+    codes = torch.zeros(FAR, 128, device="cuda", dtype=torch.uint8)
+    scales = torch.ones(1, FAR, device="cuda")
+    codes[-300:], scales[:, -300:] = ac, asc
+    check_product(mxq.mx_gemm_b128(codes, scales, bc, bsc)[-300:], a, b, 128)
+    for offsets in ([0, FAR], [0, FAR - 300, FAR - 100, FAR]):
+        E = len(offsets) - 1
+        c = mxq.mx_gemm_b128_grouped(codes, scales, bc.expand(E, -1, -1).contiguous(),
+                                     bsc.expand(E, -1, -1).contiguous(),
+                                     torch.tensor(offsets, device="cuda"))
+        check_product(c[-300:], a, b, 128)
+        del c
+
+
+def test_far_end_of_combined_rows():
+    y, dout = far_rows(6), bf16_inputs(np.random.default_rng(1), 3, WIDE, False)
+    near = y[-6:].clone()
+    small = torch.tensor([[5, 0], [1, -1], [3, 4]], device="cuda", dtype=torch.int32)
+    slots = torch.where(small >= 0, small + (FAR - 6), small)
+    weights = torch.rand(3, 2, device="cuda")
+    assert torch.equal(mxq.mx_combine(y, slots, weights), mxq.mx_combine(near, small, weights))
+    dy = torch.zeros_like(y)
+    dy, dw = mxq.mx_combine_backward(dout, y, slots, weights, dy=dy)
+    want_y, want_w = mxq.mx_combine_backward(dout, near, small, weights, dy=torch.zeros_like(near))
+    assert torch.equal(dy[-6:], want_y) and torch.equal(dw, want_w) and not dy[:-6].any()
+
+
+def test_far_end_of_routed_tokens():
+    T, E = 2_200_000, 1024
+    logits = torch.zeros(T, E, device="cuda", dtype=torch.bfloat16)
+    logits[-5:] = bf16_inputs(np.random.default_rng(2), 5, E, False)
+    near = logits[-5:].clone()
+    experts, weights = mxq.mx_route(logits, 4)
+    want_e, want_w = mxq.mx_route(near, 4)
+    assert torch.equal(experts[-5:], want_e) and torch.equal(weights[-5:], want_w)
+    g = torch.rand(T, 4, device="cuda")
+    assert torch.equal(mxq.mx_route_backward(g, logits, experts)[-5:],
+                       mxq.mx_route_backward(g[-5:].clone(), near, want_e))
+
+
+def test_far_end_of_experts():
+    rng = np.random.default_rng(9)
+    E, N, K = 1024, 1056, 2048
+    (bc, bsc), b = operand(rng, N, K, "blocks")
+    (ac, asc), a = operand(rng, 140, K, "rows")
+    codes = torch.zeros(E, N, K, device="cuda", dtype=torch.uint8)
+    scales = torch.ones(E, *bsc.shape, device="cuda")
+    codes[-1], scales[-1] = bc, bsc
+    for counts in ([0] * (E - 1) + [140], [0] * (E - 2) + [130, 10]):
+        offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), device="cuda")
+        c = mxq.mx_gemm_b128_grouped(ac, asc, codes, scales, offsets)
+        n = counts[-1]
+        check_product(c[-n:], a[-n:], b, K)
+    del codes
+    dy, x = bf16_inputs(rng, 140, N, False), bf16_inputs(rng, 140, K, False)
+    offsets = torch.tensor([0] * E + [140], device="cuda")
+    dw = mxq.mx_gemm_b128_grouped_wgrad(*mxq.mx_quantize_b128_cols(dy, None, offsets),
+                                        *mxq.mx_quantize_b128_cols(x, None, offsets), offsets)
+    one = mxq.mx_gemm_b128_grouped_wgrad(*mxq.mx_quantize_b128_cols(dy), *mxq.mx_quantize_b128_cols(x),
+                                         torch.tensor([0, 140], device="cuda"))
+    assert torch.equal(dw[-1], one[0]) and not dw[:-1].any()
