@@ -39,8 +39,7 @@
 // Every mbarrier wait is bounded (KernelArgs::wait_limit_ns); a role whose wait ran out sets the
 // device error word and stops; loads and MMAs in flight are waited for (2 s) before the CTA frees its
 // tensor memory and exits.
-#include <map>
-#include <mutex>
+#include <atomic>
 #include <utility>
 
 #include "mx_device.cuh"
@@ -1544,12 +1543,12 @@ cudaError_t launch_config(const B128GemmArgs& g, cudaStream_t stream, int q_even
 // cluster cannot cross leave SMs over. Asked once per device.
 template <typename C>
 int cluster_slots(int ctas) {
-  static std::mutex mu;
-  static std::map<std::pair<int, int>, int> cache;
+  constexpr int kDevices = 16;
+  static std::atomic<int> cache[kDevices][4];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  int& known = cache[{dev, ctas}];
+  std::atomic<int>& kept = cache[dev % kDevices][ctas == 8 ? 3 : ctas / 2];
+  int known = dev < kDevices ? kept.load(std::memory_order_relaxed) : 0;
   if (known == 0) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -1567,6 +1566,7 @@ int cluster_slots(int ctas) {
       return 0;
     }
     known = clusters * ctas;
+    if (dev < kDevices) kept.store(known, std::memory_order_relaxed);
   }
   return known;
 }

@@ -15,6 +15,17 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 mx_status from_cuda(cudaError_t err) { return err == cudaSuccess ? MX_OK : MX_ERR_CUDA; }
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
+// The status of a launch. What is kept per device is made on the host's heap: no exception of it leaves
+// a C entry.
+template <typename F>
+mx_status launched(F&& launch) {
+  try {
+    return from_cuda(launch());
+  } catch (...) {
+    return MX_ERR_CUDA;
+  }
+}
+
 // rows and columns of one operand or matrix: non-negative, 32-bit, their product far from overflow
 bool sizes_ok(int64_t M, int64_t K) {
   return M >= 0 && K >= 0 && M <= INT32_MAX && K <= INT32_MAX &&
@@ -46,9 +57,10 @@ mx_status check_b128_pointers(const void* a_codes, const float* a_scales, const 
 
 mx_status run_gemm(int mode, mxq::B128GemmArgs& g, unsigned long long limit_ns, void* stream) {
   g.wait_limit_ns = limit_ns;
-  const cudaError_t err = mxq::device_error_word(&g.err);
-  if (err != cudaSuccess) return from_cuda(err);
-  return from_cuda(mxq::launch_b128_gemm(mode, g, as_stream(stream)));
+  return launched([&] {
+    const cudaError_t err = mxq::device_error_word(&g.err);
+    return err != cudaSuccess ? err : mxq::launch_b128_gemm(mode, g, as_stream(stream));
+  });
 }
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
@@ -109,7 +121,7 @@ mx_status mx_route(const void* logits, int logits_type, const float* bias, int64
   a.scale = scale;
   a.experts = experts;
   a.weights = weights;
-  return from_cuda(mxq::launch_route(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_route(a, as_stream(stream)); });
 }
 
 mx_status mx_route_backward(const float* grad_weights, const void* logits, int logits_type,
@@ -136,7 +148,7 @@ mx_status mx_route_backward(const float* grad_weights, const void* logits, int l
   a.grad_weights = grad_weights;
   a.chosen = experts;
   a.grad_logits = grad_logits;
-  return from_cuda(mxq::launch_route_backward(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_route_backward(a, as_stream(stream)); });
 }
 
 mx_status mx_route_plan_workspace(int64_t T, int k, int E, int64_t* bytes) {
@@ -167,7 +179,7 @@ mx_status mx_route_plan(const int32_t* experts, int64_t T, int k, int E, int64_t
   a.tokens = tokens;
   a.slots = slots;
   a.workspace = static_cast<int32_t*>(workspace);
-  return from_cuda(mxq::launch_plan(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_plan(a, as_stream(stream)); });
 }
 
 mx_status mx_b128_padded_rows(int64_t R, int E, int64_t* rows) {
@@ -196,7 +208,7 @@ mx_status mx_quantize_b128_rows(const void* x, int64_t M, int64_t K, const int32
   a.R = R;
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
-  return from_cuda(mxq::launch_b128_rows(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_b128_rows(a, as_stream(stream)); });
 }
 
 mx_status mx_quantize_b128_cols(const void* x, int64_t M, int64_t K, const int32_t* index, int64_t R,
@@ -226,7 +238,7 @@ mx_status mx_quantize_b128_cols(const void* x, int64_t M, int64_t K, const int32
   a.blocks = rows / 128;
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
-  return from_cuda(mxq::launch_b128_cols(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_b128_cols(a, as_stream(stream)); });
 }
 
 mx_status mx_quantize_b128_blocks(const void* x, int64_t batch, int64_t M, int64_t K, void* codes,
@@ -250,7 +262,7 @@ mx_status mx_quantize_b128_blocks(const void* x, int64_t batch, int64_t M, int64
   a.scales = scales;
   a.codes_t = static_cast<uint8_t*>(codes_t);
   a.scales_t = scales_t;
-  return from_cuda(mxq::launch_b128_blocks(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_b128_blocks(a, as_stream(stream)); });
 }
 
 mx_status mx_gemm_b128(const void* a_codes, const float* a_scales, const void* b_codes,
@@ -359,7 +371,7 @@ mx_status mx_combine(const void* y, const int32_t* slots, const float* weights, 
   a.N = N;
   a.k = k;
   a.out = out;
-  return from_cuda(mxq::launch_combine(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_combine(a, as_stream(stream)); });
 }
 
 mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* slots,
@@ -384,7 +396,7 @@ mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* sl
   a.k = k;
   a.dy = dy;
   a.dweights = dweights;
-  return from_cuda(mxq::launch_combine_backward(a, as_stream(stream)));
+  return launched([&] { return mxq::launch_combine_backward(a, as_stream(stream)); });
 }
 
 }  // extern "C"
