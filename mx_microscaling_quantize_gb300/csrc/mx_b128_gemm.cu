@@ -995,6 +995,10 @@ __device__ __forceinline__ void store_swapped(const KernelArgs& a, const Smem& s
   uint8_t* staging = s.staging + pw * C::kStagingBytes;
   // what a lane stores of a group: token lane / 4, 8 lanes' worth from 8 (lane % 4) on
   const int part = (lane & 3) * 8;
+  // Slots are taken in turn by the groups that this warp stores (by the number of the group, every fourth
+  // one would find the same): between two uses of one lie the barriers of three others, which order the
+  // reads of the first before the writes of the second.
+  int stored = 0;
 #pragma unroll
   for (int gi = 0; gi < C::kWarpCols / 8; ++gi) {
     if (gi * 8 >= cols || gi % every != first_group) continue;
@@ -1010,7 +1014,7 @@ __device__ __forceinline__ void store_swapped(const KernelArgs& a, const Smem& s
       uint32_t h[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = bf16_pair(first(sums[gi * 4 + r]), second(sums[gi * 4 + r]));
-      uint8_t* slot = staging + (gi & 3) * 8 * 80;
+      uint8_t* slot = staging + (stored++ & 3) * 8 * 80;
       asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                        smem_u32(slot + (lane & 7) * 80 + (lane >> 3) * 16)),
                    "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
