@@ -685,15 +685,26 @@ __device__ __forceinline__ void produce(const CUtensorMap& pmap, const CUtensorM
       }
     }
   }
-  // Loads in flight land before the CTA's shared memory goes away. The first CTA of a pair sees both
-  // CTAs' on its barriers, and both leave together; after a give-up, in which the two may not have
-  // issued the same steps, each also lets a millisecond pass, a thousand times what a load takes.
-  if (C::CTAS == 2 && failed) {
+  // Loads in flight land before the CTA's shared memory goes away. A pair's are counted on its first CTA's
+  // barriers, and each release of a stage arrives at both CTAs: a CTA that has seen every stage of its own
+  // released has nothing more to come, neither a load that the pair's products needed nor an arrival
+  // from the other CTA. After a give-up, in which the two may not have issued the same steps, the first
+  // waits for what it sees, and each also lets a millisecond pass, a thousand times what a load or an
+  // arrival takes.
+  if constexpr (C::CTAS == 2) {
+    for (int i = 0; i < stages && !failed; ++i) {
+      warp_wait(smem_u32(s.empty + st), parity, &failed, a);
+      if (++st == stages) {
+        st = 0;
+        parity ^= 1;
+      }
+    }
+    if (!failed) return;
     const unsigned long long begin = global_ns();
     while (global_ns() - begin < 1000000ull) {
     }
+    if (cluster_rank() != 0) return;
   }
-  if (C::CTAS == 2 && cluster_rank() != 0) return;
   bool drain_failed = false;
   for (int i = issued > stages ? issued - stages : 0; i < issued; ++i) {
     mbar_wait(smem_u32(s.full + i % stages), (i / stages) & 1, &drain_failed, kWaitNs, a.err);
