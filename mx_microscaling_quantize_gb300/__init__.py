@@ -138,6 +138,24 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _as_stream(stream, device) -> torch.cuda.Stream:
+    """`stream` (a torch.cuda.Stream or a raw handle) as a stream that torch can allocate under."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    # the handle 1 names the default stream, as 0 does; torch knows it by 0 only
+    return torch.cuda.ExternalStream(0 if stream == 1 else stream, device)
+
+
+def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """Device memory for one call on `stream`, taken from that stream's pool: a block of another
+    stream's may still be in use by what is queued there, and so would this one be when the pool hands
+    it on."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(_as_stream(stream, like.device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def _input(x: torch.Tensor, name: str = "x") -> tuple[int, int]:
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype == torch.bfloat16):
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
@@ -527,12 +545,8 @@ def mx_route_plan(experts, E: int, *, row_offsets=None, tokens=None, slots=None,
     tokens = _output(tokens, "tokens", (T * k,), torch.int32, experts)
     slots = _output(slots, "slots", (T, k), torch.int32, experts)
     if workspace is None:
-        # the caching allocator hands memory out per stream: allocated for the stream it is used on
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=experts.device)
-            if stream is not None:
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                        torch.cuda.ExternalStream(stream, experts.device))
+            workspace = _scratch(need, experts, stream)
     elif workspace.device != experts.device or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must have {need} bytes on {experts.device}")
