@@ -146,14 +146,18 @@ def _as_stream(stream, device) -> torch.cuda.Stream:
     return torch.cuda.ExternalStream(0 if stream == 1 else stream, device)
 
 
-def _scratch(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
-    """Device memory for one call on `stream`, taken from that stream's pool: a block of another
-    stream's may still be in use by what is queued there, and so would this one be when the pool hands
-    it on."""
+def _empty(shape, dtype, like: torch.Tensor, stream, scratch: bool = False) -> torch.Tensor:
+    """Device memory for a call on `stream`, taken from that stream's pool: a block of another stream's
+    may still be in use by what is queued there. The current stream, where a caller goes on with an
+    output, is recorded: the block is not handed on before what is queued there by the time it is freed.
+    A call's own scratch memory is used on `stream` alone."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(_as_stream(stream, like.device)):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if not scratch:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
 def _input(x: torch.Tensor, name: str = "x") -> tuple[int, int]:
@@ -176,17 +180,18 @@ def code_bytes_per_row(fmt: int, K: int) -> int:
     return K if fmt == E4M3 else K // 2
 
 
-def _codes_out(codes, x, M, K, fmt):
+def _codes_out(codes, x, M, K, fmt, stream):
     if codes is None:
-        return torch.empty((M, code_bytes_per_row(fmt, K)), dtype=torch.uint8, device=x.device)
+        return _empty((M, code_bytes_per_row(fmt, K)), torch.uint8, x, stream)
     if codes.numel() * codes.element_size() != M * code_bytes_per_row(fmt, K):
         raise ValueError("codes has the wrong size")
     return codes
 
 
-def _scales_out(scales, x, rows, cols):
+def _scales_out(scales, x, shape, stream):
+    rows, cols = shape
     if scales is None:
-        return torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+        return _empty((rows, cols), torch.uint8, x, stream)
     if scales.numel() * scales.element_size() != rows * cols:
         raise ValueError("scales has the wrong size")
     return scales
@@ -212,8 +217,8 @@ def mx_quantize(x, fmt, layout=LINEAR, *, codes=None, scales=None, group=GROUP, 
                 stream=None):
     """Block quantize bf16 [M, K] -> (codes uint8, E8M0 scales uint8)."""
     M, K = _input(x)
-    codes = _codes_out(codes, x, M, K, fmt)
-    scales = _scales_out(scales, x, *mx_scales_shape(M, K, layout, group))
+    codes = _codes_out(codes, x, M, K, fmt, stream)
+    scales = _scales_out(scales, x, mx_scales_shape(M, K, layout, group), stream)
     _check(lib().mx_quantize(_ptr(x), M, K, fmt, group, layout, rounding, _ptr(codes),
                              _ptr(scales), _stream_ptr(stream, x)))
     return codes, scales
@@ -226,7 +231,7 @@ def mx_qdq(x, fmt, H=None, *, y=None, group=GROUP, rounding=RNE, rot_kind=ROT_DE
     M, K = _input(x)
     g = _rotation(H) if H is not None else 0
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x, stream)
     _check(lib().mx_qdq(_ptr(x), M, K, fmt, group, rounding, _ptr(H), g, rot_kind, _ptr(y),
                         _stream_ptr(stream, x)))
     return y
@@ -237,8 +242,8 @@ def mx_rotate_quantize(x, H, fmt, layout=SWIZZLED, *, codes=None, scales=None, g
     """Rotate each g-chunk by H, then block quantize -> (codes, scales)."""
     M, K = _input(x)
     g = _rotation(H)
-    codes = _codes_out(codes, x, M, K, fmt)
-    scales = _scales_out(scales, x, *mx_scales_shape(M, K, layout, group))
+    codes = _codes_out(codes, x, M, K, fmt, stream)
+    scales = _scales_out(scales, x, mx_scales_shape(M, K, layout, group), stream)
     _check(lib().mx_rotate_quantize(_ptr(x), M, K, _ptr(H), g, rot_kind, fmt, group, layout,
                                     rounding, _ptr(codes), _ptr(scales), _stream_ptr(stream, x)))
     return codes, scales
@@ -252,8 +257,8 @@ def mx_quantize_grouped(x, row_offsets, fmt, layout=SWIZZLED, *, codes=None, sca
             and row_offsets.is_contiguous()):
         raise TypeError("row_offsets must be a contiguous CUDA int64 [E + 1] tensor")
     E = row_offsets.numel() - 1
-    codes = _codes_out(codes, x, M, K, fmt)
-    scales = _scales_out(scales, x, *mx_grouped_scales_shape(M, E, K, layout, group))
+    codes = _codes_out(codes, x, M, K, fmt, stream)
+    scales = _scales_out(scales, x, mx_grouped_scales_shape(M, E, K, layout, group), stream)
     _check(lib().mx_quantize_grouped(_ptr(x), _ptr(row_offsets), E, M, K, fmt, group, layout,
                                      rounding, _ptr(codes), _ptr(scales), _stream_ptr(stream, x)))
     return codes, scales
@@ -274,7 +279,7 @@ def mx_dequantize(codes, scales, K, fmt, layout=LINEAR, *, y=None, group=GROUP, 
     if scales.numel() != rows * cols:
         raise ValueError("scales has the wrong size")
     if y is None:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
+        y = _empty((M, K), torch.bfloat16, codes, stream)
     elif not (y.is_cuda and y.dtype == torch.bfloat16 and y.numel() == M * K
               and y.is_contiguous()):
         raise ValueError("y must be a contiguous CUDA bfloat16 tensor of M * K elements")
@@ -302,8 +307,8 @@ def mx_quantize_nvfp4(x, global_scale, layout=SWIZZLED, H=None, *, codes=None, s
     M, K = _input(x)
     _global_scale(global_scale)
     g = _rotation(H) if H is not None else 0
-    codes = _codes_out(codes, x, M, K, E2M1)
-    scales = _scales_out(scales, x, *mx_nvfp4_scales_shape(M, K, layout))
+    codes = _codes_out(codes, x, M, K, E2M1, stream)
+    scales = _scales_out(scales, x, mx_nvfp4_scales_shape(M, K, layout), stream)
     _check(lib().mx_quantize_nvfp4(_ptr(x), M, K, _ptr(H), g, rot_kind, _ptr(global_scale),
                                    layout, _ptr(codes), _ptr(scales), _stream_ptr(stream, x)))
     return codes, scales
@@ -315,7 +320,7 @@ def mx_qdq_nvfp4(x, global_scale, H=None, *, y=None, rot_kind=ROT_DENSE, stream=
     _global_scale(global_scale)
     g = _rotation(H) if H is not None else 0
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty(x.shape, x.dtype, x, stream)
     _check(lib().mx_qdq_nvfp4(_ptr(x), M, K, _ptr(H), g, rot_kind, _ptr(global_scale), _ptr(y),
                               _stream_ptr(stream, x)))
     return y
@@ -342,8 +347,8 @@ def mx_quantize_nvfp4_grouped(x, row_offsets, global_scales, layout=SWIZZLED, *,
             and global_scales.dtype == torch.float32 and global_scales.numel() == E
             and global_scales.is_contiguous()):
         raise TypeError("global_scales must be a contiguous CUDA float32 tensor of E elements")
-    codes = _codes_out(codes, x, M, K, E2M1)
-    scales = _scales_out(scales, x, *mx_nvfp4_grouped_scales_shape(M, E, K, layout))
+    codes = _codes_out(codes, x, M, K, E2M1, stream)
+    scales = _scales_out(scales, x, mx_nvfp4_grouped_scales_shape(M, E, K, layout), stream)
     _check(lib().mx_quantize_nvfp4_grouped(_ptr(x), _ptr(row_offsets), E, M, K,
                                            _ptr(global_scales), layout, _ptr(codes),
                                            _ptr(scales), _stream_ptr(stream, x)))
@@ -367,7 +372,7 @@ def mx_dequantize_nvfp4(codes, scales, K, global_scale, layout=SWIZZLED, *, y=No
     if scales.numel() != rows * cols:
         raise ValueError("scales has the wrong size")
     if y is None:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
+        y = _empty((M, K), torch.bfloat16, codes, stream)
     elif not (y.is_cuda and y.dtype == torch.bfloat16 and y.numel() == M * K
               and y.is_contiguous()):
         raise ValueError("y must be a contiguous CUDA bfloat16 tensor of M * K elements")
@@ -381,7 +386,7 @@ def mx_rotate_debug(x, H, *, y=None, rot_kind=ROT_DENSE, stream=None):
     M, K = _input(x)
     g = _rotation(H)
     if y is None:
-        y = torch.empty((M, K), dtype=torch.float32, device=x.device)
+        y = _empty((M, K), torch.float32, x, stream)
     _check(lib().mx_rotate_debug(_ptr(x), M, K, _ptr(H), g, rot_kind, _ptr(y),
                                  _stream_ptr(stream, x)))
     return y
@@ -412,14 +417,14 @@ def mx_selftest_rotate_give_up(x, H, limit_ns: int, *, stream=None):
     mx_device_errors()). Returns the (unspecified) codes and scales buffers."""
     M, K = _input(x)
     g = _rotation(H)
-    codes = _codes_out(None, x, M, K, E2M1)
-    scales = _scales_out(None, x, *mx_scales_shape(M, K, SWIZZLED))
+    codes = _codes_out(None, x, M, K, E2M1, stream)
+    scales = _scales_out(None, x, mx_scales_shape(M, K, SWIZZLED), stream)
     _check(lib().mx_selftest_rotate_give_up(_ptr(x), M, K, _ptr(H), g, _ptr(codes), _ptr(scales),
                                             limit_ns, _stream_ptr(stream, x)))
     return codes, scales
 
 
-def _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, c):
+def _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, c, stream):
     for t in (a_codes, a_scales, b_codes, b_scales):
         if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.uint8
                 and t.is_contiguous()):
@@ -429,7 +434,7 @@ def _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, c):
             b_codes.numel() != N * code_bytes_per_row(fmt, K):
         raise ValueError("codes do not match K and the format")
     if c is None:
-        c = torch.empty((M, N), dtype=torch.bfloat16, device=a_codes.device)
+        c = _empty((M, N), torch.bfloat16, a_codes, stream)
     return M, N, c
 
 
@@ -438,7 +443,7 @@ def mx_selftest_gemm_give_up(a_codes, a_scales, b_codes, b_scales, K: int, fmt, 
     """mx_gemm with every pipeline wait of the kernel limited to limit_ns: the kernel stops
     issuing work, drains what is in flight and returns; the device error word reports it.
     Returns the (unspecified) C buffer."""
-    M, N, c = _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, None)
+    M, N, c = _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, None, stream)
     _check(lib().mx_selftest_gemm_give_up(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
                                           _ptr(b_scales), M, N, K, fmt, layout, _ptr(c), limit_ns,
                                           _stream_ptr(stream, a_codes)))
@@ -449,7 +454,7 @@ def mx_gemm(a_codes, a_scales, b_codes, b_scales, K: int, fmt, layout=SWIZZLED, 
             *, c=None, group=GROUP, stream=None):
     """C[M, N] = alpha * dequant(A) @ dequant(B)^T (bf16) from MX codes and E8M0 scales as
     mx_quantize returns them (A: [M, K/2 or K] codes, B: [N, ...])."""
-    M, N, c = _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, c)
+    M, N, c = _gemm_operands(a_codes, a_scales, b_codes, b_scales, K, fmt, c, stream)
     _check(lib().mx_gemm(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N, K,
                          fmt, group, layout, alpha, _ptr(c), _stream_ptr(stream, a_codes)))
     return c
@@ -480,10 +485,10 @@ def _tensor(t, name, dtype, *, dim=None, like=None) -> torch.Tensor:
     return t
 
 
-def _output(t, name, shape, dtype, like) -> torch.Tensor:
+def _output(t, name, shape, dtype, like, stream) -> torch.Tensor:
     """t checked against shape, or a new tensor of it on like's device."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype, like, stream)
     _tensor(t, name, dtype, like=like)
     n = 1
     for d in shape:
@@ -501,8 +506,8 @@ def mx_route(logits, k: int, score=SOFTMAX, bias=None, *, groups: int = 1, top_g
     T, E = logits.shape
     if bias is not None and _tensor(bias, "bias", torch.float32, like=logits).numel() != E:
         raise ValueError("bias must have one value per expert")
-    experts = _output(experts, "experts", (T, k), torch.int32, logits)
-    weights = _output(weights, "weights", (T, k), torch.float32, logits)
+    experts = _output(experts, "experts", (T, k), torch.int32, logits, stream)
+    weights = _output(weights, "weights", (T, k), torch.float32, logits, stream)
     _check(lib().mx_route(_ptr(logits), _TYPES[logits.dtype], _ptr(bias), T, E, k, score, groups,
                           top_groups, int(renormalize), scale, _ptr(experts), _ptr(weights),
                           _stream_ptr(stream, logits)))
@@ -519,7 +524,7 @@ def mx_route_backward(grad_weights, logits, experts, score=SOFTMAX, *, renormali
     k = experts.shape[1]
     if experts.shape[0] != T or grad_weights.shape != experts.shape:
         raise ValueError("experts and grad_weights must be [T, k]")
-    grad_logits = _output(grad_logits, "grad_logits", (T, E), logits.dtype, logits)
+    grad_logits = _output(grad_logits, "grad_logits", (T, E), logits.dtype, logits, stream)
     _check(lib().mx_route_backward(_ptr(grad_weights), _ptr(logits), _TYPES[logits.dtype],
                                    _ptr(experts), T, E, k, score, int(renormalize), scale,
                                    _ptr(grad_logits), _stream_ptr(stream, logits)))
@@ -541,12 +546,12 @@ def mx_route_plan(experts, E: int, *, row_offsets=None, tokens=None, slots=None,
     _tensor(experts, "experts", torch.int32, dim=2)
     T, k = experts.shape
     need = mx_route_plan_workspace(T, k, E)
-    row_offsets = _output(row_offsets, "row_offsets", (E + 1,), torch.int64, experts)
-    tokens = _output(tokens, "tokens", (T * k,), torch.int32, experts)
-    slots = _output(slots, "slots", (T, k), torch.int32, experts)
+    row_offsets = _output(row_offsets, "row_offsets", (E + 1,), torch.int64, experts, stream)
+    tokens = _output(tokens, "tokens", (T * k,), torch.int32, experts, stream)
+    slots = _output(slots, "slots", (T, k), torch.int32, experts, stream)
     if workspace is None:
         if need:
-            workspace = _scratch(need, experts, stream)
+            workspace = _empty((need,), torch.uint8, experts, stream, scratch=True)
     elif workspace.device != experts.device or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must have {need} bytes on {experts.device}")
@@ -581,8 +586,8 @@ def mx_quantize_b128_rows(x, index=None, *, codes=None, scales=None, stream=None
     [ceil(K / 128), R]), one scale per 128 elements of a row."""
     M, K = _input(x)
     R = _row_index(index, x, M)
-    codes = _output(codes, "codes", (R, K), torch.uint8, x)
-    scales = _output(scales, "scales", (-(-K // BLOCK128), R), torch.float32, x)
+    codes = _output(codes, "codes", (R, K), torch.uint8, x, stream)
+    scales = _output(scales, "scales", (-(-K // BLOCK128), R), torch.float32, x, stream)
     _check(lib().mx_quantize_b128_rows(_ptr(x), M, K, _ptr(index), R, _ptr(codes), _ptr(scales),
                                        _stream_ptr(stream, x)))
     return codes, scales
@@ -595,8 +600,8 @@ def mx_quantize_b128_cols(x, index=None, row_offsets=None, *, codes=None, scales
     R = _row_index(index, x, M)
     E = 1 if row_offsets is None else _offsets(row_offsets, x)
     P = mx_b128_padded_rows(R, E)
-    codes = _output(codes, "codes", (K, P), torch.uint8, x)
-    scales = _output(scales, "scales", (P // BLOCK128, K), torch.float32, x)
+    codes = _output(codes, "codes", (K, P), torch.uint8, x, stream)
+    scales = _output(scales, "scales", (P // BLOCK128, K), torch.float32, x, stream)
     _check(lib().mx_quantize_b128_cols(_ptr(x), M, K, _ptr(index), R, _ptr(row_offsets), E,
                                        _ptr(codes), _ptr(scales), _stream_ptr(stream, x)))
     return codes, scales
@@ -609,11 +614,11 @@ def mx_quantize_b128_blocks(x, *, transpose: bool = False, codes=None, scales=No
     _tensor(x, "x", torch.bfloat16, dim=(2, 3))
     lead, (M, K) = tuple(x.shape[:-2]), x.shape[-2:]
     mb, kb = -(-M // BLOCK128), -(-K // BLOCK128)
-    codes = _output(codes, "codes", (*lead, M, K), torch.uint8, x)
-    scales = _output(scales, "scales", (*lead, mb, kb), torch.float32, x)
+    codes = _output(codes, "codes", (*lead, M, K), torch.uint8, x, stream)
+    scales = _output(scales, "scales", (*lead, mb, kb), torch.float32, x, stream)
     if transpose:
-        codes_t = _output(codes_t, "codes_t", (*lead, K, M), torch.uint8, x)
-        scales_t = _output(scales_t, "scales_t", (*lead, kb, mb), torch.float32, x)
+        codes_t = _output(codes_t, "codes_t", (*lead, K, M), torch.uint8, x, stream)
+        scales_t = _output(scales_t, "scales_t", (*lead, kb, mb), torch.float32, x, stream)
     else:
         codes_t = scales_t = None
     _check(lib().mx_quantize_b128_blocks(_ptr(x), lead[0] if lead else 1, M, K, _ptr(codes),
@@ -656,7 +661,7 @@ def mx_gemm_b128(a_codes, a_scales, b_codes, b_scales, b_form=B128_BLOCKS, *,
     rows form, B's in the blocks form or (B128_ROWS) the rows form."""
     M, N, K = _b128_dense(a_codes, a_scales, b_codes, b_scales, b_form)
     dtype = _out_type(out_dtype, c)
-    c = _output(c, "c", (M, N), dtype, a_codes)
+    c = _output(c, "c", (M, N), dtype, a_codes, stream)
     _check(lib().mx_gemm_b128(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), M, N, K,
                               b_form, _TYPES[dtype], _ptr(c), _stream_ptr(stream, a_codes)))
     return c
@@ -667,7 +672,7 @@ def mx_selftest_gemm_b128_give_up(a_codes, a_scales, b_codes, b_scales, limit_ns
     """mx_gemm_b128 with every pipeline wait of the kernel limited to limit_ns; returns the
     (unspecified) C buffer. The device error word reports the give-up."""
     M, N, K = _b128_dense(a_codes, a_scales, b_codes, b_scales, b_form)
-    c = _output(None, "c", (M, N), torch.bfloat16, a_codes)
+    c = _output(None, "c", (M, N), torch.bfloat16, a_codes, stream)
     _check(lib().mx_selftest_gemm_b128_give_up(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
                                                _ptr(b_scales), M, N, K, b_form, _ptr(c), limit_ns,
                                                _stream_ptr(stream, a_codes)))
@@ -684,7 +689,7 @@ def mx_gemm_b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, *,
     if experts != E or K != Kb:
         raise ValueError("a_codes and b_codes must be [R, K] and [E, N, K]")
     dtype = _out_type(out_dtype, c)
-    c = _output(c, "c", (R, N), dtype, a_codes)
+    c = _output(c, "c", (R, N), dtype, a_codes, stream)
     _check(lib().mx_gemm_b128_grouped(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
                                       _ptr(row_offsets), E, R, N, K, _TYPES[dtype], _ptr(c),
                                       _stream_ptr(stream, a_codes)))
@@ -701,7 +706,7 @@ def mx_gemm_b128_grouped_wgrad(a_codes, a_scales, b_codes, b_scales, row_offsets
     if P != Pb:
         raise ValueError("a_codes and b_codes must be [M, P] and [N, P]")
     dtype = _out_type(out_dtype, c)
-    c = _output(c, "c", (E, M, N), dtype, a_codes)
+    c = _output(c, "c", (E, M, N), dtype, a_codes, stream)
     _check(lib().mx_gemm_b128_grouped_wgrad(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes),
                                             _ptr(b_scales), _ptr(row_offsets), E, M, N, P,
                                             _TYPES[dtype], _ptr(c), _stream_ptr(stream, a_codes)))
@@ -721,7 +726,7 @@ def mx_combine(y, slots, weights=None, *, out=None, stream=None):
     """out[t] = sum_j weights[t, j] * y[slots[t, j]]: bf16 rows [R, N] -> [T, N] (weights None: ones)."""
     T, k = _slots(y, slots, weights)
     R, N = y.shape
-    out = _output(out, "out", (T, N), torch.bfloat16, y)
+    out = _output(out, "out", (T, N), torch.bfloat16, y, stream)
     _check(lib().mx_combine(_ptr(y), _ptr(slots), _ptr(weights), T, k, R, N, _ptr(out),
                             _stream_ptr(stream, y)))
     return out
@@ -733,8 +738,8 @@ def mx_combine_backward(dout, y, slots, weights, *, dy=None, dweights=None, stre
     R, N = y.shape
     if _tensor(dout, "dout", torch.bfloat16, dim=2, like=y).shape != (T, N):
         raise ValueError("dout must be [T, N]")
-    dy = _output(dy, "dy", (R, N), torch.bfloat16, y)
-    dweights = _output(dweights, "dweights", (T, k), torch.float32, y)
+    dy = _output(dy, "dy", (R, N), torch.bfloat16, y, stream)
+    dweights = _output(dweights, "dweights", (T, k), torch.float32, y, stream)
     _check(lib().mx_combine_backward(_ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, R, N,
                                      _ptr(dy), _ptr(dweights), _stream_ptr(stream, y)))
     return dy, dweights

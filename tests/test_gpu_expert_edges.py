@@ -71,3 +71,69 @@ def test_pairs_of_few_steps_one_after_another(K):
             for _ in range(100)]
     for c2, w2 in outs:
         assert torch.equal(c2, c) and torch.equal(w2, w)
+
+
+# ---------------------------------------------------------------------------------------------
+# streams that nothing orders after one another
+# ---------------------------------------------------------------------------------------------
+def test_plans_on_two_streams_at_once():
+    """Each stream's workspaces are its own, whatever the other has queued."""
+    rng = np.random.default_rng(3)
+    cases = []
+    for T in (700, 9001):
+        experts = rng.integers(-1, 64, (T, 4)).astype(np.int32)
+        cases.append((torch.from_numpy(experts).cuda(), R.plan(experts, 64)))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for i in range(60):
+        if i % 10 == 0:
+            torch.cuda._sleep(200_000)  # the current stream falls behind
+        for j, (experts, _) in enumerate(cases):
+            got.append((j, mxq.mx_route_plan(experts, 64)))
+            got.append((j, mxq.mx_route_plan(experts, 64, stream=side if i % 2 else side.cuda_stream)))
+    torch.cuda.synchronize()
+    for j, plan in got:
+        for g, w in zip(plan, cases[j][1]):
+            assert (cpu(g) == w).all()
+
+
+def test_outputs_of_another_stream_are_not_memory_still_in_use():
+    """The current stream has writes queued into blocks that were given back: outputs of a call on
+    another stream, which runs at once, are not among them. Nor does the other stream take an output
+    back while the current stream still reads it."""
+    rng = np.random.default_rng(4)
+    x = bf16_inputs(rng, 640, 512, False)
+    logits = torch.from_numpy(rng.standard_normal((640, 16))).float().cuda()
+
+    def work(**at):
+        experts, weights = mxq.mx_route(logits, 2, **at)
+        offsets, tokens, slots = mxq.mx_route_plan(experts, 16, **at)
+        codes, scales = mxq.mx_quantize_b128_rows(x, tokens, **at)
+        return [experts, weights, offsets, tokens, slots, codes, scales,
+                *mxq.mx_quantize(x, mxq.E4M3, **at), mxq.mx_combine(x, slots, weights, **at)]
+
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in work()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(20_000_000)  # the current stream is busy for some milliseconds
+        junk = [torch.empty_like(t) for t in want]
+        for t in junk:
+            t.view(torch.uint8).fill_(0x33)
+        del junk, t
+        got = work(stream=side)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+        torch.cuda._sleep(20_000_000)
+        kept = [g.clone() for g in got]  # queued behind the pause
+        del got, g
+        work(stream=side)                # would take the blocks that the copies are yet to read
+        side.synchronize()
+        with torch.cuda.stream(side):
+            for t in [torch.empty_like(t) for t in want]:
+                t.view(torch.uint8).fill_(0x44)
+        torch.cuda.synchronize()
+        for g, w in zip(kept, want):
+            assert torch.equal(g, w)

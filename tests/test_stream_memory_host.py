@@ -56,11 +56,10 @@ def noted(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: state["recorded"].append(s))
     monkeypatch.setattr(mxq, "_lib", Library())
     monkeypatch.setattr(mxq, "_raw_stream", lambda device: 0)
-    for cached in (mxq.mx_route_plan_workspace, mxq.mx_b128_padded_rows):
-        cached.cache_clear()
+    sizes = mxq.mx_route_plan_workspace  # remembers what the library answered
+    sizes.cache_clear()
     yield state
-    for cached in (mxq.mx_route_plan_workspace, mxq.mx_b128_padded_rows):
-        cached.cache_clear()
+    sizes.cache_clear()
 
 
 def test_the_plans_workspace_is_of_the_stream_it_is_used_on(noted):
@@ -73,3 +72,68 @@ def test_the_plans_workspace_is_of_the_stream_it_is_used_on(noted):
     assert noted["taken"][1:] == [("current", 4096)]
     mxq.mx_route_plan(experts, 8, **out, stream=1)  # the default stream's other handle
     assert noted["taken"][2:] == [(0, 4096)]
+
+
+def calls():
+    """(name, a call with every output left to the binding)."""
+    bf16, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    x, H, gs = on_device(128, 256, dtype=bf16), on_device(32, 32, dtype=bf16), on_device(1)
+    codes, scales = on_device(128, 256, dtype=u8), on_device(128, 8, dtype=u8)
+    offsets = on_device(2, dtype=torch.int64)
+    logits, experts, weights = on_device(16, 8), on_device(16, 2, dtype=i32), on_device(16, 2)
+    rows = codes, on_device(2, 128)  # scales [K / 128, rows]
+    blocks = codes, on_device(1, 2)
+    y, slots = on_device(32, 256, dtype=bf16), on_device(16, 2, dtype=i32)
+    dout = on_device(16, 256, dtype=bf16)
+    return [
+        ("quantize", lambda **s: mxq.mx_quantize(x, mxq.E4M3, **s)),
+        ("qdq", lambda **s: mxq.mx_qdq(x, mxq.E4M3, **s)),
+        ("rotate_quantize", lambda **s: mxq.mx_rotate_quantize(x, H, mxq.E4M3, **s)),
+        ("quantize_grouped", lambda **s: mxq.mx_quantize_grouped(x, offsets, mxq.E4M3, **s)),
+        ("dequantize", lambda **s: mxq.mx_dequantize(codes, scales, 256, mxq.E4M3, **s)),
+        ("quantize_nvfp4", lambda **s: mxq.mx_quantize_nvfp4(x, gs, **s)),
+        ("qdq_nvfp4", lambda **s: mxq.mx_qdq_nvfp4(x, gs, **s)),
+        ("quantize_nvfp4_grouped", lambda **s: mxq.mx_quantize_nvfp4_grouped(x, offsets, gs, **s)),
+        ("dequantize_nvfp4", lambda **s: mxq.mx_dequantize_nvfp4(
+            on_device(128, 128, dtype=u8), on_device(128, 16, dtype=u8), 256, gs, **s)),
+        ("rotate_debug", lambda **s: mxq.mx_rotate_debug(x, H, **s)),
+        ("gemm", lambda **s: mxq.mx_gemm(codes, scales, codes, scales, 256, mxq.E4M3, **s)),
+        ("route", lambda **s: mxq.mx_route(logits, 2, **s)),
+        ("route_backward", lambda **s: mxq.mx_route_backward(weights, logits, experts, **s)),
+        ("route_plan", lambda **s: mxq.mx_route_plan(experts, 8, **s)),
+        ("b128_rows", lambda **s: mxq.mx_quantize_b128_rows(x, **s)),
+        ("b128_cols", lambda **s: mxq.mx_quantize_b128_cols(x, **s)),
+        ("b128_blocks", lambda **s: mxq.mx_quantize_b128_blocks(x, transpose=True, **s)),
+        ("gemm_b128", lambda **s: mxq.mx_gemm_b128(*rows, *blocks, **s)),
+        ("gemm_b128_grouped", lambda **s: mxq.mx_gemm_b128_grouped(
+            *rows, blocks[0][None], blocks[1][None], offsets, **s)),
+        ("gemm_b128_grouped_wgrad", lambda **s: mxq.mx_gemm_b128_grouped_wgrad(
+            *rows, *rows, offsets, **s)),
+        ("combine", lambda **s: mxq.mx_combine(y, slots, **s)),
+        ("combine_backward", lambda **s: mxq.mx_combine_backward(dout, y, slots, weights, **s)),
+    ]
+
+
+# shapes whose queries the accepting library answers with nothing are asked of these
+SHAPES = {"mx_scales_shape": (128, 8), "mx_grouped_scales_shape": (128, 8),
+          "mx_nvfp4_scales_shape": (128, 16), "mx_nvfp4_grouped_scales_shape": (128, 16),
+          "mx_b128_padded_rows": 128}
+
+
+@pytest.mark.parametrize("i", range(22))
+def test_outputs_are_of_the_stream_they_are_written_on(noted, monkeypatch, i):
+    for query, shape in SHAPES.items():
+        monkeypatch.setattr(mxq, query, lambda *a, shape=shape, **k: shape)
+    every = calls()
+    assert len(every) == 22
+    name, call = every[i]
+    noted["taken"].clear()
+    call(stream=SIDE)
+    taken = noted["taken"]
+    assert taken and all(stream == SIDE for stream, _ in taken), name
+    # the caller's stream is recorded on each output (a workspace is not the caller's)
+    outputs = len(taken) - (name == "route_plan")
+    assert noted["recorded"] == ["current"] * outputs
+    noted["taken"].clear()
+    call()
+    assert [stream for stream, _ in noted["taken"]] == ["current"] * len(taken)
