@@ -414,6 +414,8 @@ mx_status mx_gemm_b128_grouped_wgrad(const void* a_codes, const float* a_scales,
  * Backward: dy[slots[t, j]] = weights[t, j] * dout[t] (rows of dy that no slot names are not
  * written; every row may be named once), dweights[t, j] = <dout[t], y[slots[t, j]]> (fp32, 0 for a
  * slot that is none). dweights NULL: not wanted, y is then not read.
+ * mx_combine_backward_whole also writes the rows of dy that no slot names: zeros, their gradient.
+ * workspace: device memory of 4 * R bytes, 4-byte aligned.
  */
 mx_status mx_combine(const void* y, const int32_t* slots, const float* weights, int64_t T, int k,
                      int64_t R, int64_t N, void* out, void* stream);
@@ -421,6 +423,10 @@ mx_status mx_combine(const void* y, const int32_t* slots, const float* weights, 
 mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* slots,
                               const float* weights, int64_t T, int k, int64_t R, int64_t N,
                               void* dy, float* dweights, void* stream);
+
+mx_status mx_combine_backward_whole(const void* dout, const void* y, const int32_t* slots,
+                                    const float* weights, int64_t T, int k, int64_t R, int64_t N,
+                                    void* dy, float* dweights, void* workspace, void* stream);
 
 /*
  * Diagnostics: the rotated values y = x_chunk * H exactly as mx_rotate_quantize computes them

@@ -44,6 +44,7 @@ EXPORTS = (
     "mx_route_plan", "mx_b128_padded_rows", "mx_quantize_b128_rows", "mx_quantize_b128_cols",
     "mx_quantize_b128_blocks", "mx_gemm_b128", "mx_gemm_b128_grouped",
     "mx_gemm_b128_grouped_wgrad", "mx_combine", "mx_combine_backward",
+    "mx_combine_backward_whole",
     "mx_selftest_gemm_b128_give_up",
 )
 
@@ -100,6 +101,7 @@ def lib() -> ctypes.CDLL:
         "mx_gemm_b128_grouped_wgrad": (i32, [p, p, p, p, p, i32, i64, i64, i64, i32, p, p]),
         "mx_combine": (i32, [p, p, p, i64, i32, i64, i64, p, p]),
         "mx_combine_backward": (i32, [p, p, p, p, i64, i32, i64, i64, p, p, p]),
+        "mx_combine_backward_whole": (i32, [p, p, p, p, i64, i32, i64, i64, p, p, p, p]),
         "mx_selftest_gemm_b128_give_up": (i32, [p, p, p, p, i64, i64, i64, i32, p, i64, p]),
     }
     for name, (res, args) in sigs.items():
@@ -733,13 +735,21 @@ def mx_combine(y, slots, weights=None, *, out=None, stream=None):
 
 
 def mx_combine_backward(dout, y, slots, weights, *, dy=None, dweights=None, stream=None):
-    """Gradients of mx_combine: dout [T, N] -> (dy [R, N], dweights [T, k])."""
+    """Gradients of mx_combine: dout [T, N] -> (dy [R, N], dweights [T, k]). Rows of dy that no slot names
+    are zeros; in a dy that is passed they keep what they held."""
     T, k = _slots(y, slots, weights)
     R, N = y.shape
     if _tensor(dout, "dout", torch.bfloat16, dim=2, like=y).shape != (T, N):
         raise ValueError("dout must be [T, N]")
-    dy = _output(dy, "dy", (R, N), torch.bfloat16, y, stream)
     dweights = _output(dweights, "dweights", (T, k), torch.float32, y, stream)
-    _check(lib().mx_combine_backward(_ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, R, N,
-                                     _ptr(dy), _ptr(dweights), _stream_ptr(stream, y)))
+    if dy is None:
+        dy = _empty((R, N), torch.bfloat16, y, stream)
+        workspace = _empty((R,), torch.int32, y, stream, scratch=True)
+        _check(lib().mx_combine_backward_whole(_ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, R,
+                                               N, _ptr(dy), _ptr(dweights), _ptr(workspace),
+                                               _stream_ptr(stream, y)))
+    else:
+        _output(dy, "dy", (R, N), torch.bfloat16, y, stream)
+        _check(lib().mx_combine_backward(_ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, R, N,
+                                         _ptr(dy), _ptr(dweights), _stream_ptr(stream, y)))
     return dy, dweights

@@ -7,6 +7,11 @@
 // thread), every output row written once. The backward walks tokens, not rows, so that dout is
 // read once and not k times. 16384 tokens with 8 rows of 2048 each: 97 us (6.2 TB/s), the gradients
 // 190 us (6.0 TB/s).
+//
+// Rows of dy that no slot names have a gradient of zero. Which these are, the walk over tokens does not
+// see: it leaves the number of the choice at its row's place in a workspace, and a second kernel takes a
+// row for named where the choice noted there does name it, which needs no workspace cleared before. That
+// costs a launch and the reads of the workspace and the choices (131072 rows, none of them zeroed: 2.5 us).
 #include "mx_device.cuh"
 #include "mx_expert.h"
 #include "mx_launch.h"
@@ -96,6 +101,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(Combi
       if (row[u] >= a.R) row[u] = -1;
       w[u] = row[u] >= 0 && a.weights ? a.weights[t * a.k + j] : 1.0f;
       dot[u] = 0.0f;
+      if (a.owner && tid == 0 && row[u] >= 0) a.owner[row[u]] = (int32_t)(t * a.k + j);
     }
     for (int64_t c = tid; c < chunks; c += kCombineThreads) {
       uint32_t d[4], v[KU][4];
@@ -145,6 +151,27 @@ __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(Combi
   }
 }
 
+// Zeros to the rows of dy whose owner is no choice that names them. A warp looks at 32 rows.
+__global__ void __launch_bounds__(kCombineThreads) zero_unnamed_kernel(CombineArgs a, int64_t chunks) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = ((int64_t)blockIdx.x * kCombineThreads + threadIdx.x) - lane;
+  const int64_t n = a.T * a.k, r = r0 + lane;
+  bool named = true;
+  if (r < a.R) {
+    const int32_t o = load_s32(a.owner + r);
+    named = o >= 0 && o < n && load_s32(a.slots + o) == r;
+  }
+  uint32_t left = __ballot_sync(0xFFFFFFFFu, !named);
+  const uint32_t zeros[4] = {0u, 0u, 0u, 0u};
+  while (left) {
+    uint16_t* row = static_cast<uint16_t*>(a.dy) + (r0 + __ffs(left) - 1) * a.N;
+    for (int64_t c = lane; c < chunks; c += 32) store4(row + c * 8, zeros);
+    left &= left - 1u;
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
@@ -162,14 +189,18 @@ cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_combine_backward(const CombineArgs& a, cudaStream_t stream) {
   const int64_t chunks = a.N / 8;
-  const dim3 grid((unsigned)a.T);
-  if (a.k <= 2) {
-    return launch_pdl(&combine_backward_kernel<2>, grid, dim3(kCombineThreads), 0, stream, a, chunks);
+  const dim3 grid((unsigned)a.T), block(kCombineThreads);
+  if (a.T > 0) {
+    const cudaError_t err =
+        a.k <= 2   ? launch_pdl(&combine_backward_kernel<2>, grid, block, 0, stream, a, chunks)
+        : a.k <= 4 ? launch_pdl(&combine_backward_kernel<4>, grid, block, 0, stream, a, chunks)
+                   : launch_pdl(&combine_backward_kernel<8>, grid, block, 0, stream, a, chunks);
+    if (err != cudaSuccess) return err;
   }
-  if (a.k <= 4) {
-    return launch_pdl(&combine_backward_kernel<4>, grid, dim3(kCombineThreads), 0, stream, a, chunks);
-  }
-  return launch_pdl(&combine_backward_kernel<8>, grid, dim3(kCombineThreads), 0, stream, a, chunks);
+  if (!a.owner || a.R == 0 || a.N == 0) return cudaSuccess;
+  return launch_pdl(&zero_unnamed_kernel,
+                    dim3((unsigned)((a.R + kCombineThreads - 1) / kCombineThreads)), block, 0, stream, a,
+                    chunks);
 }
 
 }  // namespace mxq

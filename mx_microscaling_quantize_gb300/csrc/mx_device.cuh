@@ -317,6 +317,12 @@ __device__ __forceinline__ uint32_t load_u8(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ int32_t load_s32(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ int64_t load_s64(const int64_t* p) {
   int64_t v;
   asm volatile("ld.global.s64 %0, [%1];" : "=l"(v) : "l"(p));

@@ -84,6 +84,7 @@ struct CombineArgs {
   void* out;              // forward: bf16 [T, N]
   void* dy;               // backward: bf16 [R, N]
   float* dweights;        // backward: [T, k] or null
+  int32_t* owner;         // backward: workspace [R], then rows of dy that no slot names become zeros; or null
 };
 cudaError_t launch_combine(const CombineArgs& a, cudaStream_t stream);
 cudaError_t launch_combine_backward(const CombineArgs& a, cudaStream_t stream);

@@ -374,15 +374,15 @@ mx_status mx_combine(const void* y, const int32_t* slots, const float* weights, 
   return launched([&] { return mxq::launch_combine(a, as_stream(stream)); });
 }
 
-mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* slots,
-                              const float* weights, int64_t T, int k, int64_t R, int64_t N,
-                              void* dy, float* dweights, void* stream) {
-  const mx_status st = check_combine(T, k, R, N);
-  if (st != MX_OK) return st;
-  if (T == 0) return MX_OK;
-  if (!slots || (N > 0 && (!dout || (R > 0 && !dy) || (R > 0 && dweights && !y)))) return MX_ERR_NULL;
+namespace {
+mx_status combine_backward(const void* dout, const void* y, const int32_t* slots, const float* weights,
+                           int64_t T, int k, int64_t R, int64_t N, void* dy, float* dweights,
+                           int32_t* owner, void* stream) {
+  if (T > 0 && (!slots || (N > 0 && (!dout || (R > 0 && !dy) || (R > 0 && dweights && !y))))) {
+    return MX_ERR_NULL;
+  }
   if (!aligned(y, 16) || !aligned(dout, 16) || !aligned(dy, 16) || !aligned(slots, 4) ||
-      !aligned(weights, 4) || !aligned(dweights, 4)) {
+      !aligned(weights, 4) || !aligned(dweights, 4) || !aligned(owner, 4)) {
     return MX_ERR_ALIGN;
   }
   mxq::CombineArgs a{};
@@ -396,7 +396,28 @@ mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* sl
   a.k = k;
   a.dy = dy;
   a.dweights = dweights;
+  a.owner = owner;
   return launched([&] { return mxq::launch_combine_backward(a, as_stream(stream)); });
+}
+}  // namespace
+
+mx_status mx_combine_backward(const void* dout, const void* y, const int32_t* slots,
+                              const float* weights, int64_t T, int k, int64_t R, int64_t N,
+                              void* dy, float* dweights, void* stream) {
+  const mx_status st = check_combine(T, k, R, N);
+  if (st != MX_OK) return st;
+  if (T == 0) return MX_OK;
+  return combine_backward(dout, y, slots, weights, T, k, R, N, dy, dweights, nullptr, stream);
+}
+
+mx_status mx_combine_backward_whole(const void* dout, const void* y, const int32_t* slots,
+                                    const float* weights, int64_t T, int k, int64_t R, int64_t N,
+                                    void* dy, float* dweights, void* workspace, void* stream) {
+  const mx_status st = check_combine(T, k, R, N);
+  if (st != MX_OK) return st;
+  if (R > 0 && N > 0 && (!dy || !workspace)) return MX_ERR_NULL;
+  return combine_backward(dout, y, slots, weights, T, k, R, N, dy, dweights,
+                          R > 0 && N > 0 ? static_cast<int32_t*>(workspace) : nullptr, stream);
 }
 
 }  // extern "C"

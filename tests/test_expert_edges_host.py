@@ -1,0 +1,28 @@
+"""Host-side checks that go with test_gpu_expert_edges.py: refusals before any launch (fake pointers are
+never dereferenced)."""
+
+import pytest
+
+import mx_microscaling_quantize_gb300 as mxq
+from mx_microscaling_quantize_gb300 import _build
+
+OK, NULL, SHAPE, ALIGN = 0, 1, 2, 3
+P = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return mxq.lib()
+
+
+def test_combine_backward_whole(L):
+    # (dout, y, slots, weights, T, k, R, N, dy, dweights, workspace, stream)
+    def f(d=P, y=P, s=P, w=P, T=4, k=2, R=8, N=64, dy=P, dw=P, ws=P):
+        return L.mx_combine_backward_whole(d, y, s, w, T, k, R, N, dy, dw, ws, None)
+    assert f(k=0) == SHAPE and f(N=4) == SHAPE and f(R=-1) == SHAPE and f(T=-1) == SHAPE
+    for name in ("d", "y", "s", "dy", "ws"):
+        assert f(**{name: None}) == NULL
+    assert f(T=0, dy=None) == NULL and f(T=0, ws=None) == NULL  # rows are still zeroed
+    assert f(d=P + 8) == ALIGN and f(dy=P + 2) == ALIGN and f(dw=P + 2) == ALIGN and f(ws=P + 2) == ALIGN
+    assert f(T=0, R=0, d=None, y=None, s=None, dy=None, dw=None, ws=None) == OK

@@ -137,3 +137,33 @@ def test_outputs_of_another_stream_are_not_memory_still_in_use():
         torch.cuda.synchronize()
         for g, w in zip(kept, want):
             assert torch.equal(g, w)
+
+
+# ---------------------------------------------------------------------------------------------
+# gradients of rows that no choice names
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T,k,rows,N", [(0, 2, 40, 64), (1, 1, 1, 8), (3, 2, 6, 136), (50, 3, 333, 1000),
+                                        (33, 9, 500, 264), (700, 4, 2800, 128), (1000, 2, 9000, 40)])
+@pytest.mark.parametrize("missing", [0.0, 0.3, 1.0])
+@pytest.mark.parametrize("weighted", [True, False])
+def test_combine_backward_zeroes_rows_that_no_slot_names(T, k, rows, N, missing, weighted):
+    """The gradient as the call allocates it: more rows than choices, choices of none, over memory that
+    held NaN; the workspace is over memory that held choices' numbers."""
+    rng = np.random.default_rng(T + N)
+    slots = rng.permutation(rows)[:T * k].reshape(T, k).astype(np.int32)
+    slots[rng.random((T, k)) < missing] = -1
+    if T > 2 and missing < 1:
+        slots[0, 0] = rows + 2  # outside: none
+    y, dout = bf16_inputs(rng, rows, N, False), bf16_inputs(rng, T, N, False)
+    w = torch.from_numpy(rng.standard_normal((T, k))).float().cuda()
+    s = torch.from_numpy(slots).cuda()
+    given = torch.zeros(rows, N, device="cuda", dtype=torch.bfloat16)
+    want, want_w = mxq.mx_combine_backward(dout, y, s, w if weighted else None, dy=given)
+    for stale in (float("nan"), 1.0):
+        a = torch.full((rows, N), stale, device="cuda", dtype=torch.bfloat16)
+        b = torch.arange(rows, device="cuda", dtype=torch.int32) % max(T * k, 1)
+        del a, b  # the next tensors of their sizes lie where they lay
+        dy, dw = mxq.mx_combine_backward(dout, y, s, w if weighted else None)
+        assert torch.equal(dy, want) and torch.equal(dw, want_w)
+    named = slots[(slots >= 0) & (slots < rows)]
+    assert not want[np.setdiff1d(np.arange(rows), named)].any()

@@ -132,7 +132,7 @@ def test_outputs_are_of_the_stream_they_are_written_on(noted, monkeypatch, i):
     taken = noted["taken"]
     assert taken and all(stream == SIDE for stream, _ in taken), name
     # the caller's stream is recorded on each output (a workspace is not the caller's)
-    outputs = len(taken) - (name == "route_plan")
+    outputs = len(taken) - (name in ("route_plan", "combine_backward"))
     assert noted["recorded"] == ["current"] * outputs
     noted["taken"].clear()
     call()
