@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a, in
 // Gradient of the logits. With p the scores of the chosen experts and g the gradient of their
 // weights w = scale p (/ P if renormalised, P = sum p):
 //   dp_j = scale (g_j - sum_i g_i p_i / P) / P, or scale g_j;
-//   sigmoid: dl = dp s (1 - s), nothing for the others;
+//   sigmoid: dl = dp s (1 - s), nothing for the others; 1 - s is the sigmoid of -l (from s itself nothing
+//   would be left of it where the router is sure: s is 1 in fp32 from l = 17 on);
 //   softmax: dl_i = s_i (dp_i - sum_j dp_j s_j), every logit.
 // A choice of -1 (no expert) takes and gives nothing. The scores are computed again from the
 // logits: reading them back would cost what the logits cost. The row is written as if nothing had been
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
   __syncwarp();  // the row comes before its choices
   if (first) {
     store_grad<BF16>(a.grad_logits, t * a.E + expert,
-                     SIGMOID ? d * p * (1.0f - p) : p * (d - through));
+                     SIGMOID ? d * p * sigmoid(-chosen) : p * (d - through));
   }
 }
 

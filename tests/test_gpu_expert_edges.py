@@ -167,3 +167,28 @@ def test_combine_backward_zeroes_rows_that_no_slot_names(T, k, rows, N, missing,
         assert torch.equal(dy, want) and torch.equal(dw, want_w)
     named = slots[(slots >= 0) & (slots < rows)]
     assert not want[np.setdiff1d(np.arange(rows), named)].any()
+
+
+# ---------------------------------------------------------------------------------------------
+# gradients of confident routers
+# ---------------------------------------------------------------------------------------------
+def test_route_backward_of_confident_sigmoids():
+    """s (1 - s) where s is next to 1: the second factor is as small as the other expert's s. Each of
+    s and 1 - s errs by an exponential (2 ulp: 4 units), a sum and a division (1 each), their product with
+    the gradient and the scale by three roundings: 15 units, twice that allowed."""
+    rng = np.random.default_rng(21)
+    for k, E in ((1, 40), (8, 300)):
+        l = rng.uniform(8, 60, (64, E)) * rng.choice([-1, 1], (64, E))
+        l[:, :k] = np.abs(l[:, :k])
+        logits = torch.from_numpy(l).float().cuda()
+        experts, _ = mxq.mx_route(logits, k, mxq.SIGMOID, renormalize=False)
+        g = rng.standard_normal((64, k)).astype(np.float32)
+        got = cpu(mxq.mx_route_backward(torch.from_numpy(g).cuda(), logits, experts, mxq.SIGMOID,
+                                        renormalize=False, scale=1.5)).astype(np.float64)
+        l = cpu(logits).astype(np.float64)
+        want = np.zeros_like(l)
+        chosen = np.take_along_axis(l, cpu(experts).astype(np.int64), 1)
+        np.put_along_axis(want, cpu(experts).astype(np.int64),
+                          1.5 * g / (1 + np.exp(-chosen)) / (1 + np.exp(chosen)), 1)
+        assert (np.abs(got - want) <= 30 * R.U * np.abs(want) + 1e-37).all()
+
