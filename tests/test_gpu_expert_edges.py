@@ -192,3 +192,57 @@ def test_route_backward_of_confident_sigmoids():
                           1.5 * g / (1 + np.exp(-chosen)) / (1 + np.exp(chosen)), 1)
         assert (np.abs(got - want) <= 30 * R.U * np.abs(want) + 1e-37).all()
 
+
+def pairwise_gradient(l, experts, g, scale, score, renorm):
+    """The gradient as sums of differences, in 64 bits, with the sums of their magnitudes: with p the
+    scores and D the gradient of every score (scale g at the chosen ones, 0 elsewhere),
+    softmax dl_i = p_i sum_j p_j (D_i - D_j); renormalised D_i = scale sum_j p_j (g_i - g_j) / P^2 first."""
+    T, E = l.shape
+    p = R.scores(l, score)
+    at = experts.astype(np.int64)
+    c = np.take_along_axis(p, at, 1)
+    d, size = scale * g, scale * np.abs(g)
+    if renorm:
+        P = c.sum(1, keepdims=True)
+        between = (g[:, :, None] - g[:, None, :]) * c[:, None, :]
+        d = scale * between.sum(2) / P / P
+        size = scale * np.abs(between).sum(2) / P / P
+    D, S = np.zeros_like(l), np.zeros_like(l)
+    np.put_along_axis(D, at, d, 1)
+    np.put_along_axis(S, at, size, 1)
+    if score == "sigmoid":
+        q = 1 / (1 + np.exp(l))  # 1 - p
+        return D * p * q, S * p * q
+    if renorm:  # sum_j p_j D_j is 0
+        return p * D, p * (S + (p * S).sum(1, keepdims=True))
+    between = D[:, :, None] - D[:, None, :]
+    return p * (p[:, None, :] * between).sum(2), p * (p[:, None, :] * np.abs(between)).sum(2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(3, 1), (40, 2), (64, 6), (257, 8), (1024, 32)])
+@pytest.mark.parametrize("equal", [False, True])
+def test_route_backward_of_confident_routers(E, k, score, renorm, equal):
+    """Nearly all of the score at one expert (or at the chosen ones together): what is left of the
+    gradient is far below the terms that it is usually written with, and as accurate as they are."""
+    rng = np.random.default_rng(E + k)
+    T = 48
+    l = rng.standard_normal((T, E))
+    l[np.arange(T), rng.integers(0, E, T)] += rng.uniform(0, 30, T)
+    if k > 1:
+        top = np.argsort(-l, 1)[:, :k]
+        late = T // 2  # half of the tokens: all chosen experts far above the others
+        np.put_along_axis(l[late:], top[late:], np.take_along_axis(l[late:], top[late:], 1) + 15, 1)
+    l = l.astype(np.float32)
+    logits = torch.from_numpy(l).cuda()
+    experts, _ = mxq.mx_route(logits, k, mxq.SOFTMAX if score == "softmax" else mxq.SIGMOID)
+    g = np.ones((T, k), np.float32) if equal else rng.standard_normal((T, k)).astype(np.float32)
+    got = cpu(mxq.mx_route_backward(torch.from_numpy(g).cuda(), logits, experts,
+                                    mxq.SOFTMAX if score == "softmax" else mxq.SIGMOID,
+                                    renormalize=renorm, scale=2.5)).astype(np.float64)
+    want, size = pairwise_gradient(l.astype(np.float64), cpu(experts), g.astype(np.float64), 2.5, score,
+                                   renorm)
+    # a score errs by under 128 units (exponential of a rounded argument up to 40, sum of E, division);
+    # a term of the sums is a difference (1 unit) times one score, or two where renormalised, times p_i
+    assert (np.abs(got - want) <= 512 * R.U * size + 1e-37).all(), (np.abs(got - want) / (size + 1e-37)).max()
