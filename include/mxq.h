@@ -381,6 +381,9 @@ mx_status mx_quantize_b128_blocks(const void* x, int64_t batch, int64_t M, int64
  * the block of a[i][k] b[j][k]; products and sums in fp32 on the tensor cores, C rounded once to
  * c_type (MX_TYPE_BF16 or MX_TYPE_FP32). Codes [rows, K], both K-major; A's scales in the rows
  * form. K % 32 == 0, N % 8 == 0; codes and C 16-byte aligned.
+ * The factor sa[b, i] sb[b, j] is one fp32 product, taken first: where it is 2^128 or more (blocks whose
+ * abs-maxes multiply to some 2^145) the entry is infinite or NaN whatever the sum, and below 2^-126 the
+ * factor loses bits, an error of at most 2^-125 per block.
  *
  * mx_gemm_b128: A [M, K], B [N, K], B's scales in b_form; C [M, N]. K > 0.
  * mx_gemm_b128_grouped: rows [row_offsets[e], row_offsets[e + 1]) of A times B[e] [N, K] (B's

@@ -246,3 +246,86 @@ def test_route_backward_of_confident_routers(E, k, score, renorm, equal):
     # a score errs by under 128 units (exponential of a rounded argument up to 40, sum of E, division);
     # a term of the sums is a difference (1 unit) times one score, or two where renormalised, times p_i
     assert (np.abs(got - want) <= 512 * R.U * size + 1e-37).all(), (np.abs(got - want) / (size + 1e-37)).max()
+
+
+# ---------------------------------------------------------------------------------------------
+# scales at the ends of fp32
+# ---------------------------------------------------------------------------------------------
+def far_operand(rng, rows, K, form, exponent):
+    """operand() with every third row (or 128-row block) of scale 1.25 * 2^exponent; -> also which rows."""
+    (codes, scales), _ = operand(rng, rows, K, form)
+    scales = cpu(scales)
+    hot = (np.arange(rows) // (1 if form == "rows" else 128)) % 3 == 0
+    if form == "rows":
+        scales[:, hot] = 2.0 ** exponent * 1.25
+    else:
+        scales[::3] = 2.0 ** exponent * 1.25
+    return (codes, torch.from_numpy(scales).cuda()), R.values(cpu(codes), scales, form), hot
+
+
+def check_far_product(C, a, b, K, hot_a, hot_b, beyond, what=""):
+    """Against the 64-bit product. Where the factor of two scales is beyond fp32 every block's sum times it
+    is infinite, or NaN of a sum of nothing: those entries are not finite, and no others are touched."""
+    C = C.double().cpu().numpy()
+    want, S = R.product(a, b)
+    bound = R.product_bound(want, S, K, True)
+    far = hot_a[:, None] & hot_b[None, :] & beyond
+    assert not np.isfinite(C[far]).any(), what
+    assert (np.abs(C - want)[~far] <= bound[~far]).all(), what
+
+
+FAR = [
+    # exponents of the operands' scales; whether their product is beyond fp32
+    (60, 40, False), (-40, 95, False), (100, -100, False),
+    (-30, -64, False),            # results of 2^-80, their factors near the least normal number
+    (100, 40, True), (40, 100, True),
+]
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 392, 416), (100, 4096, 4096), (40, 1000, 2048), (2048, 2048, 640)])
+@pytest.mark.parametrize("form", ["blocks", "rows"])
+@pytest.mark.parametrize("ea,eb,beyond", FAR)
+def test_gemm_scales_at_the_ends_of_fp32(M, N, K, form, ea, eb, beyond):
+    rng = np.random.default_rng(M + N)
+    (ac, asc), a, hot_a = far_operand(rng, M, K, "rows", ea)
+    (bc, bsc), b, hot_b = far_operand(rng, N, K, form, eb)
+    for dtype in (torch.bfloat16, torch.float32):
+        C = mxq.mx_gemm_b128(ac, asc, bc, bsc, mxq.B128_ROWS if form == "rows" else mxq.B128_BLOCKS,
+                             out_dtype=dtype)
+        check_far_product(C, a, b, K, hot_a, hot_b, beyond)
+
+
+@pytest.mark.parametrize("ea,eb,beyond", FAR)
+def test_gemm_by_expert_scales_at_the_ends_of_fp32(ea, eb, beyond):
+    rng = np.random.default_rng(7)
+    counts, N, K = [5, 0, 300, 128, 17, 129], 520, 416
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    off = torch.from_numpy(offsets).cuda()
+    (ac, asc), a, hot_a = far_operand(rng, sum(counts), K, "rows", ea)
+    bs = [far_operand(rng, N, K, "blocks", eb) for _ in counts]
+    C = mxq.mx_gemm_b128_grouped(ac, asc, torch.stack([b[0][0] for b in bs]),
+                                 torch.stack([b[0][1] for b in bs]), off)
+    P = mxq.mx_b128_padded_rows(sum(counts), len(counts))
+    (uc, usc), u, hot_u = far_operand(rng, 288, P, "rows", ea)
+    (vc, vsc), v, hot_v = far_operand(rng, 392, P, "rows", eb)
+    W = mxq.mx_gemm_b128_grouped_wgrad(uc, usc, vc, vsc, off)
+    at = 0
+    for e, n in enumerate(counts):
+        part = slice(offsets[e], offsets[e + 1])
+        if n:
+            check_far_product(C[part], a[part], bs[e][1], K, hot_a[part], bs[e][2], beyond, e)
+            check_far_product(W[e], u[:, at:at + R.up(n)], v[:, at:at + R.up(n)], R.up(n), hot_u, hot_v,
+                              beyond, e)
+        at += R.up(n)
+
+
+def test_gemm_of_quantised_huge_tiny_and_empty_rows():
+    """What the quantisers make of blocks of zeros, of 2^-110 and of 2^100, multiplied with ordinary ones."""
+    rng = np.random.default_rng(31)
+    x, w = bf16_inputs(rng, 300, 512), bf16_inputs(rng, 264, 512, False)
+    for rows in (x[:5].contiguous(), x):
+        q = mxq.mx_quantize_b128_rows(rows)
+        a = R.values(cpu(q[0]), cpu(q[1]), "rows")
+        for (bc, bs), form, name in ((mxq.mx_quantize_b128_blocks(w), mxq.B128_BLOCKS, "blocks"),
+                                     (mxq.mx_quantize_b128_rows(w), mxq.B128_ROWS, "rows")):
+            check_product(mxq.mx_gemm_b128(*q, bc, bs, form), a, R.values(cpu(bc), cpu(bs), name), 512)
