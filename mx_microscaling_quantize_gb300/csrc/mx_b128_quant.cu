@@ -75,7 +75,7 @@ constexpr int kRowsCols = 512;  // columns of a warp's tile: 4 blocks of 128, 8 
 // block l / 8 of every row, so the RW loads of a thread are in flight together, eight lanes
 // reduce a block's abs-max in three shuffles, and the RW scales of a block, which are adjacent in
 // the [K / 128, R] layout, leave as one segment.
-template <int RW>
+template <int RW, bool GATHER>
 __global__ void __launch_bounds__(256) b128_rows_kernel(B128QuantArgs a, int64_t col_tiles,
                                                         int64_t tiles) {
   pdl_launch_dependents();
@@ -86,17 +86,19 @@ __global__ void __launch_bounds__(256) b128_rows_kernel(B128QuantArgs a, int64_t
   const int64_t r0 = tile / col_tiles * RW;
   const int64_t col = tile % col_tiles * kRowsCols + blk * kB128 + sub * 16;
   const uint16_t* x = static_cast<const uint16_t*>(a.x);
+  int32_t src[RW];  // gathered rows' sources (-1: zeros), asked for together
+  if constexpr (GATHER) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      src[i] = r0 + i < a.R && col < a.K ? load_s32(a.index + r0 + i) : -1;
+    }
+  }
   uint32_t w[RW][8];
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
-    int64_t src = r0 + i;
-    bool ok = src < a.R && col < a.K;
-    if (ok && a.index) {
-      src = a.index[src];
-      ok = src >= 0 && src < a.M;
-    }
-    if (ok) {
-      load32B(x + src * a.K + col, w[i]);
+    const int64_t row = GATHER ? src[i] : r0 + i;
+    if (GATHER ? row >= 0 && row < a.M : row < a.R && col < a.K) {
+      load32B(x + row * a.K + col, w[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[i][j] = 0u;
@@ -130,19 +132,12 @@ __global__ void __launch_bounds__(256) b128_rows_kernel(B128QuantArgs a, int64_t
 // neither side meets a bank twice, and leave as full 128-byte lines.
 constexpr int kTileThreads = 256;
 
-__device__ __forceinline__ void load_tile(const uint16_t* x, int64_t K, const int32_t* index,
-                                          int64_t src_rows, int64_t row0, int64_t row_end,
+__device__ __forceinline__ void load_tile(const uint16_t* x, int64_t K, int64_t row0, int64_t row_end,
                                           int64_t col, uint32_t (&w)[8][4]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int64_t src = row0 + i;
-    bool ok = src < row_end && col < K;
-    if (ok && index) {
-      src = index[src];
-      ok = src >= 0 && src < src_rows;
-    }
-    if (ok) {
-      load16B(x + src * K + col, w[i]);
+    if (row0 + i < row_end && col < K) {
+      load16B(x + (row0 + i) * K + col, w[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[i][j] = 0u;
@@ -239,6 +234,7 @@ struct ColsShared {
   int64_t blocks;
   int offsets[1024 + 1];
 };
+template <bool GATHER>
 __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArgs a) {
   extern __shared__ __align__(128) uint8_t cols_shared[];
   ColsShared& s = *reinterpret_cast<ColsShared*>(cols_shared);
@@ -273,20 +269,24 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArg
     }
   };
   auto load = [&] {  // tile (b, c)
-    const int64_t col = c * kB128 + cg * 8;
+    const int64_t col = c * kB128 + cg * 8, first = (int64_t)row0 + rg * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = (int64_t)row0 + rg * 8 + i;
-      int64_t src = row;
-      bool ok = row < row_end && col < a.K;
-      if (ok && a.index) {
-        src = a.index[row];
-        ok = src >= 0 && src < a.M;
+    for (int h = 0; h < 8; h += 4) {
+      int32_t src[4];  // gathered rows' sources (-1: zeros), asked for together
+      if constexpr (GATHER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          src[i] = first + h + i < row_end && col < a.K ? load_s32(a.index + first + h + i) : -1;
+        }
       }
-      if (ok) {
-        copy16B_async(&s.next[i][tid], static_cast<const uint16_t*>(a.x) + src * a.K + col);
-      } else {
-        s.next[i][tid] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t row = GATHER ? src[i] : first + h + i;
+        if (GATHER ? row >= 0 && row < a.M : row < row_end && col < a.K) {
+          copy16B_async(&s.next[h + i][tid], static_cast<const uint16_t*>(a.x) + row * a.K + col);
+        } else {
+          s.next[h + i][tid] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kTileThreads) b128_blocks_kernel(B128QuantArgs
   const int64_t r0 = rb * kB128, c0 = cb * kB128;
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + z * a.M * a.K;
   uint32_t w[8][4];
-  load_tile(x, a.K, nullptr, a.M, r0 + rg * 8, a.M, c0 + cg * 8, w);
+  load_tile(x, a.K, r0 + rg * 8, a.M, c0 + cg * 8, w);
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kTileThreads) b128_blocks_kernel(B128QuantArgs
 
 }  // namespace
 
-cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream) {
+template <bool GATHER>
+static cudaError_t rows_launch(const B128QuantArgs& a, cudaStream_t stream) {
   const int64_t col_tiles = (a.K + kRowsCols - 1) / kRowsCols;
   // Four rows per warp once that leaves every SM work (x[8192, 8192]: 30.9 us; eight rows, whose 91
   // registers halve the resident warps, 36.1); one row per warp for small calls, where the latency
@@ -427,21 +428,30 @@ cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream) {
   constexpr int kRows = 4;
   if (a.R * col_tiles >= kRows * 8 * 152) {
     const int64_t tiles = (a.R + kRows - 1) / kRows * col_tiles;
-    return launch_pdl(&b128_rows_kernel<kRows>, dim3((unsigned)((tiles + 7) / 8)), dim3(256), 0,
+    return launch_pdl(&b128_rows_kernel<kRows, GATHER>, dim3((unsigned)((tiles + 7) / 8)), dim3(256), 0,
                       stream, a, col_tiles, tiles);
   }
   const int64_t tiles = a.R * col_tiles;
-  return launch_pdl(&b128_rows_kernel<1>, dim3((unsigned)((tiles + 3) / 4)), dim3(128), 0, stream, a,
-                    col_tiles, tiles);
+  return launch_pdl(&b128_rows_kernel<1, GATHER>, dim3((unsigned)((tiles + 3) / 4)), dim3(128), 0,
+                    stream, a, col_tiles, tiles);
+}
+
+cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream) {
+  return a.index ? rows_launch<true>(a, stream) : rows_launch<false>(a, stream);
+}
+
+template <bool GATHER>
+static cudaError_t cols_launch(const B128QuantArgs& a, cudaStream_t stream) {
+  const int64_t tiles = a.blocks * ((a.K + kB128 - 1) / kB128);  // by expert: at most
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(&b128_cols_kernel<GATHER>), kTileThreads,
+                                      sizeof(ColsShared), 0);
+  if (slots <= 0) return cudaErrorInvalidConfiguration;
+  return launch_pdl(&b128_cols_kernel<GATHER>, dim3((unsigned)(tiles < slots ? tiles : slots)),
+                    dim3(kTileThreads), sizeof(ColsShared), stream, a);
 }
 
 cudaError_t launch_b128_cols(const B128QuantArgs& a, cudaStream_t stream) {
-  const int64_t tiles = a.blocks * ((a.K + kB128 - 1) / kB128);  // by expert: at most
-  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(&b128_cols_kernel), kTileThreads,
-                                      sizeof(ColsShared), 0);
-  if (slots <= 0) return cudaErrorInvalidConfiguration;
-  return launch_pdl(&b128_cols_kernel, dim3((unsigned)(tiles < slots ? tiles : slots)),
-                    dim3(kTileThreads), sizeof(ColsShared), stream, a);
+  return a.index ? cols_launch<true>(a, stream) : cols_launch<false>(a, stream);
 }
 
 cudaError_t launch_b128_blocks(const B128QuantArgs& a, cudaStream_t stream) {

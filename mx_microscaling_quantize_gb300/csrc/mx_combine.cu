@@ -38,7 +38,7 @@ __device__ __forceinline__ void store4(void* p, const uint32_t* r) {
 
 // One item = eight columns of one token; KU choices are loaded together.
 template <int KU>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a, int64_t chunks,
+__global__ void __launch_bounds__(kCombineThreads, 3) combine_kernel(CombineArgs a, int64_t chunks,
                                                                   int64_t items) {
   pdl_launch_dependents();
   pdl_wait();
@@ -50,21 +50,23 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a,
     for (int j0 = 0; j0 < a.k; j0 += KU) {
       uint32_t v[KU][4];
       float w[KU];
-      bool ok[KU];
+      int32_t row[KU];  // -1: none
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
-        const int j = j0 + u;
-        const int64_t row = j < a.k ? (int64_t)a.slots[t * a.k + j] : -1;
-        ok[u] = row >= 0 && row < a.R;
-        w[u] = 1.0f;
-        if (ok[u]) {
-          load16B(y + row * a.N + col, v[u]);
-          if (a.weights) w[u] = a.weights[t * a.k + j];
-        }
+        row[u] = j0 + u < a.k ? load_s32(a.slots + t * a.k + j0 + u) : -1;
+        if (row[u] >= a.R) row[u] = -1;
       }
 #pragma unroll
       for (int u = 0; u < KU; ++u) {
-        if (!ok[u]) continue;
+        if (row[u] >= 0) load16B(y + row[u] * a.N + col, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        w[u] = j0 + u < a.k && a.weights ? load_f32(a.weights + t * a.k + j0 + u) : 1.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
+        if (row[u] < 0) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           acc[2 * i] = fmaf(w[u], bf16_lo(v[u][i]), acc[2 * i]);
@@ -96,12 +98,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(Combi
     float w[KU], dot[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-      const int j = j0 + u;
-      row[u] = j < a.k ? (int64_t)a.slots[t * a.k + j] : -1;
-      if (row[u] >= a.R) row[u] = -1;
-      w[u] = row[u] >= 0 && a.weights ? a.weights[t * a.k + j] : 1.0f;
+      row[u] = j0 + u < a.k ? load_s32(a.slots + t * a.k + j0 + u) : -1;
+      w[u] = j0 + u < a.k && a.weights ? load_f32(a.weights + t * a.k + j0 + u) : 1.0f;
       dot[u] = 0.0f;
-      if (a.owner && tid == 0 && row[u] >= 0) a.owner[row[u]] = (int32_t)(t * a.k + j);
+    }
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      if (row[u] >= a.R) row[u] = -1;
+      if (a.owner && tid == 0 && row[u] >= 0) a.owner[row[u]] = (int32_t)(t * a.k + j0 + u);
     }
     for (int64_t c = tid; c < chunks; c += kCombineThreads) {
       uint32_t d[4], v[KU][4];

@@ -319,12 +319,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_backward_kernel(RouteA
   int32_t expert = -1;
   float g = 0.0f, p = 0.0f, chosen = 0.0f;  // gradient, score and logit of the lane's choice
   if (lane < a.k) {
-    expert = a.chosen[t * a.k + lane];
+    expert = load_s32(a.chosen + t * a.k + lane);
+    g = load_f32(a.grad_weights + t * a.k + lane);
     if (expert >= a.E || expert < 0) expert = -1;
   }
   if (expert >= 0) {
-    g = a.grad_weights[t * a.k + lane];
     chosen = load_logit<BF16>(a.logits, t * a.E + expert);
+  } else {
+    g = 0.0f;
   }
   float dl[V];
   if (SIGMOID) {
@@ -428,7 +430,7 @@ int64_t plan_chunk(int64_t n) {
 }
 
 __device__ __forceinline__ int plan_expert(const PlanArgs& a, int64_t i) {
-  const int e = a.experts[i];
+  const int e = load_s32(a.experts + i);
   return e >= 0 && e < a.E ? e : -1;
 }
 
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(PlanArgs a, in
     if (chunks > 1) {
 #pragma unroll 8
       for (int c = 0; c < chunks; ++c) {
-        const int32_t v = a.workspace[c * (int64_t)a.E + e];
+        const int32_t v = load_s32(a.workspace + c * (int64_t)a.E + e);
         total += v;
         if (c < (int)blockIdx.x) before += v;
       }

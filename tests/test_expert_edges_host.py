@@ -1,6 +1,9 @@
 """Host-side checks that go with test_gpu_expert_edges.py: refusals before any launch (fake pointers are
 never dereferenced)."""
 
+import os
+import re
+
 import pytest
 
 import mx_microscaling_quantize_gb300 as mxq
@@ -26,3 +29,15 @@ def test_combine_backward_whole(L):
     assert f(T=0, dy=None) == NULL and f(T=0, ws=None) == NULL  # rows are still zeroed
     assert f(d=P + 8) == ALIGN and f(dy=P + 2) == ALIGN and f(dw=P + 2) == ALIGN and f(ws=P + 2) == ALIGN
     assert f(T=0, R=0, d=None, y=None, s=None, dy=None, dw=None, ws=None) == OK
+
+
+def test_kernels_read_their_inputs_through_the_coherent_loads():
+    """A kernel's arrays are read by the load functions (asm volatile, after the wait for the kernel before)
+    and never by subscript, which the compiler may turn into a non-coherent or an earlier load."""
+    csrc = os.path.join(os.path.dirname(mxq.__file__), "csrc")
+    for name in ("mx_route.cu", "mx_b128_quant.cu", "mx_b128_gemm.cu", "mx_combine.cu"):
+        for number, line in enumerate(open(os.path.join(csrc, name)), 1):
+            line = line.split("//")[0]
+            for use in re.finditer(r"\ba\.\w+\[", line):
+                # what is written: the subscript's end is followed by an assignment
+                assert re.match(r"[^=]*\] = ", line[use.end():]), f"{name}:{number}: {line.strip()}"
