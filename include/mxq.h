@@ -487,12 +487,20 @@ mx_status mx_selftest_gemm_give_up(const void* a_codes, const void* a_scales, co
 
 /*
  * The same self-test of the product of operands with a scale per block of 128: mx_gemm_b128 with
- * a bf16 C and every pipeline wait limited to limit_ns.
+ * a bf16 C and every pipeline wait limited to limit_ns; and mx_gemm_b128_grouped likewise. Drains are
+ * limited to 2 s. Few tokens run the swapped shape, M = N = 2048 CTA pairs (both forms of B's scales);
+ * by expert, experts of more than 128 rows pairs, the others single CTAs.
  */
 mx_status mx_selftest_gemm_b128_give_up(const void* a_codes, const float* a_scales,
                                         const void* b_codes, const float* b_scales, int64_t M,
                                         int64_t N, int64_t K, int b_form, void* c, int64_t limit_ns,
                                         void* stream);
+
+mx_status mx_selftest_gemm_b128_grouped_give_up(const void* a_codes, const float* a_scales,
+                                                const void* b_codes, const float* b_scales,
+                                                const int64_t* row_offsets, int E, int64_t M_total,
+                                                int64_t N, int64_t K, void* c, int64_t limit_ns,
+                                                void* stream);
 
 #ifdef __cplusplus
 }

@@ -45,7 +45,7 @@ EXPORTS = (
     "mx_quantize_b128_blocks", "mx_gemm_b128", "mx_gemm_b128_grouped",
     "mx_gemm_b128_grouped_wgrad", "mx_combine", "mx_combine_backward",
     "mx_combine_backward_whole",
-    "mx_selftest_gemm_b128_give_up",
+    "mx_selftest_gemm_b128_give_up", "mx_selftest_gemm_b128_grouped_give_up",
 )
 
 
@@ -103,6 +103,7 @@ def lib() -> ctypes.CDLL:
         "mx_combine_backward": (i32, [p, p, p, p, i64, i32, i64, i64, p, p, p]),
         "mx_combine_backward_whole": (i32, [p, p, p, p, i64, i32, i64, i64, p, p, p, p]),
         "mx_selftest_gemm_b128_give_up": (i32, [p, p, p, p, i64, i64, i64, i32, p, i64, p]),
+        "mx_selftest_gemm_b128_grouped_give_up": (i32, [p, p, p, p, p, i32, i64, i64, i64, p, i64, p]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -681,20 +682,37 @@ def mx_selftest_gemm_b128_give_up(a_codes, a_scales, b_codes, b_scales, limit_ns
     return c
 
 
-def mx_gemm_b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, *,
-                         out_dtype=torch.bfloat16, c=None, stream=None):
-    """Rows of A [R, K] by expert (row_offsets int64 [E + 1]) times that expert's B [E, N, K] ->
-    C [R, N]; rows from row_offsets[E] on are not written."""
+def _b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets):
     R, K = _b128_operand(a_codes, a_scales, "a", True)
     experts, N, Kb = _b128_operand(b_codes, b_scales, "b", False, 3, a_codes)
     E = _offsets(row_offsets, a_codes)
     if experts != E or K != Kb:
         raise ValueError("a_codes and b_codes must be [R, K] and [E, N, K]")
+    return E, R, N, K
+
+
+def mx_gemm_b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, *,
+                         out_dtype=torch.bfloat16, c=None, stream=None):
+    """Rows of A [R, K] by expert (row_offsets int64 [E + 1]) times that expert's B [E, N, K] ->
+    C [R, N]; rows from row_offsets[E] on are not written."""
+    E, R, N, K = _b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets)
     dtype = _out_type(out_dtype, c)
     c = _output(c, "c", (R, N), dtype, a_codes, stream)
     _check(lib().mx_gemm_b128_grouped(_ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
                                       _ptr(row_offsets), E, R, N, K, _TYPES[dtype], _ptr(c),
                                       _stream_ptr(stream, a_codes)))
+    return c
+
+
+def mx_selftest_gemm_b128_grouped_give_up(a_codes, a_scales, b_codes, b_scales, row_offsets,
+                                          limit_ns: int, *, stream=None):
+    """mx_gemm_b128_grouped with every pipeline wait of the kernel limited to limit_ns; returns the
+    (unspecified) C buffer. The device error word reports the give-up."""
+    E, R, N, K = _b128_grouped(a_codes, a_scales, b_codes, b_scales, row_offsets)
+    c = _output(None, "c", (R, N), torch.bfloat16, a_codes, stream)
+    _check(lib().mx_selftest_gemm_b128_grouped_give_up(
+        _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), _ptr(row_offsets), E, R, N, K,
+        _ptr(c), limit_ns, _stream_ptr(stream, a_codes)))
     return c
 
 

@@ -903,7 +903,9 @@ struct Steps {
   // The steps that may have been loaded are handed back unread, so that the loading warp sees its
   // copies land. Steps it .. it + kBufs - 1 have their arrivals already and their stages may still be
   // in that phase, so the steps that follow on those stages are left out: a second arrival there would
-  // complete a phase before its copies do.
+  // complete a phase before its copies do. Where the other warps went on and such steps were loaded all
+  // the same, nothing completes their phases, and the loading warp's drain ends by its limit, long after
+  // the copies have landed.
   __device__ __forceinline__ void give_up() {
     for (int i = 0; i < C::kStages - C::kBufs; ++i) hand_back((st2 + i) % C::kStages);
   }

@@ -90,6 +90,32 @@ mx_status dense(const void* a_codes, const float* a_scales, const void* b_codes,
   return run_gemm(mxq::kB128Dense, g, limit_ns, stream);
 }
 
+mx_status grouped(const void* a_codes, const float* a_scales, const void* b_codes,
+                  const float* b_scales, const int64_t* row_offsets, int E, int64_t M_total, int64_t N,
+                  int64_t K, int c_type, void* c, unsigned long long limit_ns, void* stream) {
+  mx_status st = check_b128_gemm(M_total, N, K, c_type);
+  if (st != MX_OK) return st;
+  if (E < 1 || E > 1024 || N > INT32_MAX / E || K == 0) return MX_ERR_SHAPE;
+  if (M_total == 0 || N == 0) return MX_OK;
+  if (!row_offsets) return MX_ERR_NULL;
+  st = check_b128_pointers(a_codes, a_scales, b_codes, b_scales, c);
+  if (st != MX_OK) return st;
+  if (!aligned(row_offsets, 8)) return MX_ERR_ALIGN;
+  mxq::B128GemmArgs g{};
+  g.a_codes = a_codes;
+  g.a_scales = a_scales;
+  g.b_codes = b_codes;
+  g.b_scales = b_scales;
+  g.c = c;
+  g.M = M_total;
+  g.N = N;
+  g.K = K;
+  g.offsets = row_offsets;
+  g.E = E;
+  g.out_f32 = c_type == MX_TYPE_FP32;
+  return run_gemm(mxq::kB128Grouped, g, limit_ns, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -285,27 +311,19 @@ mx_status mx_gemm_b128_grouped(const void* a_codes, const float* a_scales, const
                                const float* b_scales, const int64_t* row_offsets, int E,
                                int64_t M_total, int64_t N, int64_t K, int c_type, void* c,
                                void* stream) {
-  mx_status st = check_b128_gemm(M_total, N, K, c_type);
-  if (st != MX_OK) return st;
-  if (E < 1 || E > 1024 || N > INT32_MAX / E || K == 0) return MX_ERR_SHAPE;
-  if (M_total == 0 || N == 0) return MX_OK;
-  if (!row_offsets) return MX_ERR_NULL;
-  st = check_b128_pointers(a_codes, a_scales, b_codes, b_scales, c);
-  if (st != MX_OK) return st;
-  if (!aligned(row_offsets, 8)) return MX_ERR_ALIGN;
-  mxq::B128GemmArgs g{};
-  g.a_codes = a_codes;
-  g.a_scales = a_scales;
-  g.b_codes = b_codes;
-  g.b_scales = b_scales;
-  g.c = c;
-  g.M = M_total;
-  g.N = N;
-  g.K = K;
-  g.offsets = row_offsets;
-  g.E = E;
-  g.out_f32 = c_type == MX_TYPE_FP32;
-  return run_gemm(mxq::kB128Grouped, g, kWaitNs, stream);
+  return grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, E, M_total, N, K, c_type, c, kWaitNs,
+                 stream);
+}
+
+mx_status mx_selftest_gemm_b128_grouped_give_up(const void* a_codes, const float* a_scales,
+                                                const void* b_codes, const float* b_scales,
+                                                const int64_t* row_offsets, int E, int64_t M_total,
+                                                int64_t N, int64_t K, void* c, int64_t limit_ns,
+                                                void* stream) {
+  if (limit_ns <= 0 || limit_ns > 100000000) return MX_ERR_SHAPE;
+  if (M_total == 0 || N == 0) return MX_ERR_SHAPE;  // a launch is the point
+  return grouped(a_codes, a_scales, b_codes, b_scales, row_offsets, E, M_total, N, K, MX_TYPE_BF16, c,
+                 (unsigned long long)limit_ns, stream);
 }
 
 mx_status mx_gemm_b128_grouped_wgrad(const void* a_codes, const float* a_scales,

@@ -41,3 +41,11 @@ def test_kernels_read_their_inputs_through_the_coherent_loads():
             for use in re.finditer(r"\ba\.\w+\[", line):
                 # what is written: the subscript's end is followed by an assignment
                 assert re.match(r"[^=]*\] = ", line[use.end():]), f"{name}:{number}: {line.strip()}"
+
+
+def test_grouped_give_up(L):
+    # (a, sa, b, sb, offsets, E, M, N, K, c, limit, stream)
+    def f(limit=1000, M=128, off=P, c=P, E=4):
+        return L.mx_selftest_gemm_b128_grouped_give_up(P, P, P, P, off, E, M, 128, 128, c, limit, None)
+    assert f(limit=0) == SHAPE and f(limit=100_000_001) == SHAPE and f(M=0) == SHAPE and f(E=0) == SHAPE
+    assert f(off=None) == NULL and f(c=None) == NULL and f(c=P + 8) == ALIGN

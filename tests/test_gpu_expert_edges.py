@@ -73,6 +73,52 @@ def test_pairs_of_few_steps_one_after_another(K):
         assert torch.equal(c2, c) and torch.equal(w2, w)
 
 
+# By the rule of the dense products' shapes: more 128-row tiles of weights than CTAs, one walk of the
+# contraction each, and still fewer waves than 256 x 256 tiles on pairs take.
+@pytest.mark.parametrize("M,N,K", [(3, 40000, 416), (64, 32768, 1056), (100, 24000, 544), (17, 20488, 96)])
+@pytest.mark.parametrize("form", ["blocks", "rows"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gemm_of_few_tokens_and_several_tiles_per_cta(M, N, K, form, dtype):
+    """A CTA's barriers, scales and staging go on from one tile to the next, whole batches or not."""
+    dense(M, N, K, form, dtype)
+
+
+def check_give_up(call, check, limit):
+    call(limit)
+    assert mxq.mx_device_errors() in (0, 1)
+    if limit == 1:
+        call(limit)
+        assert mxq.mx_device_errors() == 1
+    check()
+    assert mxq.mx_device_errors() == 0
+
+
+@pytest.mark.parametrize("form", ["blocks", "rows"])
+@pytest.mark.parametrize("limit", [1, 1000, 20000])
+def test_give_up_of_pairs(form, limit):
+    """2048 x 2048 x 2048: 64 tiles on pairs in one wave, against 256 tiles of the other shape in two."""
+    rng = np.random.default_rng(17)
+    (ac, asc), a = operand(rng, 2048, 2048, "rows")
+    (bc, bsc), b = operand(rng, 2048, 2048, form)
+    f = mxq.B128_ROWS if form == "rows" else mxq.B128_BLOCKS
+    check_give_up(lambda ns: mxq.mx_selftest_gemm_b128_give_up(ac, asc, bc, bsc, ns, f),
+                  lambda: check_product(mxq.mx_gemm_b128(ac, asc, bc, bsc, f), a, b, 2048), limit)
+
+
+@pytest.mark.parametrize("counts", [[300, 0, 129, 1000], [5, 128, 0, 77] * 20])  # pairs; single CTAs
+@pytest.mark.parametrize("limit", [1, 1000, 20000])
+def test_give_up_by_expert(counts, limit):
+    rng = np.random.default_rng(18)
+    N, K = 1024, 2048
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    off = torch.from_numpy(offsets).cuda()
+    (ac, asc), a = operand(rng, sum(counts), K, "rows")
+    (bc, bsc), b = operand(rng, N, K, "blocks")
+    bc, bsc = (t.expand(len(counts), -1, -1).contiguous() for t in (bc, bsc))
+    check_give_up(lambda ns: mxq.mx_selftest_gemm_b128_grouped_give_up(ac, asc, bc, bsc, off, ns),
+                  lambda: check_product(mxq.mx_gemm_b128_grouped(ac, asc, bc, bsc, off), a, b, K), limit)
+
+
 # ---------------------------------------------------------------------------------------------
 # streams that nothing orders after one another
 # ---------------------------------------------------------------------------------------------
