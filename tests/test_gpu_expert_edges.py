@@ -375,3 +375,142 @@ def test_gemm_of_quantised_huge_tiny_and_empty_rows():
         for (bc, bs), form, name in ((mxq.mx_quantize_b128_blocks(w), mxq.B128_BLOCKS, "blocks"),
                                      (mxq.mx_quantize_b128_rows(w), mxq.B128_ROWS, "rows")):
             check_product(mxq.mx_gemm_b128(*q, bc, bs, form), a, R.values(cpu(bc), cpu(bs), name), 512)
+
+
+# ---------------------------------------------------------------------------------------------
+# routing: bases, NaN in groups, close scores
+# ---------------------------------------------------------------------------------------------
+def off_base(t, by=1):
+    """A copy of t whose first element lies `by` elements after an allocation's start."""
+    buf = torch.empty(t.numel() + by, device="cuda", dtype=t.dtype)
+    view = buf[by:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", [mxq.SOFTMAX, mxq.SIGMOID])
+@pytest.mark.parametrize("E,k,groups,top", [(128, 8, 1, 1), (256, 8, 8, 4), (512, 6, 1, 1), (1024, 8, 16, 3)])
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_route_of_bases_that_allow_no_wide_loads(dtype, score, E, k, groups, top, by):
+    rng = np.random.default_rng(E + by)
+    logits = torch.from_numpy(rng.standard_normal((37, E))).to(dtype).cuda()
+    bias = torch.from_numpy(rng.standard_normal(E) * 0.1).float().cuda()
+    at = dict(groups=groups, top_groups=top)
+    want = mxq.mx_route(logits, k, score, bias, **at)
+    grad = torch.from_numpy(rng.standard_normal((37, k))).float().cuda()
+    want_d = mxq.mx_route_backward(grad, logits, want[0], score)
+    l, b = off_base(logits, by), off_base(bias, by)
+    assert l.data_ptr() % 16 and b.data_ptr() % 16
+    for li, bi in ((l, bias), (logits, b), (l, b)):
+        got = mxq.mx_route(li, k, score, bi, experts=off_base(want[0]), weights=off_base(want[1]), **at)
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+    for li, out in ((l, torch.zeros_like(logits)), (logits, off_base(logits, by)), (l, off_base(logits, by))):
+        got = mxq.mx_route_backward(off_base(grad), li, off_base(want[0]), score, grad_logits=out)
+        assert torch.equal(got, want_d)
+
+
+def order(c):
+    """What a choice is ordered by: excluded ones last, NaN before them, then numbers."""
+    return (0, 0.0) if c == -np.inf else (1, 0.0) if np.isnan(c) else (2, float(c))
+
+
+def plain_route(c, k, groups, top):
+    """One token's experts from its choices c, with NaN and -inf among them; and the least distance
+    between two numbers that were compared and decided something."""
+    size, near = len(c) // groups, np.inf
+    allowed = range(len(c))
+    if 1 < groups and top < groups:
+        keys = []
+        for g in range(groups):
+            best = sorted((order(x) for x in c[g * size:(g + 1) * size]), reverse=True)[:2]
+            if best[0][0] < 2 or len(best) == 1 or best[1][0] == 0:
+                keys.append(best[0])
+            else:
+                keys.append(best[0] if best[1][0] == 0 else
+                            (1, 0.0) if best[1][0] == 1 else (2, best[0][1] + best[1][1]))
+        ranked = sorted(range(groups), key=lambda g: (keys[g], -g), reverse=True)
+        if keys[ranked[top - 1]][0] == 2 and keys[ranked[top]][0] == 2:
+            near = keys[ranked[top - 1]][1] - keys[ranked[top]][1]
+        allowed = [e for g in sorted(ranked[:top]) for e in range(g * size, (g + 1) * size)]
+    ranked = sorted(allowed, key=lambda e: (order(c[e]), -e), reverse=True)
+    for a, b in zip(ranked[:k], ranked[1:k + 1]):
+        if order(c[a])[0] == 2 and order(c[b])[0] == 2:
+            near = min(near, c[a] - c[b])
+    chosen = [e if order(c[e])[0] else -1 for e in ranked[:k]]
+    return chosen + [-1] * (k - len(chosen)), near
+
+
+@pytest.mark.parametrize("E,k,groups,top", [(32, 6, 8, 3), (60, 7, 5, 2), (64, 6, 16, 5), (256, 8, 8, 4),
+                                            (32, 3, 32, 4), (24, 8, 1, 1)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_of_nan_and_masked_choices_in_groups(E, k, groups, top, biased):
+    rng = np.random.default_rng(E + k)
+    T = 200
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    l[rng.random((T, E)) < 0.25] = np.nan
+    l[rng.random((T, E)) < 0.25] = -np.inf
+    size = E // groups
+    for t in range(0, T, 4):  # groups of nothing but NaN, of nothing, of one number
+        g = rng.integers(0, groups, 3)
+        l[t, g[0] * size:(g[0] + 1) * size] = np.nan
+        l[t, g[1] * size:(g[1] + 1) * size] = -np.inf
+        l[t, g[2] * size:(g[2] + 1) * size] = -np.inf
+        l[t, g[2] * size] = 2.0
+    l[1], l[2] = np.nan, -np.inf
+    bias = (rng.standard_normal(E) * 0.2).astype(np.float32) if biased else None
+    experts, weights = mxq.mx_route(torch.from_numpy(l).cuda(), k, mxq.SIGMOID,
+                                    torch.from_numpy(bias).cuda() if biased else None, groups=groups,
+                                    top_groups=top, renormalize=False)
+    experts, weights = cpu(experts), cpu(weights)
+    sure = 0
+    with np.errstate(over="ignore"):
+        s = 1 / (1 + np.exp(-l.astype(np.float64)))
+    c = np.where(np.isneginf(l), -np.inf, s + (0 if bias is None else bias.astype(np.float64)))
+    for t in range(T):
+        want, near = plain_route(c[t], k, groups, top)
+        if near < 1e-6:
+            continue
+        sure += 1
+        assert experts[t].tolist() == want
+        w = np.where(np.array(want) >= 0, s[t][np.maximum(want, 0)], 0.0)
+        assert (np.abs(weights[t] - w) <= 8 * R.U * w)[~np.isnan(w)].all()
+        assert (np.isnan(weights[t]) == np.isnan(w)).all()
+    assert sure > 0.9 * T
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top", [(64, 6, 1, 1), (256, 8, 8, 4), (777, 8, 1, 1), (1024, 32, 16, 5)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_of_close_scores(score, E, k, groups, top, dtype):
+    """Every token of scores as they come, near ties and (in bf16) exact ones among them: no expert left
+    out is better than one chosen, nor a group, by more than the error of the scores."""
+    rng = np.random.default_rng(E)
+    T = 300
+    logits = torch.from_numpy(rng.standard_normal((T, E))).to(dtype).cuda()
+    bias = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    experts, weights = mxq.mx_route(logits, k, mxq.SOFTMAX if score == "softmax" else mxq.SIGMOID,
+                                    torch.from_numpy(bias).cuda(), groups=groups, top_groups=top)
+    e, w = cpu(experts).astype(np.int64), cpu(weights).astype(np.float64)
+    s = R.scores(logits.cpu().double().numpy(), score)
+    c = s + bias
+    eps = 1e-6  # scores and sums below 2, each a few units of 2^-24 off
+    assert (e >= 0).all() and all(len(set(row)) == k for row in e.tolist())
+    if groups > 1:
+        size = E // groups
+        two = -np.sort(-c.reshape(T, groups, size), 2)[:, :, :2].sum(2)
+        used = np.zeros((T, groups), bool)
+        np.put_along_axis(used, e // size, True, 1)
+        assert (used.sum(1) <= top).all()
+        # any group used is within eps of the best `top`, any clearly among them is open to choice
+        bar = -np.sort(-two, 1)[:, top - 1:top]
+        assert (two[used] >= np.broadcast_to(bar, two.shape)[used] - eps).all()
+        c = np.where(np.repeat(used | (two > bar + eps), size, 1), c, -10.0)
+    got = np.take_along_axis(c, e, 1)
+    assert (np.diff(got, axis=1) <= eps).all()
+    rest = c.copy()
+    np.put_along_axis(rest, e, -10.0, 1)
+    assert (rest.max(1) <= got.min(1) + eps).all()
+    p = np.take_along_axis(s, e, 1)
+    p = p / p.sum(1, keepdims=True)
+    assert (np.abs(w - p) <= 512 * R.U * p).all()
