@@ -14,6 +14,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -31,6 +32,7 @@ class Route(torch.autograd.Function):
         return experts, weights
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, _, grad_weights):
         logits, experts = ctx.saved_tensors
         return mxq.mx_route_backward(grad_weights.contiguous(), logits, experts, mxq.SOFTMAX), None
@@ -45,6 +47,7 @@ class Combine(torch.autograd.Function):
         return mxq.mx_combine(y, slots, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         dy, dweights = mxq.mx_combine_backward(dout.contiguous(), *ctx.saved_tensors)
         return dy, None, dweights
@@ -60,12 +63,15 @@ class Linear(torch.autograd.Function):
         return mxq.mx_gemm_b128(*mxq.mx_quantize_b128_rows(x), codes, scales)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, codes_t, scales_t = ctx.saved_tensors
-        dy = dy.contiguous()
-        dx = mxq.mx_gemm_b128(*mxq.mx_quantize_b128_rows(dy), codes_t, scales_t)
-        dw = mxq.mx_gemm_b128(*mxq.mx_quantize_b128_cols(dy), *mxq.mx_quantize_b128_cols(x),
-                              mxq.B128_ROWS, out_dtype=torch.float32)
+        dy, dx, dw = dy.contiguous(), None, None
+        if ctx.needs_input_grad[0]:
+            dx = mxq.mx_gemm_b128(*mxq.mx_quantize_b128_rows(dy), codes_t, scales_t)
+        if ctx.needs_input_grad[1]:
+            dw = mxq.mx_gemm_b128(*mxq.mx_quantize_b128_cols(dy), *mxq.mx_quantize_b128_cols(x),
+                                  mxq.B128_ROWS, out_dtype=torch.float32)
         return dx, dw
 
 
@@ -76,21 +82,22 @@ class ExpertLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, row_offsets, tokens=None, slots=None):
         codes, scales, codes_t, scales_t = mxq.mx_quantize_b128_blocks(w.bfloat16(), transpose=True)
-        ctx.save_for_backward(x, codes_t, scales_t, row_offsets)
-        ctx.order = tokens, slots
+        ctx.save_for_backward(x, codes_t, scales_t, row_offsets, tokens, slots)
         return mxq.mx_gemm_b128_grouped(*mxq.mx_quantize_b128_rows(x, tokens), codes, scales, row_offsets)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
-        x, codes_t, scales_t, row_offsets = ctx.saved_tensors
-        tokens, slots = ctx.order
-        dy = dy.contiguous()
-        dx = mxq.mx_gemm_b128_grouped(*mxq.mx_quantize_b128_rows(dy), codes_t, scales_t, row_offsets)
-        if slots is not None:
-            dx = mxq.mx_combine(dx, slots)  # weights of one: the sum of a token's rows
-        dw = mxq.mx_gemm_b128_grouped_wgrad(*mxq.mx_quantize_b128_cols(dy, None, row_offsets),
-                                            *mxq.mx_quantize_b128_cols(x, tokens, row_offsets),
-                                            row_offsets)
+        x, codes_t, scales_t, row_offsets, tokens, slots = ctx.saved_tensors
+        dy, dx, dw = dy.contiguous(), None, None
+        if ctx.needs_input_grad[0]:
+            dx = mxq.mx_gemm_b128_grouped(*mxq.mx_quantize_b128_rows(dy), codes_t, scales_t, row_offsets)
+            if slots is not None:
+                dx = mxq.mx_combine(dx, slots)  # weights of one: the sum of a token's rows
+        if ctx.needs_input_grad[1]:
+            dw = mxq.mx_gemm_b128_grouped_wgrad(*mxq.mx_quantize_b128_cols(dy, None, row_offsets),
+                                                *mxq.mx_quantize_b128_cols(x, tokens, row_offsets),
+                                                row_offsets)
         return dx, dw, None, None, None
 
 

@@ -4,7 +4,8 @@ Every function here has the name of the C entry point it calls (include/mxq.h) a
 argument marshalling only: it checks tensor device/dtype/shape, allocates outputs with torch
 when the caller passes none, and hands raw device pointers and the current CUDA stream to the
 library. All computation runs in the library's sm_103a kernels. If libmxq.so is missing the
-calls raise; there is no fallback.
+calls raise; there is no fallback. No call records anything for autograd: results are cut from the
+graph of their inputs, gradients have calls of their own (examples/expert_layer.py joins them).
 """
 
 from __future__ import annotations

@@ -514,3 +514,60 @@ def test_route_of_close_scores(score, E, k, groups, top, dtype):
     p = np.take_along_axis(s, e, 1)
     p = p / p.sum(1, keepdims=True)
     assert (np.abs(w - p) <= 512 * R.U * p).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# the example's autograd functions
+# ---------------------------------------------------------------------------------------------
+def example_layer():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer_edges", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("frozen", [("up",), ("up", "down", "shared"), ("router",)])
+def test_example_computes_the_gradients_that_are_asked_for(monkeypatch, frozen):
+    example = example_layer()
+    torch.manual_seed(1)
+    layer = example.ExpertLayer(256, 128, 8, 2).cuda()
+    x = torch.randn(50, 256, device="cuda").bfloat16().requires_grad_()
+    dy = torch.randn(50, 256, device="cuda").bfloat16()
+    layer(x).backward(dy)
+    want = {n: p.grad.clone() for n, p in layer.named_parameters()}
+    layer.zero_grad()
+    for name in frozen:
+        getattr(layer, name).requires_grad_(False)
+    calls = []
+    real = mxq.mx_gemm_b128_grouped_wgrad
+    monkeypatch.setattr(mxq, "mx_gemm_b128_grouped_wgrad", lambda *a, **k: calls.append(1) or real(*a, **k))
+    layer(x).backward(dy)
+    assert len(calls) == 2 - len({"up", "down"} & set(frozen))
+    for name, p in layer.named_parameters():
+        assert p.grad is None if name in frozen else torch.equal(p.grad, want[name])
+
+
+def test_example_refuses_second_derivatives():
+    example = example_layer()
+    layer = example.ExpertLayer(128, 64, 4, 2).cuda()
+    x = torch.randn(9, 128, device="cuda").bfloat16().requires_grad_()
+    (dx,) = torch.autograd.grad(layer(x).float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.float().square().sum().backward()
+
+
+def test_example_keeps_no_tensor_outside_autograds_own_list():
+    example = example_layer()
+    torch.manual_seed(2)
+    w = torch.randn(4, 64, 128, device="cuda", requires_grad=True)
+    x = torch.randn(9, 128, device="cuda").bfloat16().requires_grad_()
+    experts, _ = mxq.mx_route(torch.randn(9, 4, device="cuda"), 2)
+    row_offsets, tokens, slots = mxq.mx_route_plan(experts, 4)
+    y = example.ExpertLinear.apply(x, w, row_offsets, tokens, slots)
+    tokens.add_(0)  # a change between forward and backward is noticed
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
