@@ -348,7 +348,7 @@ mx_status mx_route_plan(const int32_t* experts, int64_t T, int k, int E, int64_t
  * 32-byte and scales 4-byte aligned. A last block may be shorter than 128.
  *
  * rows: 1 x 128 blocks along K of R rows. index (DEVICE int32 [R]) names the row of x [M, K] that
- * each of them is (an entry outside [0, M) gives a row of zeros); index NULL: R = M, row for row.
+ * each of them is (an entry outside [0, M) gives a row of zeros); index NULL: R = M, row for row, or R = 0.
  *   codes [R, K]; scales [ceil(K / 128), R].
  * cols: 128 x 1 blocks along the rows, written transposed, for products that contract over the
  * rows of x. Rows as above; row_offsets (DEVICE int64 [E + 1]) makes each expert's rows start a

@@ -219,7 +219,7 @@ mx_status mx_b128_padded_rows(int64_t R, int E, int64_t* rows) {
 mx_status mx_quantize_b128_rows(const void* x, int64_t M, int64_t K, const int32_t* index, int64_t R,
                                 void* codes, float* scales, void* stream) {
   if (!sizes_ok(M, K) || !sizes_ok(R, K) || K % 32 != 0) return MX_ERR_SHAPE;
-  if (!index && R != M) return MX_ERR_SHAPE;
+  if (!index && R != M && R != 0) return MX_ERR_SHAPE;
   if (R == 0 || K == 0) return MX_OK;
   if ((M > 0 && !x) || !codes || !scales) return MX_ERR_NULL;
   if (!aligned(x, 32) || !aligned(codes, 32) || !aligned(scales, 4) || !aligned(index, 4)) {
@@ -241,7 +241,7 @@ mx_status mx_quantize_b128_cols(const void* x, int64_t M, int64_t K, const int32
                                 const int64_t* row_offsets, int E, void* codes, float* scales,
                                 void* stream) {
   if (!sizes_ok(M, K) || !sizes_ok(R, K) || K % 32 != 0) return MX_ERR_SHAPE;
-  if (!index && R != M) return MX_ERR_SHAPE;
+  if (!index && R != M && R != 0) return MX_ERR_SHAPE;
   if (!row_offsets && E != 1) return MX_ERR_SHAPE;
   int64_t rows = 0;
   const mx_status st = mx_b128_padded_rows(R, E, &rows);

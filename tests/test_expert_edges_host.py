@@ -49,3 +49,13 @@ def test_grouped_give_up(L):
         return L.mx_selftest_gemm_b128_grouped_give_up(P, P, P, P, off, E, M, 128, 128, c, limit, None)
     assert f(limit=0) == SHAPE and f(limit=100_000_001) == SHAPE and f(M=0) == SHAPE and f(E=0) == SHAPE
     assert f(off=None) == NULL and f(c=None) == NULL and f(c=P + 8) == ALIGN
+
+
+def test_no_rows_need_no_index(L):
+    """An empty index has no address: without rows there is nothing that it could name."""
+    r = L.mx_quantize_b128_rows  # (x, M, K, index, R, codes, scales, stream)
+    assert r(P, 4, 64, None, 0, None, None, None) == OK
+    assert r(P, 4, 64, None, 3, P, P, None) == SHAPE
+    c = L.mx_quantize_b128_cols  # (x, M, K, index, R, offsets, E, codes, scales, stream)
+    assert c(P, 4, 64, None, 0, None, 1, None, None, None) == OK
+    assert c(P, 4, 64, None, 3, P, 2, P, P, None) == SHAPE

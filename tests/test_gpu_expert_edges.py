@@ -571,3 +571,17 @@ def test_example_keeps_no_tensor_outside_autograds_own_list():
     tokens.add_(0)  # a change between forward and backward is noticed
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def test_an_empty_index_gathers_no_rows():
+    x = torch.ones(40, 256, device="cuda", dtype=torch.bfloat16)
+    none = torch.empty(0, device="cuda", dtype=torch.int32)
+    codes, scales = mxq.mx_quantize_b128_rows(x, none)
+    assert codes.shape == (0, 256) and scales.shape == (2, 0)
+    codes, scales = mxq.mx_quantize_b128_cols(x, none)
+    assert codes.shape == (256, 0) and scales.shape == (0, 256)
+    offsets = torch.zeros(4, device="cuda", dtype=torch.int64)
+    u = mxq.mx_quantize_b128_cols(x, none, offsets)
+    assert not mxq.mx_gemm_b128_grouped_wgrad(*u, *u, offsets).any()
+    b = mxq.mx_quantize_b128_blocks(torch.ones(3, 64, 256, device="cuda", dtype=torch.bfloat16))
+    assert mxq.mx_gemm_b128_grouped(*mxq.mx_quantize_b128_rows(x, none), *b, offsets).shape == (0, 64)
