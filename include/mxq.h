@@ -358,7 +358,8 @@ mx_status mx_route_plan(const int32_t* experts, int64_t T, int k, int E, int64_t
  *   what lies past the last expert's is not written.
  * blocks: 128 x 128 squares of each of `batch` matrices [M, K] (M * K rows following one another).
  *   codes [batch, M, K], scales [batch, ceil(M / 128), ceil(K / 128)], and unless NULL the
- *   transposed operand: codes_t [batch, K, M], scales_t [batch, ceil(K / 128), ceil(M / 128)].
+ *   transposed operand: codes_t [batch, K, M], scales_t [batch, ceil(K / 128), ceil(M / 128)]
+ *   (five times slower where M is no multiple of 16, whose columns are then written byte by byte).
  */
 mx_status mx_b128_padded_rows(int64_t R, int E, int64_t* rows);
 

@@ -10,8 +10,9 @@
 //
 // All three kernels are bound by memory: 2 bytes read and 1 written per element (2 written when
 // the square kernel writes both orders), scales 1/32 of a byte. x[8192, 8192], where a plain copy of
-// as many bytes takes 30 us: rows 31 us (6.6 TB/s), columns 31 (6.5), squares 30 (6.7), squares in both
-// orders 42 (6.4).
+// as many bytes takes 30 us: rows 30 us (6.7 TB/s), columns 32 (6.3), squares 30 (6.7), squares in both
+// orders 42 (6.4). The transposed squares of a matrix whose rows are no multiple of 16 leave byte by byte:
+// 8200 rows 210 us.
 #include "mx_device.cuh"
 #include "mx_expert.h"
 #include "mx_launch.h"
@@ -224,7 +225,7 @@ __device__ __forceinline__ int64_t count_blocks(const int* offsets, int E) {
 // of a product that contracts over the rows of x. The transposition goes through shared memory, a tile
 // of 128 rows being one block. A CTA walks a run of tiles along x's rows, and while it reduces, converts
 // and writes one, the next is on its way into shared memory, every thread's pieces to places of its
-// own: four CTAs keep 128 KB of an SM's loads in flight (x[8192, 8192] 31.3 us; a tile's own loads in
+// own: four CTAs keep 128 KB of an SM's loads in flight (x[8192, 8192] 32 us; a tile's own loads in
 // registers, nothing on its way meanwhile, 36.6).
 struct ColsShared {
   uint4 next[8][kTileThreads];  // the tile on its way

@@ -483,9 +483,9 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 // L2 prefetch of [p, p + bytes) (p 16-byte aligned, bytes a multiple of 16, inside one
 // allocation). A prefetch is a hint: it returns no data to the thread and has no effect on the
-// values any load observes. The kernels issue it for their first input bytes BEFORE pdl_wait,
-// while the previous kernel on the stream drains: L2 is the point of coherence of every SM of
-// the device, so if that kernel still writes those bytes, its writes update the L2 lines and
+// values any load observes. The kernels (those of expert layers aside) issue it for their first
+// input bytes BEFORE pdl_wait, while the previous kernel on the stream drains: L2 is the point of
+// coherence of every SM of the device, so if that kernel still writes those bytes, its writes update the L2 lines and
 // the loads issued after pdl_wait read the new values; they only find the lines on chip
 // instead of waiting for DRAM. Measured on GB300, back to back: QDQ of x[8192, 8192]
 // 43.4 -> 41.4 us, quantize 2-5% faster, rotate+quantize about 1.1 us less per launch.

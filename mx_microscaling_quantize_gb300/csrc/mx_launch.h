@@ -107,8 +107,8 @@ struct GemmArgs {
   unsigned long long wait_limit_ns;  // pipeline waits (drains always allow 2 s)
 };
 
-// Tensor map of a row-major [rows, cols] matrix of 1- or 2-byte elements, boxes of box_rows x
-// box_cols, the given swizzle; loads read zeros out of bounds, stores drop what falls outside.
+// Tensor map of a row-major [rows, cols] matrix of elements of elem_bytes, boxes of box_rows x box_cols,
+// the given swizzle; loads read zeros out of bounds, stores drop what falls outside.
 cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                                CUtensorMapDataType type, int elem_bytes, int box_cols,
                                int box_rows, CUtensorMapSwizzle swizzle);

@@ -819,8 +819,7 @@ cudaError_t launch_fmt(int out_kind, bool swz, int g, const RotArgs& a, cudaStre
 
 }  // namespace
 
-// Tensor map of a row-major [rows, cols] matrix of 1- or 2-byte elements, boxes of box_rows x
-// box_cols, the given swizzle; loads read zeros out of bounds, stores drop what falls outside.
+// The driver's entry point that encodes tensor maps, looked up once (null where it is missing).
 static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
@@ -836,6 +835,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return encode;
 }
 
+// Tensor map of a row-major [rows, cols] matrix, boxes of box_rows x box_cols, the given swizzle; loads
+// read zeros out of bounds, stores drop what falls outside.
 cudaError_t make_tensor_map_2d(CUtensorMap* map, const void* base, int64_t rows, int64_t cols,
                                CUtensorMapDataType type, int elem_bytes, int box_cols,
                                int box_rows, CUtensorMapSwizzle swizzle) {

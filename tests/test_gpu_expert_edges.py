@@ -585,3 +585,86 @@ def test_an_empty_index_gathers_no_rows():
     assert not mxq.mx_gemm_b128_grouped_wgrad(*u, *u, offsets).any()
     b = mxq.mx_quantize_b128_blocks(torch.ones(3, 64, 256, device="cuda", dtype=torch.bfloat16))
     assert mxq.mx_gemm_b128_grouped(*mxq.mx_quantize_b128_rows(x, none), *b, offsets).shape == (0, 64)
+
+
+# ---------------------------------------------------------------------------------------------
+# stream order under programmatic dependent launch
+# ---------------------------------------------------------------------------------------------
+def test_dependent_expert_calls_keep_stream_order():
+    """A chain in which every kernel of an expert layer reads what the launch before it has just written,
+    index lists, slots, weights and workspaces among it, into buffers that the steps before read: back to
+    back, and in a graph, the bytes are those of a synchronization after every call."""
+    rng = np.random.default_rng(41)
+    T, E, k, N, K = 3000, 24, 4, 512, 1024
+    sources = [bf16_inputs(rng, T, K, False) for _ in range(3)]
+    logit_sources = [torch.from_numpy(rng.standard_normal((T, E))).float().cuda() for _ in range(3)]
+    w = mxq.mx_quantize_b128_blocks(torch.stack([bf16_inputs(rng, N, K, False) for _ in range(E)]))
+    shared = mxq.mx_quantize_b128_blocks(bf16_inputs(rng, N, K, False))
+    rows, P = T * k, mxq.mx_b128_padded_rows(T * k, E)
+    new = lambda *s, dtype=torch.float32: torch.zeros(*s, device="cuda", dtype=dtype)  # noqa: E731
+    bf, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    b = dict(x=new(T, K, dtype=bf), logits=new(T, E), experts=new(T, k, dtype=i32), weights=new(T, k),
+             offsets=new(E + 1, dtype=torch.int64), tokens=new(rows, dtype=i32), slots=new(T, k, dtype=i32),
+             work=new(mxq.mx_route_plan_workspace(T, k, E), dtype=u8),
+             rc=new(rows, K, dtype=u8), rs=new(K // 128, rows), y=new(rows, N, dtype=bf),
+             out=new(T, N, dtype=bf), dy=new(rows, N, dtype=bf), dw=new(T, k), dl=new(T, E),
+             uc=new(N, P, dtype=u8), us=new(P // 128, N), vc=new(K, P, dtype=u8), vs=new(P // 128, K),
+             grad=new(E, N, K), dc=new(T, K, dtype=u8), ds=new(K // 128, T), one=new(T, N, dtype=bf),
+             few=new(7, N, dtype=bf), fc=new(7, K, dtype=u8), fs=new(K // 128, 7), wc=new(N, N, dtype=u8),
+             ws=new(N // 128, N // 128), wt=new(N, N, dtype=u8), wst=new(N // 128, N // 128))
+
+    def chain(sync=False):
+        seen = []
+        for i in range(3):
+            for step in (
+                lambda: b["x"].copy_(sources[i]), lambda: b["logits"].copy_(logit_sources[i]),
+                lambda: mxq.mx_route(b["logits"], k, experts=b["experts"], weights=b["weights"]),
+                lambda: mxq.mx_route_plan(b["experts"], E, row_offsets=b["offsets"], tokens=b["tokens"],
+                                          slots=b["slots"], workspace=b["work"]),
+                lambda: mxq.mx_quantize_b128_rows(b["x"], b["tokens"], codes=b["rc"], scales=b["rs"]),
+                lambda: mxq.mx_gemm_b128_grouped(b["rc"], b["rs"], *w, b["offsets"], c=b["y"]),
+                lambda: mxq.mx_combine(b["y"], b["slots"], b["weights"], out=b["out"]),
+                lambda: mxq.mx_combine_backward(b["out"], b["y"], b["slots"], b["weights"], dy=b["dy"],
+                                                dweights=b["dw"]),
+                lambda: mxq.mx_route_backward(b["dw"], b["logits"], b["experts"], grad_logits=b["dl"]),
+                lambda: mxq.mx_quantize_b128_cols(b["dy"], None, b["offsets"], codes=b["uc"], scales=b["us"]),
+                lambda: mxq.mx_quantize_b128_cols(b["x"], b["tokens"], b["offsets"], codes=b["vc"],
+                                                  scales=b["vs"]),
+                lambda: mxq.mx_gemm_b128_grouped_wgrad(b["uc"], b["us"], b["vc"], b["vs"], b["offsets"],
+                                                       c=b["grad"]),
+                lambda: mxq.mx_quantize_b128_rows(b["x"], codes=b["dc"], scales=b["ds"]),
+                lambda: mxq.mx_gemm_b128(b["dc"], b["ds"], *shared, c=b["one"]),
+                lambda: mxq.mx_quantize_b128_blocks(b["one"][:N], transpose=True, codes=b["wc"],
+                                                    scales=b["ws"], codes_t=b["wt"], scales_t=b["wst"]),
+                lambda: mxq.mx_quantize_b128_rows(b["x"][:7], codes=b["fc"], scales=b["fs"]),
+                lambda: mxq.mx_gemm_b128(b["fc"], b["fs"], *shared, c=b["few"]),
+            ):
+                step()
+                if sync:
+                    torch.cuda.synchronize()
+            seen.append({name: t.clone() for name, t in b.items() if name != "work"})
+            if sync:
+                torch.cuda.synchronize()
+        return seen
+
+    def same(got):
+        torch.cuda.synchronize()
+        for g, h in zip(got, want):
+            for name in g:
+                used = slice(None)
+                if name in ("uc", "vc", "us", "vs"):  # past the last expert's blocks nothing is written
+                    n = int(((h["offsets"].diff() + 127) // 128).sum())
+                    used = (slice(None), slice(n * 128)) if name in ("uc", "vc") else slice(n)
+                assert torch.equal(g[name][used], h[name][used]), name
+
+    want = chain(sync=True)
+    for _ in range(5):
+        same(chain())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured = chain()
+    for _ in range(3):
+        graph.replay()
+        same(captured)
