@@ -687,21 +687,20 @@ __device__ __forceinline__ void produce(const CUtensorMap& pmap, const CUtensorM
       }
     }
   }
-  // Loads in flight land before the CTA's shared memory goes away. A pair's are counted on its first CTA's
-  // barriers, and each release of a stage arrives at both CTAs: a CTA that has seen every stage of its own
-  // released has nothing more to come, neither a load that the pair's products needed nor an arrival
-  // from the other CTA. After a give-up, in which the two may not have issued the same steps, the first
-  // waits for what it sees, and each also lets a millisecond pass, a thousand times what a load or an
-  // arrival takes.
-  if constexpr (C::CTAS == 2) {
-    for (int i = 0; i < stages && !failed; ++i) {
-      warp_wait(smem_u32(s.empty + st), parity, &failed, a);
-      if (++st == stages) {
-        st = 0;
-        parity ^= 1;
-      }
+  // A CTA that has seen every stage released has nothing more to come: its loads have landed, and the
+  // commits' arrivals at its stages' barriers, which nothing else waits for (in a pair they come from the
+  // other CTA), are in. After a give-up the loads are waited for by their own barriers; a
+  // pair's are counted on its first CTA's, and as the two may then not have issued the same steps, each
+  // also lets a millisecond pass, a thousand times what a load or an arrival takes.
+  for (int i = 0; i < stages && !failed; ++i) {
+    warp_wait(smem_u32(s.empty + st), parity, &failed, a);
+    if (++st == stages) {
+      st = 0;
+      parity ^= 1;
     }
-    if (!failed) return;
+  }
+  if (!failed) return;
+  if constexpr (C::CTAS == 2) {
     const unsigned long long begin = global_ns();
     while (global_ns() - begin < 1000000ull) {
     }
