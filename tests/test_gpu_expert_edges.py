@@ -668,3 +668,43 @@ def test_dependent_expert_calls_keep_stream_order():
     for _ in range(3):
         graph.replay()
         same(captured)
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])  # the default stream by both its handles, the thread's own
+def test_streams_by_their_special_handles(handle):
+    rng = np.random.default_rng(5)
+    x = bf16_inputs(rng, 640, 512, False)
+    logits = torch.from_numpy(rng.standard_normal((640, 16))).float().cuda()
+
+    def work(**at):
+        experts, weights = mxq.mx_route(logits, 2, **at)
+        offsets, tokens, slots = mxq.mx_route_plan(experts, 16, **at)
+        return [experts, weights, offsets, tokens, slots, *mxq.mx_quantize_b128_rows(x, tokens, **at),
+                *mxq.mx_quantize(x, mxq.E4M3, **at), mxq.mx_combine(x, slots, weights, **at)]
+
+    want = work()
+    torch.cuda.synchronize()
+    for current in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(current):
+            got = work(stream=handle)
+            torch.cuda.synchronize()
+            assert all(torch.equal(g, w) for g, w in zip(got, want))
+            del got
+
+
+def test_stream_argument_inside_a_capture():
+    rng = np.random.default_rng(6)
+    logits = torch.from_numpy(rng.standard_normal((700, 16))).float().cuda()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+    def work(**at):
+        experts, weights = mxq.mx_route(logits, 2, **at)
+        return [experts, weights, *mxq.mx_route_plan(experts, 16, **at)]
+
+    want = work()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        got = work(stream=side.cuda_stream)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
