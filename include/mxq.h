@@ -432,6 +432,101 @@ mx_status mx_combine_backward_whole(const void* dout, const void* y, const int32
                                     const float* weights, int64_t T, int k, int64_t R, int64_t N,
                                     void* dy, float* dweights, void* workspace, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Between the products of an 8-bit training step: layer norm and activation whose output is an
+ * operand of the next product, activation checkpoints in 8 bits, and what the backward pass makes of
+ * them. A checkpoint is E4M3 codes [M, K] with scales [ceil(K / 128), M] as mx_quantize_b128_rows
+ * writes them; it stands for the values code * scale, one fp32 product each (a block with a NaN or an
+ * infinity: NaN). The conventions at the top of this file hold; alignment is stated per call. These
+ * have no counterpart on the pages.
+ * ------------------------------------------------------------------------------------------ */
+
+/* a checkpoint, where a call takes one in place of bf16 or fp32 */
+#define MX_TYPE_E4M3_B128 2
+
+/*
+ * Layer norm of the M rows of x [M, K] (x_type: MX_TYPE_BF16 or MX_TYPE_FP32):
+ *   mean = sum_i x_i / K (0 when center == 0: the root-mean-square form),
+ *   rstd = 1 / sqrt(sum_i (x_i - mean)^2 / K + eps),  y_i = (x_i - mean) rstd weight_i + bias_i.
+ * In fp32, the variance from the differences to the mean; y rounded once. weight, bias: [K] of w_type,
+ * NULL for ones and zeros (w_type is then not used, but must be valid). mean, rstd: fp32 [M] or NULL,
+ * what mx_layer_norm_backward takes. K <= 16384.
+ *
+ * mx_layer_norm: y [M, K] of y_type. Alignment: that of the elements; x and y on 32 and weight and
+ *   bias on 16 bytes with K % 16 == 0 take wide loads.
+ * mx_layer_norm_b128: y as the operand that mx_quantize_b128_rows makes of the unrounded y: codes
+ *   [M, K], scales [ceil(K / 128), M]. x_codes, x_scales: unless NULL, a checkpoint of x. K % 32 == 0;
+ *   x and codes 32-byte, weight and bias 16-byte aligned.
+ */
+mx_status mx_layer_norm(const void* x, int x_type, const void* weight, const void* bias, int w_type,
+                        int64_t M, int64_t K, float eps, int center, void* y, int y_type, float* mean,
+                        float* rstd, void* stream);
+
+mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, const void* bias, int w_type,
+                             int64_t M, int64_t K, float eps, int center, void* codes, float* scales,
+                             void* x_codes, float* x_scales, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of mx_layer_norm. dy [M, K] of dy_type; x as the forward call read it (bf16 or fp32), or a
+ * checkpoint of it (MX_TYPE_E4M3_B128 with x_scales, K % 32 == 0); mean, rstd: as the forward call wrote
+ * them (mean NULL: not centred). With xhat_i = (x_i - mean) rstd and g_i = dy_i weight_i:
+ *   dx_i = rstd (g_i - sum g / K - xhat_i sum(g xhat) / K), the second term only when centred,
+ *   dweight_i = sum over the rows of dy_i xhat_i,  dbias_i = sum over the rows of dy_i,
+ * dx of dx_type, dweight and dbias fp32 [K] or NULL (not wanted; zeros when M == 0). Sums in fp32, in an
+ * order that the sizes and the device alone decide. workspace: device memory of
+ * mx_layer_norm_backward_workspace() bytes, 4-byte aligned (NULL will do without dweight and dbias); two
+ * calls that may run at the same time need one each. Alignment: that of the elements; dy, x and dx on 16
+ * bytes with K % 8 == 0 take wide loads. dx must not overlap the inputs.
+ */
+mx_status mx_layer_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes);
+
+mx_status mx_layer_norm_backward(const void* dy, int dy_type, const void* x, int x_type,
+                                 const float* x_scales, const float* mean, const float* rstd,
+                                 const void* weight, int w_type, int64_t M, int64_t K, void* dx,
+                                 int dx_type, float* dweight, float* dbias, void* workspace,
+                                 void* stream);
+
+/* activations: x s(x) with s the logistic function; x Phi(x); x s(2 z), z = sqrt(2 / pi) (x + 0.044715 x^3) */
+#define MX_ACT_SILU 0
+#define MX_ACT_GELU 1
+#define MX_ACT_GELU_TANH 2
+
+/*
+ * Activation of R rows into the operand of the next product. gated != 0: u is [R, 2 H] = [gate | up],
+ * h = f(gate) * up; else u is [R, H], h = f(u). u: bf16; h in fp32, then codes [R, H] and scales
+ * [ceil(H / 128), R] as mx_quantize_b128_rows makes them of the unrounded h. u_codes, u_scales: unless
+ * NULL, a checkpoint of u (what mx_quantize_b128_rows makes of it). H % 32 == 0; gated with a checkpoint
+ * H % 128 == 0. u and codes 32-byte aligned.
+ *
+ * Backward: dh bf16 [R, H]; u bf16 or a checkpoint (u_type MX_TYPE_E4M3_B128 with u_scales). du, bf16
+ * like u, is dh up f'(gate) | dh f(gate), or dh f'(u); du_codes, du_scales: the operand that
+ * mx_quantize_b128_rows makes of the unrounded du, for the product that goes on backward. Either may be
+ * NULL, not both. H % 32 == 0; gated with a checkpoint or an operand H % 128 == 0. All but the scales
+ * 32-byte aligned.
+ */
+mx_status mx_activation_b128(const void* u, int64_t R, int64_t H, int kind, int gated, void* codes,
+                             float* scales, void* u_codes, float* u_scales, void* stream);
+
+mx_status mx_activation_backward(const void* dh, const void* u, int u_type, const float* u_scales,
+                                 int64_t R, int64_t H, int kind, int gated, void* du, void* du_codes,
+                                 float* du_scales, void* stream);
+
+/*
+ * mx_quantize_b128_cols of the values of a checkpoint (codes [M, K], scales [ceil(K / 128), M]): the
+ * operand of the weights' gradient, without bf16 rows. index, R, row_offsets, E and the results as
+ * there. codes and out_codes 32-byte aligned.
+ */
+mx_status mx_requantize_b128_cols(const void* codes, const float* scales, int64_t M, int64_t K,
+                                  const int32_t* index, int64_t R, const int64_t* row_offsets, int E,
+                                  void* out_codes, float* out_scales, void* stream);
+
+/*
+ * Values of a checkpoint (rows `index` of it, as in mx_quantize_b128_rows): y [R, K] of y_type
+ * (MX_TYPE_BF16, rounded once, or MX_TYPE_FP32). codes and y 32-byte aligned, K % 32 == 0.
+ */
+mx_status mx_dequantize_b128_rows(const void* codes, const float* scales, int64_t M, int64_t K,
+                                  const int32_t* index, int64_t R, void* y, int y_type, void* stream);
+
 /*
  * Diagnostics: the rotated values y = x_chunk * H exactly as mx_rotate_quantize computes them
  * before quantization with the same rot_kind (same device code), written as fp32 [M, K] to

@@ -30,6 +30,7 @@ ROT_AUTO = 2      # the same statement; the library takes the kernel measured fa
 SOFTMAX, SIGMOID = 0, 1          # scores of mx_route
 B128_BLOCKS, B128_ROWS = 0, 1    # forms of B's scales in mx_gemm_b128
 BLOCK128 = 128
+SILU, GELU, GELU_TANH = 0, 1, 2  # activations of mx_activation_b128
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmxq.so")
@@ -47,6 +48,9 @@ EXPORTS = (
     "mx_gemm_b128_grouped_wgrad", "mx_combine", "mx_combine_backward",
     "mx_combine_backward_whole",
     "mx_selftest_gemm_b128_give_up", "mx_selftest_gemm_b128_grouped_give_up",
+    "mx_layer_norm", "mx_layer_norm_b128", "mx_layer_norm_backward_workspace",
+    "mx_layer_norm_backward", "mx_activation_b128", "mx_activation_backward",
+    "mx_requantize_b128_cols", "mx_dequantize_b128_rows",
 )
 
 
@@ -105,6 +109,16 @@ def lib() -> ctypes.CDLL:
         "mx_combine_backward_whole": (i32, [p, p, p, p, i64, i32, i64, i64, p, p, p, p]),
         "mx_selftest_gemm_b128_give_up": (i32, [p, p, p, p, i64, i64, i64, i32, p, i64, p]),
         "mx_selftest_gemm_b128_grouped_give_up": (i32, [p, p, p, p, p, i32, i64, i64, i64, p, i64, p]),
+        "mx_layer_norm": (i32, [p, i32, p, p, i32, i64, i64, ctypes.c_float, i32, p, i32, p, p, p]),
+        "mx_layer_norm_b128": (i32, [p, i32, p, p, i32, i64, i64, ctypes.c_float, i32, p, p, p, p, p,
+                                     p, p]),
+        "mx_layer_norm_backward_workspace": (i32, [i64, i64, pi64]),
+        "mx_layer_norm_backward": (i32, [p, i32, p, i32, p, p, p, p, i32, i64, i64, p, i32, p, p, p,
+                                         p]),
+        "mx_activation_b128": (i32, [p, i64, i64, i32, i32, p, p, p, p, p]),
+        "mx_activation_backward": (i32, [p, p, i32, p, i64, i64, i32, i32, p, p, p, p]),
+        "mx_requantize_b128_cols": (i32, [p, p, i64, i64, p, i64, p, i32, p, p, p]),
+        "mx_dequantize_b128_rows": (i32, [p, p, i64, i64, p, i64, p, i32, p]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -772,3 +786,211 @@ def mx_combine_backward(dout, y, slots, weights, *, dy=None, dweights=None, stre
         _check(lib().mx_combine_backward(_ptr(dout), _ptr(y), _ptr(slots), _ptr(weights), T, k, R, N,
                                          _ptr(dy), _ptr(dweights), _stream_ptr(stream, y)))
     return dy, dweights
+
+
+# ---------------------------------------------------------------------------------------------
+# between the products of an 8-bit training step: layer norm, activation, activation checkpoints
+# ---------------------------------------------------------------------------------------------
+_CHECKPOINT = 2  # MX_TYPE_E4M3_B128
+
+
+def _norm_params(weight, bias, K, like) -> int:
+    """Checks weight and bias; returns their type."""
+    kind = 1
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            if _tensor(t, name, _TYPES, dim=1, like=like).shape[0] != K:
+                raise ValueError(f"{name} must have one value per column")
+            kind = _TYPES[t.dtype]
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same type")
+    return kind
+
+
+def _norm_stats(x, M, center, stats, mean, rstd, stream):
+    if not center and mean is not None:
+        raise ValueError("mean is for a centred norm")
+    if stats or mean is not None or rstd is not None:
+        rstd = _output(rstd, "rstd", (M,), torch.float32, x, stream)
+        if center:
+            mean = _output(mean, "mean", (M,), torch.float32, x, stream)
+    return mean, rstd
+
+
+def mx_layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, center: bool = True,
+                  out_dtype=None, stats: bool = False, y=None, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of x [M, K] (bfloat16 or float32) -> y (of out_dtype, else x's); with stats
+    (y, mean, rstd), float32 [M] for mx_layer_norm_backward. center=False: the root-mean-square form
+    (mean None). weight, bias: [K], bfloat16 or float32."""
+    _tensor(x, "x", _TYPES, dim=2)
+    M, K = x.shape
+    w_type = _norm_params(weight, bias, K, x)
+    dtype = _out_type(out_dtype or x.dtype, y)
+    y = _output(y, "y", (M, K), dtype, x, stream)
+    mean, rstd = _norm_stats(x, M, center, stats, mean, rstd, stream)
+    _check(lib().mx_layer_norm(_ptr(x), _TYPES[x.dtype], _ptr(weight), _ptr(bias), w_type, M, K, eps,
+                               int(center), _ptr(y), _TYPES[dtype], _ptr(mean), _ptr(rstd),
+                               _stream_ptr(stream, x)))
+    return (y, mean, rstd) if rstd is not None else y
+
+
+def mx_layer_norm_b128(x, weight=None, bias=None, *, eps: float = 1e-5, center: bool = True,
+                       stats: bool = False, checkpoint: bool = False, codes=None, scales=None,
+                       mean=None, rstd=None, x_codes=None, x_scales=None, stream=None):
+    """Layer norm of the rows of x [M, K] as an operand: (codes uint8 [M, K], scales float32
+    [ceil(K / 128), M]) as mx_quantize_b128_rows; with stats followed by (mean, rstd), with checkpoint
+    by x in 8 bits (x_codes, x_scales)."""
+    _tensor(x, "x", _TYPES, dim=2)
+    M, K = x.shape
+    w_type = _norm_params(weight, bias, K, x)
+    kb = -(-K // BLOCK128)
+    codes = _output(codes, "codes", (M, K), torch.uint8, x, stream)
+    scales = _output(scales, "scales", (kb, M), torch.float32, x, stream)
+    mean, rstd = _norm_stats(x, M, center, stats, mean, rstd, stream)
+    if checkpoint or x_codes is not None or x_scales is not None:
+        x_codes = _output(x_codes, "x_codes", (M, K), torch.uint8, x, stream)
+        x_scales = _output(x_scales, "x_scales", (kb, M), torch.float32, x, stream)
+    _check(lib().mx_layer_norm_b128(_ptr(x), _TYPES[x.dtype], _ptr(weight), _ptr(bias), w_type, M, K,
+                                    eps, int(center), _ptr(codes), _ptr(scales), _ptr(x_codes),
+                                    _ptr(x_scales), _ptr(mean), _ptr(rstd), _stream_ptr(stream, x)))
+    out = (codes, scales)
+    if rstd is not None:
+        out += (mean, rstd)
+    return out if x_codes is None else out + (x_codes, x_scales)
+
+
+@functools.lru_cache(maxsize=4096)
+def mx_layer_norm_backward_workspace(M: int, K: int) -> int:
+    """Bytes of device memory mx_layer_norm_backward works in."""
+    n = ctypes.c_int64()
+    _check(lib().mx_layer_norm_backward_workspace(M, K, ctypes.byref(n)))
+    return n.value
+
+
+def _checkpoint(codes, scales, name, like=None):
+    """Checks a checkpoint [M, K]; returns its shape."""
+    _tensor(codes, name, torch.uint8, dim=2, like=like)
+    M, K = codes.shape
+    if _tensor(scales, f"{name}'s scales", torch.float32, like=codes).shape != (-(-K // BLOCK128), M):
+        raise ValueError(f"{name}'s scales must be {[-(-K // BLOCK128), M]}")
+    return M, K
+
+
+def mx_layer_norm_backward(dy, x, mean, rstd, weight=None, *, x_scales=None, weight_grad: bool = True,
+                           bias_grad: bool = True, out_dtype=None, dx=None, dweight=None, dbias=None,
+                           workspace=None, stream=None):
+    """Gradients of mx_layer_norm from dy [M, K]: (dx, dweight, dbias), float32 [K], None where not
+    wanted. x: what the norm read, or with x_scales its checkpoint (codes uint8); mean None: not centred.
+    dx is of out_dtype, else of x's type (dy's, where x is a checkpoint)."""
+    _tensor(dy, "dy", _TYPES, dim=2)
+    M, K = dy.shape
+    if x_scales is None:
+        x_type = _TYPES[_tensor(x, "x", _TYPES, dim=2, like=dy).dtype]
+    else:
+        _checkpoint(x, x_scales, "x", like=dy)
+        x_type = _CHECKPOINT
+    if x.shape != dy.shape:
+        raise ValueError("dy and x must be [M, K]")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if (t is not None or name == "rstd") and \
+                _tensor(t, name, torch.float32, dim=1, like=dy).shape[0] != M:
+            raise ValueError(f"{name} must have one value per row")
+    w_type = _norm_params(weight, None, K, dy)
+    dtype = _out_type(out_dtype or (dy.dtype if x_type == _CHECKPOINT else x.dtype), dx)
+    dx = _output(dx, "dx", (M, K), dtype, dy, stream)
+    if weight_grad or dweight is not None:
+        dweight = _output(dweight, "dweight", (K,), torch.float32, dy, stream)
+    if bias_grad or dbias is not None:
+        dbias = _output(dbias, "dbias", (K,), torch.float32, dy, stream)
+    if dweight is not None or dbias is not None:
+        need = mx_layer_norm_backward_workspace(M, K)
+        if workspace is None:
+            workspace = _empty((need,), torch.uint8, dy, stream, scratch=True)
+        elif workspace.device != dy.device or workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace must have {need} bytes on {dy.device}")
+    _check(lib().mx_layer_norm_backward(_ptr(dy), _TYPES[dy.dtype], _ptr(x), x_type, _ptr(x_scales),
+                                        _ptr(mean), _ptr(rstd), _ptr(weight), w_type, M, K, _ptr(dx),
+                                        _TYPES[dtype], _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                        _stream_ptr(stream, dy)))
+    return dx, dweight, dbias
+
+
+def _gate(U: int, gated) -> int:
+    if gated and U % 2:
+        raise ValueError("u must be [R, 2 H]: gate and up")
+    return U // 2 if gated else U
+
+
+def mx_activation_b128(u, kind=SILU, *, gated: bool = True, checkpoint: bool = False, codes=None,
+                       scales=None, u_codes=None, u_scales=None, stream=None):
+    """f(gate) * up of bf16 u = [gate | up] [R, 2 H], or f(u) of [R, H], as an operand: (codes uint8
+    [R, H], scales float32 [ceil(H / 128), R]); with checkpoint followed by u in 8 bits (u_codes,
+    u_scales). kind: SILU, GELU or GELU_TANH."""
+    R, U = _input(u, "u")
+    H = _gate(U, gated)
+    codes = _output(codes, "codes", (R, H), torch.uint8, u, stream)
+    scales = _output(scales, "scales", (-(-H // BLOCK128), R), torch.float32, u, stream)
+    if checkpoint or u_codes is not None or u_scales is not None:
+        u_codes = _output(u_codes, "u_codes", (R, U), torch.uint8, u, stream)
+        u_scales = _output(u_scales, "u_scales", (-(-U // BLOCK128), R), torch.float32, u, stream)
+    _check(lib().mx_activation_b128(_ptr(u), R, H, kind, int(gated), _ptr(codes), _ptr(scales),
+                                    _ptr(u_codes), _ptr(u_scales), _stream_ptr(stream, u)))
+    return (codes, scales) if u_codes is None else (codes, scales, u_codes, u_scales)
+
+
+def mx_activation_backward(dh, u, kind=SILU, *, gated: bool = True, u_scales=None, grad: bool = True,
+                           operand: bool = False, du=None, codes=None, scales=None, stream=None):
+    """Gradient of u from bf16 dh [R, H]: du (bf16, as u); with operand (du, codes, scales), du in 8 bits
+    as mx_quantize_b128_rows, and without grad those two alone. u: bf16, or with u_scales its checkpoint."""
+    R, H = _input(dh, "dh")
+    if u_scales is None:
+        Ru, U = _input(u, "u")
+        u_type = 0
+    else:
+        Ru, U = _checkpoint(u, u_scales, "u")
+        u_type = _CHECKPOINT
+    if u.device != dh.device or Ru != R or _gate(U, gated) != H:
+        raise ValueError(f"u must be {[R, 2 * H if gated else H]} on {dh.device}")
+    operand = operand or codes is not None or scales is not None
+    if not grad and du is None and not operand:
+        raise ValueError("neither the gradient nor its operand is wanted")
+    if grad or du is not None:
+        du = _output(du, "du", (R, U), torch.bfloat16, dh, stream)
+    if operand:
+        codes = _output(codes, "codes", (R, U), torch.uint8, dh, stream)
+        scales = _output(scales, "scales", (-(-U // BLOCK128), R), torch.float32, dh, stream)
+    _check(lib().mx_activation_backward(_ptr(dh), _ptr(u), u_type, _ptr(u_scales), R, H, kind,
+                                        int(gated), _ptr(du), _ptr(codes), _ptr(scales),
+                                        _stream_ptr(stream, dh)))
+    if not operand:
+        return du
+    return (codes, scales) if du is None else (du, codes, scales)
+
+
+def mx_requantize_b128_cols(codes, scales, index=None, row_offsets=None, *, out_codes=None,
+                            out_scales=None, stream=None):
+    """mx_quantize_b128_cols of the values of a checkpoint (codes uint8 [M, K], scales float32
+    [ceil(K / 128), M]) -> (codes uint8 [K, P], scales float32 [P / 128, K])."""
+    M, K = _checkpoint(codes, scales, "codes")
+    R = _row_index(index, codes, M)
+    E = 1 if row_offsets is None else _offsets(row_offsets, codes)
+    P = mx_b128_padded_rows(R, E)
+    out_codes = _output(out_codes, "out_codes", (K, P), torch.uint8, codes, stream)
+    out_scales = _output(out_scales, "out_scales", (P // BLOCK128, K), torch.float32, codes, stream)
+    _check(lib().mx_requantize_b128_cols(_ptr(codes), _ptr(scales), M, K, _ptr(index), R,
+                                         _ptr(row_offsets), E, _ptr(out_codes), _ptr(out_scales),
+                                         _stream_ptr(stream, codes)))
+    return out_codes, out_scales
+
+
+def mx_dequantize_b128_rows(codes, scales, index=None, *, out_dtype=torch.bfloat16, y=None,
+                            stream=None):
+    """Values of a checkpoint (codes uint8 [M, K], scales float32 [ceil(K / 128), M]), rows `index` of
+    it -> [R, K], bfloat16 or float32."""
+    M, K = _checkpoint(codes, scales, "codes")
+    R = _row_index(index, codes, M)
+    dtype = _out_type(out_dtype, y)
+    y = _output(y, "y", (R, K), dtype, codes, stream)
+    _check(lib().mx_dequantize_b128_rows(_ptr(codes), _ptr(scales), M, K, _ptr(index), R, _ptr(y),
+                                         _TYPES[dtype], _stream_ptr(stream, codes)))
+    return y

@@ -20,8 +20,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxq.so")
 SOURCES = ("mx_api.cu", "mx_stream.cu", "mx_dequant.cu", "mx_rotate.cu", "mx_hadamard.cu",
            "mx_gemm.cu", "mx_expert_api.cu", "mx_route.cu", "mx_b128_quant.cu", "mx_b128_gemm.cu",
-           "mx_combine.cu")
-HEADERS = ("mx_device.cuh", "mx_launch.h", "mx_expert.h", "mx_tcgen05.cuh")
+           "mx_combine.cu", "mx_train_api.cu", "mx_norm.cu", "mx_activation.cu", "mx_checkpoint.cu")
+HEADERS = ("mx_device.cuh", "mx_launch.h", "mx_expert.h", "mx_tcgen05.cuh", "mx_b128.cuh", "mx_train.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

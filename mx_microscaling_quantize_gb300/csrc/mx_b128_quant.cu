@@ -13,6 +13,7 @@
 // as many bytes takes 30 us: rows 30 us (6.7 TB/s), columns 32 (6.3), squares 30 (6.7), squares in both
 // orders 42 (6.4). The transposed squares of a matrix whose rows are no multiple of 16 leave byte by byte:
 // 8200 rows 210 us.
+#include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_expert.h"
 #include "mx_launch.h"
@@ -20,55 +21,6 @@
 namespace mxq {
 
 namespace {
-
-struct Factors {
-  float r, scale;
-};
-
-__device__ __forceinline__ Factors block_factors_b128(uint32_t amax_bits) {
-  Factors f;
-  const float a = fmaxf(__uint_as_float(amax_bits), kB128AmaxFloor);
-  f.r = __fdiv_rn(448.0f, a);
-  f.scale = __fdiv_rn(a, 448.0f);
-  if (amax_bits >= 0x7F800000u) f.r = f.scale = __uint_as_float(0x7FC00000u);
-  return f;
-}
-
-// Sign-free bf16x2 abs-max accumulation; the two halves are joined by amax_bits. NaN propagates:
-// the patterns are compared as integers, and those of NaN lie above that of infinity.
-__device__ __forceinline__ uint32_t amax2(uint32_t m, uint32_t w) {
-  return __vmaxu2(m, w & 0x7FFF7FFFu);
-}
-__device__ __forceinline__ uint32_t amax_join(uint32_t m) {  // -> fp32 bits
-  return max(m & 0xFFFFu, m >> 16) << 16;
-}
-
-// four values (bf16x2 words w0, w1: lower index in the low half) times r -> four code bytes
-__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float r) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-      "mov.b32 %0, {lo, hi};\n\t}"
-      : "=r"(d)
-      : "f"(__fmul_rn(bf16_lo(w0), r)), "f"(__fmul_rn(bf16_hi(w0), r)),
-        "f"(__fmul_rn(bf16_lo(w1), r)), "f"(__fmul_rn(bf16_hi(w1), r)));
-  return d;
-}
-
-// two values (separate fp32) -> two code bytes
-__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
-  uint16_t d;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-
-// Codes are written once and not read again here: evict-first.
-__device__ __forceinline__ void store16B(void* p, const uint32_t* r) {
-  asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3])
-               : "memory");
-}
 
 constexpr int kRowsCols = 512;  // columns of a warp's tile: 4 blocks of 128, 8 lanes each
 
@@ -159,12 +111,13 @@ __device__ __forceinline__ void stage_transposed(uint8_t* sm, int rg, int cg, in
 }
 
 // Writes the staged tile: column c of the tile to dst + c * pitch, `valid` bytes of each.
+template <int THREADS = kTileThreads>
 __device__ __forceinline__ void store_transposed(const uint8_t* sm, uint8_t* dst, int64_t pitch,
                                                  int valid, int cols) {
   const int q = threadIdx.x & 7;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int c = p * 32 + (threadIdx.x >> 3);
+  for (int p = 0; p < 128 * 8 / THREADS; ++p) {
+    const int c = p * (THREADS / 8) + (threadIdx.x >> 3);
     const int s = c >> 3;
     uint4 v = *reinterpret_cast<const uint4*>(sm + c * 128 + ((q ^ (s >> 1)) << 4));
     if (s & 1) v = make_uint4(v.z, v.w, v.x, v.y);
@@ -361,6 +314,160 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArg
   }
 }
 
+// The same operand from rows already in 8 bits (codes [M, K] under scales [ceil(K / 128), M], values
+// v = code * scale in fp32): a checkpoint's way into the weights' gradient, at half of the bytes that bf16
+// rows take. A tile is one block of rows and one of its scales' blocks, so every row of it has one scale.
+// 512 threads: thread (rg, cg) holds rows 4 rg .. and columns 8 cg .. as fp32. kRecolStages tiles are on
+// their way meanwhile; a block's gathered rows are looked up once, not per tile.
+constexpr int kRecolThreads = 512, kRecolStages = 2;
+struct RecolsShared {
+  uint2 next[kRecolStages][4][kRecolThreads];  // codes on their way, to places of each thread's own
+  float row_scale[kRecolStages][128];
+  uint8_t out[128 * 128];
+  uint32_t part[16][128];
+  float factor[128];
+  int64_t blocks;
+  int offsets[1024 + 1];
+};
+template <bool GATHER>
+__global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128QuantArgs a) {
+  extern __shared__ __align__(128) uint8_t recols_shared[];
+  RecolsShared& s = *reinterpret_cast<RecolsShared*>(recols_shared);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4, warp = tid >> 5;
+  int64_t blocks = a.blocks;
+  if (a.offsets) {
+    for (int e = tid; e <= a.E; e += kRecolThreads) {
+      s.offsets[e] = (int)min(max(load_s64(a.offsets + e), (int64_t)0), a.R);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int64_t n = count_blocks(s.offsets, a.E);
+      if (tid == 0) s.blocks = min(n, a.blocks);
+    }
+    __syncthreads();
+    blocks = s.blocks;
+  }
+  const int64_t cols = (a.K + kB128 - 1) / kB128, tiles = blocks * cols;
+  const int64_t t0 = tiles * blockIdx.x / gridDim.x, t1 = tiles * (blockIdx.x + 1) / gridDim.x;
+  if (t0 == t1) return;
+  const int64_t pitch = a.blocks * kB128;
+  const uint8_t* x = static_cast<const uint8_t*>(a.x);
+  int64_t lt = t0, lb = t0 / cols, lc = t0 - lb * cols;  // the tile to ask for next
+  int32_t src[4], scale_src = -1;  // rows of the checkpoint, -1: none
+  auto source = [&](int64_t row, int64_t row_end) -> int32_t {
+    if (row >= row_end) return -1;
+    const int32_t r = GATHER ? load_s32(a.index + row) : (int32_t)row;
+    return r < a.M ? r : -1;
+  };
+  auto find = [&] {
+    int row0 = 0, row_end = 0;
+    if (a.offsets) {
+      find_block(s.offsets, a.E, lb, &row0, &row_end);
+    } else {
+      row0 = (int)(lb * kB128);
+      row_end = (int)a.R;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) src[i] = source((int64_t)row0 + 4 * rg + i, row_end);
+    if (tid < 128) scale_src = source((int64_t)row0 + tid, row_end);
+  };
+  auto load = [&](int stage) {
+    if (lt < t1) {
+      const int64_t col = lc * kB128 + cg * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint2* to = &s.next[stage][i][tid];
+        if (src[i] >= 0 && col < a.K) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                       "l"(x + src[i] * a.K + col)
+                       : "memory");
+        } else {
+          *to = make_uint2(0u, 0u);
+        }
+      }
+      if (tid < 128) {
+        float* to = &s.row_scale[stage][tid];
+        if (scale_src >= 0) {
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                       "l"(a.x_scales + lc * a.M + scale_src)
+                       : "memory");
+        } else {
+          *to = 0.0f;
+        }
+      }
+      ++lt;
+      if (++lc == cols && lt < t1) {
+        lc = 0;
+        ++lb;
+        find();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t b = lb, c = lc;
+  find();
+  for (int i = 0; i < kRecolStages; ++i) load(i);
+  int stage = 0;
+  for (int64_t t = t0; t < t1; ++t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRecolStages - 1) : "memory");
+    __syncthreads();  // the rows' scales are other threads' copies
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint2 q = s.next[stage][i][tid];
+      const float f = s.row_scale[stage][4 * rg + i];
+      e4m3x2_to_f32(q.x & 0xFFFFu, v[i][0], v[i][1]);
+      e4m3x2_to_f32(q.x >> 16, v[i][2], v[i][3]);
+      e4m3x2_to_f32(q.y & 0xFFFFu, v[i][4], v[i][5]);
+      e4m3x2_to_f32(q.y >> 16, v[i][6], v[i][7]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], f);
+    }
+    uint32_t m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float top = absmax3(absmax3(v[0][j], v[1][j], v[2][j]), v[3][j], v[3][j]);
+      m[j] = __float_as_uint(top) & 0x7FFFFFFFu;
+      m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+    }
+    if ((tid & 16) == 0) {
+      *reinterpret_cast<uint4*>(&s.part[warp][cg * 8]) = make_uint4(m[0], m[1], m[2], m[3]);
+      *reinterpret_cast<uint4*>(&s.part[warp][cg * 8 + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+    }
+    __syncthreads();
+    load(stage);  // the stage has been read by everyone
+    stage = stage + 1 == kRecolStages ? 0 : stage + 1;
+    const int64_t c0 = c * kB128;
+    if (tid < 128) {
+      uint32_t top = s.part[0][tid];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = max(top, s.part[i][tid]);
+      const Factors f = block_factors_b128(top);
+      s.factor[tid] = f.r;
+      if (c0 + tid < a.K) a.scales[b * a.K + c0 + tid] = f.scale;
+    }
+    __syncthreads();
+    float r8[8];
+    *reinterpret_cast<float4*>(r8) = *reinterpret_cast<const float4*>(s.factor + cg * 8);
+    *reinterpret_cast<float4*>(r8 + 4) = *reinterpret_cast<const float4*>(s.factor + cg * 8 + 4);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {  // four rows of a column: word rg of it, at the place of stage_transposed
+      const uint32_t w = codes2(__fmul_rn(v[0][j], r8[j]), __fmul_rn(v[1][j], r8[j])) |
+                         codes2(__fmul_rn(v[2][j], r8[j]), __fmul_rn(v[3][j], r8[j])) << 16;
+      *reinterpret_cast<uint32_t*>(s.out + (cg * 8 + j) * 128 + ((rg ^ (2 * cg)) << 2)) = w;
+    }
+    __syncthreads();
+    store_transposed<kRecolThreads>(s.out, a.codes + c0 * pitch + b * kB128, pitch, kB128,
+                                    (int)min((int64_t)kB128, a.K - c0));
+    if (++c == cols) {
+      c = 0;
+      ++b;
+    }
+  }
+}
+
 // 128 x 128 squares of every matrix of a batch (blockIdx.z), in the order of x and, when codes_t
 // is given, transposed as well.
 __global__ void __launch_bounds__(kTileThreads) b128_blocks_kernel(B128QuantArgs a) {
@@ -453,6 +560,20 @@ static cudaError_t cols_launch(const B128QuantArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_b128_cols(const B128QuantArgs& a, cudaStream_t stream) {
   return a.index ? cols_launch<true>(a, stream) : cols_launch<false>(a, stream);
+}
+
+template <bool GATHER>
+static cudaError_t recols_launch(const B128QuantArgs& a, cudaStream_t stream) {
+  const int64_t tiles = a.blocks * ((a.K + kB128 - 1) / kB128);
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(&b128_recols_kernel<GATHER>),
+                                      kRecolThreads, sizeof(RecolsShared), 0);
+  if (slots <= 0) return cudaErrorInvalidConfiguration;
+  return launch_pdl(&b128_recols_kernel<GATHER>, dim3((unsigned)(tiles < slots ? tiles : slots)),
+                    dim3(kRecolThreads), sizeof(RecolsShared), stream, a);
+}
+
+cudaError_t launch_b128_recols(const B128QuantArgs& a, cudaStream_t stream) {
+  return a.index ? recols_launch<true>(a, stream) : recols_launch<false>(a, stream);
 }
 
 cudaError_t launch_b128_blocks(const B128QuantArgs& a, cudaStream_t stream) {

@@ -40,10 +40,11 @@ int64_t plan_workspace_ints(int64_t n, int E);
 cudaError_t launch_plan(const PlanArgs& a, cudaStream_t stream);
 
 struct B128QuantArgs {
-  const void* x;           // bf16 [batch, M, K]
+  const void* x;           // bf16 [batch, M, K]; recols: codes [M, K]
+  const float* x_scales;   // recols: [ceil(K / 128), M]
   const int32_t* index;    // rows / cols: source row of each of R rows (< 0: zeros), or null
   int64_t batch, M, K, R;
-  const int64_t* offsets;  // cols: [E + 1] or null (one run of R rows)
+  const int64_t* offsets;  // cols, recols: [E + 1] or null (one run of R rows)
   int E;
   int64_t blocks;          // cols: 128-row blocks of the output
   uint8_t* codes;
@@ -53,6 +54,7 @@ struct B128QuantArgs {
 };
 cudaError_t launch_b128_rows(const B128QuantArgs& a, cudaStream_t stream);
 cudaError_t launch_b128_cols(const B128QuantArgs& a, cudaStream_t stream);
+cudaError_t launch_b128_recols(const B128QuantArgs& a, cudaStream_t stream);
 cudaError_t launch_b128_blocks(const B128QuantArgs& a, cudaStream_t stream);
 
 enum B128Mode { kB128Dense = 0, kB128Grouped = 1, kB128Wgrad = 2 };

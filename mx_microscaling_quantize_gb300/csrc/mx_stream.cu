@@ -717,11 +717,9 @@ int resident_ctas(const void* kernel, int threads, size_t dyn_smem, int max_per_
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   const auto key = std::make_tuple(dev, kernel, threads, dyn_smem, max_per_sm);
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    auto it = cache.find(key);
-    if (it != cache.end()) return it->second;
-  }
+  std::lock_guard<std::mutex> lock(mu);
+  const auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
   int sms = 0, thr_sm = 0, regs_sm = 0, smem_sm = 0, smem_reserved = 0, blocks_sm = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&thr_sm, cudaDevAttrMaxThreadsPerMultiProcessor, dev) != cudaSuccess ||
@@ -734,13 +732,14 @@ int resident_ctas(const void* kernel, int threads, size_t dyn_smem, int max_per_
           cudaSuccess) {
     return 0;
   }
-  if (dyn_smem > 48 * 1024 &&
+  cudaFuncAttributes fa{};
+  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return 0;
+  // raised only: a kernel may run with more shared memory in other calls
+  if (dyn_smem > 48 * 1024 && (size_t)fa.maxDynamicSharedSizeBytes < dyn_smem &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn_smem) !=
           cudaSuccess) {
     return 0;
   }
-  cudaFuncAttributes fa{};
-  if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return 0;
   const int warps = (threads + 31) / 32;
   const int regs_per_warp = ((fa.numRegs * 32 + 255) / 256) * 256;  // 256-register granules
   int per_sm = blocks_sm;
@@ -749,7 +748,6 @@ int resident_ctas(const void* kernel, int threads, size_t dyn_smem, int max_per_
   const size_t smem_block = fa.sharedSizeBytes + dyn_smem + (size_t)smem_reserved;
   per_sm = std::min(per_sm, (int)((size_t)smem_sm / smem_block));
   if (max_per_sm > 0) per_sm = std::min(per_sm, max_per_sm);
-  std::lock_guard<std::mutex> lock(mu);
   cache[key] = sms * per_sm;
   return sms * per_sm;
 }
