@@ -452,11 +452,11 @@ mx_status mx_combine_backward_whole(const void* dout, const void* y, const int32
  * NULL for ones and zeros (w_type is then not used, but must be valid). mean, rstd: fp32 [M] or NULL,
  * what mx_layer_norm_backward takes. K <= 16384.
  *
- * mx_layer_norm: y [M, K] of y_type. Alignment: that of the elements; x and y on 32 and weight and
- *   bias on 16 bytes with K % 16 == 0 take wide loads.
+ * mx_layer_norm: y [M, K] of y_type. Alignment: that of the elements; all four on 32 bytes with
+ *   K % 8 == 0 take wide loads.
  * mx_layer_norm_b128: y as the operand that mx_quantize_b128_rows makes of the unrounded y: codes
  *   [M, K], scales [ceil(K / 128), M]. x_codes, x_scales: unless NULL, a checkpoint of x. K % 32 == 0;
- *   x and codes 32-byte, weight and bias 16-byte aligned.
+ *   x, codes, weight and bias 32-byte aligned.
  */
 mx_status mx_layer_norm(const void* x, int x_type, const void* weight, const void* bias, int w_type,
                         int64_t M, int64_t K, float eps, int center, void* y, int y_type, float* mean,
@@ -476,7 +476,7 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
  * order that the sizes and the device alone decide. workspace: device memory of
  * mx_layer_norm_backward_workspace() bytes, 4-byte aligned (NULL will do without dweight and dbias); two
  * calls that may run at the same time need one each. Alignment: that of the elements; dy, x and dx on 16
- * bytes with K % 8 == 0 take wide loads. dx must not overlap the inputs.
+ * bytes and weight on 32 with K % 8 == 0 take wide loads. dx must not overlap the inputs.
  */
 mx_status mx_layer_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes);
 

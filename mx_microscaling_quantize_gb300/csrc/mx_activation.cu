@@ -8,8 +8,7 @@
 // All in fp32, rounded once: to codes under the scale of the block of 128 that they form, or to bf16.
 //
 // Bound by memory: u is read once, h and (asked for) its checkpoint are written by the same pass. A warp
-// takes RW rows of 512 columns, a lane 16 of each, as in the quantisation of rows; eight lanes hold a
-// block.
+// takes 512 columns of a row, a lane two runs of 8 in packed pairs; 16 lanes hold a block.
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"
@@ -21,252 +20,225 @@ namespace mxq {
 namespace {
 
 constexpr int kActThreads = 256;
-constexpr int kActCols = 512;  // columns of a warp's tile
+constexpr int kActRuns = 2;                 // runs of 8 columns per lane
+constexpr int kActCols = kActRuns * 32 * 8;  // columns of a warp's tile
 
-__device__ __forceinline__ float rcp(float v) { return __fdividef(1.0f, v); }
+// The hardware's approximate exponential of two and reciprocal (relative 2^-22 and 2^-23; results below
+// 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float v) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(v));
+  return d;
+}
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t v) { return pair(exp2_fast(lo_of(v)), exp2_fast(hi_of(v))); }
+__device__ __forceinline__ uint64_t rcp_pair(uint64_t v) { return pair(rcp_fast(lo_of(v)), rcp_fast(hi_of(v))); }
+__device__ __forceinline__ uint64_t scaled(uint64_t v, float s) { return mul_pair(v, pair(s)); }
 
-// s(g) and 1 - s(g). exp(-g) beyond fp32 leaves 0 and 1 (kept from infinity times zero).
-__device__ __forceinline__ void logistic(float g, float& s, float& one_minus) {
-  const float e = __expf(-g);
-  s = rcp(1.0f + e);
-  one_minus = s * fminf(e, 3.402823466e38f);
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanhGain = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+// Phi(g), and e = exp(-g^2 / 2). The tail Phi(-|g|) is e t Q(t), t = 1 / (1 + 0.38 |g| / sqrt 2): Mills'
+// ratio, smooth in t, by a polynomial fitted (least squares at Chebyshev nodes, reweighted towards the
+// smallest largest error) to relative 2e-8; 4e-7 in fp32. Beside the exponential and the reciprocal it takes
+// 9 FMAs, and the exponential is the gradient's too.
+__device__ __forceinline__ uint64_t normal_cdf(uint64_t g, uint64_t& e) {
+  e = exp2_pair(mul_pair(scaled(g, -0.5f * kLog2e), g));
+  const uint64_t t = rcp_pair(fma_pair(pair(0.26870056986808777f), pair(fabsf(lo_of(g)), fabsf(hi_of(g))), pair(1.0f)));
+  uint64_t p = pair(0.029425911605358124f);
+  p = fma_pair(p, t, pair(-0.13084791600704193f));
+  p = fma_pair(p, t, pair(0.18129514157772064f));
+  p = fma_pair(p, t, pair(-0.07996146380901337f));
+  p = fma_pair(p, t, pair(0.1144489124417305f));
+  p = fma_pair(p, t, pair(0.06958147138357162f));
+  p = fma_pair(p, t, pair(0.10188283026218414f));
+  p = fma_pair(p, t, pair(0.10697033256292343f));
+  p = fma_pair(p, t, pair(0.10720480233430862f));
+  const uint64_t tail = mul_pair(mul_pair(p, t), e);
+  const uint64_t rest = fma_pair(tail, pair(-1.0f), pair(1.0f));
+  return pair(lo_of(g) < 0.0f ? lo_of(tail) : lo_of(rest), hi_of(g) < 0.0f ? hi_of(tail) : hi_of(rest));
 }
 
-template <int KIND>
-__device__ __forceinline__ float act(float g) {
-  if (KIND == MX_ACT_SILU) return g * rcp(1.0f + __expf(-g));
-  if (KIND == MX_ACT_GELU) return g * 0.5f * erfcf(g * -0.70710678118654752f);
-  const float z2 = 1.5957691216057308f * fmaf(0.044715f * g * g, g, g);
-  return g * rcp(1.0f + __expf(-z2));
+// The logistic function of z, from -z log2 e: 0 below exp(-88), where its value is under 2^-126.
+__device__ __forceinline__ uint64_t logistic(uint64_t z) {
+  return rcp_pair(add_pair(exp2_pair(z), pair(1.0f)));
 }
 
-// f(g) and f'(g)
-template <int KIND>
-__device__ __forceinline__ void act_grad(float g, float& h, float& d) {
-  if (KIND == MX_ACT_GELU) {
-    const float p = 0.5f * erfcf(g * -0.70710678118654752f);
-    h = g * p;
-    d = fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p);
-    return;
+// f(g) of a pair, and with GRAD its derivative d.
+template <int KIND, bool GRAD>
+__device__ __forceinline__ uint64_t act(uint64_t g, uint64_t& d) {
+  uint64_t s, h;
+  if constexpr (KIND == MX_ACT_GELU) {
+    uint64_t e;
+    s = normal_cdf(g, e);
+    h = mul_pair(g, s);
+    if constexpr (GRAD) d = fma_pair(scaled(g, 0.39894228040143268f), e, s);
+    return h;
   }
-  float s, q;
-  if (KIND == MX_ACT_SILU) {
-    logistic(g, s, q);
-    h = g * s;
-    d = fmaf(h, q, s);
-  } else {
-    const float g2 = 0.044715f * g * g;
-    logistic(1.5957691216057308f * fmaf(g2, g, g), s, q);
-    h = g * s;
-    d = fmaf(h * q, 1.5957691216057308f * fmaf(3.0f, g2, 1.0f), s);
+  if constexpr (KIND == MX_ACT_SILU) {
+    s = logistic(scaled(g, -kLog2e));
+    h = mul_pair(g, s);
+    if constexpr (GRAD) d = fma_pair(h, fma_pair(s, pair(-1.0f), pair(1.0f)), s);
+    return h;
   }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-__device__ __forceinline__ void unpack(const uint32_t (&w)[8], float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
+  const uint64_t g2 = mul_pair(scaled(g, 0.044715f), g);
+  s = logistic(mul_pair(scaled(g, -kLog2e * kTanhGain), add_pair(g2, pair(1.0f))));
+  h = mul_pair(g, s);
+  if constexpr (GRAD) {
+    const uint64_t q = mul_pair(h, fma_pair(s, pair(-1.0f), pair(1.0f)));  // h (1 - s)
+    d = fma_pair(q, scaled(fma_pair(g2, pair(3.0f), pair(1.0f)), kTanhGain), s);
   }
+  return h;
 }
 
-// Factors of the block that this lane's 16 values and those of its seven neighbours form.
-__device__ __forceinline__ Factors block_of(uint32_t m) {
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-  return block_factors_b128(m);
+// What a warp's tile is of: a row, and a lane's runs of 8 columns of it.
+struct ActTile {
+  int64_t row, H, R, U;
+  int col0;
+  __device__ __forceinline__ int column(int p) const { return col0 + p * 256 + (threadIdx.x & 31) * 8; }
+  __device__ __forceinline__ bool has(int p) const { return column(p) < H; }
+};
+__device__ __forceinline__ bool act_tile(const ActArgs& a, bool gated, int col_tiles, int64_t tiles, ActTile& t) {
+  const int64_t tile = (int64_t)blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5);
+  if (tile >= tiles) return false;
+  t.row = tile / col_tiles;
+  t.col0 = (int)(tile - t.row * col_tiles) * kActCols;
+  t.H = a.H;
+  t.R = a.R;
+  t.U = gated ? 2 * a.H : a.H;
+  return true;
 }
 
-__device__ __forceinline__ void store_codes(const float (&v)[16], float r, uint8_t* to) {
-  uint32_t w[4];
+// N runs (kActRuns of each of N / kActRuns parts of rows of `width` columns, a part H columns) as codes and
+// scales.
+template <int N>
+__device__ __forceinline__ void store_runs(const uint64_t (&v)[N][4], const ActTile& t, int64_t width,
+                                           uint8_t* codes, float* scales) {
+  uint8_t* to = codes + t.row * width;
+  run_codes<N>(
+      v,
+      [&](int n, uint32_t lo, uint32_t hi) {
+        const int p = n % kActRuns;
+        if (t.has(p)) store8B(to + (n / kActRuns) * t.H + t.column(p), lo, hi);
+      },
+      [&](int n, float s) {
+        const int p = n % kActRuns;
+        const int64_t kb = ((n / kActRuns) * t.H + t.column(p)) / kB128;
+        if ((t.column(p) & ~(kB128 - 1)) < t.H) scales[kb * t.R + t.row] = s;
+      });
+}
+
+// A lane's runs of `part` (0: gate, 1: up) of its row of u, bf16 or codes, or of dh.
+template <bool CODES>
+struct ActRuns {
+  uint32_t raw[kActRuns][CODES ? 2 : 4];
+  float scale[kActRuns];
+
+  __device__ __forceinline__ void load(const void* u, const float* scales, const ActTile& t, int64_t width,
+                                       int part) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    w[j] = codes2(__fmul_rn(v[4 * j], r), __fmul_rn(v[4 * j + 1], r)) |
-           codes2(__fmul_rn(v[4 * j + 2], r), __fmul_rn(v[4 * j + 3], r)) << 16;
+    for (int p = 0; p < kActRuns; ++p) {
+      scale[p] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < (CODES ? 2 : 4); ++j) raw[p][j] = 0u;
+      if (!t.has(p)) continue;
+      const int64_t col = part * t.H + t.column(p);
+      if constexpr (CODES) {
+        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(raw[p][0]), "=r"(raw[p][1])
+                     : "l"(static_cast<const uint8_t*>(u) + t.row * width + col));
+        scale[p] = load_f32(scales + col / kB128 * t.R + t.row);
+      } else {
+        load16B(static_cast<const uint16_t*>(u) + t.row * width + col, raw[p]);
+      }
+    }
   }
-  store16B(to, w);
-}
-
-// 16 codes times their scale, in fp32.
-__device__ __forceinline__ void decode(const uint32_t* w, float s, float (&v)[16]) {
+  __device__ __forceinline__ void values(int p, uint64_t (&v)[4]) const {
+    if constexpr (CODES) {
+      values4(raw[p][0], v[0], v[1]);
+      values4(raw[p][1], v[2], v[3]);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    e4m3x2_to_f32(w[j] & 0xFFFFu, v[4 * j], v[4 * j + 1]);
-    e4m3x2_to_f32(w[j] >> 16, v[4 * j + 2], v[4 * j + 3]);
-  }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], s);
-}
-
-template <int KIND, bool GATED, int RW>
-__global__ void __launch_bounds__(kActThreads) activation_kernel(ActArgs a, int64_t col_tiles,
-                                                                 int64_t tiles) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, sub = lane & 7, blk = lane >> 3;
-  const int64_t tile = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (tile >= tiles) return;
-  const int64_t r0 = tile / col_tiles * RW;
-  const int64_t col = tile % col_tiles * kActCols + lane * 16, U = GATED ? 2 * a.H : a.H;
-  const int64_t kb = col / kB128, up_blocks = a.H / kB128;
-  const uint16_t* u = static_cast<const uint16_t*>(a.u);
-  uint32_t g[RW][8], p[GATED ? RW : 1][8];
-#pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    if (r0 + i < a.R && col < a.H) {
-      load32B(u + (r0 + i) * U + col, g[i]);
-      if constexpr (GATED) load32B(u + (r0 + i) * U + a.H + col, p[i]);
+      for (int j = 0; j < 4; ++j) v[j] = mul_pair(v[j], pair(scale[p]));
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[i][j] = 0u;
-      if constexpr (GATED) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[i][j] = 0u;
-      }
+      for (int j = 0; j < 4; ++j) v[j] = bf16_pair(raw[p][j]);
     }
   }
-  float mine = 0.0f, mine_g = 0.0f, mine_p = 0.0f;  // lane sub keeps the scales of row sub
+};
+
+template <int KIND, bool GATED>
+__global__ void __launch_bounds__(kActThreads) activation_kernel(ActArgs a, int col_tiles, int64_t tiles) {
+  pdl_launch_dependents();
+  pdl_wait();
+  ActTile t;
+  if (!act_tile(a, GATED, col_tiles, tiles, t)) return;
+  constexpr int kParts = GATED ? 2 : 1;
+  ActRuns<false> in[kParts];
 #pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    const bool there = r0 + i < a.R && col < a.H;
-    float v[16], h[16];
-    unpack(g[i], v);
-    const int64_t at = (r0 + i) * U + col;
-    if (a.u_codes) {
-      const Factors f = block_of(absmax_f32x16(v));
-      if (sub == i) mine_g = f.scale;
-      if (there) store_codes(v, f.r, a.u_codes + at);
-    }
+  for (int k = 0; k < kParts; ++k) in[k].load(a.u, nullptr, t, t.U, k);
+  uint64_t u[kParts * kActRuns][4], h[kActRuns][4];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) h[j] = act<KIND>(v[j]);
-    if constexpr (GATED) {
-      unpack(p[i], v);
-      if (a.u_codes) {
-        const Factors f = block_of(absmax_f32x16(v));
-        if (sub == i) mine_p = f.scale;
-        if (there) store_codes(v, f.r, a.u_codes + at + a.H);
-      }
+  for (int n = 0; n < kParts * kActRuns; ++n) in[n / kActRuns].values(n % kActRuns, u[n]);
+  if (a.u_codes) store_runs<kParts * kActRuns>(u, t, t.U, a.u_codes, a.u_scales_out);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) h[j] *= v[j];
-    }
-    const Factors f = block_of(absmax_f32x16(h));
-    if (sub == i) mine = f.scale;
-    if (there) store_codes(h, f.r, a.codes + (r0 + i) * a.H + col);
-  }
-  if (sub < RW && r0 + sub < a.R && col - sub * 16 < a.H) {
-    a.scales[kb * a.R + r0 + sub] = mine;
-    if (a.u_codes) {
-      a.u_scales_out[kb * a.R + r0 + sub] = mine_g;
-      if constexpr (GATED) a.u_scales_out[(up_blocks + kb) * a.R + r0 + sub] = mine_p;
+  for (int p = 0; p < kActRuns; ++p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint64_t none;
+      h[p][j] = act<KIND, false>(u[p][j], none);
+      if constexpr (GATED) h[p][j] = mul_pair(h[p][j], u[kActRuns + p][j]);
     }
   }
+  store_runs<kActRuns>(h, t, a.H, a.codes, a.scales);
 }
 
-template <int KIND, bool GATED, bool CODES, int RW>
-__global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArgs a, int64_t col_tiles,
+template <int KIND, bool GATED, bool CODES>
+__global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArgs a, int col_tiles,
                                                                           int64_t tiles) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, sub = lane & 7;
-  const int64_t tile = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (tile >= tiles) return;
-  const int64_t r0 = tile / col_tiles * RW;
-  const int64_t col = tile % col_tiles * kActCols + lane * 16, U = GATED ? 2 * a.H : a.H;
-  const int64_t kb = col / kB128, up_blocks = a.H / kB128;
-  constexpr int kWords = CODES ? 4 : 8;
-  uint32_t dh[RW][8], g[RW][kWords], p[GATED ? RW : 1][kWords];
-  float gs[RW], ps[RW];
+  ActTile t;
+  if (!act_tile(a, GATED, col_tiles, tiles, t)) return;
+  constexpr int kParts = GATED ? 2 : 1;
+  ActRuns<CODES> in[kParts];
+  ActRuns<false> dh;
 #pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    gs[i] = ps[i] = 0.0f;
-    if (r0 + i < a.R && col < a.H) {
-      const int64_t at = (r0 + i) * U + col;
-      if constexpr (CODES) {
-        const uint8_t* u = static_cast<const uint8_t*>(a.u);
-        load16B(u + at, g[i]);
-        gs[i] = load_f32(a.u_scales + kb * a.R + r0 + i);
-        if constexpr (GATED) {
-          load16B(u + at + a.H, p[i]);
-          ps[i] = load_f32(a.u_scales + (up_blocks + kb) * a.R + r0 + i);
-        }
-      } else {
-        const uint16_t* u = static_cast<const uint16_t*>(a.u);
-        load32B(u + at, g[i]);
-        if constexpr (GATED) load32B(u + at + a.H, p[i]);
-      }
-      load32B(static_cast<const uint16_t*>(a.dh) + (r0 + i) * a.H + col, dh[i]);
-    } else {
+  for (int k = 0; k < kParts; ++k) in[k].load(a.u, a.u_scales, t, t.U, k);
+  dh.load(a.dh, nullptr, t, a.H, 0);
+  uint64_t du[kParts * kActRuns][4];
 #pragma unroll
-      for (int j = 0; j < kWords; ++j) g[i][j] = 0u;
+  for (int p = 0; p < kActRuns; ++p) {
+    uint64_t g[4], up[4], e[4];
+    in[0].values(p, g);
+    if constexpr (GATED) in[kParts - 1].values(p, up);
+    dh.values(p, e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint64_t d;
+      const uint64_t h = act<KIND, true>(g[j], d);
       if constexpr (GATED) {
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) p[i][j] = 0u;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dh[i][j] = 0u;
-    }
-  }
-  float mine_g = 0.0f, mine_p = 0.0f;
-  auto put = [&](const float (&v)[16], int64_t at, bool there, float& mine, bool keep) {
-    if (a.du && there) {
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-      store32B(static_cast<uint16_t*>(a.du) + at, o);
-    }
-    if (a.codes) {
-      const Factors f = block_of(absmax_f32x16(v));
-      if (keep) mine = f.scale;
-      if (there) store_codes(v, f.r, a.codes + at);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    const bool there = r0 + i < a.R && col < a.H;
-    const int64_t at = (r0 + i) * U + col;
-    float v[16], d[16], e[16];
-    if constexpr (CODES) {
-      decode(g[i], gs[i], v);
-    } else {
-      unpack(g[i], v);
-    }
-    unpack(dh[i], e);
-    if constexpr (GATED) {
-      float up[16];
-      if constexpr (CODES) {
-        decode(p[i], ps[i], up);
+        du[kActRuns + p][j] = mul_pair(e[j], h);
+        du[p][j] = mul_pair(mul_pair(e[j], up[j]), d);
       } else {
-        unpack(p[i], up);
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float h, der;
-        act_grad<KIND>(v[j], h, der);
-        d[j] = e[j] * up[j] * der;
-        e[j] *= h;
-      }
-      put(e, at + a.H, there, mine_p, sub == i);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        float h, der;
-        act_grad<KIND>(v[j], h, der);
-        d[j] = e[j] * der;
+        du[p][j] = mul_pair(e[j], d);
       }
     }
-    put(d, at, there, mine_g, sub == i);
   }
-  if (a.codes && sub < RW && r0 + sub < a.R && col - sub * 16 < a.H) {
-    a.scales[kb * a.R + r0 + sub] = mine_g;
-    if constexpr (GATED) a.scales[(up_blocks + kb) * a.R + r0 + sub] = mine_p;
+  if (a.du) {
+#pragma unroll
+    for (int n = 0; n < kParts * kActRuns; ++n) {
+      if (!t.has(n % kActRuns)) continue;
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = bf16_word(du[n][j]);
+      store16B(static_cast<uint16_t*>(a.du) + t.row * t.U + (n / kActRuns) * a.H + t.column(n % kActRuns), o);
+    }
   }
+  if (a.codes) store_runs<kParts * kActRuns>(du, t, t.U, a.codes, a.scales);
 }
 
 template <typename F>
@@ -276,12 +248,11 @@ cudaError_t by_kind(int kind, F&& f) {
   return f(std::integral_constant<int, MX_ACT_GELU_TANH>());
 }
 
-template <int RW, typename K>
-cudaError_t run(K kernel, const ActArgs& a, int threads, cudaStream_t stream) {
-  const int64_t col_tiles = (a.H + kActCols - 1) / kActCols, warps = threads / 32;
-  const int64_t tiles = (a.R + RW - 1) / RW * col_tiles;
-  return launch_pdl(kernel, dim3((unsigned)((tiles + warps - 1) / warps)), dim3(threads), 0, stream, a,
-                    col_tiles, tiles);
+cudaError_t run(void (*kernel)(ActArgs, int, int64_t), const ActArgs& a, cudaStream_t stream) {
+  const int64_t col_tiles = (a.H + kActCols - 1) / kActCols, tiles = a.R * col_tiles;
+  constexpr int kWarps = kActThreads / 32;
+  return launch_pdl(kernel, dim3((unsigned)((tiles + kWarps - 1) / kWarps)), dim3(kActThreads), 0, stream, a,
+                    (int)col_tiles, tiles);
 }
 
 }  // namespace
@@ -289,8 +260,7 @@ cudaError_t run(K kernel, const ActArgs& a, int threads, cudaStream_t stream) {
 cudaError_t launch_activation(const ActArgs& a, cudaStream_t stream) {
   return by_kind(a.kind, [&](auto kind) {
     constexpr int KIND = decltype(kind)::value;
-    return a.gated ? run<1>(&activation_kernel<KIND, true, 1>, a, kActThreads, stream)
-                   : run<1>(&activation_kernel<KIND, false, 1>, a, kActThreads, stream);
+    return run(a.gated ? &activation_kernel<KIND, true> : &activation_kernel<KIND, false>, a, stream);
   });
 }
 
@@ -298,11 +268,11 @@ cudaError_t launch_activation_backward(const ActArgs& a, cudaStream_t stream) {
   return by_kind(a.kind, [&](auto kind) {
     constexpr int KIND = decltype(kind)::value;
     if (a.u_scales) {
-      return a.gated ? run<1>(&activation_backward_kernel<KIND, true, true, 1>, a, kActThreads, stream)
-                     : run<1>(&activation_backward_kernel<KIND, false, true, 1>, a, kActThreads, stream);
+      return run(a.gated ? &activation_backward_kernel<KIND, true, true>
+                         : &activation_backward_kernel<KIND, false, true>, a, stream);
     }
-    return a.gated ? run<1>(&activation_backward_kernel<KIND, true, false, 1>, a, kActThreads, stream)
-                   : run<1>(&activation_backward_kernel<KIND, false, false, 1>, a, kActThreads, stream);
+    return run(a.gated ? &activation_backward_kernel<KIND, true, false>
+                       : &activation_backward_kernel<KIND, false, false>, a, stream);
   });
 }
 

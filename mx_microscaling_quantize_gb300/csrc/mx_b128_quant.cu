@@ -111,13 +111,12 @@ __device__ __forceinline__ void stage_transposed(uint8_t* sm, int rg, int cg, in
 }
 
 // Writes the staged tile: column c of the tile to dst + c * pitch, `valid` bytes of each.
-template <int THREADS = kTileThreads>
 __device__ __forceinline__ void store_transposed(const uint8_t* sm, uint8_t* dst, int64_t pitch,
                                                  int valid, int cols) {
   const int q = threadIdx.x & 7;
 #pragma unroll
-  for (int p = 0; p < 128 * 8 / THREADS; ++p) {
-    const int c = p * (THREADS / 8) + (threadIdx.x >> 3);
+  for (int p = 0; p < 4; ++p) {
+    const int c = p * 32 + (threadIdx.x >> 3);
     const int s = c >> 3;
     uint4 v = *reinterpret_cast<const uint4*>(sm + c * 128 + ((q ^ (s >> 1)) << 4));
     if (s & 1) v = make_uint4(v.z, v.w, v.x, v.y);
@@ -316,16 +315,16 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArg
 
 // The same operand from rows already in 8 bits (codes [M, K] under scales [ceil(K / 128), M], values
 // v = code * scale in fp32): a checkpoint's way into the weights' gradient, at half of the bytes that bf16
-// rows take. A tile is one block of rows and one of its scales' blocks, so every row of it has one scale.
-// 512 threads: thread (rg, cg) holds rows 4 rg .. and columns 8 cg .. as fp32. kRecolStages tiles are on
-// their way meanwhile; a block's gathered rows are looked up once, not per tile.
-constexpr int kRecolThreads = 512, kRecolStages = 2;
+// rows take. A tile is 128 rows of one block of their scales, copied to shared memory kRecolStages - 1 tiles
+// ahead (16-byte pieces, those of row r at places permuted by r / 8; missing rows are filled with zeros).
+// A warp makes 16 columns of it alone: lane (q, h) holds rows 8 q .. and columns 8 h .. of these as fp32, the
+// columns' abs-maxes are reduced over the 16 lanes q, and the codes leave through 2 KB of the warp's own. One barrier a
+// tile, for the copies of the other threads.
+constexpr int kRecolThreads = 256, kRecolStages = 4;
 struct RecolsShared {
-  uint2 next[kRecolStages][4][kRecolThreads];  // codes on their way, to places of each thread's own
+  uint4 in[kRecolStages][128 * 8];
+  uint4 out[kRecolThreads / 32][128];
   float row_scale[kRecolStages][128];
-  uint8_t out[128 * 128];
-  uint32_t part[16][128];
-  float factor[128];
   int64_t blocks;
   int offsets[1024 + 1];
 };
@@ -335,7 +334,8 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
   RecolsShared& s = *reinterpret_cast<RecolsShared*>(recols_shared);
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane & 15, h = lane >> 4;
+  using Max = RunMax<8, 4>;
   int64_t blocks = a.blocks;
   if (a.offsets) {
     for (int e = tid; e <= a.E; e += kRecolThreads) {
@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
   const int64_t pitch = a.blocks * kB128;
   const uint8_t* x = static_cast<const uint8_t*>(a.x);
   int64_t lt = t0, lb = t0 / cols, lc = t0 - lb * cols;  // the tile to ask for next
-  int32_t src[4], scale_src = -1;  // rows of the checkpoint, -1: none
+  int32_t src[4], scale_src = -1;  // this thread's rows of the checkpoint, -1: none
+  const int piece = tid & 7, first = tid >> 3;  // its pieces: of rows first + 32 i
   auto source = [&](int64_t row, int64_t row_end) -> int32_t {
     if (row >= row_end) return -1;
     const int32_t r = GATHER ? load_s32(a.index + row) : (int32_t)row;
@@ -370,21 +371,20 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
       row_end = (int)a.R;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) src[i] = source((int64_t)row0 + 4 * rg + i, row_end);
+    for (int i = 0; i < 4; ++i) src[i] = source((int64_t)row0 + first + 32 * i, row_end);
     if (tid < 128) scale_src = source((int64_t)row0 + tid, row_end);
   };
   auto load = [&](int stage) {
     if (lt < t1) {
-      const int64_t col = lc * kB128 + cg * 8;
+      const int64_t col = lc * kB128 + piece * 16;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint2* to = &s.next[stage][i][tid];
+        const int r = first + 32 * i;
+        uint4* to = &s.in[stage][r * 8 + (piece ^ ((r >> 3) & 7))];
         if (src[i] >= 0 && col < a.K) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
-                       "l"(x + src[i] * a.K + col)
-                       : "memory");
+          copy16B_async(to, x + src[i] * a.K + col);
         } else {
-          *to = make_uint2(0u, 0u);
+          *to = make_uint4(0u, 0u, 0u, 0u);
         }
       }
       if (tid < 128) {
@@ -408,59 +408,60 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
   };
   int64_t b = lb, c = lc;
   find();
-  for (int i = 0; i < kRecolStages; ++i) load(i);
-  int stage = 0;
+  for (int i = 0; i < kRecolStages - 1; ++i) load(i);
+  uint8_t* out = reinterpret_cast<uint8_t*>(s.out[warp]);
   for (int64_t t = t0; t < t1; ++t) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRecolStages - 1) : "memory");
-    __syncthreads();  // the rows' scales are other threads' copies
-    float v[4][8];
+    const int stage = (int)((t - t0) % kRecolStages);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRecolStages - 2) : "memory");
+    __syncthreads();
+    load((stage + kRecolStages - 1) % kRecolStages);  // into the tile before this one, read by all
+    uint64_t v[8][4];  // pairs of columns
+    float f[8];
+    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&s.row_scale[stage][8 * q]);
+    *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(&s.row_scale[stage][8 * q + 4]);
+    const uint4* in = &s.in[stage][q * 64 + (warp ^ (q & 7))];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint2 q = s.next[stage][i][tid];
-      const float f = s.row_scale[stage][4 * rg + i];
-      e4m3x2_to_f32(q.x & 0xFFFFu, v[i][0], v[i][1]);
-      e4m3x2_to_f32(q.x >> 16, v[i][2], v[i][3]);
-      e4m3x2_to_f32(q.y & 0xFFFFu, v[i][4], v[i][5]);
-      e4m3x2_to_f32(q.y >> 16, v[i][6], v[i][7]);
+    for (int i = 0; i < 8; ++i) {
+      const uint2 w = reinterpret_cast<const uint2*>(in + i * 8)[h];
+      values4(w.x, v[i][0], v[i][1]);
+      values4(w.y, v[i][2], v[i][3]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], f);
+      for (int j = 0; j < 4; ++j) v[i][j] = mul_pair(v[i][j], pair(f[i]));
     }
     uint32_t m[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float top = absmax3(absmax3(v[0][j], v[1][j], v[2][j]), v[3][j], v[3][j]);
-      m[j] = __float_as_uint(top) & 0x7FFFFFFFu;
-      m[j] = max(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+      auto at = [&](int i) { return j & 1 ? hi_of(v[i][j / 2]) : lo_of(v[i][j / 2]); };
+      const float p = absmax3(at(0), at(1), at(2)), r = absmax3(at(3), at(4), at(5));
+      m[j] = __float_as_uint(absmax3(absmax3(p, r, at(6)), at(7), at(7))) & 0x7FFFFFFFu;
     }
-    if ((tid & 16) == 0) {
-      *reinterpret_cast<uint4*>(&s.part[warp][cg * 8]) = make_uint4(m[0], m[1], m[2], m[3]);
-      *reinterpret_cast<uint4*>(&s.part[warp][cg * 8 + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
-    }
-    __syncthreads();
-    load(stage);  // the stage has been read by everyone
-    stage = stage + 1 == kRecolStages ? 0 : stage + 1;
-    const int64_t c0 = c * kB128;
-    if (tid < 128) {
-      uint32_t top = s.part[0][tid];
+    const Factors mine = block_factors_b128(Max::reduce(m));  // of column Max::index() of half h
+    const int64_t c0 = c * kB128 + warp * 16;
+    const int own = h * 8 + Max::index();
+    if (Max::first() && c0 + own < a.K) a.scales[b * a.K + c0 + own] = mine.scale;
+    __syncwarp();  // the codes of the tile before have been read
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = max(top, s.part[i][tid]);
-      const Factors f = block_factors_b128(top);
-      s.factor[tid] = f.r;
-      if (c0 + tid < a.K) a.scales[b * a.K + c0 + tid] = f.scale;
-    }
-    __syncthreads();
-    float r8[8];
-    *reinterpret_cast<float4*>(r8) = *reinterpret_cast<const float4*>(s.factor + cg * 8);
-    *reinterpret_cast<float4*>(r8 + 4) = *reinterpret_cast<const float4*>(s.factor + cg * 8 + 4);
+    for (int j = 0; j < 8; j += 2) {
+      const uint64_t r = pair(Max::take(mine.r, j), Max::take(mine.r, j + 1));
+      uint64_t u[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {  // four rows of a column: word rg of it, at the place of stage_transposed
-      const uint32_t w = codes2(__fmul_rn(v[0][j], r8[j]), __fmul_rn(v[1][j], r8[j])) |
-                         codes2(__fmul_rn(v[2][j], r8[j]), __fmul_rn(v[3][j], r8[j])) << 16;
-      *reinterpret_cast<uint32_t*>(s.out + (cg * 8 + j) * 128 + ((rg ^ (2 * cg)) << 2)) = w;
+      for (int i = 0; i < 8; ++i) u[i] = mul_pair(v[i][j / 2], r);
+      uint8_t* to = out + (h * 8 + j) * 128 + q * 8;
+      *reinterpret_cast<uint2*>(to) =
+          make_uint2(codes4(pair(lo_of(u[0]), lo_of(u[1])), pair(lo_of(u[2]), lo_of(u[3]))),
+                     codes4(pair(lo_of(u[4]), lo_of(u[5])), pair(lo_of(u[6]), lo_of(u[7]))));
+      *reinterpret_cast<uint2*>(to + 128) =
+          make_uint2(codes4(pair(hi_of(u[0]), hi_of(u[1])), pair(hi_of(u[2]), hi_of(u[3]))),
+                     codes4(pair(hi_of(u[4]), hi_of(u[5])), pair(hi_of(u[6]), hi_of(u[7]))));
     }
-    __syncthreads();
-    store_transposed<kRecolThreads>(s.out, a.codes + c0 * pitch + b * kB128, pitch, kB128,
-                                    (int)min((int64_t)kB128, a.K - c0));
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t col = c0 + i * 4 + (lane >> 3);
+      const uint4 w = s.out[warp][i * 32 + lane];
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      if (col < a.K) store16B(a.codes + col * pitch + b * kB128 + (lane & 7) * 16, u);
+    }
     if (++c == cols) {
       c = 0;
       ++b;

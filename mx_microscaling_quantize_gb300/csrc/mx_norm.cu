@@ -18,19 +18,19 @@ namespace mxq {
 
 namespace {
 
-constexpr int kForwardWarps = 8;  // of a CTA, and of a group that holds one row
-constexpr int kMaxWarps = 16;     // the same of the backward pass
-constexpr int kRingBytes = 200 * 1024;
 constexpr int kMaxParts = 304;  // of the weight's gradient: rows are split over at most so many CTAs
+constexpr int kBackwardThreads = 512;
 
 // Barrier of one group of warps (ids 1 ..; a group of one warp needs none beyond its own order).
 __device__ __forceinline__ void group_sync(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
 
+// Sum over the lanes that differ in the bits below N; over the warp.
+template <int N = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int s = 16; s; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
+  for (int s = N / 2; s; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
   return v;
 }
 
@@ -45,36 +45,57 @@ __device__ __forceinline__ float load_as_f32(const void* p, bool f32, int64_t i)
              : __uint_as_float(load_u16(static_cast<const uint16_t*>(p) + i) << 16);
 }
 
-__device__ __forceinline__ void store_from_f32(void* p, bool f32, int64_t i, float v) {
+// 8 consecutive values of a weight or a bias (aligned to 32 bytes), kept in L1 for the next rows.
+__device__ __forceinline__ void load_param(const void* p, bool f32, int i, uint64_t (&v)[4]) {
   if (f32) {
-    static_cast<float*>(p)[i] = v;
+    asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                 : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3])
+                 : "l"(static_cast<const float*>(p) + i));
   } else {
-    static_cast<uint16_t*>(p)[i] = (uint16_t)pack_bf16(v, 0.0f);
+    const uint4 q = load_v4(static_cast<const uint16_t*>(p) + i);
+    v[0] = bf16_pair(q.x);
+    v[1] = bf16_pair(q.y);
+    v[2] = bf16_pair(q.z);
+    v[3] = bf16_pair(q.w);
   }
 }
 
-// N consecutive values of a weight or a bias (aligned to 16 bytes), kept in L1 for the next rows.
-template <int N>
-__device__ __forceinline__ void load_param(const void* p, bool f32, int64_t i, float* v) {
+// N values of a weight or a bias (fallback where there is none), a group's width apart.
+template <int N, typename F>
+__device__ __forceinline__ void load_params(const void* p, bool f32, int K, F&& column, float fallback,
+                                            float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = fallback;
+  if (!p) return;
   if (f32) {
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-      const uint4 q = load_v4(static_cast<const float*>(p) + i + j);
-      v[j] = __uint_as_float(q.x);
-      v[j + 1] = __uint_as_float(q.y);
-      v[j + 2] = __uint_as_float(q.z);
-      v[j + 3] = __uint_as_float(q.w);
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) v[i] = load_f32(static_cast<const float*>(p) + column(i));
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < N; j += 8) {
-      const uint4 q = load_v4(static_cast<const uint16_t*>(p) + i + j);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) v[i] = load_as_f32(p, false, column(i));
+    }
+  }
+}
+
+// N values of a row (0 where there is none) and their way back.
+template <int N, typename F>
+__device__ __forceinline__ void load_values(const char* row, bool f32, int K, F&& column, float (&v)[N]) {
+  load_params(row, f32, K, column, 0.0f, v);
+}
+template <int N, typename F>
+__device__ __forceinline__ void store_values(char* row, bool f32, int K, F&& column, const float (&v)[N]) {
+  if (f32) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[j + 2 * k] = bf16_lo(w[k]);
-        v[j + 2 * k + 1] = bf16_hi(w[k]);
-      }
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) reinterpret_cast<float*>(row)[column(i)] = v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) reinterpret_cast<uint16_t*>(row)[column(i)] = (uint16_t)pack_bf16(v[i], 0.0f);
     }
   }
 }
@@ -82,259 +103,403 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, int64_t i, f
 // ------------------------------------------------------------------------------------------
 // forward
 // ------------------------------------------------------------------------------------------
-// C chunks of 16 values per lane: with VEC a lane's chunk is 16 consecutive columns (32-byte loads),
-// else its columns are the group's width apart, for rows of any length and alignment.
-template <bool XF32, int C, bool VEC, bool QUANT>
-struct NormRow {
-  static constexpr int kWords = C * (XF32 || !VEC ? 16 : 8);
-  uint32_t raw[kWords];
-
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int t, int T) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if constexpr (VEC) {
-        const int64_t col = (int64_t)(c * T + t) * 16;
-        if (col < a.K) {
-          const char* p = static_cast<const char*>(a.x) + (row * a.K + col) * (XF32 ? 4 : 2);
-          load32B(p, raw + c * (XF32 ? 16 : 8));
-          if constexpr (XF32) load32B(p + 32, raw + c * 16 + 8);
-        } else {
-#pragma unroll
-          for (int j = 0; j < (XF32 ? 16 : 8); ++j) raw[c * (XF32 ? 16 : 8) + j] = 0u;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int64_t col = (int64_t)(c * 16 + j) * T + t;
-          raw[c * 16 + j] = col < a.K ? __float_as_uint(load_as_f32(a.x, XF32, row * a.K + col)) : 0u;
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void values(float (&v)[16 * C]) const {
-    if constexpr (XF32 || !VEC) {
-#pragma unroll
-      for (int i = 0; i < 16 * C; ++i) v[i] = __uint_as_float(raw[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8 * C; ++i) {
-        v[2 * i] = bf16_lo(raw[i]);
-        v[2 * i + 1] = bf16_hi(raw[i]);
-      }
-    }
-  }
-};
-
-// 16 values of one row's block (eight lanes hold a block) as codes and a scale.
-__device__ __forceinline__ void store_block_codes(const float* v, uint8_t* codes, float* scales, int64_t M,
-                                                  int64_t K, int64_t row, int64_t col) {
-  uint32_t m = absmax_f32x16(v);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-  if (col >= K) return;
-  const Factors f = block_factors_b128(m);
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    w[j] = codes2(__fmul_rn(v[4 * j], f.r), __fmul_rn(v[4 * j + 1], f.r)) |
-           codes2(__fmul_rn(v[4 * j + 2], f.r), __fmul_rn(v[4 * j + 3], f.r)) << 16;
-  }
-  store16B(codes + row * K + col, w);
-  if ((col & (kB128 - 1)) == 0) scales[col / kB128 * M + row] = f.scale;
+// Mean and 1 / deviation of a row from each warp's mean and sum of squared differences from it (part: of the
+// CTA's warps), count(w) values in warp w of the group: the warps' sums about their own means are joined with
+// their means' distance from the row's.
+template <int WARPS, typename F>
+__device__ __forceinline__ void join_stats(const NormArgs& a, float2* part, int group, int W, F&& count,
+                                           float& mean, float& sq) {
+  const int lane = threadIdx.x & 31, i = lane & (WARPS - 1), w0 = group * W;
+  if (lane == 0) part[threadIdx.x >> 5] = make_float2(mean, sq);
+  group_sync(group, 32 * W);
+  const float2 p = i < W ? part[w0 + i] : make_float2(0.0f, 0.0f);
+  const float n = i < W ? (float)count(i) : 0.0f;
+  mean = a.center ? __fdividef(warp_sum<WARPS>(p.x * n), (float)a.K) : 0.0f;
+  sq = warp_sum<WARPS>(fmaf((p.x - mean) * n, p.x - mean, p.y));
 }
 
-template <bool XF32, int C, bool VEC, bool QUANT>
-__global__ void __launch_bounds__(32 * kForwardWarps) norm_kernel(NormArgs a, int W) {
-  __shared__ float2 part[2][kForwardWarps];  // a warp's mean and sum of squared differences from it
-  __shared__ float count[kForwardWarps];
+// 1 / sqrt(sq / K + eps), within 2^-22 (an approximate root; 1 / K and the quotient round too).
+__device__ __forceinline__ float deviation(const NormArgs& a, float sq) {
+  return rsqrtf(fmaf(sq, __fdividef(1.0f, (float)a.K), a.eps));
+}
+
+__device__ __forceinline__ void store_stats(const NormArgs& a, int64_t row, float mean, float rstd) {
+  if (a.mean) a.mean[row] = mean;
+  if (a.rstd) a.rstd[row] = rstd;
+}
+
+// P runs of 8 columns per lane (run p: columns 8 (p T + t) ..) as codes, with their blocks' scales.
+template <int P>
+__device__ __forceinline__ void store_codes(const uint64_t (&v)[P][4], uint8_t* codes, float* scales,
+                                            int64_t M, int K, int64_t row, int t, int T) {
+  run_codes<P>(
+      v,
+      [&](int p, uint32_t lo, uint32_t hi) {
+        const int col = (p * T + t) * 8;
+        if (col < K) store8B(codes + row * K + col, lo, hi);
+      },
+      [&](int p, float scale) {
+        const int kb = (p * T + t) >> 4;
+        if (kb * kB128 < K) scales[kb * M + row] = scale;
+      });
+}
+
+// A group of W warps per row, P runs of 8 columns per lane in fp32 pairs: the loads of a row are in flight
+// together, and what hides its chain (load, two sums over the group, weights, stores) is the other rows of
+// the SM. THREADS: of a CTA, at most.
+template <bool XF32, int P, bool QUANT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) norm_kernel(NormArgs a, int W) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ float2 part[kWarps];
   pdl_launch_dependents();
   pdl_wait();
-  const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T;
-  const int lane = threadIdx.x & 31, w0 = group * W, wi = t >> 5;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
-  int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
-  int mine = 0;  // columns of this lane
+  const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+  if (row >= a.M) return;
+  auto column = [&](int p) { return (p * T + t) * 8; };
+  auto count = [&](int w) {  // columns of the group's warp w
+    int n = 0;
 #pragma unroll
-  for (int i = 0; i < 16 * C; ++i) {
-    mine += (VEC ? (int64_t)((i / 16) * T + t) * 16 + i % 16 : (int64_t)i * T + t) < a.K;
+    for (int p = 0; p < P; ++p) n += min(max(K - (p * T + 32 * w) * 8, 0), 256);
+    return n;
+  };
+  uint64_t x[P][4];
+  const char* from = static_cast<const char*>(a.x) + row * K * (XF32 ? 4 : 2);
+  uint32_t raw[P][XF32 ? 8 : 4];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (column(p) < K) {
+      if constexpr (XF32) {
+        load32B(from + column(p) * 4, raw[p]);
+      } else {
+        load16B(from + column(p) * 2, raw[p]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < (XF32 ? 8 : 4); ++j) raw[p][j] = 0u;
+    }
   }
-  const float n = (float)__reduce_add_sync(0xFFFFFFFFu, (unsigned)mine);
-  if (lane == 0) count[w0 + wi] = n;
-  if (W > 1) group_sync(group, T);
-  const float per_n = n > 0.0f ? __fdiv_rn(1.0f, n) : 0.0f, per_k = __fdiv_rn(1.0f, (float)a.K);
-  NormRow<XF32, C, VEC, QUANT> next;
-  if (row < a.M) next.load(a, row, t, T);
-  for (int slot = 0; row < a.M; row += step, slot ^= 1) {
-    float v[16 * C];
-    next.values(v);
-    if (row + step < a.M) next.load(a, row + step, t, T);
-    float mean = 0.0f;
-    if (a.center) {
-      float s[4] = {};
 #pragma unroll
-      for (int i = 0; i < 16 * C; ++i) s[i & 3] += v[i];
-      mean = warp_sum((s[0] + s[1]) + (s[2] + s[3])) * per_n;
-    }
-    float s[4] = {};
+  for (int p = 0; p < P; ++p) {
 #pragma unroll
-    for (int i = 0; i < 16 * C; ++i) {
-      const bool there = (VEC ? (int64_t)((i / 16) * T + t) * 16 : (int64_t)i * T + t) < a.K;
-      const float d = there ? v[i] - mean : 0.0f;
-      s[i & 3] = fmaf(d, d, s[i & 3]);
-    }
-    float sq = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (W > 1) {
-      if (lane == 0) part[slot][w0 + wi] = make_float2(mean, sq);
-      group_sync(group, T);
-      float total = 0.0f, m = 0.0f;
-      if (a.center) {
-        for (int i = 0; i < W; ++i) m = fmaf(part[slot][w0 + i].x, count[w0 + i], m);
-        m *= per_k;
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (XF32) {
+        x[p][j] = pair(__uint_as_float(raw[p][2 * j]), __uint_as_float(raw[p][2 * j + 1]));
+      } else {
+        x[p][j] = bf16_pair(raw[p][j]);
       }
-      for (int i = 0; i < W; ++i) {
-        const float2 p = part[slot][w0 + i];
-        total += fmaf((p.x - m) * count[w0 + i], p.x - m, p.y);
-      }
-      mean = m;
-      sq = total;
     }
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sq, per_k, a.eps)));
-    if (t == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+  }
+  if constexpr (QUANT) {
+    if (a.x_codes) store_codes<P>(x, a.x_codes, a.x_scales_out, a.M, K, row, t, T);
+  }
+  float mean = 0.0f;
+  if (a.center) {
+    uint64_t s[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[i / 4][i % 4]);
+    s[0] = add_pair(s[0], s[1]);
+    const int n = count(t >> 5);
+    mean = n > 0 ? __fdividef(warp_sum(lo_of(s[0]) + hi_of(s[0])), (float)n) : 0.0f;
+  }
+  uint64_t s[2] = {0u, 0u};
+  const uint64_t less = pair(-mean);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (column(p) >= K) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t d = add_pair(x[p][j], less);
+      s[j & 1] = fma_pair(d, d, s[j & 1]);
     }
+  }
+  s[0] = add_pair(s[0], s[1]);
+  float sq = warp_sum(lo_of(s[0]) + hi_of(s[0]));
+  if (W > 1) join_stats<kWarps>(a, part, group, W, count, mean, sq);
+  const float rstd = deviation(a, sq);
+  if (t == 0) store_stats(a, row, mean, rstd);
+  const uint64_t minus = pair(-mean), r2 = pair(rstd);
+  const bool w_f32 = a.w_type == kTypeFp32;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      if constexpr (VEC) {
-        const int64_t col = (int64_t)(c * T + t) * 16;
-        if constexpr (QUANT) {
-          if (a.x_codes) store_block_codes(v + 16 * c, a.x_codes, a.x_scales_out, a.M, a.K, row, col);
+  for (int p = 0; p < P; ++p) {
+    if (column(p) >= K) continue;  // zeros
+    uint64_t w[4], b[4];
+    if (a.weight) load_param(a.weight, w_f32, column(p), w);
+    if (a.bias) load_param(a.bias, w_f32, column(p), b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[p][j] = mul_pair(add_pair(x[p][j], minus), r2);
+    if (a.weight) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[p][j] = mul_pair(x[p][j], w[j]);
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[p][j] = add_pair(x[p][j], b[j]);
+    }
+    if constexpr (!QUANT) {
+      uint32_t o[8];
+      if (a.y_type == kTypeFp32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o[2 * j] = __float_as_uint(lo_of(x[p][j]));
+          o[2 * j + 1] = __float_as_uint(hi_of(x[p][j]));
         }
-        float y[16];
-        if (col < a.K) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = (v[16 * c + j] - mean) * rstd;
-          float p[16];
-          if (a.weight) {
-            load_param<16>(a.weight, a.w_type == kTypeFp32, col, p);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] *= p[j];
-          }
-          if (a.bias) {
-            load_param<16>(a.bias, a.w_type == kTypeFp32, col, p);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] += p[j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = 0.0f;
-        }
-        if constexpr (QUANT) {
-          store_block_codes(y, a.codes, a.scales, a.M, a.K, row, col);
-        } else if (col < a.K) {
-          uint32_t o[8];
-          if (a.y_type == kTypeFp32) {
-            float* to = static_cast<float*>(a.y) + row * a.K + col;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(y[8 * h + j]);
-              store32B(to + 8 * h, o);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
-            store32B(static_cast<uint16_t*>(a.y) + row * a.K + col, o);
-          }
-        }
+        store32B(static_cast<float*>(a.y) + row * K + column(p), o);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int64_t col = (int64_t)(c * 16 + j) * T + t;
-          if (col >= a.K) continue;
-          float y = (v[16 * c + j] - mean) * rstd;
-          if (a.weight) y *= load_as_f32(a.weight, a.w_type == kTypeFp32, col);
-          if (a.bias) y += load_as_f32(a.bias, a.w_type == kTypeFp32, col);
-          store_from_f32(a.y, a.y_type == kTypeFp32, row * a.K + col, y);
-        }
+        for (int j = 0; j < 4; ++j) o[j] = bf16_word(x[p][j]);
+        store16B(static_cast<uint16_t*>(a.y) + row * K + column(p), o);
       }
     }
   }
+  if constexpr (QUANT) store_codes<P>(x, a.codes, a.scales, a.M, K, row, t, T);
+}
+
+// The same for rows of any length and alignment: 16 columns per lane, a group's width apart, loaded and
+// stored one by one.
+template <bool XF32, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) norm_any_kernel(NormArgs a, int W) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ float2 part[kWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+  if (row >= a.M) return;
+  auto column = [&](int i) { return i * T + t; };
+  auto count = [&](int w) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) n += min(max(K - i * T - 32 * w, 0), 32);
+    return n;
+  };
+  float x[16], p[16];
+  load_values(static_cast<const char*>(a.x) + row * K * (XF32 ? 4 : 2), XF32, K, column, x);
+  float mean = 0.0f;
+  if (a.center) {
+    float s[2] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i & 1] += x[i];
+    const int n = count(t >> 5);
+    mean = n > 0 ? __fdividef(warp_sum(s[0] + s[1]), (float)n) : 0.0f;
+  }
+  float s[2] = {};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float d = column(i) < K ? x[i] - mean : 0.0f;
+    s[i & 1] = fmaf(d, d, s[i & 1]);
+  }
+  float sq = warp_sum(s[0] + s[1]);
+  if (W > 1) join_stats<kWarps>(a, part, group, W, count, mean, sq);
+  const float rstd = deviation(a, sq);
+  if (t == 0) store_stats(a, row, mean, rstd);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = (x[i] - mean) * rstd;
+  const bool w_f32 = a.w_type == kTypeFp32;
+  load_params(a.weight, w_f32, K, column, 1.0f, p);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] *= p[i];
+  load_params(a.bias, w_f32, K, column, 0.0f, p);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] += p[i];
+  const bool y_f32 = a.y_type == kTypeFp32;
+  store_values(static_cast<char*>(a.y) + row * K * (y_f32 ? 4 : 2), y_f32, K, column, x);
 }
 
 // ------------------------------------------------------------------------------------------
 // backward
 // ------------------------------------------------------------------------------------------
-// Gradient of the input, and each CTA's share of the parameters' gradients, which norm_reduce_kernel
-// adds up. C chunks of 8 values per lane. With VEC a thread's pieces of the next rows are on their way
-// into places of its own in shared memory (cp.async: no barrier); without, values are loaded one by one.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+
+__device__ __forceinline__ void unpack8(uint4 q, uint64_t* v) {
+  v[0] = bf16_pair(q.x);
+  v[1] = bf16_pair(q.y);
+  v[2] = bf16_pair(q.z);
+  v[3] = bf16_pair(q.w);
+}
+
+// Chunks of 8 values per lane: the pieces of a row that a thread copies into places of its own in shared
+// memory (so no barrier is needed), `stages` rows ahead.
+template <int C, int XT, bool DYF32>
 struct NormRing {
-  int stages, bytes;             // of shared memory
-  int x_piece, x_pieces;         // bytes of a copy of x and copies per chunk
-  int dy_at, dy_pieces, scale_at;  // within a stage
+  static constexpr int kX = XT == kTypeB128 ? 8 : XT == kTypeFp32 ? 32 : 16, kDy = DYF32 ? 32 : 16;
+  static constexpr int kScale = XT == kTypeB128 ? 4 : 0;
+  static constexpr int kChunk = kX + kDy + kScale;  // bytes of shared memory per thread, chunk and stage
+  static constexpr int kFit = 200 * 1024 / (kBackwardThreads * C * kChunk);
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static_assert(kStages >= 1, "a row fits shared memory");
+
+  uint8_t* sm;
+  int threads, tid;
+
+  __device__ __forceinline__ uint8_t* place(int stage, int c) const {
+    return sm + (stage * C + c) * kChunk * threads;
+  }
+  __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int col, int stage, int c) const {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(place(stage, c));
+    const char* x = static_cast<const char*>(a.x) + (row * a.K + col) * (kX / 8);
+    const char* dy = static_cast<const char*>(a.y) + (row * a.K + col) * (kDy / 8);
+    if constexpr (XT == kTypeB128) {
+      copy8(at + tid * 8, x);
+    } else {
+#pragma unroll
+      for (int p = 0; p < kX / 16; ++p) copy16(at + (p * threads + tid) * 16, x + p * 16);
+    }
+#pragma unroll
+    for (int p = 0; p < kDy / 16; ++p) copy16(at + kX * threads + (p * threads + tid) * 16, dy + p * 16);
+    if constexpr (XT == kTypeB128) {
+      copy4(at + (kX + kDy) * threads + tid * 4, a.x_scales + col / kB128 * a.M + row);
+    }
+  }
+  __device__ __forceinline__ void read(int stage, int c, uint64_t* x, uint64_t* dy) const {
+    const uint8_t* at = place(stage, c);
+    if constexpr (XT == kTypeBf16) {
+      unpack8(reinterpret_cast<const uint4*>(at)[tid], x);
+    } else if constexpr (XT == kTypeFp32) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        *reinterpret_cast<ulonglong2*>(x + 2 * p) = reinterpret_cast<const ulonglong2*>(at)[p * threads + tid];
+      }
+    } else {
+      const uint2 q = reinterpret_cast<const uint2*>(at)[tid];
+      const float s = reinterpret_cast<const float*>(at + (kX + kDy) * threads)[tid];
+      values4(q.x, x[0], x[1]);
+      values4(q.y, x[2], x[3]);
+      // (not packed: ptxas joins a packed product and the sum after it, and with it two roundings)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = pair(__fmul_rn(lo_of(x[j]), s), __fmul_rn(hi_of(x[j]), s));
+    }
+    const uint8_t* dys = at + kX * threads;
+    if constexpr (DYF32) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        *reinterpret_cast<ulonglong2*>(dy + 2 * p) = reinterpret_cast<const ulonglong2*>(dys)[p * threads + tid];
+      }
+    } else {
+      unpack8(reinterpret_cast<const uint4*>(dys)[tid], dy);
+    }
+  }
 };
 
-__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
-  if (bytes == 16) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-  } else if (bytes == 8) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
-  } else {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+// Two sums over the row of a group of W warps (slot: of two, taken in turn): the two halves of a warp take one
+// each, so that five exchanges do for both.
+__device__ __forceinline__ void row_sums(float (&part)[2][2][kBackwardThreads / 32], int slot, int group, int W,
+                                         float& s1, float& s2) {
+  constexpr int kWarps = kBackwardThreads / 32;
+  const int lane = threadIdx.x & 31, half = lane >> 4;
+  float mine = half ? s2 : s1;
+  mine += __shfl_xor_sync(0xFFFFFFFFu, half ? s1 : s2, 16);
+  mine = warp_sum<16>(mine);
+  if (W > 1) {
+    const int i = lane & (kWarps - 1);
+    if (i == 0) part[slot][half][threadIdx.x >> 5] = mine;
+    group_sync(group, 32 * W);
+    mine = warp_sum<kWarps>(i < W ? part[slot][half][group * W + i] : 0.0f);
+  }
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, mine, 16);
+  s1 = half ? other : mine;
+  s2 = half ? mine : other;
+}
+
+// The groups' shares of dw and db (N columns of a thread), joined in their order through shared memory, to
+// this CTA's row of the workspace; of a single CTA to where they belong.
+template <int N, typename F, typename W1, typename W2>
+__device__ __forceinline__ void store_shares(const NormArgs& a, float* sm, int W, F&& column, W1&& dw,
+                                             W2&& db) {
+  const int T = 32 * W, groups = blockDim.x / T, group = threadIdx.x / T, K = (int)a.K;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* whole = k ? a.dbias : a.dweight;
+    if (!whole) continue;
+    float* out = gridDim.x == 1 ? whole : a.workspace + (k * (int64_t)gridDim.x + blockIdx.x) * K;
+    float* to = groups > 1 ? sm + group * K : out;
+    if (groups > 1) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) to[column(i)] = k ? db(i) : dw(i);
+    }
+    if (groups == 1) continue;
+    __syncthreads();
+    for (int col = threadIdx.x; col < K; col += blockDim.x) {
+      float s = 0.0f;
+      for (int i = 0; i < groups; ++i) s += sm[i * K + col];
+      out[col] = s;
+    }
   }
 }
 
-template <int C, bool VEC, int XT>
-__global__ void __launch_bounds__(32 * kMaxWarps, 1) norm_backward_kernel(NormArgs a, int W, NormRing r) {
-  extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float2 part[2][kMaxWarps];
+// Gradient of the input, and each CTA's share of the parameters' gradients, which norm_reduce_kernel
+// adds up. A CTA walks rows gridDim.x groups apart, its sums of dw and db in registers. With two chunks a
+// lane keeps xhat and g over the sums of the row, with four it reads the row from its places again.
+template <int C, int XT, bool DYF32>
+__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(NormArgs a, int W) {
+  extern __shared__ __align__(16) uint8_t ring_shared[];
+  __shared__ float part[2][2][kBackwardThreads / 32];
+  using Ring = NormRing<C, XT, DYF32>;
+  constexpr bool kKeep = C <= 2;
   pdl_launch_dependents();
   pdl_wait();
-  const int threads = blockDim.x, T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T;
-  const int lane = threadIdx.x & 31, w0 = group * W, wi = t >> 5, tid = threadIdx.x;
-  const int64_t step = (int64_t)gridDim.x * (threads / T);
-  int64_t row = (int64_t)blockIdx.x * (threads / T) + group;
-  const bool dy_f32 = a.y_type == kTypeFp32, dx_f32 = a.dx_type == kTypeFp32;
-  const float per_k = __fdiv_rn(1.0f, (float)a.K);
-  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring);
+  const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
+  const Ring ring{ring_shared, (int)blockDim.x, (int)threadIdx.x};
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
+  int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+  const bool dx_f32 = a.dx_type == kTypeFp32, w_f32 = a.w_type == kTypeFp32;
+  const float per_k = __fdiv_rn(1.0f, (float)K);
 
-  auto column = [&](int c, int j) -> int64_t {
-    return VEC ? (int64_t)(c * T + t) * 8 + j : (int64_t)(c * 8 + j) * T + t;
-  };
-  auto request = [&](int64_t at, int stage) {  // VEC: this thread's pieces of a row
+  auto column = [&](int i) { return ((i / 8) * T + t) * 8 + i % 8; };
+  auto request = [&](int64_t at, int stage) {
     if (at < a.M) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int64_t col = column(c, 0);
-        if (col >= a.K) break;
-        const uint32_t to = base + stage * r.bytes;
-        const char* x = static_cast<const char*>(a.x) + (at * a.K + col) * (r.x_piece * r.x_pieces / 8);
-        for (int p = 0; p < r.x_pieces; ++p) {
-          copy_async(to + ((c * r.x_pieces + p) * threads + tid) * r.x_piece, x + p * r.x_piece, r.x_piece);
-        }
-        const char* dy = static_cast<const char*>(a.y) + (at * a.K + col) * (2 * r.dy_pieces);
-        for (int p = 0; p < r.dy_pieces; ++p) {
-          copy_async(to + r.dy_at + ((c * r.dy_pieces + p) * threads + tid) * 16, dy + p * 16, 16);
-        }
-        if (XT == kTypeB128) {
-          copy_async(to + r.scale_at + (c * threads + tid) * 4, a.x_scales + col / kB128 * a.M + at, 4);
-        }
+        if (column(8 * c) < K) ring.request(a, at, column(8 * c), stage, c);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-
-  float w[8 * C], dw[8 * C], db[8 * C];
+  auto load_weight = [&](int c, uint64_t (&w)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8 * C; ++i) {
-    const int64_t col = column(i / 8, i % 8);
-    w[i] = a.weight && col < a.K ? load_as_f32(a.weight, a.w_type == kTypeFp32, col) : 1.0f;
-    dw[i] = db[i] = 0.0f;
+    for (int j = 0; j < 4; ++j) w[j] = pair(1.0f);
+    if (a.weight && column(8 * c) < K) load_param(a.weight, w_f32, column(8 * c), w);
+  };
+  auto store = [&](int c, const uint64_t* g, const uint64_t* xh, float s1, float s2, float rstd) {
+    uint64_t d[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d[j] = mul_pair(fma_pair(xh[j], pair(-s2), add_pair(g[j], pair(-s1))), pair(rstd));
+    }
+    uint32_t o[8];
+    if (dx_f32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[2 * j] = __float_as_uint(lo_of(d[j]));
+        o[2 * j + 1] = __float_as_uint(hi_of(d[j]));
+      }
+      store16B(static_cast<float*>(a.dx) + row * K + column(8 * c), o);
+      store16B(static_cast<float*>(a.dx) + row * K + column(8 * c) + 4, o + 4);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = bf16_word(d[j]);
+      store16B(static_cast<uint16_t*>(a.dx) + row * K + column(8 * c), o);
+    }
+  };
+
+  uint64_t w[kKeep ? C : 1][4], dw[4 * C], db[4 * C];
+#pragma unroll
+  for (int i = 0; i < 4 * C; ++i) dw[i] = db[i] = 0u;
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_weight(c, w[c]);
   }
-  if constexpr (VEC) {
-    for (int s = 0; s < r.stages; ++s) request(row + s * step, s);
-  }
+#pragma unroll
+  for (int s = 0; s < Ring::kStages; ++s) request(row + s * step, s);
   float mean_next = 0.0f, rstd_next = 0.0f;
   if (row < a.M) {
     rstd_next = load_f32(a.rstd + row);
@@ -343,186 +508,127 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) norm_backward_kernel(NormAr
   int stage = 0;
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
     const float mean = mean_next, rstd = rstd_next;
+    const uint64_t minus = pair(-mean), r2 = pair(rstd);
     if (row + step < a.M) {
       rstd_next = load_f32(a.rstd + row + step);
       if (a.mean) mean_next = load_f32(a.mean + row + step);
     }
-    float xh[8 * C], g[8 * C];
-    if constexpr (VEC) {
-      if (r.stages == 4) {
-        asm volatile("cp.async.wait_group 3;" ::: "memory");
-      } else if (r.stages == 2) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(Ring::kStages - 1) : "memory");
+    uint64_t xh[kKeep ? C : 1][4], g[kKeep ? C : 1][4];
+    uint64_t c1 = 0u, c2 = 0u;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if constexpr (VEC) {
-        if (column(c, 0) < a.K) {
-          const uint8_t* at = ring + stage * r.bytes;
-          if (XT == kTypeBf16) {
-            const uint4 q = reinterpret_cast<const uint4*>(at)[c * threads + tid];
-            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+      constexpr int kOne = 0;
+      uint64_t(&x)[4] = xh[kKeep ? c : kOne];
+      uint64_t(&y)[4] = g[kKeep ? c : kOne];
+      uint64_t(&u)[4] = w[kKeep ? c : kOne];
+      if (column(8 * c) < K) {
+        ring.read(stage, c, x, y);
+        if constexpr (!kKeep) load_weight(c, u);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              xh[8 * c + 2 * j] = bf16_lo(u[j]);
-              xh[8 * c + 2 * j + 1] = bf16_hi(u[j]);
-            }
-          } else if (XT == kTypeFp32) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const float4 q = reinterpret_cast<const float4*>(at)[(2 * c + p) * threads + tid];
-              xh[8 * c + 4 * p] = q.x;
-              xh[8 * c + 4 * p + 1] = q.y;
-              xh[8 * c + 4 * p + 2] = q.z;
-              xh[8 * c + 4 * p + 3] = q.w;
-            }
-          } else {
-            const uint2 q = reinterpret_cast<const uint2*>(at)[c * threads + tid];
-            const float s = reinterpret_cast<const float*>(at + r.scale_at)[c * threads + tid];
-            const uint32_t u[2] = {q.x, q.y};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              e4m3x2_to_f32(u[j] & 0xFFFFu, xh[8 * c + 4 * j], xh[8 * c + 4 * j + 1]);
-              e4m3x2_to_f32(u[j] >> 16, xh[8 * c + 4 * j + 2], xh[8 * c + 4 * j + 3]);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) xh[8 * c + j] = __fmul_rn(xh[8 * c + j], s);
-          }
-          if (dy_f32) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-              const float4 q = reinterpret_cast<const float4*>(at + r.dy_at)[(2 * c + p) * threads + tid];
-              g[8 * c + 4 * p] = q.x;
-              g[8 * c + 4 * p + 1] = q.y;
-              g[8 * c + 4 * p + 2] = q.z;
-              g[8 * c + 4 * p + 3] = q.w;
-            }
-          } else {
-            const uint4 q = reinterpret_cast<const uint4*>(at + r.dy_at)[c * threads + tid];
-            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              g[8 * c + 2 * j] = bf16_lo(u[j]);
-              g[8 * c + 2 * j + 1] = bf16_hi(u[j]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            xh[8 * c + j] = mean;  // xhat 0
-            g[8 * c + j] = 0.0f;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t col = column(c, j), i = row * a.K + col;
-          xh[8 * c + j] = mean;
-          g[8 * c + j] = 0.0f;
-          if (col >= a.K) continue;
-          if (XT == kTypeB128) {
-            float lo, hi;
-            e4m3x2_to_f32(load_u8(static_cast<const uint8_t*>(a.x) + i), lo, hi);
-            xh[8 * c + j] = __fmul_rn(lo, load_f32(a.x_scales + col / kB128 * a.M + row));
-          } else {
-            xh[8 * c + j] = load_as_f32(a.x, XT == kTypeFp32, i);
-          }
-          g[8 * c + j] = load_as_f32(a.y, dy_f32, i);
+        for (int j = 0; j < 4; ++j) {
+          x[j] = mul_pair(add_pair(x[j], minus), r2);
+          dw[4 * c + j] = fma_pair(y[j], x[j], dw[4 * c + j]);
+          db[4 * c + j] = add_pair(db[4 * c + j], y[j]);
+          y[j] = mul_pair(y[j], u[j]);
+          c1 = add_pair(c1, y[j]);
+          c2 = fma_pair(y[j], x[j], c2);
         }
       }
     }
-    if constexpr (VEC) {  // into the places just read, by this thread alone
-      request(row + r.stages * step, stage);
-      stage = stage + 1 == r.stages ? 0 : stage + 1;
+    if constexpr (kKeep) {  // into the places just read, by this thread alone
+      request(row + Ring::kStages * step, stage);
     }
-    float c1[2] = {}, c2[2] = {};
-#pragma unroll
-    for (int i = 0; i < 8 * C; ++i) {
-      xh[i] = (xh[i] - mean) * rstd;
-      dw[i] = fmaf(g[i], xh[i], dw[i]);
-      db[i] += g[i];
-      g[i] *= w[i];
-      c1[i & 1] += g[i];
-      c2[i & 1] = fmaf(g[i], xh[i], c2[i & 1]);
-    }
-    float s1 = warp_sum(c1[0] + c1[1]), s2 = warp_sum(c2[0] + c2[1]);
-    if (W > 1) {
-      if (lane == 0) part[slot][w0 + wi] = make_float2(s1, s2);
-      group_sync(group, T);
-      s1 = s2 = 0.0f;
-      for (int i = 0; i < W; ++i) {
-        const float2 p = part[slot][w0 + i];
-        s1 += p.x;
-        s2 += p.y;
-      }
-    }
+    float s1 = lo_of(c1) + hi_of(c1), s2 = lo_of(c2) + hi_of(c2);
+    row_sums(part, slot, group, W, s1, s2);
     s1 = a.mean ? s1 * per_k : 0.0f;
     s2 *= per_k;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if constexpr (VEC) {
-        const int64_t col = column(c, 0);
-        if (col >= a.K) continue;
-        float d[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = (g[8 * c + j] - s1 - xh[8 * c + j] * s2) * rstd;
-        if (dx_f32) {
-          uint32_t o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(d[j]);
-          float* to = static_cast<float*>(a.dx) + row * a.K + col;
-          store16B(to, o);
-          store16B(to + 4, o + 4);
-        } else {
-          uint32_t o[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = pack_bf16(d[2 * j], d[2 * j + 1]);
-          store16B(static_cast<uint16_t*>(a.dx) + row * a.K + col, o);
-        }
+      if (column(8 * c) >= K) continue;
+      if constexpr (kKeep) {
+        store(c, g[c], xh[c], s1, s2, rstd);
       } else {
+        ring.read(stage, c, xh[0], g[0]);
+        load_weight(c, w[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t col = column(c, j);
-          if (col >= a.K) continue;
-          store_from_f32(a.dx, dx_f32, row * a.K + col,
-                         (g[8 * c + j] - s1 - xh[8 * c + j] * s2) * rstd);
+        for (int j = 0; j < 4; ++j) {
+          xh[0][j] = mul_pair(add_pair(xh[0][j], minus), r2);
+          g[0][j] = mul_pair(g[0][j], w[0][j]);
         }
+        store(c, g[0], xh[0], s1, s2, rstd);
       }
     }
+    if constexpr (!kKeep) request(row + Ring::kStages * step, stage);
+    stage = stage + 1 == Ring::kStages ? 0 : stage + 1;
   }
-  if (!a.dweight && !a.dbias) return;
-  // The groups' shares, joined in their order through shared memory, the first gradient after the other.
-  const int groups = threads / T;
-  float* out = a.workspace + (int64_t)blockIdx.x * a.K;
-  const int64_t whole = (int64_t)gridDim.x * a.K;
-  if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  float* sm = reinterpret_cast<float*>(ring);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (a.dweight || a.dbias) {
+    store_shares<8 * C>(
+        a, reinterpret_cast<float*>(ring_shared), W, column,
+        [&](int i) { return i & 1 ? hi_of(dw[i / 2]) : lo_of(dw[i / 2]); },
+        [&](int i) { return i & 1 ? hi_of(db[i / 2]) : lo_of(db[i / 2]); });
+  }
+}
+
+// The same for rows of any length and alignment: N values of a lane, a group's width apart, loaded one by
+// one.
+template <int N>
+__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_any_kernel(NormArgs a, int W) {
+  extern __shared__ __align__(16) uint8_t ring_shared[];
+  __shared__ float part[2][2][kBackwardThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
+  int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+  const bool x_f32 = a.x_type == kTypeFp32, dy_f32 = a.y_type == kTypeFp32, dx_f32 = a.dx_type == kTypeFp32;
+  const bool codes = a.x_type == kTypeB128, w_f32 = a.w_type == kTypeFp32;
+  const float per_k = __fdiv_rn(1.0f, (float)K);
+  auto column = [&](int i) { return i * T + t; };
+  float dw[N], db[N];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!(k ? a.dbias : a.dweight)) continue;
-    if (groups > 1) {
-      __syncthreads();
+  for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.0f;
+  for (int slot = 0; row < a.M; row += step, slot ^= 1) {
+    const float rstd = load_f32(a.rstd + row), mean = a.mean ? load_f32(a.mean + row) : 0.0f;
+    const char* x = static_cast<const char*>(a.x) + row * K * (codes ? 1 : x_f32 ? 4 : 2);
+    const char* dy = static_cast<const char*>(a.y) + row * K * (dy_f32 ? 4 : 2);
+    float xh[N], g[N], w[N];
+    if (codes) {
 #pragma unroll
-      for (int i = 0; i < 8 * C; ++i) {
-        const int64_t col = column(i / 8, i % 8);
-        if (col < a.K) sm[group * a.K + col] = k ? db[i] : dw[i];
-      }
-      __syncthreads();
-      for (int64_t col = tid; col < a.K; col += threads) {
-        float s = 0.0f;
-        for (int i = 0; i < groups; ++i) s += sm[i * a.K + col];
-        out[k * whole + col] = s;
+      for (int i = 0; i < N; ++i) {
+        xh[i] = 0.0f;
+        if (column(i) >= K) continue;
+        float lo, hi;
+        e4m3x2_to_f32(load_u8(x + column(i)), lo, hi);
+        xh[i] = __fmul_rn(lo, load_f32(a.x_scales + column(i) / kB128 * a.M + row));
       }
     } else {
-#pragma unroll
-      for (int i = 0; i < 8 * C; ++i) {
-        const int64_t col = column(i / 8, i % 8);
-        if (col < a.K) out[k * whole + col] = k ? db[i] : dw[i];
-      }
+      load_values(x, x_f32, K, column, xh);
     }
+    load_values(dy, dy_f32, K, column, g);
+    load_params(a.weight, w_f32, K, column, 1.0f, w);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {  // (g is 0 where there is no column)
+      xh[i] = (xh[i] - mean) * rstd;
+      dw[i] = fmaf(g[i], xh[i], dw[i]);
+      db[i] += g[i];
+      g[i] *= w[i];
+      s1 += g[i];
+      s2 = fmaf(g[i], xh[i], s2);
+    }
+    row_sums(part, slot, group, W, s1, s2);
+    s1 = a.mean ? s1 * per_k : 0.0f;
+    s2 *= per_k;
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = fmaf(-xh[i], s2, g[i] - s1) * rstd;
+    store_values(static_cast<char*>(a.dx) + row * K * (dx_f32 ? 4 : 2), dx_f32, K, column, g);
+  }
+  if (a.dweight || a.dbias) {
+    store_shares<N>(
+        a, reinterpret_cast<float*>(ring_shared), W, column, [&](int i) { return dw[i]; },
+        [&](int i) { return db[i]; });
   }
 }
 
@@ -554,57 +660,62 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(NormArgs a, int parts)
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-template <bool XF32, int C, bool VEC, bool QUANT>
-cudaError_t run_norm(const NormArgs& a, int W, int G, cudaStream_t stream) {
-  const auto kernel = &norm_kernel<XF32, C, VEC, QUANT>;
-  const int threads = 32 * W * G;
-  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, 0, 0);
-  if (slots <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t ctas = (a.M + G - 1) / G;
-  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(threads), 0, stream, a, W);
+cudaError_t run_norm(void (*kernel)(NormArgs, int), const NormArgs& a, int W, cudaStream_t stream) {
+  const int G = W >= 8 ? 1 : 8 / W;  // rows of a CTA
+  return launch_pdl(kernel, dim3((unsigned)((a.M + G - 1) / G)), dim3(32 * W * G), 0, stream, a, W);
 }
 
-template <bool XF32, int C>
-cudaError_t pick_norm(const NormArgs& a, int W, int G, bool vec, cudaStream_t stream) {
-  if (a.codes) return run_norm<XF32, C, true, true>(a, W, G, stream);
-  if (vec) return run_norm<XF32, C, true, false>(a, W, G, stream);
-  return run_norm<XF32, C, false, false>(a, W, G, stream);
+// Rows of up to 512 columns are one warp's with one or two runs per lane; longer ones a group's with four.
+template <bool XF32, bool QUANT>
+cudaError_t pick_norm(const NormArgs& a, cudaStream_t stream) {
+  if (a.K <= 256) return run_norm(&norm_kernel<XF32, 1, QUANT, 256>, a, 1, stream);
+  if (a.K <= 512) return run_norm(&norm_kernel<XF32, 2, QUANT, 256>, a, 1, stream);
+  const int W = (int)((a.K + 1023) / 1024);
+  return run_norm(W <= 8 ? &norm_kernel<XF32, 4, QUANT, 256> : &norm_kernel<XF32, 4, QUANT, 512>, a, W, stream);
 }
 
-template <int C, bool VEC, int XT>
-cudaError_t run_backward(const NormArgs& a, int W, int G, cudaStream_t stream) {
-  const auto kernel = &norm_backward_kernel<C, VEC, XT>;
-  const int threads = 32 * W * G;
-  NormRing r{};
-  if (VEC) {
-    r.x_piece = XT == kTypeB128 ? 8 : 16;
-    r.x_pieces = XT == kTypeFp32 ? 2 : 1;
-    r.dy_pieces = a.y_type == kTypeFp32 ? 2 : 1;
-    r.dy_at = C * threads * r.x_piece * r.x_pieces;
-    r.scale_at = r.dy_at + C * threads * 16 * r.dy_pieces;
-    r.bytes = r.scale_at + (XT == kTypeB128 ? C * threads * 4 : 0);
-    r.stages = r.bytes * 4 <= kRingBytes ? 4 : r.bytes * 2 <= kRingBytes ? 2 : 1;
-  }
+template <bool XF32>
+cudaError_t pick_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
+  if (a.codes) return pick_norm<XF32, true>(a, stream);
+  if (vec) return pick_norm<XF32, false>(a, stream);
+  const int W = (int)((a.K + 511) / 512);
+  return run_norm(W <= 8 ? &norm_any_kernel<XF32, 256> : &norm_any_kernel<XF32, 1024>, a, W, stream);
+}
+
+cudaError_t run_backward(void (*kernel)(NormArgs, int), int ring_bytes, const NormArgs& a, int W,
+                         cudaStream_t stream) {
+  const int G = kBackwardThreads / 32 / W, threads = 32 * W * G;  // G rows of a CTA at once
   const bool params = a.dweight || a.dbias;
-  size_t smem = (size_t)r.stages * r.bytes;
+  size_t smem = (size_t)ring_bytes * threads;
   if (params && G > 1 && smem < (size_t)G * a.K * 4) smem = (size_t)G * a.K * 4;
   const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, 0);
   if (slots <= 0) return cudaErrorInvalidConfiguration;
   int64_t ctas = (a.M + G - 1) / G;
   if (ctas > slots) ctas = slots;
   if (params && ctas > kMaxParts) ctas = kMaxParts;
-  const cudaError_t err =
-      launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), smem, stream, a, W, r);
-  if (err != cudaSuccess || !params) return err;
+  const cudaError_t err = launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), smem, stream, a, W);
+  if (err != cudaSuccess || !params || ctas == 1) return err;
   return launch_pdl(&norm_reduce_kernel, dim3((unsigned)((a.K + 31) / 32), 2), dim3(512), 0, stream, a,
                     (int)ctas);
 }
 
-template <int C, bool VEC>
-cudaError_t pick_backward(const NormArgs& a, int W, int G, cudaStream_t stream) {
-  if (a.x_type == kTypeBf16) return run_backward<C, VEC, kTypeBf16>(a, W, G, stream);
-  if (a.x_type == kTypeFp32) return run_backward<C, VEC, kTypeFp32>(a, W, G, stream);
-  return run_backward<C, VEC, kTypeB128>(a, W, G, stream);
+template <int C, int XT, bool DYF32>
+cudaError_t run_ring(const NormArgs& a, int W, cudaStream_t stream) {
+  using Ring = NormRing<C, XT, DYF32>;
+  return run_backward(&norm_backward_kernel<C, XT, DYF32>, Ring::kStages * C * Ring::kChunk, a, W, stream);
+}
+
+template <int C>
+cudaError_t pick_ring(const NormArgs& a, cudaStream_t stream) {
+  const int W = (int)((a.K + 256 * C - 1) / (256 * C));
+  const bool dy_f32 = a.y_type == kTypeFp32;
+  if (a.x_type == kTypeBf16) {
+    return dy_f32 ? run_ring<C, kTypeBf16, true>(a, W, stream) : run_ring<C, kTypeBf16, false>(a, W, stream);
+  }
+  if (a.x_type == kTypeFp32) {
+    return dy_f32 ? run_ring<C, kTypeFp32, true>(a, W, stream) : run_ring<C, kTypeFp32, false>(a, W, stream);
+  }
+  return dy_f32 ? run_ring<C, kTypeB128, true>(a, W, stream) : run_ring<C, kTypeB128, false>(a, W, stream);
 }
 
 }  // namespace
@@ -612,25 +723,18 @@ cudaError_t pick_backward(const NormArgs& a, int W, int G, cudaStream_t stream) 
 int64_t norm_workspace_floats(int64_t M, int64_t K) { return 2 * (M < kMaxParts ? M : kMaxParts) * K; }
 
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
-  const bool vec = a.codes || (a.K % 16 == 0 && aligned_to(a.x, 32) && aligned_to(a.y, 32) &&
-                               aligned_to(a.weight, 16) && aligned_to(a.bias, 16));
-  const int C = a.K <= kForwardWarps * 1024 ? 2 : 4;
-  const int W = (int)((a.K + 512 * C - 1) / (512 * C));
-  const int G = kForwardWarps / W;
-  if (a.x_type == kTypeFp32) {
-    return C == 2 ? pick_norm<true, 2>(a, W, G, vec, stream) : pick_norm<true, 4>(a, W, G, vec, stream);
-  }
-  return C == 2 ? pick_norm<false, 2>(a, W, G, vec, stream) : pick_norm<false, 4>(a, W, G, vec, stream);
+  const bool vec = a.codes || (a.K % 8 == 0 && aligned_to(a.x, 32) && aligned_to(a.y, 32) &&
+                               aligned_to(a.weight, 32) && aligned_to(a.bias, 32));
+  return a.x_type == kTypeFp32 ? pick_norm<true>(a, vec, stream) : pick_norm<false>(a, vec, stream);
 }
 
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream) {
   const bool vec = a.K % 8 == 0 && aligned_to(a.x, a.x_type == kTypeB128 ? 8 : 16) &&
-                   aligned_to(a.y, 16) && aligned_to(a.dx, 16);
-  const int C = a.K <= kMaxWarps * 512 ? 2 : 4;
-  const int W = (int)((a.K + 256 * C - 1) / (256 * C));
-  const int G = kMaxWarps / W;
-  if (C == 2) return vec ? pick_backward<2, true>(a, W, G, stream) : pick_backward<2, false>(a, W, G, stream);
-  return vec ? pick_backward<4, true>(a, W, G, stream) : pick_backward<4, false>(a, W, G, stream);
+                   aligned_to(a.y, 16) && aligned_to(a.dx, 16) && aligned_to(a.weight, 32);
+  if (vec) return a.K <= 8192 ? pick_ring<2>(a, stream) : pick_ring<4>(a, stream);
+  const int W = (int)((a.K + (a.K <= 8192 ? 511 : 1023)) / (a.K <= 8192 ? 512 : 1024));
+  return a.K <= 8192 ? run_backward(&norm_backward_any_kernel<16>, 0, a, W, stream)
+                     : run_backward(&norm_backward_any_kernel<32>, 0, a, W, stream);
 }
 
 }  // namespace mxq

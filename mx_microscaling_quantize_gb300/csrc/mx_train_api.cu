@@ -87,7 +87,7 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
   if (M == 0 || K == 0) return MX_OK;
   if (!x || !codes || !scales || (x_codes == nullptr) != (x_scales == nullptr)) return MX_ERR_NULL;
   if (!aligned(x, 32) || !aligned(codes, 32) || !aligned(scales, 4) || !aligned(x_codes, 32) ||
-      !aligned(x_scales, 4) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(mean, 4) ||
+      !aligned(x_scales, 4) || !aligned(weight, 32) || !aligned(bias, 32) || !aligned(mean, 4) ||
       !aligned(rstd, 4)) {
     return MX_ERR_ALIGN;
   }
