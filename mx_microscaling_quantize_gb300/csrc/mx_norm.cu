@@ -12,6 +12,7 @@
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"
+#include "mx_tcgen05.cuh"
 #include "mx_train.h"
 
 namespace mxq {
@@ -19,11 +20,21 @@ namespace mxq {
 namespace {
 
 constexpr int kMaxParts = 304;  // of the weight's gradient: rows are split over at most so many CTAs
-constexpr int kBackwardThreads = 512;
+#ifndef FT
+#define FT 768
+#endif
+constexpr int kForwardThreads = FT, kBackwardThreads = 512, kMaxStages = 4;
+constexpr int kNormSmem = 224 * 1024;  // of a CTA, dynamic
+constexpr int kMaxGroups = 15;         // of several warps: a barrier each, beside the CTA's
+constexpr unsigned long long kNormDrainNs = 2000000000ull;  // 2 s, whatever the limit of other waits
 
-// Barrier of one group of warps (ids 1 ..; a group of one warp needs none beyond its own order).
+// Barrier of one group of warps: of several warps barrier group + 1 (there are 16), of one warp the warp's.
 __device__ __forceinline__ void group_sync(int group, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+  if (threads == 32) {
+    __syncwarp();
+  } else {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+  }
 }
 
 // Sum over the lanes that differ in the bits below N; over the warp.
@@ -101,6 +112,70 @@ __device__ __forceinline__ void store_values(char* row, bool f32, int K, F&& col
 }
 
 // ------------------------------------------------------------------------------------------
+// rows through shared memory
+// ------------------------------------------------------------------------------------------
+__device__ __forceinline__ void unpack8(uint4 q, uint64_t* v) {
+  v[0] = bf16_pair(q.x);
+  v[1] = bf16_pair(q.y);
+  v[2] = bf16_pair(q.z);
+  v[3] = bf16_pair(q.w);
+}
+// 8 values of a row at a shared address
+template <bool F32>
+__device__ __forceinline__ void read8(uint32_t at, uint64_t* v) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[2 * p]), "=l"(v[2 * p + 1]) : "r"(at + 16 * p));
+    }
+  } else {
+    uint4 q;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at));
+    unpack8(q, v);
+  }
+}
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+      "l"(from), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// A parameter of the columns of a group, in fp32: run c of lane l of warp w as two pieces of 16 bytes 512 apart,
+// so that a warp's reads meet no bank twice. store: each lane of a group its own runs; at: of (w, l), run 0.
+template <int P>
+struct ParamRuns {
+  static constexpr int kBytes = P * 32;  // per thread
+  static __device__ __forceinline__ uint32_t at(uint32_t base, int w, int lane) { return base + w * P * 1024 + lane * 16; }
+  static __device__ __forceinline__ void store(uint32_t at, const void* p, bool f32, int col, int K, float none) {
+    uint64_t v[P][4];
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[c][j] = pair(none);
+      if (p && col + c * 256 < K) load_param(p, f32, col + c * 256, v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + c * 1024 + h * 512), "l"(v[c][2 * h]),
+                     "l"(v[c][2 * h + 1])
+                     : "memory");
+      }
+    }
+  }
+  static __device__ __forceinline__ void read(uint32_t at, int c, uint64_t* v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                   : "=l"(v[2 * h]), "=l"(v[2 * h + 1])
+                   : "r"(at + c * 1024 + h * 512));
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------------------
 // forward
 // ------------------------------------------------------------------------------------------
 // Mean and 1 / deviation of a row from each warp's mean and sum of squared differences from it (part: of the
@@ -128,131 +203,156 @@ __device__ __forceinline__ void store_stats(const NormArgs& a, int64_t row, floa
   if (a.rstd) a.rstd[row] = rstd;
 }
 
-// P runs of 8 columns per lane (run p: columns 8 (p T + t) ..) as codes, with their blocks' scales.
+// P runs of 8 columns per lane, 256 apart from col on, as codes with their blocks' scales.
 template <int P>
 __device__ __forceinline__ void store_codes(const uint64_t (&v)[P][4], uint8_t* codes, float* scales,
-                                            int64_t M, int K, int64_t row, int t, int T) {
+                                            int64_t M, int K, int64_t row, int col) {
+  uint8_t* to = codes + row * K + col;
   run_codes<P>(
       v,
       [&](int p, uint32_t lo, uint32_t hi) {
-        const int col = (p * T + t) * 8;
-        if (col < K) store8B(codes + row * K + col, lo, hi);
+        if (col + p * 256 < K) store8B(to + p * 256, lo, hi);
       },
       [&](int p, float scale) {
-        const int kb = (p * T + t) >> 4;
+        const int kb = (col + p * 256) / kB128;
         if (kb * kB128 < K) scales[kb * M + row] = scale;
       });
 }
 
-// A group of W warps per row, P runs of 8 columns per lane in fp32 pairs: the loads of a row are in flight
-// together, and what hides its chain (load, two sums over the group, weights, stores) is the other rows of
-// the SM. THREADS: of a CTA, at most.
-template <bool XF32, int P, bool QUANT, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) norm_kernel(NormArgs a, int W) {
-  constexpr int kWarps = THREADS / 32;
-  __shared__ float2 part[kWarps];
-  pdl_launch_dependents();
-  pdl_wait();
+// A group of W warps per row, a warp's lanes P runs of 8 columns each, 256 apart, in fp32 pairs. One CTA an SM:
+// its groups walk rows, each with S rows on their way into its own shared memory (bulk copies; a row's place
+// is free once the group has it in registers and met for its sums), beside one copy of the parameters for all.
+// What bounds it is the instructions. FULL: K is a multiple of a warp's columns.
+template <bool XF32, int P, bool QUANT, bool FULL>
+__global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(NormArgs a, int W, int S) {
+  extern __shared__ __align__(16) uint8_t norm_shared[];
+  using Param = ParamRuns<P>;
+  constexpr int kSize = XF32 ? 4 : 2, kStage = P * 8 * kSize;  // bytes of a row per thread
+  __shared__ float2 part[2][kForwardThreads / 32];
+  __shared__ __align__(8) uint64_t full[kForwardThreads / 32][kMaxStages];
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
-  if (row >= a.M) return;
-  auto column = [&](int p) { return (p * T + t) * 8; };
-  auto count = [&](int w) {  // columns of the group's warp w
-    int n = 0;
-#pragma unroll
-    for (int p = 0; p < P; ++p) n += min(max(K - (p * T + 32 * w) * 8, 0), 256);
-    return n;
+  const int lane = threadIdx.x & 31, wi = t >> 5, col = wi * (P * 256) + lane * 8;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(norm_shared);
+  const uint32_t w_at = Param::at(base, wi, lane), b_at = Param::at(base + T * Param::kBytes, wi, lane);
+  const uint32_t rows_at = base + 2 * T * Param::kBytes + group * S * T * kStage;
+  const uint32_t bars = (uint32_t)__cvta_generic_to_shared(full[group]);
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) tc::mbar_init(bars + s * 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::fence_proxy_async_smem();
+  }
+  pdl_launch_dependents();
+  __syncthreads();
+  pdl_wait();
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
+  int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+  const uint32_t row_bytes = K * kSize;
+  auto request = [&](int64_t at, int stage) {
+    if (t != 0 || at >= a.M) return;
+    tc::mbar_arrive_expect_tx(bars + stage * 8, row_bytes);
+    bulk_copy(rows_at + stage * T * kStage, static_cast<const char*>(a.x) + at * row_bytes, row_bytes,
+              bars + stage * 8);
   };
-  uint64_t x[P][4];
-  const char* from = static_cast<const char*>(a.x) + row * K * (XF32 ? 4 : 2);
-  uint32_t raw[P][XF32 ? 8 : 4];
+  for (int s = 0; s < S; ++s) request(row + s * step, s);
+  const bool w_f32 = a.w_type == kTypeFp32, y_f32 = a.y_type == kTypeFp32;
+  if (group == 0) {
+    Param::store(w_at, a.weight, w_f32, col, K, 1.0f);
+    Param::store(b_at, a.bias, w_f32, col, K, 0.0f);
+  }
+  __syncthreads();
+  auto there = [&](int p) { return FULL || col + p * 256 < K; };
+  auto count = [&](int w) { return (float)min(max(K - w * (P * 256), 0), P * 256); };  // columns of warp w
+  const float per_mine = __fdividef(1.0f, count(wi)), per_k = __fdividef(1.0f, (float)K);
+  const float theirs = lane < W ? count(lane) : 0.0f;
+  int stage = 0, parity = 0;
+  bool failed = false;
+  for (int slot = 0; row < a.M; row += step, slot ^= 1) {
+    tc::mbar_wait(bars + stage * 8, parity, &failed, a.wait_limit_ns, a.err);
+    uint64_t x[P][4];
+    const uint32_t from = rows_at + stage * T * kStage + col * kSize;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    if (column(p) < K) {
-      if constexpr (XF32) {
-        load32B(from + column(p) * 4, raw[p]);
+    for (int p = 0; p < P; ++p) {
+      if (there(p)) {
+        read8<XF32>(from + p * 256 * kSize, x[p]);
       } else {
-        load16B(from + column(p) * 2, raw[p]);
-      }
-    } else {
 #pragma unroll
-      for (int j = 0; j < (XF32 ? 8 : 4); ++j) raw[p][j] = 0u;
-    }
-  }
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (XF32) {
-        x[p][j] = pair(__uint_as_float(raw[p][2 * j]), __uint_as_float(raw[p][2 * j + 1]));
-      } else {
-        x[p][j] = bf16_pair(raw[p][j]);
+        for (int j = 0; j < 4; ++j) x[p][j] = 0u;
       }
     }
-  }
-  if constexpr (QUANT) {
-    if (a.x_codes) store_codes<P>(x, a.x_codes, a.x_scales_out, a.M, K, row, t, T);
-  }
-  float mean = 0.0f;
-  if (a.center) {
     uint64_t s[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[i / 4][i % 4]);
     s[0] = add_pair(s[0], s[1]);
-    const int n = count(t >> 5);
-    mean = n > 0 ? __fdividef(warp_sum(lo_of(s[0]) + hi_of(s[0])), (float)n) : 0.0f;
-  }
-  uint64_t s[2] = {0u, 0u};
-  const uint64_t less = pair(-mean);
+    float mean = warp_sum(lo_of(s[0]) + hi_of(s[0])) * per_mine;
+    if (!a.center) mean = 0.0f;
+    uint64_t minus = pair(-mean);
+    s[0] = s[1] = 0u;
 #pragma unroll
-  for (int p = 0; p < P; ++p) {
-    if (column(p) >= K) continue;
+    for (int p = 0; p < P; ++p) {
+      if (!there(p)) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t d = add_pair(x[p][j], less);
-      s[j & 1] = fma_pair(d, d, s[j & 1]);
-    }
-  }
-  s[0] = add_pair(s[0], s[1]);
-  float sq = warp_sum(lo_of(s[0]) + hi_of(s[0]));
-  if (W > 1) join_stats<kWarps>(a, part, group, W, count, mean, sq);
-  const float rstd = deviation(a, sq);
-  if (t == 0) store_stats(a, row, mean, rstd);
-  const uint64_t minus = pair(-mean), r2 = pair(rstd);
-  const bool w_f32 = a.w_type == kTypeFp32;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    if (column(p) >= K) continue;  // zeros
-    uint64_t w[4], b[4];
-    if (a.weight) load_param(a.weight, w_f32, column(p), w);
-    if (a.bias) load_param(a.bias, w_f32, column(p), b);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[p][j] = mul_pair(add_pair(x[p][j], minus), r2);
-    if (a.weight) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[p][j] = mul_pair(x[p][j], w[j]);
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[p][j] = add_pair(x[p][j], b[j]);
-    }
-    if constexpr (!QUANT) {
-      uint32_t o[8];
-      if (a.y_type == kTypeFp32) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o[2 * j] = __float_as_uint(lo_of(x[p][j]));
-          o[2 * j + 1] = __float_as_uint(hi_of(x[p][j]));
-        }
-        store32B(static_cast<float*>(a.y) + row * K + column(p), o);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = bf16_word(x[p][j]);
-        store16B(static_cast<uint16_t*>(a.y) + row * K + column(p), o);
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t d = add_pair(x[p][j], minus);
+        s[j & 1] = fma_pair(d, d, s[j & 1]);
       }
     }
+    s[0] = add_pair(s[0], s[1]);
+    float sq = warp_sum(lo_of(s[0]) + hi_of(s[0]));
+    if (W > 1) {  // the warps' sums about their own means, joined with the means' distances from the row's
+      if (lane == 0) part[slot][threadIdx.x >> 5] = make_float2(mean, sq);
+      group_sync(group, T);
+      const float2 q = lane < W ? part[slot][group * W + lane] : make_float2(0.0f, 0.0f);
+      mean = warp_sum(q.x * theirs) * per_k;
+      sq = warp_sum(fmaf((q.x - mean) * theirs, q.x - mean, q.y));
+      minus = pair(-mean);
+    } else {
+      __syncwarp();
+    }
+    request(row + S * step, stage);
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+    // 1 / deviation, within 2^-22 (an approximate root; 1 / K rounds too)
+    const float rstd = rsqrtf(fmaf(sq, per_k, a.eps));
+    if (t == 0) store_stats(a, row, mean, rstd);
+    if constexpr (QUANT) {
+      if (a.x_codes) store_codes<P>(x, a.x_codes, a.x_scales_out, a.M, K, row, col);
+    }
+    const uint64_t r2 = pair(rstd);
+    const int64_t at = row * K + col;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      if (!there(p)) continue;  // zeros
+      uint64_t w[4], b[4];
+      Param::read(w_at, p, w);
+      Param::read(b_at, p, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[p][j] = fma_pair(mul_pair(add_pair(x[p][j], minus), r2), w[j], b[j]);
+      if constexpr (!QUANT) {
+        uint32_t o[8];
+        if (y_f32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[2 * j] = __float_as_uint(lo_of(x[p][j]));
+            o[2 * j + 1] = __float_as_uint(hi_of(x[p][j]));
+          }
+          store32B(static_cast<float*>(a.y) + at + p * 256, o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = bf16_word(x[p][j]);
+          store16B(static_cast<uint16_t*>(a.y) + at + p * 256, o);
+        }
+      }
+    }
+    if constexpr (QUANT) store_codes<P>(x, a.codes, a.scales, a.M, K, row, col);
   }
-  if constexpr (QUANT) store_codes<P>(x, a.codes, a.scales, a.M, K, row, t, T);
+  if (failed) {  // the copies asked for land before this CTA's shared memory is another's
+    for (int s = 0; s < S; ++s) {
+      bool late = false;
+      tc::mbar_wait(bars + s * 8, s < stage ? parity : parity ^ 1, &late, kNormDrainNs, a.err);
+    }
+  }
 }
 
 // The same for rows of any length and alignment: 16 columns per lane, a group's width apart, loaded and
@@ -309,83 +409,56 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) norm_any_kernel(NormA
 // ------------------------------------------------------------------------------------------
 // backward
 // ------------------------------------------------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
-
-__device__ __forceinline__ void unpack8(uint4 q, uint64_t* v) {
-  v[0] = bf16_pair(q.x);
-  v[1] = bf16_pair(q.y);
-  v[2] = bf16_pair(q.z);
-  v[3] = bf16_pair(q.w);
-}
-
-// Chunks of 8 values per lane: the pieces of a row that a thread copies into places of its own in shared
-// memory (so no barrier is needed), `stages` rows ahead.
-template <int C, int XT, bool DYF32>
+// Rows of x and dy on their way into a group's shared memory, one bulk copy each; a lane reads four runs of 8
+// columns, 256 apart from `col` on.
+template <int XT, bool DYF32>
 struct NormRing {
-  static constexpr int kX = XT == kTypeB128 ? 8 : XT == kTypeFp32 ? 32 : 16, kDy = DYF32 ? 32 : 16;
-  static constexpr int kScale = XT == kTypeB128 ? 4 : 0;
-  static constexpr int kChunk = kX + kDy + kScale;  // bytes of shared memory per thread, chunk and stage
-  static constexpr int kFit = 200 * 1024 / (kBackwardThreads * C * kChunk);
-  static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static_assert(kStages >= 1, "a row fits shared memory");
+  static constexpr int kRuns = 4, kX = XT == kTypeB128 ? 8 : XT == kTypeFp32 ? 32 : 16, kDy = DYF32 ? 32 : 16;
+  // bytes of shared memory per thread: the weights (of a group) in fp32, and for each stage its columns of
+  // both with a scale per block of 128
+  static constexpr int kWeights = ParamRuns<kRuns>::kBytes, kStage = kRuns * (kX + kDy) + (XT == kTypeB128 ? 1 : 0);
 
-  uint8_t* sm;
-  int threads, tid;
+  uint32_t sm, full;  // this group's stages, and a barrier for each
+  int t, T, K, col;
 
-  __device__ __forceinline__ uint8_t* place(int stage, int c) const {
-    return sm + (stage * C + c) * kChunk * threads;
-  }
-  __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int col, int stage, int c) const {
-    const uint32_t at = (uint32_t)__cvta_generic_to_shared(place(stage, c));
-    const char* x = static_cast<const char*>(a.x) + (row * a.K + col) * (kX / 8);
-    const char* dy = static_cast<const char*>(a.y) + (row * a.K + col) * (kDy / 8);
+  __device__ __forceinline__ uint32_t x_at(int stage) const { return sm + stage * kStage * T; }
+  __device__ __forceinline__ uint32_t dy_at(int stage) const { return x_at(stage) + kRuns * T * kX; }
+  __device__ __forceinline__ uint32_t scale_at(int stage) const { return dy_at(stage) + kRuns * T * kDy; }
+
+  // Asks for a row: called by all of the group, once the stage has been read by all of them.
+  __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int stage) const {
+    if (row >= a.M) return;
+    const uint32_t bar = full + stage * 8;
     if constexpr (XT == kTypeB128) {
-      copy8(at + tid * 8, x);
-    } else {
-#pragma unroll
-      for (int p = 0; p < kX / 16; ++p) copy16(at + (p * threads + tid) * 16, x + p * 16);
+      if (t < (K + kB128 - 1) / kB128) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale_at(stage) + t * 4),
+                     "l"(a.x_scales + t * a.M + row)
+                     : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
     }
-#pragma unroll
-    for (int p = 0; p < kDy / 16; ++p) copy16(at + kX * threads + (p * threads + tid) * 16, dy + p * 16);
-    if constexpr (XT == kTypeB128) {
-      copy4(at + (kX + kDy) * threads + tid * 4, a.x_scales + col / kB128 * a.M + row);
+    if (t == 0) {
+      const uint32_t xb = K / 8 * kX, dyb = K / 8 * kDy;
+      tc::mbar_arrive_expect_tx(bar, xb + dyb);
+      bulk_copy(x_at(stage), static_cast<const char*>(a.x) + row * xb, xb, bar);
+      bulk_copy(dy_at(stage), static_cast<const char*>(a.y) + row * dyb, dyb, bar);
     }
   }
   __device__ __forceinline__ void read(int stage, int c, uint64_t* x, uint64_t* dy) const {
-    const uint8_t* at = place(stage, c);
-    if constexpr (XT == kTypeBf16) {
-      unpack8(reinterpret_cast<const uint4*>(at)[tid], x);
-    } else if constexpr (XT == kTypeFp32) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        *reinterpret_cast<ulonglong2*>(x + 2 * p) = reinterpret_cast<const ulonglong2*>(at)[p * threads + tid];
-      }
-    } else {
-      const uint2 q = reinterpret_cast<const uint2*>(at)[tid];
-      const float s = reinterpret_cast<const float*>(at + (kX + kDy) * threads)[tid];
-      values4(q.x, x[0], x[1]);
-      values4(q.y, x[2], x[3]);
+    if constexpr (XT == kTypeB128) {
+      uint32_t lo, hi;
+      float s;
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(lo), "=r"(hi) : "r"(x_at(stage) + col + c * 256));
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(scale_at(stage) + col / kB128 * 4 + c * 8));
+      values4(lo, x[0], x[1]);
+      values4(hi, x[2], x[3]);
       // (not packed: ptxas joins a packed product and the sum after it, and with it two roundings)
 #pragma unroll
       for (int j = 0; j < 4; ++j) x[j] = pair(__fmul_rn(lo_of(x[j]), s), __fmul_rn(hi_of(x[j]), s));
-    }
-    const uint8_t* dys = at + kX * threads;
-    if constexpr (DYF32) {
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        *reinterpret_cast<ulonglong2*>(dy + 2 * p) = reinterpret_cast<const ulonglong2*>(dys)[p * threads + tid];
-      }
     } else {
-      unpack8(reinterpret_cast<const uint4*>(dys)[tid], dy);
+      read8<XT == kTypeFp32>(x_at(stage) + (col + c * 256) * (kX / 8), x);
     }
+    read8<DYF32>(dy_at(stage) + (col + c * 256) * (kDy / 8), dy);
   }
 };
 
@@ -393,188 +466,183 @@ struct NormRing {
 // each, so that five exchanges do for both.
 __device__ __forceinline__ void row_sums(float (&part)[2][2][kBackwardThreads / 32], int slot, int group, int W,
                                          float& s1, float& s2) {
-  constexpr int kWarps = kBackwardThreads / 32;
   const int lane = threadIdx.x & 31, half = lane >> 4;
   float mine = half ? s2 : s1;
   mine += __shfl_xor_sync(0xFFFFFFFFu, half ? s1 : s2, 16);
   mine = warp_sum<16>(mine);
-  if (W > 1) {
-    const int i = lane & (kWarps - 1);
+  if (W == 1) {
+    __syncwarp();
+  } else {
+    const int i = lane & 15;
     if (i == 0) part[slot][half][threadIdx.x >> 5] = mine;
     group_sync(group, 32 * W);
-    mine = warp_sum<kWarps>(i < W ? part[slot][half][group * W + i] : 0.0f);
+    mine = warp_sum<16>(i < W ? part[slot][half][group * W + i] : 0.0f);
   }
   const float other = __shfl_xor_sync(0xFFFFFFFFu, mine, 16);
   s1 = half ? other : mine;
   s2 = half ? mine : other;
 }
 
-// The groups' shares of dw and db (N columns of a thread), joined in their order through shared memory, to
-// this CTA's row of the workspace; of a single CTA to where they belong.
-template <int N, typename F, typename W1, typename W2>
-__device__ __forceinline__ void store_shares(const NormArgs& a, float* sm, int W, F&& column, W1&& dw,
-                                             W2&& db) {
-  const int T = 32 * W, groups = blockDim.x / T, group = threadIdx.x / T, K = (int)a.K;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float* whole = k ? a.dbias : a.dweight;
-    if (!whole) continue;
-    float* out = gridDim.x == 1 ? whole : a.workspace + (k * (int64_t)gridDim.x + blockIdx.x) * K;
-    float* to = groups > 1 ? sm + group * K : out;
-    if (groups > 1) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) to[column(i)] = k ? db(i) : dw(i);
-    }
-    if (groups == 1) continue;
-    __syncthreads();
-    for (int col = threadIdx.x; col < K; col += blockDim.x) {
-      float s = 0.0f;
-      for (int i = 0; i < groups; ++i) s += sm[i * K + col];
-      out[col] = s;
-    }
+// Where this CTA's share of a gradient (k: 0 dw, 1 db) goes: its row of the workspace, or of a single CTA the
+// gradient itself.
+__device__ __forceinline__ float* share(const NormArgs& a, int k) {
+  float* whole = k ? a.dbias : a.dweight;
+  return !whole || gridDim.x == 1 ? whole : a.workspace + (k * (int64_t)gridDim.x + blockIdx.x) * a.K;
+}
+// Adds up the groups' rows [groups][K] in shared memory, in their order.
+__device__ __forceinline__ void join_shares(const float* sm, int groups, int K, float* out) {
+  __syncthreads();
+  for (int col = threadIdx.x; col < K; col += blockDim.x) {
+    float s = 0.0f;
+    for (int i = 0; i < groups; ++i) s += sm[i * K + col];
+    out[col] = s;
   }
+  __syncthreads();
 }
 
 // Gradient of the input, and each CTA's share of the parameters' gradients, which norm_reduce_kernel
-// adds up. A CTA walks rows gridDim.x groups apart, its sums of dw and db in registers. With two chunks a
-// lane keeps xhat and g over the sums of the row, with four it reads the row from its places again.
-template <int C, int XT, bool DYF32>
-__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(NormArgs a, int W) {
+// adds up. Groups of W warps walk rows, their sums of dw and db in registers, the next rows on their way into
+// the group's stages, the weights in shared memory. A row is read from its stage twice, for the sums over it
+// and for dx: dw and db leave no registers to keep it in. Two groups and more work beside each other up to
+// 8192 columns, one while the other waits for its sums. FULL: K is a multiple of a warp's 1024 columns.
+template <int XT, bool DYF32, bool FULL>
+__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(NormArgs a, int W, int S) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
+  using Ring = NormRing<XT, DYF32>;
+  constexpr int C = Ring::kRuns;
   __shared__ float part[2][2][kBackwardThreads / 32];
-  using Ring = NormRing<C, XT, DYF32>;
-  constexpr bool kKeep = C <= 2;
-  pdl_launch_dependents();
-  pdl_wait();
+  __shared__ __align__(8) uint64_t full[kBackwardThreads / 32][kMaxStages];
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
-  const Ring ring{ring_shared, (int)blockDim.x, (int)threadIdx.x};
+  const int col = (t >> 5) * 1024 + (threadIdx.x & 31) * 8;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring_shared);
+  const Ring ring{base + T * Ring::kWeights + group * T * S * Ring::kStage,
+                  (uint32_t)__cvta_generic_to_shared(full[group]), t, T, K, col};
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) tc::mbar_init(ring.full + s * 8, XT == kTypeB128 ? T + 1 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::fence_proxy_async_smem();
+  }
+  pdl_launch_dependents();
+  __syncthreads();
+  pdl_wait();
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
   int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
-  const bool dx_f32 = a.dx_type == kTypeFp32, w_f32 = a.w_type == kTypeFp32;
-  const float per_k = __fdiv_rn(1.0f, (float)K);
+  for (int s = 0; s < (S > 1 ? S - 1 : 1); ++s) ring.request(a, row + s * step, s);
+  using Param = ParamRuns<C>;
+  const uint32_t w_at = Param::at(base, t >> 5, threadIdx.x & 31);
+  if (group == 0) Param::store(w_at, a.weight, a.w_type == kTypeFp32, col, K, 1.0f);
+  __syncthreads();
+  const bool dx_f32 = a.dx_type == kTypeFp32;
+  const float per_k = __fdividef(1.0f, (float)K);
+  auto there = [&](int c) { return FULL || col + c * 256 < K; };
 
-  auto column = [&](int i) { return ((i / 8) * T + t) * 8 + i % 8; };
-  auto request = [&](int64_t at, int stage) {
-    if (at < a.M) {
+  uint64_t dw[C][4], db[C][4];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (column(8 * c) < K) ring.request(a, at, column(8 * c), stage, c);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto load_weight = [&](int c, uint64_t (&w)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = pair(1.0f);
-    if (a.weight && column(8 * c) < K) load_param(a.weight, w_f32, column(8 * c), w);
-  };
-  auto store = [&](int c, const uint64_t* g, const uint64_t* xh, float s1, float s2, float rstd) {
-    uint64_t d[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      d[j] = mul_pair(fma_pair(xh[j], pair(-s2), add_pair(g[j], pair(-s1))), pair(rstd));
-    }
-    uint32_t o[8];
-    if (dx_f32) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[2 * j] = __float_as_uint(lo_of(d[j]));
-        o[2 * j + 1] = __float_as_uint(hi_of(d[j]));
-      }
-      store16B(static_cast<float*>(a.dx) + row * K + column(8 * c), o);
-      store16B(static_cast<float*>(a.dx) + row * K + column(8 * c) + 4, o + 4);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = bf16_word(d[j]);
-      store16B(static_cast<uint16_t*>(a.dx) + row * K + column(8 * c), o);
-    }
-  };
-
-  uint64_t w[kKeep ? C : 1][4], dw[4 * C], db[4 * C];
-#pragma unroll
-  for (int i = 0; i < 4 * C; ++i) dw[i] = db[i] = 0u;
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) load_weight(c, w[c]);
-  }
-#pragma unroll
-  for (int s = 0; s < Ring::kStages; ++s) request(row + s * step, s);
+  for (int i = 0; i < 4 * C; ++i) dw[i / 4][i % 4] = db[i / 4][i % 4] = 0u;
   float mean_next = 0.0f, rstd_next = 0.0f;
   if (row < a.M) {
     rstd_next = load_f32(a.rstd + row);
     if (a.mean) mean_next = load_f32(a.mean + row);
   }
-  int stage = 0;
+  int stage = 0, parity = 0;
+  bool failed = false;
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
-    const float mean = mean_next, rstd = rstd_next;
-    const uint64_t minus = pair(-mean), r2 = pair(rstd);
+    const float rstd = rstd_next;
+    const uint64_t minus = pair(-mean_next), r2 = pair(rstd);
     if (row + step < a.M) {
       rstd_next = load_f32(a.rstd + row + step);
       if (a.mean) mean_next = load_f32(a.mean + row + step);
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(Ring::kStages - 1) : "memory");
-    uint64_t xh[kKeep ? C : 1][4], g[kKeep ? C : 1][4];
+    tc::mbar_wait(ring.full + stage * 8, parity, &failed, a.wait_limit_ns, a.err);
     uint64_t c1 = 0u, c2 = 0u;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      constexpr int kOne = 0;
-      uint64_t(&x)[4] = xh[kKeep ? c : kOne];
-      uint64_t(&y)[4] = g[kKeep ? c : kOne];
-      uint64_t(&u)[4] = w[kKeep ? c : kOne];
-      if (column(8 * c) < K) {
-        ring.read(stage, c, x, y);
-        if constexpr (!kKeep) load_weight(c, u);
+      if (!there(c)) continue;
+      uint64_t x[4], y[4], w[4];
+      ring.read(stage, c, x, y);
+      Param::read(w_at, c, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = mul_pair(add_pair(x[j], minus), r2);
-          dw[4 * c + j] = fma_pair(y[j], x[j], dw[4 * c + j]);
-          db[4 * c + j] = add_pair(db[4 * c + j], y[j]);
-          y[j] = mul_pair(y[j], u[j]);
-          c1 = add_pair(c1, y[j]);
-          c2 = fma_pair(y[j], x[j], c2);
-        }
+      for (int j = 0; j < 4; ++j) {
+        x[j] = mul_pair(add_pair(x[j], minus), r2);
+        dw[c][j] = fma_pair(y[j], x[j], dw[c][j]);
+        db[c][j] = add_pair(db[c][j], y[j]);
+        y[j] = mul_pair(y[j], w[j]);
+        c1 = add_pair(c1, y[j]);
+        c2 = fma_pair(y[j], x[j], c2);
       }
-    }
-    if constexpr (kKeep) {  // into the places just read, by this thread alone
-      request(row + Ring::kStages * step, stage);
     }
     float s1 = lo_of(c1) + hi_of(c1), s2 = lo_of(c2) + hi_of(c2);
     row_sums(part, slot, group, W, s1, s2);
-    s1 = a.mean ? s1 * per_k : 0.0f;
-    s2 *= per_k;
+    // all of the group have read the row before this one for the last time
+    if (S > 1) ring.request(a, row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    // dx = rstd g - rstd s1 - (x - mean) rstd^2 s2
+    const uint64_t m1 = pair(a.mean ? -s1 * per_k * rstd : 0.0f), m2 = pair(-s2 * per_k * rstd * rstd);
+    const int64_t at = row * K + col;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (column(8 * c) >= K) continue;
-      if constexpr (kKeep) {
-        store(c, g[c], xh[c], s1, s2, rstd);
-      } else {
-        ring.read(stage, c, xh[0], g[0]);
-        load_weight(c, w[0]);
+      if (!there(c)) continue;
+      uint64_t x[4], y[4], w[4];
+      ring.read(stage, c, x, y);
+      Param::read(w_at, c, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = add_pair(x[j], minus);
+        y[j] = fma_pair(mul_pair(y[j], w[j]), r2, fma_pair(x[j], m2, m1));
+      }
+      uint32_t o[8];
+      if (dx_f32) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          xh[0][j] = mul_pair(add_pair(xh[0][j], minus), r2);
-          g[0][j] = mul_pair(g[0][j], w[0][j]);
+          o[2 * j] = __float_as_uint(lo_of(y[j]));
+          o[2 * j + 1] = __float_as_uint(hi_of(y[j]));
         }
-        store(c, g[0], xh[0], s1, s2, rstd);
+        store16B(static_cast<float*>(a.dx) + at + c * 256, o);
+        store16B(static_cast<float*>(a.dx) + at + c * 256 + 4, o + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = bf16_word(y[j]);
+        store16B(static_cast<uint16_t*>(a.dx) + at + c * 256, o);
       }
     }
-    if constexpr (!kKeep) request(row + Ring::kStages * step, stage);
-    stage = stage + 1 == Ring::kStages ? 0 : stage + 1;
+    if (S == 1) {
+      group_sync(group, T);
+      ring.request(a, row + step, 0);
+    }
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  if (a.dweight || a.dbias) {
-    store_shares<8 * C>(
-        a, reinterpret_cast<float*>(ring_shared), W, column,
-        [&](int i) { return i & 1 ? hi_of(dw[i / 2]) : lo_of(dw[i / 2]); },
-        [&](int i) { return i & 1 ? hi_of(db[i / 2]) : lo_of(db[i / 2]); });
+  if (failed) {  // the copies asked for land before this CTA's shared memory is another's
+    for (int s = 0; s < S; ++s) {
+      bool late = false;
+      tc::mbar_wait(ring.full + s * 8, s < stage ? parity : parity ^ 1, &late, kNormDrainNs, a.err);
+    }
+  }
+  const int groups = blockDim.x / T;
+  __syncthreads();
+  for (int k = 0; k < 2; ++k) {
+    float* out = share(a, k);
+    if (!out) continue;
+    // through shared memory in any case: a lane's runs of 8 columns would leave as many partial lines
+    float* to = reinterpret_cast<float*>(ring_shared) + group * K + col;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (!there(c)) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint64_t p = k ? db[c][2 * j] : dw[c][2 * j], q = k ? db[c][2 * j + 1] : dw[c][2 * j + 1];
+        *reinterpret_cast<float4*>(to + c * 256 + 4 * j) = make_float4(lo_of(p), hi_of(p), lo_of(q), hi_of(q));
+      }
+    }
+    join_shares(reinterpret_cast<const float*>(ring_shared), groups, K, out);
   }
 }
 
 // The same for rows of any length and alignment: N values of a lane, a group's width apart, loaded one by
 // one.
 template <int N>
-__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_any_kernel(NormArgs a, int W) {
+__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_any_kernel(NormArgs a, int W, int) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
   __shared__ float part[2][2][kBackwardThreads / 32];
   pdl_launch_dependents();
@@ -625,10 +693,18 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_any_kernel(
     for (int i = 0; i < N; ++i) g[i] = fmaf(-xh[i], s2, g[i] - s1) * rstd;
     store_values(static_cast<char*>(a.dx) + row * K * (dx_f32 ? 4 : 2), dx_f32, K, column, g);
   }
-  if (a.dweight || a.dbias) {
-    store_shares<N>(
-        a, reinterpret_cast<float*>(ring_shared), W, column, [&](int i) { return dw[i]; },
-        [&](int i) { return db[i]; });
+  const int groups = blockDim.x / T;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* out = share(a, k);
+    if (!out) continue;
+    float* sm = reinterpret_cast<float*>(ring_shared);
+    float* to = groups > 1 ? sm + group * K : out;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) to[column(i)] = k ? db[i] : dw[i];
+    }
+    if (groups > 1) join_shares(sm, groups, K, out);
   }
 }
 
@@ -660,62 +736,94 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(NormArgs a, int parts)
 
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-cudaError_t run_norm(void (*kernel)(NormArgs, int), const NormArgs& a, int W, cudaStream_t stream) {
-  const int G = W >= 8 ? 1 : 8 / W;  // rows of a CTA
-  return launch_pdl(kernel, dim3((unsigned)((a.M + G - 1) / G)), dim3(32 * W * G), 0, stream, a, W);
+// Groups of a CTA of `most` threads that rows of W warps and their shared memory leave room for: `fixed` bytes
+// once and `stage` bytes per group for each of `stages` rows on their way (most of at most kMaxStages).
+struct Groups {
+  int count, stages;
+  size_t smem;
+};
+Groups fit_groups(int most, int W, size_t fixed, size_t stage) {
+  Groups g{most / 32 / W, 0, 0};
+  if (W > 1 && g.count > kMaxGroups) g.count = kMaxGroups;
+  while (g.count > 1 && fixed + g.count * stage > kNormSmem) --g.count;
+  if (fixed + g.count * stage > kNormSmem) return Groups{0, 0, 0};
+  g.stages = stage ? (int)((kNormSmem - fixed) / (g.count * stage)) : 0;
+  if (g.stages > kMaxStages) g.stages = kMaxStages;
+  g.smem = fixed + g.count * stage * g.stages;
+  return g;
 }
 
 // Rows of up to 512 columns are one warp's with one or two runs per lane; longer ones a group's with four.
+template <bool XF32, int P, bool QUANT>
+cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
+  const int W = (int)((a.K + P * 256 - 1) / (P * 256));
+  const auto kernel = a.K % (P * 256) == 0 ? &norm_kernel<XF32, P, QUANT, true> : &norm_kernel<XF32, P, QUANT, false>;
+  const Groups g = fit_groups(kForwardThreads, W, (size_t)64 * W * ParamRuns<P>::kBytes,
+                              (size_t)32 * W * P * 8 * (XF32 ? 4 : 2));
+  if (!g.count) return cudaErrorInvalidConfiguration;
+  const int threads = 32 * W * g.count;
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, g.smem, 1);
+  if (slots <= 0) return cudaErrorInvalidConfiguration;
+  const int64_t ctas = (a.M + g.count - 1) / g.count;
+  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(threads), g.smem, stream, a, W,
+                    g.stages);
+}
 template <bool XF32, bool QUANT>
-cudaError_t pick_norm(const NormArgs& a, cudaStream_t stream) {
-  if (a.K <= 256) return run_norm(&norm_kernel<XF32, 1, QUANT, 256>, a, 1, stream);
-  if (a.K <= 512) return run_norm(&norm_kernel<XF32, 2, QUANT, 256>, a, 1, stream);
-  const int W = (int)((a.K + 1023) / 1024);
-  return run_norm(W <= 8 ? &norm_kernel<XF32, 4, QUANT, 256> : &norm_kernel<XF32, 4, QUANT, 512>, a, W, stream);
+cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
+  if (a.K <= 256) return run_norm<XF32, 1, QUANT>(a, stream);
+  return a.K <= 512 ? run_norm<XF32, 2, QUANT>(a, stream) : run_norm<XF32, 4, QUANT>(a, stream);
+}
+
+cudaError_t run_any(void (*kernel)(NormArgs, int), const NormArgs& a, int W, cudaStream_t stream) {
+  const int G = W >= 8 ? 1 : 8 / W;
+  return launch_pdl(kernel, dim3((unsigned)((a.M + G - 1) / G)), dim3(32 * W * G), 0, stream, a, W);
 }
 
 template <bool XF32>
 cudaError_t pick_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
-  if (a.codes) return pick_norm<XF32, true>(a, stream);
-  if (vec) return pick_norm<XF32, false>(a, stream);
+  if (a.codes) return run_norm<XF32, true>(a, stream);
+  if (vec) return run_norm<XF32, false>(a, stream);
   const int W = (int)((a.K + 511) / 512);
-  return run_norm(W <= 8 ? &norm_any_kernel<XF32, 256> : &norm_any_kernel<XF32, 1024>, a, W, stream);
+  return run_any(W <= 8 ? &norm_any_kernel<XF32, 256> : &norm_any_kernel<XF32, 1024>, a, W, stream);
 }
 
-cudaError_t run_backward(void (*kernel)(NormArgs, int), int ring_bytes, const NormArgs& a, int W,
+// `cols` columns of a row per warp; bytes of shared memory per thread of a group once, and per thread and stage.
+cudaError_t run_backward(void (*kernel)(NormArgs, int, int), int fixed, int stage, const NormArgs& a, int cols,
                          cudaStream_t stream) {
-  const int G = kBackwardThreads / 32 / W, threads = 32 * W * G;  // G rows of a CTA at once
+  const int W = (int)((a.K + cols - 1) / cols);
+  Groups g = fit_groups(kBackwardThreads, W, (size_t)fixed * 32 * W, (size_t)stage * 32 * W);
+  if (!g.count) return cudaErrorInvalidConfiguration;
+  const int threads = 32 * W * g.count;
   const bool params = a.dweight || a.dbias;
-  size_t smem = (size_t)ring_bytes * threads;
-  if (params && G > 1 && smem < (size_t)G * a.K * 4) smem = (size_t)G * a.K * 4;
-  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, smem, 0);
+  if (params && g.smem < (size_t)g.count * a.K * 4) g.smem = (size_t)g.count * a.K * 4;  // the groups' shares
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, g.smem, 1);
   if (slots <= 0) return cudaErrorInvalidConfiguration;
-  int64_t ctas = (a.M + G - 1) / G;
+  int64_t ctas = (a.M + g.count - 1) / g.count;
   if (ctas > slots) ctas = slots;
   if (params && ctas > kMaxParts) ctas = kMaxParts;
-  const cudaError_t err = launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), smem, stream, a, W);
+  const cudaError_t err =
+      launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), g.smem, stream, a, W, g.stages);
   if (err != cudaSuccess || !params || ctas == 1) return err;
   return launch_pdl(&norm_reduce_kernel, dim3((unsigned)((a.K + 31) / 32), 2), dim3(512), 0, stream, a,
                     (int)ctas);
 }
 
-template <int C, int XT, bool DYF32>
-cudaError_t run_ring(const NormArgs& a, int W, cudaStream_t stream) {
-  using Ring = NormRing<C, XT, DYF32>;
-  return run_backward(&norm_backward_kernel<C, XT, DYF32>, Ring::kStages * C * Ring::kChunk, a, W, stream);
+template <int XT, bool DYF32>
+cudaError_t run_ring(const NormArgs& a, cudaStream_t stream) {
+  using Ring = NormRing<XT, DYF32>;
+  return run_backward(a.K % 1024 == 0 ? &norm_backward_kernel<XT, DYF32, true> : &norm_backward_kernel<XT, DYF32, false>,
+                      Ring::kWeights, Ring::kStage, a, 1024, stream);
 }
 
-template <int C>
 cudaError_t pick_ring(const NormArgs& a, cudaStream_t stream) {
-  const int W = (int)((a.K + 256 * C - 1) / (256 * C));
   const bool dy_f32 = a.y_type == kTypeFp32;
   if (a.x_type == kTypeBf16) {
-    return dy_f32 ? run_ring<C, kTypeBf16, true>(a, W, stream) : run_ring<C, kTypeBf16, false>(a, W, stream);
+    return dy_f32 ? run_ring<kTypeBf16, true>(a, stream) : run_ring<kTypeBf16, false>(a, stream);
   }
   if (a.x_type == kTypeFp32) {
-    return dy_f32 ? run_ring<C, kTypeFp32, true>(a, W, stream) : run_ring<C, kTypeFp32, false>(a, W, stream);
+    return dy_f32 ? run_ring<kTypeFp32, true>(a, stream) : run_ring<kTypeFp32, false>(a, stream);
   }
-  return dy_f32 ? run_ring<C, kTypeB128, true>(a, W, stream) : run_ring<C, kTypeB128, false>(a, W, stream);
+  return dy_f32 ? run_ring<kTypeB128, true>(a, stream) : run_ring<kTypeB128, false>(a, stream);
 }
 
 }  // namespace
@@ -729,12 +837,11 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream) {
-  const bool vec = a.K % 8 == 0 && aligned_to(a.x, a.x_type == kTypeB128 ? 8 : 16) &&
-                   aligned_to(a.y, 16) && aligned_to(a.dx, 16) && aligned_to(a.weight, 32);
-  if (vec) return a.K <= 8192 ? pick_ring<2>(a, stream) : pick_ring<4>(a, stream);
-  const int W = (int)((a.K + (a.K <= 8192 ? 511 : 1023)) / (a.K <= 8192 ? 512 : 1024));
-  return a.K <= 8192 ? run_backward(&norm_backward_any_kernel<16>, 0, a, W, stream)
-                     : run_backward(&norm_backward_any_kernel<32>, 0, a, W, stream);
+  const bool vec = a.K % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) && aligned_to(a.dx, 16) &&
+                   aligned_to(a.weight, 32);
+  if (vec) return pick_ring(a, stream);
+  return a.K <= 8192 ? run_backward(&norm_backward_any_kernel<16>, 0, 0, a, 512, stream)
+                     : run_backward(&norm_backward_any_kernel<32>, 0, 0, a, 1024, stream);
 }
 
 }  // namespace mxq

@@ -33,6 +33,8 @@ struct NormArgs {
   float* dweight;       // backward: [K] or null
   float* dbias;         // backward: [K] or null
   float* workspace;     // backward: norm_workspace_floats
+  unsigned int* err;    // device error word
+  unsigned long long wait_limit_ns;  // of each wait for a row
 };
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream);

@@ -32,6 +32,16 @@ bool sizes_ok(int64_t M, int64_t K) {
 bool float_type(int t) { return t == MX_TYPE_BF16 || t == MX_TYPE_FP32; }
 uintptr_t size_of(int t) { return t == MX_TYPE_FP32 ? 4 : t == MX_TYPE_BF16 ? 2 : 1; }
 
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+mx_status run_norm(cudaError_t (*launch)(const mxq::NormArgs&, cudaStream_t), mxq::NormArgs& a, void* stream) {
+  a.wait_limit_ns = kWaitNs;
+  return launched([&] {
+    const cudaError_t err = mxq::device_error_word(&a.err);
+    return err != cudaSuccess ? err : launch(a, as_stream(stream));
+  });
+}
+
 mx_status check_norm(int64_t M, int64_t K) {
   return sizes_ok(M, K) && K <= mxq::kNormMaxCols ? MX_OK : MX_ERR_SHAPE;
 }
@@ -74,7 +84,7 @@ mx_status mx_layer_norm(const void* x, int x_type, const void* weight, const voi
   a.y_type = y_type;
   a.mean = mean;
   a.rstd = rstd;
-  return launched([&] { return mxq::launch_norm(a, as_stream(stream)); });
+  return run_norm(&mxq::launch_norm, a, stream);
 }
 
 mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, const void* bias, int w_type,
@@ -107,7 +117,7 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
   a.x_scales_out = x_scales;
   a.mean = mean;
   a.rstd = rstd;
-  return launched([&] { return mxq::launch_norm(a, as_stream(stream)); });
+  return run_norm(&mxq::launch_norm, a, stream);
 }
 
 mx_status mx_layer_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes) {
@@ -162,7 +172,7 @@ mx_status mx_layer_norm_backward(const void* dy, int dy_type, const void* x, int
   a.dweight = dweight;
   a.dbias = dbias;
   a.workspace = static_cast<float*>(workspace);
-  return launched([&] { return mxq::launch_norm_backward(a, as_stream(stream)); });
+  return run_norm(&mxq::launch_norm_backward, a, stream);
 }
 
 mx_status mx_activation_b128(const void* u, int64_t R, int64_t H, int kind, int gated, void* codes,
