@@ -98,8 +98,8 @@ __device__ __forceinline__ uint64_t act(uint64_t g, uint64_t& d) {
 // What a warp's tile is of: a row, and a lane's runs of 8 columns of it.
 struct ActTile {
   int64_t row, H, R, U;
-  int col0;
-  __device__ __forceinline__ int column(int p) const { return col0 + p * 256 + (threadIdx.x & 31) * 8; }
+  int col0, lane;
+  __device__ __forceinline__ int column(int p) const { return col0 + p * 256 + lane * 8; }
   __device__ __forceinline__ bool has(int p) const { return column(p) < H; }
 };
 __device__ __forceinline__ bool act_tile(const ActArgs& a, bool gated, int col_tiles, int64_t tiles, ActTile& t) {
@@ -107,6 +107,7 @@ __device__ __forceinline__ bool act_tile(const ActArgs& a, bool gated, int col_t
   if (tile >= tiles) return false;
   t.row = tile / col_tiles;
   t.col0 = (int)(tile - t.row * col_tiles) * kActCols;
+  t.lane = threadIdx.x & 31;
   t.H = a.H;
   t.R = a.R;
   t.U = gated ? 2 * a.H : a.H;
@@ -120,7 +121,7 @@ __device__ __forceinline__ void store_runs(const uint64_t (&v)[N][4], const ActT
                                            uint8_t* codes, float* scales) {
   uint8_t* to = codes + t.row * width;
   run_codes<N>(
-      v,
+      v, t.lane,
       [&](int n, uint32_t lo, uint32_t hi) {
         const int p = n % kActRuns;
         if (t.has(p)) store8B(to + (n / kActRuns) * t.H + t.column(p), lo, hi);

@@ -127,17 +127,16 @@ struct RunMax {
   static_assert(N == 1 || N == 2 || N == 4 || N == 8, "values of a lane");
   static_assert(kHalvings <= STEPS, "more values than lanes");
 
-  static __device__ __forceinline__ int index() {
-    return (threadIdx.x & ((1 << STEPS) - 1)) >> (STEPS - kHalvings);
-  }
+  int lane;
+  __device__ __forceinline__ int index() const { return (lane & ((1 << STEPS) - 1)) >> (STEPS - kHalvings); }
   // whether this lane is the first that has its value
-  static __device__ __forceinline__ bool first() { return (threadIdx.x & ((1 << (STEPS - kHalvings)) - 1)) == 0; }
-  static __device__ __forceinline__ uint32_t reduce(uint32_t (&m)[N]) {
+  __device__ __forceinline__ bool first() const { return (lane & ((1 << (STEPS - kHalvings)) - 1)) == 0; }
+  __device__ __forceinline__ uint32_t reduce(uint32_t (&m)[N]) const {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
       const int d = 1 << (STEPS - 1 - s), left = N >> (s + 1);
       if (s < kHalvings) {
-        const bool high = threadIdx.x & d;
+        const bool high = lane & d;
 #pragma unroll
         for (int j = 0; j < left; ++j) {
           const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, high ? m[j] : m[j + left], d);
@@ -149,8 +148,8 @@ struct RunMax {
     }
     return m[0];
   }
-  static __device__ __forceinline__ float take(float v, int j) {
-    return __shfl_sync(0xFFFFFFFFu, v, (threadIdx.x & 31 & ~((1 << STEPS) - 1)) | j << (STEPS - kHalvings));
+  __device__ __forceinline__ float take(float v, int j) const {
+    return __shfl_sync(0xFFFFFFFFu, v, (lane & ~((1 << STEPS) - 1)) | j << (STEPS - kHalvings));
   }
 };
 
@@ -159,16 +158,16 @@ struct RunMax {
 // factors of one of the runs' blocks: a block's two quotients take as many instructions as the codes of ten
 // values.
 template <int N, typename Put, typename Scale>
-__device__ __forceinline__ void run_codes(const uint64_t (&v)[N][4], Put&& put, Scale&& scale) {
-  using Max = RunMax<N, 4>;
+__device__ __forceinline__ void run_codes(const uint64_t (&v)[N][4], int lane, Put&& put, Scale&& scale) {
+  const RunMax<N, 4> max_of{lane};
   uint32_t m[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) m[n] = absmax_pairs<4>(v[n]);
-  const Factors f = block_factors_b128(Max::reduce(m));
-  if (Max::first()) scale(Max::index(), f.scale);
+  const Factors f = block_factors_b128(max_of.reduce(m));
+  if (max_of.first()) scale(max_of.index(), f.scale);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const uint64_t r = pair(Max::take(f.r, n));
+    const uint64_t r = pair(max_of.take(f.r, n));
     put(n, codes4(mul_pair(v[n][0], r), mul_pair(v[n][1], r)),
         codes4(mul_pair(v[n][2], r), mul_pair(v[n][3], r)));
   }

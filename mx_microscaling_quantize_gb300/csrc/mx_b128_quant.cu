@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane & 15, h = lane >> 4;
-  using Max = RunMax<8, 4>;
+  const RunMax<8, 4> max_of{lane};
   int64_t blocks = a.blocks;
   if (a.offsets) {
     for (int e = tid; e <= a.E; e += kRecolThreads) {
@@ -435,14 +435,14 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
       const float p = absmax3(at(0), at(1), at(2)), r = absmax3(at(3), at(4), at(5));
       m[j] = __float_as_uint(absmax3(absmax3(p, r, at(6)), at(7), at(7))) & 0x7FFFFFFFu;
     }
-    const Factors mine = block_factors_b128(Max::reduce(m));  // of column Max::index() of half h
+    const Factors mine = block_factors_b128(max_of.reduce(m));  // of column max_of.index() of half h
     const int64_t c0 = c * kB128 + warp * 16;
-    const int own = h * 8 + Max::index();
-    if (Max::first() && c0 + own < a.K) a.scales[b * a.K + c0 + own] = mine.scale;
+    const int own = h * 8 + max_of.index();
+    if (max_of.first() && c0 + own < a.K) a.scales[b * a.K + c0 + own] = mine.scale;
     __syncwarp();  // the codes of the tile before have been read
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const uint64_t r = pair(Max::take(mine.r, j), Max::take(mine.r, j + 1));
+      const uint64_t r = pair(max_of.take(mine.r, j), max_of.take(mine.r, j + 1));
       uint64_t u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = mul_pair(v[i][j / 2], r);

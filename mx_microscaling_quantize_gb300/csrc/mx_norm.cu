@@ -20,10 +20,7 @@ namespace mxq {
 namespace {
 
 constexpr int kMaxParts = 304;  // of the weight's gradient: rows are split over at most so many CTAs
-#ifndef FT
-#define FT 768
-#endif
-constexpr int kForwardThreads = FT, kBackwardThreads = 512, kMaxStages = 4;
+constexpr int kNormThreads = 512, kMaxStages = 4;  // of a CTA
 constexpr int kNormSmem = 224 * 1024;  // of a CTA, dynamic
 constexpr int kMaxGroups = 15;         // of several warps: a barrier each, beside the CTA's
 constexpr unsigned long long kNormDrainNs = 2000000000ull;  // 2 s, whatever the limit of other waits
@@ -203,35 +200,54 @@ __device__ __forceinline__ void store_stats(const NormArgs& a, int64_t row, floa
   if (a.rstd) a.rstd[row] = rstd;
 }
 
-// P runs of 8 columns per lane, 256 apart from col on, as codes with their blocks' scales.
-template <int P>
-__device__ __forceinline__ void store_codes(const uint64_t (&v)[P][4], uint8_t* codes, float* scales,
+// R rows from `row` on, P runs of 8 columns per lane and row, 256 apart from col on, as codes with their
+// blocks' scales.
+template <int R, int P>
+__device__ __forceinline__ void store_codes(const uint64_t (&v)[R * P][4], int lane, uint8_t* codes, float* scales,
                                             int64_t M, int K, int64_t row, int col) {
-  uint8_t* to = codes + row * K + col;
-  run_codes<P>(
-      v,
-      [&](int p, uint32_t lo, uint32_t hi) {
-        if (col + p * 256 < K) store8B(to + p * 256, lo, hi);
+  run_codes<R * P>(
+      v, lane,
+      [&](int n, uint32_t lo, uint32_t hi) {
+        const int p = n % P, r = n / P;
+        if (col + p * 256 < K && row + r < M) store8B(codes + (row + r) * K + col + p * 256, lo, hi);
       },
-      [&](int p, float scale) {
-        const int kb = (col + p * 256) / kB128;
-        if (kb * kB128 < K) scales[kb * M + row] = scale;
+      [&](int n, float scale) {
+        const int p = n % P, r = n / P, kb = (col + p * 256) / kB128;
+        if (kb * kB128 < K && row + r < M) scales[kb * M + row + r] = scale;
       });
 }
 
-// A group of W warps per row, a warp's lanes P runs of 8 columns each, 256 apart, in fp32 pairs. One CTA an SM:
-// its groups walk rows, each with S rows on their way into its own shared memory (bulk copies; a row's place
-// is free once the group has it in registers and met for its sums), beside one copy of the parameters for all.
-// What bounds it is the instructions. FULL: K is a multiple of a warp's columns.
-template <bool XF32, int P, bool QUANT, bool FULL>
-__global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(NormArgs a, int W, int S) {
+// Sums over a warp of a value of each of R rows: of two rows, the halves of the warp take one each.
+template <int R>
+__device__ __forceinline__ void warp_sums(float (&v)[R], bool high) {
+  static_assert(R == 1 || R == 2, "rows of a group");
+  if constexpr (R == 1) {
+    v[0] = warp_sum(v[0]);
+  } else {
+    float mine = high ? v[1] : v[0];
+    mine = warp_sum<16>(mine + __shfl_xor_sync(0xFFFFFFFFu, high ? v[0] : v[1], 16));
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, mine, 16);
+    v[0] = high ? other : mine;
+    v[1] = high ? mine : other;
+  }
+}
+
+// A group of W warps for R adjacent rows, a warp's lanes P runs of 8 columns of each, 256 apart, in fp32 pairs.
+// One CTA an SM: its groups walk rows, each with S times R rows on their way into its own shared memory (bulk
+// copies; their place is free once the group has them in registers and met for the sums), beside one copy of
+// the parameters for all. Two rows share what is done once: the reads of the parameters (which with the
+// rows' own are as much of the shared memory's time as a row's bytes are of the memory's), the steps of the
+// sums and a block's quotients. FULL: K is a multiple of a warp's columns.
+template <bool XF32, int P, int R, bool QUANT, bool FULL>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W, int S) {
   extern __shared__ __align__(16) uint8_t norm_shared[];
   using Param = ParamRuns<P>;
-  constexpr int kSize = XF32 ? 4 : 2, kStage = P * 8 * kSize;  // bytes of a row per thread
-  __shared__ float2 part[2][kForwardThreads / 32];
-  __shared__ __align__(8) uint64_t full[kForwardThreads / 32][kMaxStages];
+  constexpr int kSize = XF32 ? 4 : 2, kStage = R * P * 8 * kSize;  // bytes of R rows per thread
+  __shared__ float2 part[2][R][kNormThreads / 32];
+  __shared__ __align__(8) uint64_t full[kNormThreads / 32][kMaxStages];
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
   const int lane = threadIdx.x & 31, wi = t >> 5, col = wi * (P * 256) + lane * 8;
+  const bool high = lane & 16;
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(norm_shared);
   const uint32_t w_at = Param::at(base, wi, lane), b_at = Param::at(base + T * Param::kBytes, wi, lane);
   const uint32_t rows_at = base + 2 * T * Param::kBytes + group * S * T * kStage;
@@ -244,13 +260,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(NormArgs a, in
   pdl_launch_dependents();
   __syncthreads();
   pdl_wait();
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
-  int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T) * R;
+  int64_t row = ((int64_t)blockIdx.x * (blockDim.x / T) + group) * R;
   const uint32_t row_bytes = K * kSize;
   auto request = [&](int64_t at, int stage) {
     if (t != 0 || at >= a.M) return;
-    tc::mbar_arrive_expect_tx(bars + stage * 8, row_bytes);
-    bulk_copy(rows_at + stage * T * kStage, static_cast<const char*>(a.x) + at * row_bytes, row_bytes,
+    const uint32_t bytes = (uint32_t)(a.M - at < R ? a.M - at : R) * row_bytes;
+    tc::mbar_arrive_expect_tx(bars + stage * 8, bytes);
+    bulk_copy(rows_at + stage * T * kStage, static_cast<const char*>(a.x) + at * row_bytes, bytes,
               bars + stage * 8);
   };
   for (int s = 0; s < S; ++s) request(row + s * step, s);
@@ -263,48 +280,71 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(NormArgs a, in
   auto there = [&](int p) { return FULL || col + p * 256 < K; };
   auto count = [&](int w) { return (float)min(max(K - w * (P * 256), 0), P * 256); };  // columns of warp w
   const float per_mine = __fdividef(1.0f, count(wi)), per_k = __fdividef(1.0f, (float)K);
-  const float theirs = lane < W ? count(lane) : 0.0f;
+  // lanes of the sums over warps: of all 32 for one row, of a half for each of two
+  const int w_of = R == 1 ? lane : lane & 15;
+  const float theirs = w_of < W ? count(w_of) : 0.0f;
   int stage = 0, parity = 0;
   bool failed = false;
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
     tc::mbar_wait(bars + stage * 8, parity, &failed, a.wait_limit_ns, a.err);
-    uint64_t x[P][4];
+    uint64_t x[R * P][4];
     const uint32_t from = rows_at + stage * T * kStage + col * kSize;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (there(p)) {
-        read8<XF32>(from + p * 256 * kSize, x[p]);
+    for (int n = 0; n < R * P; ++n) {
+      if (there(n % P) && (n < P || row + 1 < a.M)) {
+        read8<XF32>(from + (n / P) * row_bytes + (n % P) * 256 * kSize, x[n]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[p][j] = 0u;
+        for (int j = 0; j < 4; ++j) x[n][j] = 0u;
       }
     }
-    uint64_t s[2] = {0u, 0u};
+    float mean[R], sq[R];
 #pragma unroll
-    for (int i = 0; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[i / 4][i % 4]);
-    s[0] = add_pair(s[0], s[1]);
-    float mean = warp_sum(lo_of(s[0]) + hi_of(s[0])) * per_mine;
-    if (!a.center) mean = 0.0f;
-    uint64_t minus = pair(-mean);
-    s[0] = s[1] = 0u;
+    for (int r = 0; r < R; ++r) {
+      uint64_t s[2] = {0u, 0u};
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (!there(p)) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t d = add_pair(x[p][j], minus);
-        s[j & 1] = fma_pair(d, d, s[j & 1]);
-      }
+      for (int i = 0; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[r * P + i / 4][i % 4]);
+      s[0] = add_pair(s[0], s[1]);
+      mean[r] = lo_of(s[0]) + hi_of(s[0]);
     }
-    s[0] = add_pair(s[0], s[1]);
-    float sq = warp_sum(lo_of(s[0]) + hi_of(s[0]));
+    warp_sums<R>(mean, high);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = a.center ? mean[r] * per_mine : 0.0f;
+      const uint64_t minus = pair(-mean[r]);
+      uint64_t s[2] = {0u, 0u};
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (!there(p)) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t d = add_pair(x[r * P + p][j], minus);
+          s[j & 1] = fma_pair(d, d, s[j & 1]);
+        }
+      }
+      s[0] = add_pair(s[0], s[1]);
+      sq[r] = lo_of(s[0]) + hi_of(s[0]);
+    }
+    warp_sums<R>(sq, high);
     if (W > 1) {  // the warps' sums about their own means, joined with the means' distances from the row's
-      if (lane == 0) part[slot][threadIdx.x >> 5] = make_float2(mean, sq);
+      if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) part[slot][r][threadIdx.x >> 5] = make_float2(mean[r], sq[r]);
+      }
       group_sync(group, T);
-      const float2 q = lane < W ? part[slot][group * W + lane] : make_float2(0.0f, 0.0f);
-      mean = warp_sum(q.x * theirs) * per_k;
-      sq = warp_sum(fmaf((q.x - mean) * theirs, q.x - mean, q.y));
-      minus = pair(-mean);
+      constexpr int kLanes = R == 1 ? 32 : 16;
+      const float2 q = w_of < W ? part[slot][R == 1 ? 0 : high][group * W + w_of] : make_float2(0.0f, 0.0f);
+      const float m = warp_sum<kLanes>(q.x * theirs) * per_k;
+      const float v = warp_sum<kLanes>(fmaf((q.x - m) * theirs, q.x - m, q.y));
+      mean[0] = m;
+      sq[0] = v;
+      if constexpr (R == 2) {
+        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, 16), v2 = __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+        mean[0] = high ? m2 : m;
+        mean[R - 1] = high ? m : m2;
+        sq[0] = high ? v2 : v;
+        sq[R - 1] = high ? v : v2;
+      }
     } else {
       __syncwarp();
     }
@@ -313,13 +353,18 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(NormArgs a, in
       stage = 0;
       parity ^= 1;
     }
-    // 1 / deviation, within 2^-22 (an approximate root; 1 / K rounds too)
-    const float rstd = rsqrtf(fmaf(sq, per_k, a.eps));
-    if (t == 0) store_stats(a, row, mean, rstd);
     if constexpr (QUANT) {
-      if (a.x_codes) store_codes<P>(x, a.x_codes, a.x_scales_out, a.M, K, row, col);
+      if (a.x_codes) store_codes<R, P>(x, lane, a.x_codes, a.x_scales_out, a.M, K, row, col);
     }
-    const uint64_t r2 = pair(rstd);
+    uint64_t minus[R], r2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // 1 / deviation, within 2^-22 (an approximate root; 1 / K rounds too)
+      const float rstd = rsqrtf(fmaf(sq[r], per_k, a.eps));
+      if (t == 0 && row + r < a.M) store_stats(a, row + r, mean[r], rstd);
+      minus[r] = pair(-mean[r]);
+      r2[r] = pair(rstd);
+    }
     const int64_t at = row * K + col;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -328,24 +373,29 @@ __global__ void __launch_bounds__(kForwardThreads, 1) norm_kernel(NormArgs a, in
       Param::read(w_at, p, w);
       Param::read(b_at, p, b);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[p][j] = fma_pair(mul_pair(add_pair(x[p][j], minus), r2), w[j], b[j]);
-      if constexpr (!QUANT) {
-        uint32_t o[8];
-        if (y_f32) {
+      for (int r = 0; r < R; ++r) {
+        uint64_t(&y)[4] = x[r * P + p];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            o[2 * j] = __float_as_uint(lo_of(x[p][j]));
-            o[2 * j + 1] = __float_as_uint(hi_of(x[p][j]));
+        for (int j = 0; j < 4; ++j) y[j] = fma_pair(mul_pair(add_pair(y[j], minus[r]), r2[r]), w[j], b[j]);
+        if constexpr (!QUANT) {
+          if (row + r >= a.M) continue;
+          uint32_t o[8];
+          if (y_f32) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[2 * j] = __float_as_uint(lo_of(y[j]));
+              o[2 * j + 1] = __float_as_uint(hi_of(y[j]));
+            }
+            store32B(static_cast<float*>(a.y) + at + (int64_t)r * K + p * 256, o);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = bf16_word(y[j]);
+            store16B(static_cast<uint16_t*>(a.y) + at + (int64_t)r * K + p * 256, o);
           }
-          store32B(static_cast<float*>(a.y) + at + p * 256, o);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = bf16_word(x[p][j]);
-          store16B(static_cast<uint16_t*>(a.y) + at + p * 256, o);
         }
       }
     }
-    if constexpr (QUANT) store_codes<P>(x, a.codes, a.scales, a.M, K, row, col);
+    if constexpr (QUANT) store_codes<R, P>(x, lane, a.codes, a.scales, a.M, K, row, col);
   }
   if (failed) {  // the copies asked for land before this CTA's shared memory is another's
     for (int s = 0; s < S; ++s) {
@@ -464,7 +514,7 @@ struct NormRing {
 
 // Two sums over the row of a group of W warps (slot: of two, taken in turn): the two halves of a warp take one
 // each, so that five exchanges do for both.
-__device__ __forceinline__ void row_sums(float (&part)[2][2][kBackwardThreads / 32], int slot, int group, int W,
+__device__ __forceinline__ void row_sums(float (&part)[2][2][kNormThreads / 32], int slot, int group, int W,
                                          float& s1, float& s2) {
   const int lane = threadIdx.x & 31, half = lane >> 4;
   float mine = half ? s2 : s1;
@@ -506,12 +556,12 @@ __device__ __forceinline__ void join_shares(const float* sm, int groups, int K, 
 // and for dx: dw and db leave no registers to keep it in. Two groups and more work beside each other up to
 // 8192 columns, one while the other waits for its sums. FULL: K is a multiple of a warp's 1024 columns.
 template <int XT, bool DYF32, bool FULL>
-__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(NormArgs a, int W, int S) {
+__global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs a, int W, int S) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
   using Ring = NormRing<XT, DYF32>;
   constexpr int C = Ring::kRuns;
-  __shared__ float part[2][2][kBackwardThreads / 32];
-  __shared__ __align__(8) uint64_t full[kBackwardThreads / 32][kMaxStages];
+  __shared__ float part[2][2][kNormThreads / 32];
+  __shared__ __align__(8) uint64_t full[kNormThreads / 32][kMaxStages];
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
   const int col = (t >> 5) * 1024 + (threadIdx.x & 31) * 8;
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring_shared);
@@ -642,9 +692,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_kernel(Norm
 // The same for rows of any length and alignment: N values of a lane, a group's width apart, loaded one by
 // one.
 template <int N>
-__global__ void __launch_bounds__(kBackwardThreads, 1) norm_backward_any_kernel(NormArgs a, int W, int) {
+__global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(NormArgs a, int W, int) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
-  __shared__ float part[2][2][kBackwardThreads / 32];
+  __shared__ float part[2][2][kNormThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
@@ -753,25 +803,30 @@ Groups fit_groups(int most, int W, size_t fixed, size_t stage) {
   return g;
 }
 
-// Rows of up to 512 columns are one warp's with one or two runs per lane; longer ones a group's with four.
-template <bool XF32, int P, bool QUANT>
+template <bool XF32, int P, int R, bool QUANT>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
   const int W = (int)((a.K + P * 256 - 1) / (P * 256));
-  const auto kernel = a.K % (P * 256) == 0 ? &norm_kernel<XF32, P, QUANT, true> : &norm_kernel<XF32, P, QUANT, false>;
-  const Groups g = fit_groups(kForwardThreads, W, (size_t)64 * W * ParamRuns<P>::kBytes,
-                              (size_t)32 * W * P * 8 * (XF32 ? 4 : 2));
+  const auto kernel =
+      a.K % (P * 256) == 0 ? &norm_kernel<XF32, P, R, QUANT, true> : &norm_kernel<XF32, P, R, QUANT, false>;
+  const Groups g = fit_groups(kNormThreads, W, (size_t)64 * W * ParamRuns<P>::kBytes,
+                              (size_t)32 * W * R * P * 8 * (XF32 ? 4 : 2));
+  // two rows of more than 14336 columns of fp32 do not fit beside their parameters
+  if constexpr (R > 1 && P == 4 && XF32) {
+    if (!g.count) return run_norm<XF32, P, 1, QUANT>(a, stream);
+  }
   if (!g.count) return cudaErrorInvalidConfiguration;
   const int threads = 32 * W * g.count;
   const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, g.smem, 1);
   if (slots <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t ctas = (a.M + g.count - 1) / g.count;
+  const int64_t ctas = (a.M + g.count * R - 1) / (g.count * R);
   return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(threads), g.smem, stream, a, W,
                     g.stages);
 }
+// Rows of up to 512 columns are one warp's with one or two runs per lane; longer ones a group's with four.
 template <bool XF32, bool QUANT>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
-  if (a.K <= 256) return run_norm<XF32, 1, QUANT>(a, stream);
-  return a.K <= 512 ? run_norm<XF32, 2, QUANT>(a, stream) : run_norm<XF32, 4, QUANT>(a, stream);
+  if (a.K <= 256) return run_norm<XF32, 1, 2, QUANT>(a, stream);
+  return a.K <= 512 ? run_norm<XF32, 2, 2, QUANT>(a, stream) : run_norm<XF32, 4, 2, QUANT>(a, stream);
 }
 
 cudaError_t run_any(void (*kernel)(NormArgs, int), const NormArgs& a, int W, cudaStream_t stream) {
@@ -791,7 +846,7 @@ cudaError_t pick_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
 cudaError_t run_backward(void (*kernel)(NormArgs, int, int), int fixed, int stage, const NormArgs& a, int cols,
                          cudaStream_t stream) {
   const int W = (int)((a.K + cols - 1) / cols);
-  Groups g = fit_groups(kBackwardThreads, W, (size_t)fixed * 32 * W, (size_t)stage * 32 * W);
+  Groups g = fit_groups(kNormThreads, W, (size_t)fixed * 32 * W, (size_t)stage * 32 * W);
   if (!g.count) return cudaErrorInvalidConfiguration;
   const int threads = 32 * W * g.count;
   const bool params = a.dweight || a.dbias;
