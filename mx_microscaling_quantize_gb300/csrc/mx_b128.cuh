@@ -45,16 +45,15 @@ __device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float r) {
   return d;
 }
 
-// four fp32 values (a pair each, lower index first) -> four code bytes
-__device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b) {
+// four fp32 values (lower index first) -> four code bytes
+__device__ __forceinline__ uint32_t codes4(float w, float x, float y, float z) {
   uint32_t d;
-  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .f32 w, x, y, z;\n\t"
-      "mov.b64 {w, x}, %1;\n\tmov.b64 {y, z}, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 lo, x, w;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 hi, z, y;\n\t"
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
       "mov.b32 %0, {lo, hi};\n\t}"
       : "=r"(d)
-      : "l"(a), "l"(b));
+      : "f"(w), "f"(x), "f"(y), "f"(z));
   return d;
 }
 
@@ -87,6 +86,9 @@ __device__ __forceinline__ float hi_of(uint64_t p) {
   float hi;
   asm("mov.b64 {_, %0}, %1;" : "=f"(hi) : "l"(p));
   return hi;
+}
+__device__ __forceinline__ uint32_t codes4(uint64_t a, uint64_t b) {
+  return codes4(lo_of(a), hi_of(a), lo_of(b), hi_of(b));
 }
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   uint64_t d;

@@ -349,18 +349,28 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
     __syncthreads();
     blocks = s.blocks;
   }
-  const int64_t cols = (a.K + kB128 - 1) / kB128, tiles = blocks * cols;
+  const int K = (int)a.K, cols = (K + kB128 - 1) / kB128;
+  const int64_t tiles = blocks * cols, pitch = a.blocks * kB128;
   const int64_t t0 = tiles * blockIdx.x / gridDim.x, t1 = tiles * (blockIdx.x + 1) / gridDim.x;
   if (t0 == t1) return;
-  const int64_t pitch = a.blocks * kB128;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x);
-  int64_t lt = t0, lb = t0 / cols, lc = t0 - lb * cols;  // the tile to ask for next
-  int32_t src[4], scale_src = -1;  // this thread's rows of the checkpoint, -1: none
-  const int piece = tid & 7, first = tid >> 3;  // its pieces: of rows first + 32 i
-  auto source = [&](int64_t row, int64_t row_end) -> int32_t {
+  // the tile to ask for next: `left` of them, block lb, column lc; this thread's pieces of it and a row's scale
+  // (null: there is no such row, which is zeros)
+  int64_t left = t1 - t0, lb = t0 / cols;
+  int lc = (int)(t0 - lb * cols);
+  const uint8_t* from[4];
+  const float* scale_from = nullptr;
+  const int piece = tid & 7, first = tid >> 3;  // pieces of rows first + 32 i
+  uint32_t to[4];                               // their places, in the first stage
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = first + 32 * i;
+    to[i] = (uint32_t)__cvta_generic_to_shared(&s.in[0][r * 8 + (piece ^ ((r >> 3) & 7))]);
+  }
+  const uint32_t scale_to = (uint32_t)__cvta_generic_to_shared(&s.row_scale[0][tid & 127]);
+  auto source = [&](int64_t row, int64_t row_end) -> int64_t {  // -1: none
     if (row >= row_end) return -1;
-    const int32_t r = GATHER ? load_s32(a.index + row) : (int32_t)row;
-    return r < a.M ? r : -1;
+    const int64_t r = GATHER ? load_s32(a.index + row) : row;
+    return r >= 0 && r < a.M ? r : -1;
   };
   auto find = [&] {
     int row0 = 0, row_end = 0;
@@ -370,35 +380,36 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
       row0 = (int)(lb * kB128);
       row_end = (int)a.R;
     }
+    int64_t src[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) src[i] = source((int64_t)row0 + first + 32 * i, row_end);
-    if (tid < 128) scale_src = source((int64_t)row0 + tid, row_end);
+    const int64_t scale_src = tid < 128 ? source((int64_t)row0 + tid, row_end) : -1;
+    const int64_t col = (int64_t)lc * kB128 + piece * 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      from[i] = src[i] < 0 ? nullptr : static_cast<const uint8_t*>(a.x) + src[i] * K + col;
+    }
+    scale_from = scale_src < 0 ? nullptr : a.x_scales + lc * a.M + scale_src;
   };
   auto load = [&](int stage) {
-    if (lt < t1) {
-      const int64_t col = lc * kB128 + piece * 16;
+    if (left > 0) {
+      const bool there = lc * kB128 + piece * 16 < K;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = first + 32 * i;
-        uint4* to = &s.in[stage][r * 8 + (piece ^ ((r >> 3) & 7))];
-        if (src[i] >= 0 && col < a.K) {
-          copy16B_async(to, x + src[i] * a.K + col);
-        } else {
-          *to = make_uint4(0u, 0u, 0u, 0u);
-        }
+      for (int i = 0; i < 4; ++i) {  // (a size of zero reads nothing, from an address that is there in any case, and fills with zeros)
+        const uint32_t size = there && from[i] ? 16 : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to[i] + stage * (uint32_t)sizeof(s.in[0])),
+                     "l"(size ? from[i] : a.codes), "r"(size)
+                     : "memory");
+        from[i] = from[i] ? from[i] + kB128 : nullptr;
       }
       if (tid < 128) {
-        float* to = &s.row_scale[stage][tid];
-        if (scale_src >= 0) {
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
-                       "l"(a.x_scales + lc * a.M + scale_src)
-                       : "memory");
-        } else {
-          *to = 0.0f;
-        }
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(scale_to + stage * (uint32_t)sizeof(s.row_scale[0])),
+                     "l"(scale_from ? scale_from : a.scales), "r"(scale_from ? 4 : 0)
+                     : "memory");
+        if (scale_from) scale_from += a.M;
       }
-      ++lt;
-      if (++lc == cols && lt < t1) {
+      --left;
+      if (++lc == cols && left > 0) {
         lc = 0;
         ++lb;
         find();
@@ -406,15 +417,16 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int64_t b = lb, c = lc;
+  int64_t b = lb;
+  int c = lc;
   find();
   for (int i = 0; i < kRecolStages - 1; ++i) load(i);
   uint8_t* out = reinterpret_cast<uint8_t*>(s.out[warp]);
+  int stage = 0;
   for (int64_t t = t0; t < t1; ++t) {
-    const int stage = (int)((t - t0) % kRecolStages);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRecolStages - 2) : "memory");
     __syncthreads();
-    load((stage + kRecolStages - 1) % kRecolStages);  // into the tile before this one, read by all
+    load(stage == 0 ? kRecolStages - 1 : stage - 1);  // into the tile before this one, read by all
     uint64_t v[8][4];  // pairs of columns
     float f[8];
     *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(&s.row_scale[stage][8 * q]);
@@ -436,9 +448,8 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
       m[j] = __float_as_uint(absmax3(absmax3(p, r, at(6)), at(7), at(7))) & 0x7FFFFFFFu;
     }
     const Factors mine = block_factors_b128(max_of.reduce(m));  // of column max_of.index() of half h
-    const int64_t c0 = c * kB128 + warp * 16;
-    const int own = h * 8 + max_of.index();
-    if (max_of.first() && c0 + own < a.K) a.scales[b * a.K + c0 + own] = mine.scale;
+    const int c0 = c * kB128 + warp * 16, own = h * 8 + max_of.index();
+    if (max_of.first() && c0 + own < K) a.scales[b * K + c0 + own] = mine.scale;
     __syncwarp();  // the codes of the tile before have been read
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -447,21 +458,21 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = mul_pair(v[i][j / 2], r);
       uint8_t* to = out + (h * 8 + j) * 128 + q * 8;
-      *reinterpret_cast<uint2*>(to) =
-          make_uint2(codes4(pair(lo_of(u[0]), lo_of(u[1])), pair(lo_of(u[2]), lo_of(u[3]))),
-                     codes4(pair(lo_of(u[4]), lo_of(u[5])), pair(lo_of(u[6]), lo_of(u[7]))));
+      *reinterpret_cast<uint2*>(to) = make_uint2(codes4(lo_of(u[0]), lo_of(u[1]), lo_of(u[2]), lo_of(u[3])),
+                                                 codes4(lo_of(u[4]), lo_of(u[5]), lo_of(u[6]), lo_of(u[7])));
       *reinterpret_cast<uint2*>(to + 128) =
-          make_uint2(codes4(pair(hi_of(u[0]), hi_of(u[1])), pair(hi_of(u[2]), hi_of(u[3]))),
-                     codes4(pair(hi_of(u[4]), hi_of(u[5])), pair(hi_of(u[6]), hi_of(u[7]))));
+          make_uint2(codes4(hi_of(u[0]), hi_of(u[1]), hi_of(u[2]), hi_of(u[3])),
+                     codes4(hi_of(u[4]), hi_of(u[5]), hi_of(u[6]), hi_of(u[7])));
     }
     __syncwarp();
+    uint8_t* dst = a.codes + (c0 + (lane >> 3)) * pitch + b * kB128 + (lane & 7) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t col = c0 + i * 4 + (lane >> 3);
       const uint4 w = s.out[warp][i * 32 + lane];
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      if (col < a.K) store16B(a.codes + col * pitch + b * kB128 + (lane & 7) * 16, u);
+      if (c0 + i * 4 + (lane >> 3) < K) store16B(dst + i * 4 * pitch, u);
     }
+    stage = stage + 1 == kRecolStages ? 0 : stage + 1;
     if (++c == cols) {
       c = 0;
       ++b;

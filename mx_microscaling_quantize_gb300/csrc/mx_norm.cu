@@ -186,13 +186,12 @@ __device__ __forceinline__ void join_stats(const NormArgs& a, float2* part, int 
   group_sync(group, 32 * W);
   const float2 p = i < W ? part[w0 + i] : make_float2(0.0f, 0.0f);
   const float n = i < W ? (float)count(i) : 0.0f;
-  mean = a.center ? __fdividef(warp_sum<WARPS>(p.x * n), (float)a.K) : 0.0f;
+  mean = a.center ? __fdiv_rn(warp_sum<WARPS>(p.x * n), (float)a.K) : 0.0f;
   sq = warp_sum<WARPS>(fmaf((p.x - mean) * n, p.x - mean, p.y));
 }
 
-// 1 / sqrt(sq / K + eps), within 2^-22 (an approximate root; 1 / K and the quotient round too).
 __device__ __forceinline__ float deviation(const NormArgs& a, float sq) {
-  return rsqrtf(fmaf(sq, __fdividef(1.0f, (float)a.K), a.eps));
+  return __frsqrt_rn(fmaf(sq, __fdiv_rn(1.0f, (float)a.K), a.eps));
 }
 
 __device__ __forceinline__ void store_stats(const NormArgs& a, int64_t row, float mean, float rstd) {
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   __syncthreads();
   auto there = [&](int p) { return FULL || col + p * 256 < K; };
   auto count = [&](int w) { return (float)min(max(K - w * (P * 256), 0), P * 256); };  // columns of warp w
-  const float per_mine = __fdividef(1.0f, count(wi)), per_k = __fdividef(1.0f, (float)K);
+  const float per_mine = __fdiv_rn(1.0f, count(wi)), per_k = __fdiv_rn(1.0f, (float)K);
   // lanes of the sums over warps: of all 32 for one row, of a half for each of two
   const int w_of = R == 1 ? lane : lane & 15;
   const float theirs = w_of < W ? count(w_of) : 0.0f;
@@ -359,8 +358,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
     uint64_t minus[R], r2[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // 1 / deviation, within 2^-22 (an approximate root; 1 / K rounds too)
-      const float rstd = rsqrtf(fmaf(sq[r], per_k, a.eps));
+      const float rstd = __frsqrt_rn(fmaf(sq[r], per_k, a.eps));
       if (t == 0 && row + r < a.M) store_stats(a, row + r, mean[r], rstd);
       minus[r] = pair(-mean[r]);
       r2[r] = pair(rstd);
@@ -431,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) norm_any_kernel(NormA
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i & 1] += x[i];
     const int n = count(t >> 5);
-    mean = n > 0 ? __fdividef(warp_sum(s[0] + s[1]), (float)n) : 0.0f;
+    mean = n > 0 ? __fdiv_rn(warp_sum(s[0] + s[1]), (float)n) : 0.0f;
   }
   float s[2] = {};
 #pragma unroll
@@ -583,7 +581,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   if (group == 0) Param::store(w_at, a.weight, a.w_type == kTypeFp32, col, K, 1.0f);
   __syncthreads();
   const bool dx_f32 = a.dx_type == kTypeFp32;
-  const float per_k = __fdividef(1.0f, (float)K);
+  const float per_k = __fdiv_rn(1.0f, (float)K);
   auto there = [&](int c) { return FULL || col + c * 256 < K; };
 
   uint64_t dw[C][4], db[C][4];
