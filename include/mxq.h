@@ -495,8 +495,8 @@ mx_status mx_layer_norm_backward(const void* dy, int dy_type, const void* x, int
  * Activation of R rows into the operand of the next product. gated != 0: u is [R, 2 H] = [gate | up],
  * h = f(gate) * up; else u is [R, H], h = f(u). u: bf16; h in fp32, then codes [R, H] and scales
  * [ceil(H / 128), R] as mx_quantize_b128_rows makes them of the unrounded h. u_codes, u_scales: unless
- * NULL, a checkpoint of u (what mx_quantize_b128_rows makes of it). H % 32 == 0; gated with a checkpoint
- * H % 128 == 0. u and codes 32-byte aligned.
+ * NULL, a checkpoint of u (what mx_quantize_b128_rows makes of it). H % 32 == 0, H <= 2^27; gated with a
+ * checkpoint H % 128 == 0. u and codes 32-byte aligned.
  *
  * Backward: dh bf16 [R, H]; u bf16 or a checkpoint (u_type MX_TYPE_E4M3_B128 with u_scales). du, bf16
  * like u, is dh up f'(gate) | dh f(gate), or dh f'(u); du_codes, du_scales: the operand that

@@ -95,29 +95,31 @@ __device__ __forceinline__ uint64_t act(uint64_t g, uint64_t& d) {
   return h;
 }
 
-// What a warp's tile is of: a row, and a lane's runs of 8 columns of it.
+// What a warp's tile is of: a row, and a lane's runs of 8 columns of it. A CTA has 2^across warps side by side
+// on a row and the others on rows below (no quotient of indexes: a 64-bit one takes a fifth of the instructions
+// of a tile).
 struct ActTile {
-  int64_t row, H, R, U;
-  int col0, lane;
-  __device__ __forceinline__ int column(int p) const { return col0 + p * 256 + lane * 8; }
+  int64_t row, R;
+  int H, U, col0, lane;  // columns of h and of u, first column of the lane's runs
+  __device__ __forceinline__ int column(int p) const { return col0 + p * 256; }
   __device__ __forceinline__ bool has(int p) const { return column(p) < H; }
 };
-__device__ __forceinline__ bool act_tile(const ActArgs& a, bool gated, int col_tiles, int64_t tiles, ActTile& t) {
-  const int64_t tile = (int64_t)blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5);
-  if (tile >= tiles) return false;
-  t.row = tile / col_tiles;
-  t.col0 = (int)(tile - t.row * col_tiles) * kActCols;
+__device__ __forceinline__ bool act_tile(const ActArgs& a, bool gated, int across, ActTile& t) {
+  constexpr int kWarps = kActThreads / 32;
+  const int warp = threadIdx.x >> 5;
   t.lane = threadIdx.x & 31;
-  t.H = a.H;
+  t.row = (int64_t)blockIdx.x * (kWarps >> across) + (warp >> across);
+  t.col0 = (((int)blockIdx.y << across) + (warp & ((1 << across) - 1))) * kActCols + t.lane * 8;
+  t.H = (int)a.H;
+  t.U = gated ? 2 * t.H : t.H;
   t.R = a.R;
-  t.U = gated ? 2 * a.H : a.H;
-  return true;
+  return t.row < t.R && t.col0 - t.lane * 8 < t.H;
 }
 
 // N runs (kActRuns of each of N / kActRuns parts of rows of `width` columns, a part H columns) as codes and
 // scales.
 template <int N>
-__device__ __forceinline__ void store_runs(const uint64_t (&v)[N][4], const ActTile& t, int64_t width,
+__device__ __forceinline__ void store_runs(const uint64_t (&v)[N][4], const ActTile& t, int width,
                                            uint8_t* codes, float* scales) {
   uint8_t* to = codes + t.row * width;
   run_codes<N>(
@@ -128,7 +130,7 @@ __device__ __forceinline__ void store_runs(const uint64_t (&v)[N][4], const ActT
       },
       [&](int n, float s) {
         const int p = n % kActRuns;
-        const int64_t kb = ((n / kActRuns) * t.H + t.column(p)) / kB128;
+        const int kb = ((n / kActRuns) * t.H + t.column(p)) / kB128;
         if ((t.column(p) & ~(kB128 - 1)) < t.H) scales[kb * t.R + t.row] = s;
       });
 }
@@ -139,7 +141,7 @@ struct ActRuns {
   uint32_t raw[kActRuns][CODES ? 2 : 4];
   float scale[kActRuns];
 
-  __device__ __forceinline__ void load(const void* u, const float* scales, const ActTile& t, int64_t width,
+  __device__ __forceinline__ void load(const void* u, const float* scales, const ActTile& t, int width,
                                        int part) {
 #pragma unroll
     for (int p = 0; p < kActRuns; ++p) {
@@ -147,7 +149,7 @@ struct ActRuns {
 #pragma unroll
       for (int j = 0; j < (CODES ? 2 : 4); ++j) raw[p][j] = 0u;
       if (!t.has(p)) continue;
-      const int64_t col = part * t.H + t.column(p);
+      const int col = part * t.H + t.column(p);
       if constexpr (CODES) {
         asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
                      : "=r"(raw[p][0]), "=r"(raw[p][1])
@@ -172,11 +174,11 @@ struct ActRuns {
 };
 
 template <int KIND, bool GATED>
-__global__ void __launch_bounds__(kActThreads) activation_kernel(ActArgs a, int col_tiles, int64_t tiles) {
+__global__ void __launch_bounds__(kActThreads) activation_kernel(ActArgs a, int across) {
   pdl_launch_dependents();
   pdl_wait();
   ActTile t;
-  if (!act_tile(a, GATED, col_tiles, tiles, t)) return;
+  if (!act_tile(a, GATED, across, t)) return;
   constexpr int kParts = GATED ? 2 : 1;
   ActRuns<false> in[kParts];
 #pragma unroll
@@ -198,12 +200,11 @@ __global__ void __launch_bounds__(kActThreads) activation_kernel(ActArgs a, int 
 }
 
 template <int KIND, bool GATED, bool CODES>
-__global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArgs a, int col_tiles,
-                                                                          int64_t tiles) {
+__global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArgs a, int across) {
   pdl_launch_dependents();
   pdl_wait();
   ActTile t;
-  if (!act_tile(a, GATED, col_tiles, tiles, t)) return;
+  if (!act_tile(a, GATED, across, t)) return;
   constexpr int kParts = GATED ? 2 : 1;
   ActRuns<CODES> in[kParts];
   ActRuns<false> dh;
@@ -249,11 +250,14 @@ cudaError_t by_kind(int kind, F&& f) {
   return f(std::integral_constant<int, MX_ACT_GELU_TANH>());
 }
 
-cudaError_t run(void (*kernel)(ActArgs, int, int64_t), const ActArgs& a, cudaStream_t stream) {
-  const int64_t col_tiles = (a.H + kActCols - 1) / kActCols, tiles = a.R * col_tiles;
+cudaError_t run(void (*kernel)(ActArgs, int), const ActArgs& a, cudaStream_t stream) {
+  const int64_t col_tiles = (a.H + kActCols - 1) / kActCols;
   constexpr int kWarps = kActThreads / 32;
-  return launch_pdl(kernel, dim3((unsigned)((tiles + kWarps - 1) / kWarps)), dim3(kActThreads), 0, stream, a,
-                    (int)col_tiles, tiles);
+  int across = 0;
+  while ((1 << across) < kWarps && (1 << across) < col_tiles) ++across;
+  const int rows = kWarps >> across;
+  const dim3 grid((unsigned)((a.R + rows - 1) / rows), (unsigned)((col_tiles + (1 << across) - 1) >> across));
+  return launch_pdl(kernel, grid, dim3(kActThreads), 0, stream, a, across);
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ mx_status check_norm(int64_t M, int64_t K) {
 // own.
 mx_status check_activation(int64_t R, int64_t H, int kind, int gated, bool codes_of_u) {
   if (kind != MX_ACT_SILU && kind != MX_ACT_GELU && kind != MX_ACT_GELU_TANH) return MX_ERR_UNSUPPORTED;
-  if (!sizes_ok(R, H) || H > INT32_MAX / 2 || !sizes_ok(R, 2 * H)) return MX_ERR_SHAPE;
+  if (!sizes_ok(R, H) || H > (1 << 27) || !sizes_ok(R, 2 * H)) return MX_ERR_SHAPE;
   return H % (gated && codes_of_u ? 128 : 32) == 0 ? MX_OK : MX_ERR_SHAPE;
 }
 
