@@ -50,7 +50,8 @@ EXPORTS = (
     "mx_selftest_gemm_b128_give_up", "mx_selftest_gemm_b128_grouped_give_up",
     "mx_layer_norm", "mx_layer_norm_b128", "mx_layer_norm_backward_workspace",
     "mx_layer_norm_backward", "mx_activation_b128", "mx_activation_backward",
-    "mx_requantize_b128_cols", "mx_dequantize_b128_rows",
+    "mx_requantize_b128_cols", "mx_dequantize_b128_rows", "mx_selftest_layer_norm_give_up",
+    "mx_selftest_layer_norm_backward_give_up",
 )
 
 
@@ -119,6 +120,8 @@ def lib() -> ctypes.CDLL:
         "mx_activation_backward": (i32, [p, p, i32, p, i64, i64, i32, i32, p, p, p, p]),
         "mx_requantize_b128_cols": (i32, [p, p, i64, i64, p, i64, p, i32, p, p, p]),
         "mx_dequantize_b128_rows": (i32, [p, p, i64, i64, p, i64, p, i32, p]),
+        "mx_selftest_layer_norm_give_up": (i32, [p, i64, i64, p, i64, p]),
+        "mx_selftest_layer_norm_backward_give_up": (i32, [p, p, i32, p, p, p, i64, i64, p, i64, p]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -913,6 +916,33 @@ def mx_layer_norm_backward(dy, x, mean, rstd, weight=None, *, x_scales=None, wei
                                         _TYPES[dtype], _ptr(dweight), _ptr(dbias), _ptr(workspace),
                                         _stream_ptr(stream, dy)))
     return dx, dweight, dbias
+
+
+def mx_selftest_layer_norm_give_up(x, limit_ns: int, *, stream=None):
+    """mx_layer_norm of bf16 x with every wait of the kernel limited to limit_ns; returns the (unspecified)
+    output. The device error word reports the give-up."""
+    M, K = _input(x)
+    y = _empty((M, K), torch.bfloat16, x, stream)
+    _check(lib().mx_selftest_layer_norm_give_up(_ptr(x), M, K, _ptr(y), limit_ns,
+                                                _stream_ptr(stream, x)))
+    return y
+
+
+def mx_selftest_layer_norm_backward_give_up(dy, x, mean, rstd, limit_ns: int, *, x_scales=None,
+                                            stream=None):
+    """mx_layer_norm_backward from bf16 dy and bf16 or checkpointed x, without the parameters' gradients,
+    with every wait of the kernel limited to limit_ns; returns the (unspecified) dx."""
+    M, K = _input(dy, "dy")
+    if (_input(x) if x_scales is None else _checkpoint(x, x_scales, "x", like=dy)) != (M, K):
+        raise ValueError("dy and x must be [M, K]")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if _tensor(t, name, torch.float32, dim=1, like=dy).shape[0] != M:
+            raise ValueError(f"{name} must have one value per row")
+    dx = _empty((M, K), torch.bfloat16, dy, stream)
+    _check(lib().mx_selftest_layer_norm_backward_give_up(
+        _ptr(dy), _ptr(x), 0 if x_scales is None else _CHECKPOINT, _ptr(x_scales), _ptr(mean),
+        _ptr(rstd), M, K, _ptr(dx), limit_ns, _stream_ptr(stream, dy)))
+    return dx
 
 
 def _gate(U: int, gated) -> int:

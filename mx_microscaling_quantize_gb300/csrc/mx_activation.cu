@@ -90,7 +90,9 @@ __device__ __forceinline__ uint64_t act(uint64_t g, uint64_t& d) {
   h = mul_pair(g, s);
   if constexpr (GRAD) {
     const uint64_t q = mul_pair(h, fma_pair(s, pair(-1.0f), pair(1.0f)));  // h (1 - s)
-    d = fma_pair(q, scaled(fma_pair(g2, pair(3.0f), pair(1.0f)), kTanhGain), s);
+    // (bounded: where g^2 overflows q is 0)
+    const uint64_t some = pair(fminf(lo_of(g2), 1e30f), fminf(hi_of(g2), 1e30f));
+    d = fma_pair(q, scaled(fma_pair(some, pair(3.0f), pair(1.0f)), kTanhGain), s);
   }
   return h;
 }

@@ -138,6 +138,40 @@ __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_
       : "memory");
 }
 
+// The rows that a group asks for: S stages, each with a barrier, taken in turn. Thread 0 of the group asks;
+// where its wait runs out it waits for all that it has asked for and asks for
+// nothing more, so that no copy outlives the CTA.
+struct RowStages {
+  uint32_t bars;
+  int S, ahead, stage = 0, parity = 0;  // ahead: rows asked for when one is waited for
+  bool failed = false;
+
+  __device__ __forceinline__ RowStages(uint64_t* full, int S_, int ahead_)
+      : bars((uint32_t)__cvta_generic_to_shared(full)), S(S_), ahead(ahead_) {}
+  __device__ __forceinline__ void init(uint32_t arrivals) const {
+    for (int s = 0; s < S; ++s) tc::mbar_init(bars + s * 8, arrivals);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tc::fence_proxy_async_smem();
+  }
+  __device__ __forceinline__ uint32_t bar(int s) const { return bars + s * 8; }
+  __device__ __forceinline__ void wait(const NormArgs& a, int64_t row, int64_t step, int t) {
+    if (failed) return;
+    tc::mbar_wait(bar(stage), parity, &failed, a.wait_limit_ns, a.err);
+    if (!failed || t != 0) return;
+    for (int k = 0; k < ahead && row + k * step < a.M; ++k) {
+      const int s = stage + k < S ? stage + k : stage + k - S;
+      bool late = false;
+      tc::mbar_wait(bar(s), s == stage + k ? parity : parity ^ 1, &late, kNormDrainNs, a.err);
+    }
+  }
+  __device__ __forceinline__ void next() {
+    if (++stage == S) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // A parameter of the columns of a group, in fp32: run c of lane l of warp w as two pieces of 16 bytes 512 apart,
 // so that a warp's reads meet no bank twice. store: each lane of a group its own runs; at: of (w, l), run 0.
 template <int P>
@@ -250,12 +284,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(norm_shared);
   const uint32_t w_at = Param::at(base, wi, lane), b_at = Param::at(base + T * Param::kBytes, wi, lane);
   const uint32_t rows_at = base + 2 * T * Param::kBytes + group * S * T * kStage;
-  const uint32_t bars = (uint32_t)__cvta_generic_to_shared(full[group]);
-  if (t == 0) {
-    for (int s = 0; s < S; ++s) tc::mbar_init(bars + s * 8, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tc::fence_proxy_async_smem();
-  }
+  RowStages rows(full[group], S, S);
+  if (t == 0) rows.init(1);
   pdl_launch_dependents();
   __syncthreads();
   pdl_wait();
@@ -263,11 +293,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   int64_t row = ((int64_t)blockIdx.x * (blockDim.x / T) + group) * R;
   const uint32_t row_bytes = K * kSize;
   auto request = [&](int64_t at, int stage) {
-    if (t != 0 || at >= a.M) return;
+    if (t != 0 || at >= a.M || rows.failed) return;
     const uint32_t bytes = (uint32_t)(a.M - at < R ? a.M - at : R) * row_bytes;
-    tc::mbar_arrive_expect_tx(bars + stage * 8, bytes);
+    tc::mbar_arrive_expect_tx(rows.bar(stage), bytes);
     bulk_copy(rows_at + stage * T * kStage, static_cast<const char*>(a.x) + at * row_bytes, bytes,
-              bars + stage * 8);
+              rows.bar(stage));
   };
   for (int s = 0; s < S; ++s) request(row + s * step, s);
   const bool w_f32 = a.w_type == kTypeFp32, y_f32 = a.y_type == kTypeFp32;
@@ -282,12 +312,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   // lanes of the sums over warps: of all 32 for one row, of a half for each of two
   const int w_of = R == 1 ? lane : lane & 15;
   const float theirs = w_of < W ? count(w_of) : 0.0f;
-  int stage = 0, parity = 0;
-  bool failed = false;
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
-    tc::mbar_wait(bars + stage * 8, parity, &failed, a.wait_limit_ns, a.err);
+    rows.wait(a, row, step, t);
     uint64_t x[R * P][4];
-    const uint32_t from = rows_at + stage * T * kStage + col * kSize;
+    const uint32_t from = rows_at + rows.stage * T * kStage + col * kSize;
 #pragma unroll
     for (int n = 0; n < R * P; ++n) {
       if (there(n % P) && (n < P || row + 1 < a.M)) {
@@ -347,11 +375,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
     } else {
       __syncwarp();
     }
-    request(row + S * step, stage);
-    if (++stage == S) {
-      stage = 0;
-      parity ^= 1;
-    }
+    request(row + S * step, rows.stage);
+    rows.next();
     if constexpr (QUANT) {
       if (a.x_codes) store_codes<R, P>(x, lane, a.x_codes, a.x_scales_out, a.M, K, row, col);
     }
@@ -394,12 +419,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
       }
     }
     if constexpr (QUANT) store_codes<R, P>(x, lane, a.codes, a.scales, a.M, K, row, col);
-  }
-  if (failed) {  // the copies asked for land before this CTA's shared memory is another's
-    for (int s = 0; s < S; ++s) {
-      bool late = false;
-      tc::mbar_wait(bars + s * 8, s < stage ? parity : parity ^ 1, &late, kNormDrainNs, a.err);
-    }
   }
 }
 
@@ -466,7 +485,7 @@ struct NormRing {
   // both with a scale per block of 128
   static constexpr int kWeights = ParamRuns<kRuns>::kBytes, kStage = kRuns * (kX + kDy) + (XT == kTypeB128 ? 1 : 0);
 
-  uint32_t sm, full;  // this group's stages, and a barrier for each
+  uint32_t sm;  // this group's stages
   int t, T, K, col;
 
   __device__ __forceinline__ uint32_t x_at(int stage) const { return sm + stage * kStage * T; }
@@ -474,9 +493,9 @@ struct NormRing {
   __device__ __forceinline__ uint32_t scale_at(int stage) const { return dy_at(stage) + kRuns * T * kDy; }
 
   // Asks for a row: called by all of the group, once the stage has been read by all of them.
-  __device__ __forceinline__ void request(const NormArgs& a, int64_t row, int stage) const {
-    if (row >= a.M) return;
-    const uint32_t bar = full + stage * 8;
+  __device__ __forceinline__ void request(const NormArgs& a, const RowStages& rows, int64_t row, int stage) const {
+    if (row >= a.M || rows.failed) return;
+    const uint32_t bar = rows.bar(stage);
     if constexpr (XT == kTypeB128) {
       if (t < (K + kB128 - 1) / kB128) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale_at(stage) + t * 4),
@@ -563,19 +582,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
   const int col = (t >> 5) * 1024 + (threadIdx.x & 31) * 8;
   const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring_shared);
-  const Ring ring{base + T * Ring::kWeights + group * T * S * Ring::kStage,
-                  (uint32_t)__cvta_generic_to_shared(full[group]), t, T, K, col};
-  if (t == 0) {
-    for (int s = 0; s < S; ++s) tc::mbar_init(ring.full + s * 8, XT == kTypeB128 ? T + 1 : 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tc::fence_proxy_async_smem();
-  }
+  const Ring ring{base + T * Ring::kWeights + group * T * S * Ring::kStage, t, T, K, col};
+  RowStages rows(full[group], S, S > 1 ? S - 1 : 1);
+  if (t == 0) rows.init(XT == kTypeB128 ? T + 1 : 1);
   pdl_launch_dependents();
   __syncthreads();
   pdl_wait();
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
   int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
-  for (int s = 0; s < (S > 1 ? S - 1 : 1); ++s) ring.request(a, row + s * step, s);
+  for (int s = 0; s < rows.ahead; ++s) ring.request(a, rows, row + s * step, s);
   using Param = ParamRuns<C>;
   const uint32_t w_at = Param::at(base, t >> 5, threadIdx.x & 31);
   if (group == 0) Param::store(w_at, a.weight, a.w_type == kTypeFp32, col, K, 1.0f);
@@ -592,16 +607,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     rstd_next = load_f32(a.rstd + row);
     if (a.mean) mean_next = load_f32(a.mean + row);
   }
-  int stage = 0, parity = 0;
-  bool failed = false;
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
+    const int stage = rows.stage;
     const float rstd = rstd_next;
     const uint64_t minus = pair(-mean_next), r2 = pair(rstd);
     if (row + step < a.M) {
       rstd_next = load_f32(a.rstd + row + step);
       if (a.mean) mean_next = load_f32(a.mean + row + step);
     }
-    tc::mbar_wait(ring.full + stage * 8, parity, &failed, a.wait_limit_ns, a.err);
+    rows.wait(a, row, step, t);
     uint64_t c1 = 0u, c2 = 0u;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -622,7 +636,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     float s1 = lo_of(c1) + hi_of(c1), s2 = lo_of(c2) + hi_of(c2);
     row_sums(part, slot, group, W, s1, s2);
     // all of the group have read the row before this one for the last time
-    if (S > 1) ring.request(a, row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
+    if (S > 1) ring.request(a, rows, row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
     // dx = rstd g - rstd s1 - (x - mean) rstd^2 s2
     const uint64_t m1 = pair(a.mean ? -s1 * per_k * rstd : 0.0f), m2 = pair(-s2 * per_k * rstd * rstd);
     const int64_t at = row * K + col;
@@ -654,19 +668,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     }
     if (S == 1) {
       group_sync(group, T);
-      ring.request(a, row + step, 0);
+      ring.request(a, rows, row + step, 0);
     }
-    if (++stage == S) {
-      stage = 0;
-      parity ^= 1;
-    }
+    rows.next();
   }
-  if (failed) {  // the copies asked for land before this CTA's shared memory is another's
-    for (int s = 0; s < S; ++s) {
-      bool late = false;
-      tc::mbar_wait(ring.full + s * 8, s < stage ? parity : parity ^ 1, &late, kNormDrainNs, a.err);
-    }
-  }
+  if (XT == kTypeB128) asm volatile("cp.async.wait_all;" ::: "memory");  // scales asked for after a give-up
   const int groups = blockDim.x / T;
   __syncthreads();
   for (int k = 0; k < 2; ++k) {

@@ -34,8 +34,9 @@ uintptr_t size_of(int t) { return t == MX_TYPE_FP32 ? 4 : t == MX_TYPE_BF16 ? 2 
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-mx_status run_norm(cudaError_t (*launch)(const mxq::NormArgs&, cudaStream_t), mxq::NormArgs& a, void* stream) {
-  a.wait_limit_ns = kWaitNs;
+mx_status run_norm(cudaError_t (*launch)(const mxq::NormArgs&, cudaStream_t), mxq::NormArgs& a,
+                   unsigned long long limit_ns, void* stream) {
+  a.wait_limit_ns = limit_ns;
   return launched([&] {
     const cudaError_t err = mxq::device_error_word(&a.err);
     return err != cudaSuccess ? err : launch(a, as_stream(stream));
@@ -46,21 +47,9 @@ mx_status check_norm(int64_t M, int64_t K) {
   return sizes_ok(M, K) && K <= mxq::kNormMaxCols ? MX_OK : MX_ERR_SHAPE;
 }
 
-// Activations: R rows of H outputs, `parts` inputs each; whole blocks where two parts have codes of their
-// own.
-mx_status check_activation(int64_t R, int64_t H, int kind, int gated, bool codes_of_u) {
-  if (kind != MX_ACT_SILU && kind != MX_ACT_GELU && kind != MX_ACT_GELU_TANH) return MX_ERR_UNSUPPORTED;
-  if (!sizes_ok(R, H) || H > (1 << 27) || !sizes_ok(R, 2 * H)) return MX_ERR_SHAPE;
-  return H % (gated && codes_of_u ? 128 : 32) == 0 ? MX_OK : MX_ERR_SHAPE;
-}
-
-}  // namespace
-
-extern "C" {
-
-mx_status mx_layer_norm(const void* x, int x_type, const void* weight, const void* bias, int w_type,
-                        int64_t M, int64_t K, float eps, int center, void* y, int y_type, float* mean,
-                        float* rstd, void* stream) {
+mx_status layer_norm(const void* x, int x_type, const void* weight, const void* bias, int w_type, int64_t M,
+                     int64_t K, float eps, int center, void* y, int y_type, float* mean, float* rstd,
+                     unsigned long long limit_ns, void* stream) {
   const mx_status st = check_norm(M, K);
   if (st != MX_OK) return st;
   if (!float_type(x_type) || !float_type(w_type) || !float_type(y_type)) return MX_ERR_UNSUPPORTED;
@@ -84,55 +73,13 @@ mx_status mx_layer_norm(const void* x, int x_type, const void* weight, const voi
   a.y_type = y_type;
   a.mean = mean;
   a.rstd = rstd;
-  return run_norm(&mxq::launch_norm, a, stream);
+  return run_norm(&mxq::launch_norm, a, limit_ns, stream);
 }
 
-mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, const void* bias, int w_type,
-                             int64_t M, int64_t K, float eps, int center, void* codes, float* scales,
-                             void* x_codes, float* x_scales, float* mean, float* rstd, void* stream) {
-  const mx_status st = check_norm(M, K);
-  if (st != MX_OK) return st;
-  if (K % 32 != 0) return MX_ERR_SHAPE;
-  if (!float_type(x_type) || !float_type(w_type)) return MX_ERR_UNSUPPORTED;
-  if (M == 0 || K == 0) return MX_OK;
-  if (!x || !codes || !scales || (x_codes == nullptr) != (x_scales == nullptr)) return MX_ERR_NULL;
-  if (!aligned(x, 32) || !aligned(codes, 32) || !aligned(scales, 4) || !aligned(x_codes, 32) ||
-      !aligned(x_scales, 4) || !aligned(weight, 32) || !aligned(bias, 32) || !aligned(mean, 4) ||
-      !aligned(rstd, 4)) {
-    return MX_ERR_ALIGN;
-  }
-  mxq::NormArgs a{};
-  a.x = x;
-  a.x_type = x_type;
-  a.weight = weight;
-  a.bias = bias;
-  a.w_type = w_type;
-  a.M = M;
-  a.K = K;
-  a.eps = eps;
-  a.center = center != 0;
-  a.codes = static_cast<uint8_t*>(codes);
-  a.scales = scales;
-  a.x_codes = static_cast<uint8_t*>(x_codes);
-  a.x_scales_out = x_scales;
-  a.mean = mean;
-  a.rstd = rstd;
-  return run_norm(&mxq::launch_norm, a, stream);
-}
-
-mx_status mx_layer_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes) {
-  if (!bytes) return MX_ERR_NULL;
-  const mx_status st = check_norm(M, K);
-  if (st != MX_OK) return st;
-  *bytes = mxq::norm_workspace_floats(M, K) * 4;
-  return MX_OK;
-}
-
-mx_status mx_layer_norm_backward(const void* dy, int dy_type, const void* x, int x_type,
-                                 const float* x_scales, const float* mean, const float* rstd,
-                                 const void* weight, int w_type, int64_t M, int64_t K, void* dx,
-                                 int dx_type, float* dweight, float* dbias, void* workspace,
-                                 void* stream) {
+mx_status layer_norm_backward(const void* dy, int dy_type, const void* x, int x_type, const float* x_scales,
+                              const float* mean, const float* rstd, const void* weight, int w_type, int64_t M,
+                              int64_t K, void* dx, int dx_type, float* dweight, float* dbias, void* workspace,
+                              unsigned long long limit_ns, void* stream) {
   const mx_status st = check_norm(M, K);
   if (st != MX_OK) return st;
   if (!float_type(dy_type) || !float_type(w_type) || !float_type(dx_type) ||
@@ -172,7 +119,91 @@ mx_status mx_layer_norm_backward(const void* dy, int dy_type, const void* x, int
   a.dweight = dweight;
   a.dbias = dbias;
   a.workspace = static_cast<float*>(workspace);
-  return run_norm(&mxq::launch_norm_backward, a, stream);
+  return run_norm(&mxq::launch_norm_backward, a, limit_ns, stream);
+}
+
+// Activations: R rows of H outputs, `parts` inputs each; whole blocks where two parts have codes of their
+// own.
+mx_status check_activation(int64_t R, int64_t H, int kind, int gated, bool codes_of_u) {
+  if (kind != MX_ACT_SILU && kind != MX_ACT_GELU && kind != MX_ACT_GELU_TANH) return MX_ERR_UNSUPPORTED;
+  if (!sizes_ok(R, H) || H > (1 << 27) || !sizes_ok(R, 2 * H)) return MX_ERR_SHAPE;
+  return H % (gated && codes_of_u ? 128 : 32) == 0 ? MX_OK : MX_ERR_SHAPE;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_layer_norm(const void* x, int x_type, const void* weight, const void* bias, int w_type,
+                        int64_t M, int64_t K, float eps, int center, void* y, int y_type, float* mean,
+                        float* rstd, void* stream) {
+  return layer_norm(x, x_type, weight, bias, w_type, M, K, eps, center, y, y_type, mean, rstd, kWaitNs, stream);
+}
+
+mx_status mx_selftest_layer_norm_give_up(const void* x, int64_t M, int64_t K, void* y, int64_t limit_ns,
+                                         void* stream) {
+  if (limit_ns <= 0 || limit_ns > 100000000 || M == 0 || K == 0) return MX_ERR_SHAPE;
+  return layer_norm(x, MX_TYPE_BF16, nullptr, nullptr, MX_TYPE_FP32, M, K, 1e-5f, 1, y, MX_TYPE_BF16, nullptr,
+                    nullptr, (unsigned long long)limit_ns, stream);
+}
+
+mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, const void* bias, int w_type,
+                             int64_t M, int64_t K, float eps, int center, void* codes, float* scales,
+                             void* x_codes, float* x_scales, float* mean, float* rstd, void* stream) {
+  const mx_status st = check_norm(M, K);
+  if (st != MX_OK) return st;
+  if (K % 32 != 0) return MX_ERR_SHAPE;
+  if (!float_type(x_type) || !float_type(w_type)) return MX_ERR_UNSUPPORTED;
+  if (M == 0 || K == 0) return MX_OK;
+  if (!x || !codes || !scales || (x_codes == nullptr) != (x_scales == nullptr)) return MX_ERR_NULL;
+  if (!aligned(x, 32) || !aligned(codes, 32) || !aligned(scales, 4) || !aligned(x_codes, 32) ||
+      !aligned(x_scales, 4) || !aligned(weight, 32) || !aligned(bias, 32) || !aligned(mean, 4) ||
+      !aligned(rstd, 4)) {
+    return MX_ERR_ALIGN;
+  }
+  mxq::NormArgs a{};
+  a.x = x;
+  a.x_type = x_type;
+  a.weight = weight;
+  a.bias = bias;
+  a.w_type = w_type;
+  a.M = M;
+  a.K = K;
+  a.eps = eps;
+  a.center = center != 0;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.x_codes = static_cast<uint8_t*>(x_codes);
+  a.x_scales_out = x_scales;
+  a.mean = mean;
+  a.rstd = rstd;
+  return run_norm(&mxq::launch_norm, a, kWaitNs, stream);
+}
+
+mx_status mx_layer_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes) {
+  if (!bytes) return MX_ERR_NULL;
+  const mx_status st = check_norm(M, K);
+  if (st != MX_OK) return st;
+  *bytes = mxq::norm_workspace_floats(M, K) * 4;
+  return MX_OK;
+}
+
+mx_status mx_layer_norm_backward(const void* dy, int dy_type, const void* x, int x_type,
+                                 const float* x_scales, const float* mean, const float* rstd,
+                                 const void* weight, int w_type, int64_t M, int64_t K, void* dx,
+                                 int dx_type, float* dweight, float* dbias, void* workspace,
+                                 void* stream) {
+  return layer_norm_backward(dy, dy_type, x, x_type, x_scales, mean, rstd, weight, w_type, M, K, dx, dx_type,
+                             dweight, dbias, workspace, kWaitNs, stream);
+}
+
+mx_status mx_selftest_layer_norm_backward_give_up(const void* dy, const void* x, int x_type,
+                                                  const float* x_scales, const float* mean,
+                                                  const float* rstd, int64_t M, int64_t K, void* dx,
+                                                  int64_t limit_ns, void* stream) {
+  if (limit_ns <= 0 || limit_ns > 100000000 || M == 0 || K == 0) return MX_ERR_SHAPE;
+  return layer_norm_backward(dy, MX_TYPE_BF16, x, x_type, x_scales, mean, rstd, nullptr, MX_TYPE_FP32, M, K, dx,
+                             MX_TYPE_BF16, nullptr, nullptr, nullptr, (unsigned long long)limit_ns, stream);
 }
 
 mx_status mx_activation_b128(const void* u, int64_t R, int64_t H, int kind, int gated, void* codes,
