@@ -154,9 +154,29 @@ struct RowStages {
     tc::fence_proxy_async_smem();
   }
   __device__ __forceinline__ uint32_t bar(int s) const { return bars + s * 8; }
+  // One attempt, of at most `ns`.
+  static __device__ __forceinline__ bool landed(uint32_t bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+  }
   __device__ __forceinline__ void wait(const NormArgs& a, int64_t row, int64_t step, int t) {
     if (failed) return;
-    tc::mbar_wait(bar(stage), parity, &failed, a.wait_limit_ns, a.err);
+    const uint32_t ns = (uint32_t)min(a.wait_limit_ns, 1000000ull);
+    if (landed(bar(stage), parity, ns)) return;
+    const unsigned long long t0 = tc::global_ns();
+    while (!landed(bar(stage), parity, ns)) {
+      if (tc::global_ns() - t0 > a.wait_limit_ns) {
+        failed = true;
+        atomicOr(a.err, 1u);
+        break;
+      }
+    }
     if (!failed || t != 0) return;
     for (int k = 0; k < ahead && row + k * step < a.M; ++k) {
       const int s = stage + k < S ? stage + k : stage + k - S;
@@ -556,15 +576,36 @@ __device__ __forceinline__ float* share(const NormArgs& a, int k) {
   float* whole = k ? a.dbias : a.dweight;
   return !whole || gridDim.x == 1 ? whole : a.workspace + (k * (int64_t)gridDim.x + blockIdx.x) * a.K;
 }
-// Adds up the groups' rows [groups][K] in shared memory, in their order.
-__device__ __forceinline__ void join_shares(const float* sm, int groups, int K, float* out) {
+// Adds up the groups' rows [2][groups][K] in shared memory (first dw's, then db's), in their order.
+__device__ __forceinline__ void join_shares(const NormArgs& a, const float* sm, int groups) {
+  const int K = (int)a.K;
   __syncthreads();
-  for (int col = threadIdx.x; col < K; col += blockDim.x) {
-    float s = 0.0f;
-    for (int i = 0; i < groups; ++i) s += sm[i * K + col];
-    out[col] = s;
+  constexpr int kAhead = 4;  // columns of a thread whose reads are on their way together
+  const int threads = blockDim.x;
+  const uint32_t base = (uint32_t)__cvta_generic_to_shared(sm);
+  for (int k = 0; k < 2; ++k) {
+    float* out = share(a, k);
+    if (!out) continue;
+    for (int col0 = threadIdx.x; col0 < K; col0 += kAhead * threads) {
+      float s[kAhead] = {};
+#pragma unroll 2
+      for (int i = 0; i < groups; ++i) {
+        const uint32_t at = base + ((k * groups + i) * K + col0) * 4;
+        float v[kAhead] = {};
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (col0 + j * threads >= K) continue;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[j]) : "r"(at + j * threads * 4));
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) s[j] += v[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (col0 + j * threads < K) out[col0 + j * threads] = s[j];
+      }
+    }
   }
-  __syncthreads();
 }
 
 // Gradient of the input, and each CTA's share of the parameters' gradients, which norm_reduce_kernel
@@ -673,13 +714,13 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     rows.next();
   }
   if (XT == kTypeB128) asm volatile("cp.async.wait_all;" ::: "memory");  // scales asked for after a give-up
+  if (!a.dweight && !a.dbias) return;
+  // through shared memory in any case: a lane's runs of 8 columns would leave as many partial lines
   const int groups = blockDim.x / T;
   __syncthreads();
+#pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float* out = share(a, k);
-    if (!out) continue;
-    // through shared memory in any case: a lane's runs of 8 columns would leave as many partial lines
-    float* to = reinterpret_cast<float*>(ring_shared) + group * K + col;
+    float* to = reinterpret_cast<float*>(ring_shared) + (k * groups + group) * K + col;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (!there(c)) continue;
@@ -689,8 +730,8 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
         *reinterpret_cast<float4*>(to + c * 256 + 4 * j) = make_float4(lo_of(p), hi_of(p), lo_of(q), hi_of(q));
       }
     }
-    join_shares(reinterpret_cast<const float*>(ring_shared), groups, K, out);
   }
+  join_shares(a, reinterpret_cast<const float*>(ring_shared), groups);
 }
 
 // The same for rows of any length and alignment: N values of a lane, a group's width apart, loaded one by
@@ -747,40 +788,45 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(Norm
     for (int i = 0; i < N; ++i) g[i] = fmaf(-xh[i], s2, g[i] - s1) * rstd;
     store_values(static_cast<char*>(a.dx) + row * K * (dx_f32 ? 4 : 2), dx_f32, K, column, g);
   }
+  if (!a.dweight && !a.dbias) return;
   const int groups = blockDim.x / T;
+  float* sm = reinterpret_cast<float*>(ring_shared);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    float* out = share(a, k);
-    if (!out) continue;
-    float* sm = reinterpret_cast<float*>(ring_shared);
-    float* to = groups > 1 ? sm + group * K : out;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (column(i) < K) to[column(i)] = k ? db[i] : dw[i];
+      if (column(i) < K) sm[(k * groups + group) * K + column(i)] = k ? db[i] : dw[i];
     }
-    if (groups > 1) join_shares(sm, groups, K, out);
   }
+  join_shares(a, sm, groups);
 }
 
-// Adds up the CTAs' shares of a parameter's gradient (blockIdx.y: which): 32 columns a CTA, the shares
-// over 16 warps.
+// Adds up the CTAs' shares of a parameter's gradient (blockIdx.y: which): 32 columns a CTA, the shares over 16
+// warps, ten of a warp's on their way together.
 __global__ void __launch_bounds__(512) norm_reduce_kernel(NormArgs a, int parts) {
   __shared__ float sum[16][33];
   pdl_launch_dependents();
   pdl_wait();
   float* to = blockIdx.y ? a.dbias : a.dweight;
   if (!to) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + lane;
-  const float* from = a.workspace + (int64_t)blockIdx.y * parts * a.K;
+  constexpr int kAhead = 10;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = (int)a.K, col = (int)blockIdx.x * 32 + lane;
+  const float* from = a.workspace + (int64_t)blockIdx.y * parts * K + col;
   float s = 0.0f;
-  if (col < a.K) {
-#pragma unroll 4
-    for (int p = warp; p < parts; p += 16) s += load_f32(from + p * a.K + col);
+  if (col < K) {
+    for (int p0 = warp; p0 < parts; p0 += 16 * kAhead) {
+      float v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        v[i] = p0 + 16 * i < parts ? load_f32(from + (int64_t)(p0 + 16 * i) * K) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) s += v[i];
+    }
   }
   sum[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < a.K) {
+  if (warp == 0 && col < K) {
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s += sum[i][lane];
@@ -854,7 +900,7 @@ cudaError_t run_backward(void (*kernel)(NormArgs, int, int), int fixed, int stag
   if (!g.count) return cudaErrorInvalidConfiguration;
   const int threads = 32 * W * g.count;
   const bool params = a.dweight || a.dbias;
-  if (params && g.smem < (size_t)g.count * a.K * 4) g.smem = (size_t)g.count * a.K * 4;  // the groups' shares
+  if (params && g.smem < (size_t)g.count * a.K * 8) g.smem = (size_t)g.count * a.K * 8;  // the groups' shares
   const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, g.smem, 1);
   if (slots <= 0) return cudaErrorInvalidConfiguration;
   int64_t ctas = (a.M + g.count - 1) / g.count;
