@@ -88,11 +88,25 @@ __device__ __forceinline__ void load_params(const void* p, bool f32, int K, F&& 
   }
 }
 
-// N values of a row (0 where there is none) and their way back.
+// N values of a row (0 where there is none) as they lie in memory, so that nothing waits for them before they are
+// used (value_of), and their way back.
 template <int N, typename F>
-__device__ __forceinline__ void load_values(const char* row, bool f32, int K, F&& column, float (&v)[N]) {
-  load_params(row, f32, K, column, 0.0f, v);
+__device__ __forceinline__ void load_values(const char* row, bool f32, int K, F&& column, uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0u;
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) v[i] = __float_as_uint(load_f32(reinterpret_cast<const float*>(row) + column(i)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (column(i) < K) v[i] = load_u16(reinterpret_cast<const uint16_t*>(row) + column(i));
+    }
+  }
 }
+__device__ __forceinline__ float value_of(uint32_t raw, bool f32) { return __uint_as_float(raw << (f32 ? 0 : 16)); }
 template <int N, typename F>
 __device__ __forceinline__ void store_values(char* row, bool f32, int K, F&& column, const float (&v)[N]) {
   if (f32) {
@@ -229,21 +243,6 @@ struct ParamRuns {
 // ------------------------------------------------------------------------------------------
 // forward
 // ------------------------------------------------------------------------------------------
-// Mean and 1 / deviation of a row from each warp's mean and sum of squared differences from it (part: of the
-// CTA's warps), count(w) values in warp w of the group: the warps' sums about their own means are joined with
-// their means' distance from the row's.
-template <int WARPS, typename F>
-__device__ __forceinline__ void join_stats(const NormArgs& a, float2* part, int group, int W, F&& count,
-                                           float& mean, float& sq) {
-  const int lane = threadIdx.x & 31, i = lane & (WARPS - 1), w0 = group * W;
-  if (lane == 0) part[threadIdx.x >> 5] = make_float2(mean, sq);
-  group_sync(group, 32 * W);
-  const float2 p = i < W ? part[w0 + i] : make_float2(0.0f, 0.0f);
-  const float n = i < W ? (float)count(i) : 0.0f;
-  mean = a.center ? __fdiv_rn(warp_sum<WARPS>(p.x * n), (float)a.K) : 0.0f;
-  sq = warp_sum<WARPS>(fmaf((p.x - mean) * n, p.x - mean, p.y));
-}
-
 __device__ __forceinline__ float deviation(const NormArgs& a, float sq) {
   return __frsqrt_rn(fmaf(sq, __fdiv_rn(1.0f, (float)a.K), a.eps));
 }
@@ -443,54 +442,74 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
 }
 
 // The same for rows of any length and alignment: 16 columns per lane, a group's width apart, loaded and
-// stored one by one.
+// stored one by one. Such loads and stores are what bounds it, so up to 8192 columns the parameters stay in
+// registers (they would be half of the loads) and the next row is on its way.
 template <bool XF32, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) norm_any_kernel(NormArgs a, int W) {
+__global__ void __launch_bounds__(THREADS, 1) norm_any_kernel(NormArgs a, int W) {
   constexpr int kWarps = THREADS / 32;
-  __shared__ float2 part[kWarps];
+  constexpr bool kKeep = THREADS <= 512;
+  __shared__ float2 part[2][kWarps];
   pdl_launch_dependents();
   pdl_wait();
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
-  if (row >= a.M) return;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
+  int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
   auto column = [&](int i) { return i * T + t; };
-  auto count = [&](int w) {
+  auto count = [&](int w) {  // columns of the group's warp w
     int n = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) n += min(max(K - i * T - 32 * w, 0), 32);
-    return n;
+    return (float)n;
   };
-  float x[16], p[16];
-  load_values(static_cast<const char*>(a.x) + row * K * (XF32 ? 4 : 2), XF32, K, column, x);
-  float mean = 0.0f;
-  if (a.center) {
+  const int lane = threadIdx.x & 31;
+  const float mine = count(t >> 5), theirs = lane < W ? count(lane) : 0.0f;
+  const bool w_f32 = a.w_type == kTypeFp32, y_f32 = a.y_type == kTypeFp32;
+  float x[16], w[16], b[16];
+  uint32_t raw[16];
+  auto load = [&](int64_t at) {
+    load_values(static_cast<const char*>(a.x) + at * K * (XF32 ? 4 : 2), XF32, K, column, raw);
+  };
+  auto params = [&] {
+    load_params(a.weight, w_f32, K, column, 1.0f, w);
+    load_params(a.bias, w_f32, K, column, 0.0f, b);
+  };
+  if constexpr (kKeep) {
+    if (row < a.M) load(row);
+    params();
+  }
+  for (int slot = 0; row < a.M; row += step, slot ^= 1) {
+    if constexpr (!kKeep) load(row);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = value_of(raw[i], XF32);
+    if (kKeep && row + step < a.M) load(row + step);
+    float mean = 0.0f;
+    if (a.center) {
+      float s[2] = {};
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i & 1] += x[i];
+      mean = mine > 0.0f ? __fdiv_rn(warp_sum(s[0] + s[1]), mine) : 0.0f;
+    }
     float s[2] = {};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i & 1] += x[i];
-    const int n = count(t >> 5);
-    mean = n > 0 ? __fdiv_rn(warp_sum(s[0] + s[1]), (float)n) : 0.0f;
+    for (int i = 0; i < 16; ++i) {
+      const float d = column(i) < K ? x[i] - mean : 0.0f;
+      s[i & 1] = fmaf(d, d, s[i & 1]);
+    }
+    float sq = warp_sum(s[0] + s[1]);
+    if (W > 1) {  // the warps' sums about their own means, joined with the means' distances from the row's
+      if (lane == 0) part[slot][threadIdx.x >> 5] = make_float2(mean, sq);
+      group_sync(group, T);
+      const float2 q = lane < W ? part[slot][group * W + lane] : make_float2(0.0f, 0.0f);
+      mean = __fdiv_rn(warp_sum(q.x * theirs), (float)K);
+      sq = warp_sum(fmaf((q.x - mean) * theirs, q.x - mean, q.y));
+    }
+    const float rstd = deviation(a, sq);
+    if (t == 0) store_stats(a, row, mean, rstd);
+    if constexpr (!kKeep) params();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = fmaf((x[i] - mean) * rstd, w[i], b[i]);
+    store_values(static_cast<char*>(a.y) + row * K * (y_f32 ? 4 : 2), y_f32, K, column, x);
   }
-  float s[2] = {};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float d = column(i) < K ? x[i] - mean : 0.0f;
-    s[i & 1] = fmaf(d, d, s[i & 1]);
-  }
-  float sq = warp_sum(s[0] + s[1]);
-  if (W > 1) join_stats<kWarps>(a, part, group, W, count, mean, sq);
-  const float rstd = deviation(a, sq);
-  if (t == 0) store_stats(a, row, mean, rstd);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = (x[i] - mean) * rstd;
-  const bool w_f32 = a.w_type == kTypeFp32;
-  load_params(a.weight, w_f32, K, column, 1.0f, p);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] *= p[i];
-  load_params(a.bias, w_f32, K, column, 0.0f, p);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] += p[i];
-  const bool y_f32 = a.y_type == kTypeFp32;
-  store_values(static_cast<char*>(a.y) + row * K * (y_f32 ? 4 : 2), y_f32, K, column, x);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -735,11 +754,12 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
 }
 
 // The same for rows of any length and alignment: N values of a lane, a group's width apart, loaded one by
-// one.
+// one; up to 8192 columns (16 values) with the weights in registers and the next row on its way.
 template <int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(NormArgs a, int W, int) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
   __shared__ float part[2][2][kNormThreads / 32];
+  constexpr bool kKeep = N <= 16;
   pdl_launch_dependents();
   pdl_wait();
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
@@ -749,37 +769,49 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(Norm
   const bool codes = a.x_type == kTypeB128, w_f32 = a.w_type == kTypeFp32;
   const float per_k = __fdiv_rn(1.0f, (float)K);
   auto column = [&](int i) { return i * T + t; };
-  float dw[N], db[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.0f;
-  for (int slot = 0; row < a.M; row += step, slot ^= 1) {
-    const float rstd = load_f32(a.rstd + row), mean = a.mean ? load_f32(a.mean + row) : 0.0f;
-    const char* x = static_cast<const char*>(a.x) + row * K * (codes ? 1 : x_f32 ? 4 : 2);
-    const char* dy = static_cast<const char*>(a.y) + row * K * (dy_f32 ? 4 : 2);
-    float xh[N], g[N], w[N];
+  float dw[N], db[N], w[N];
+  uint32_t x[N], dy[N];
+  auto load = [&](int64_t at) {
+    const char* from = static_cast<const char*>(a.x) + at * K * (codes ? 1 : x_f32 ? 4 : 2);
     if (codes) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        xh[i] = 0.0f;
+        x[i] = 0u;
         if (column(i) >= K) continue;
         float lo, hi;
-        e4m3x2_to_f32(load_u8(x + column(i)), lo, hi);
-        xh[i] = __fmul_rn(lo, load_f32(a.x_scales + column(i) / kB128 * a.M + row));
+        e4m3x2_to_f32(load_u8(from + column(i)), lo, hi);
+        x[i] = __float_as_uint(__fmul_rn(lo, load_f32(a.x_scales + column(i) / kB128 * a.M + at)));
       }
     } else {
-      load_values(x, x_f32, K, column, xh);
+      load_values(from, x_f32, K, column, x);
     }
-    load_values(dy, dy_f32, K, column, g);
-    load_params(a.weight, w_f32, K, column, 1.0f, w);
-    float s1 = 0.0f, s2 = 0.0f;
+    load_values(static_cast<const char*>(a.y) + at * K * (dy_f32 ? 4 : 2), dy_f32, K, column, dy);
+  };
 #pragma unroll
-    for (int i = 0; i < N; ++i) {  // (g is 0 where there is no column)
-      xh[i] = (xh[i] - mean) * rstd;
+  for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.0f;
+  if constexpr (kKeep) {
+    if (row < a.M) load(row);
+    load_params(a.weight, w_f32, K, column, 1.0f, w);
+  }
+  for (int slot = 0; row < a.M; row += step, slot ^= 1) {
+    const float rstd = load_f32(a.rstd + row), mean = a.mean ? load_f32(a.mean + row) : 0.0f;
+    if constexpr (!kKeep) {
+      load(row);
+      load_params(a.weight, w_f32, K, column, 1.0f, w);
+    }
+    float xh[N], g[N], s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {  // (dy is 0 where there is no column)
+      xh[i] = (value_of(x[i], codes || x_f32) - mean) * rstd;
+      g[i] = value_of(dy[i], dy_f32);
       dw[i] = fmaf(g[i], xh[i], dw[i]);
       db[i] += g[i];
       g[i] *= w[i];
       s1 += g[i];
       s2 = fmaf(g[i], xh[i], s2);
+    }
+    if constexpr (kKeep) {
+      if (row + step < a.M) load(row + step);
     }
     row_sums(part, slot, group, W, s1, s2);
     s1 = a.mean ? s1 * per_k : 0.0f;
@@ -879,9 +911,13 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
   return a.K <= 512 ? run_norm<XF32, 2, 2, QUANT>(a, stream) : run_norm<XF32, 4, 2, QUANT>(a, stream);
 }
 
+// G rows of a CTA at once.
 cudaError_t run_any(void (*kernel)(NormArgs, int), const NormArgs& a, int W, cudaStream_t stream) {
-  const int G = W >= 8 ? 1 : 8 / W;
-  return launch_pdl(kernel, dim3((unsigned)((a.M + G - 1) / G)), dim3(32 * W * G), 0, stream, a, W);
+  const int G = W >= 16 ? 1 : 16 / W;
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), 32 * W * G, 0, 0);
+  if (slots <= 0) return cudaErrorInvalidConfiguration;
+  const int64_t ctas = (a.M + G - 1) / G;
+  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(32 * W * G), 0, stream, a, W);
 }
 
 template <bool XF32>
@@ -889,7 +925,7 @@ cudaError_t pick_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
   if (a.codes) return run_norm<XF32, true>(a, stream);
   if (vec) return run_norm<XF32, false>(a, stream);
   const int W = (int)((a.K + 511) / 512);
-  return run_any(W <= 8 ? &norm_any_kernel<XF32, 256> : &norm_any_kernel<XF32, 1024>, a, W, stream);
+  return run_any(W <= 16 ? &norm_any_kernel<XF32, 512> : &norm_any_kernel<XF32, 1024>, a, W, stream);
 }
 
 // `cols` columns of a row per warp; bytes of shared memory per thread of a group once, and per thread and stage.
