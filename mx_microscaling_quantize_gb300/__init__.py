@@ -800,13 +800,16 @@ _CHECKPOINT = 2  # MX_TYPE_E4M3_B128
 def _norm_params(weight, bias, K, like) -> int:
     """Checks weight and bias; returns their type."""
     kind = 1
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            if _tensor(t, name, _TYPES, dim=1, like=like).shape[0] != K:
-                raise ValueError(f"{name} must have one value per column")
-            kind = _TYPES[t.dtype]
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have the same type")
+    if weight is not None:
+        if _tensor(weight, "weight", _TYPES, dim=1, like=like).numel() != K:
+            raise ValueError("weight must have one value per column")
+        kind = _TYPES[weight.dtype]
+    if bias is not None:
+        if _tensor(bias, "bias", _TYPES, dim=1, like=like).numel() != K:
+            raise ValueError("bias must have one value per column")
+        if weight is not None and bias.dtype is not weight.dtype:
+            raise TypeError("weight and bias must have the same type")
+        kind = _TYPES[bias.dtype]
     return kind
 
 
@@ -894,10 +897,9 @@ def mx_layer_norm_backward(dy, x, mean, rstd, weight=None, *, x_scales=None, wei
         x_type = _CHECKPOINT
     if x.shape != dy.shape:
         raise ValueError("dy and x must be [M, K]")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if (t is not None or name == "rstd") and \
-                _tensor(t, name, torch.float32, dim=1, like=dy).shape[0] != M:
-            raise ValueError(f"{name} must have one value per row")
+    if _tensor(rstd, "rstd", torch.float32, dim=1, like=dy).numel() != M or \
+            mean is not None and _tensor(mean, "mean", torch.float32, dim=1, like=dy).numel() != M:
+        raise ValueError("mean and rstd must have one value per row")
     w_type = _norm_params(weight, None, K, dy)
     dtype = _out_type(out_dtype or (dy.dtype if x_type == _CHECKPOINT else x.dtype), dx)
     dx = _output(dx, "dx", (M, K), dtype, dy, stream)
