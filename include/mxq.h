@@ -472,7 +472,8 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
  * them (mean NULL: not centred). With xhat_i = (x_i - mean) rstd and g_i = dy_i weight_i:
  *   dx_i = rstd (g_i - sum g / K - xhat_i sum(g xhat) / K), the second term only when centred,
  *   dweight_i = sum over the rows of dy_i xhat_i,  dbias_i = sum over the rows of dy_i,
- * dx of dx_type, dweight and dbias fp32 [K] or NULL (not wanted; zeros when M == 0). Sums in fp32, in an
+ * dx of dx_type, dweight and dbias fp32 [K] or NULL (not wanted; zeros when M == 0). A checkpoint's value
+ * may be rounded with what is done to it (code * (scale rstd) - mean rstd), not on its own first. Sums in fp32, in an
  * order that the sizes and the device alone decide. workspace: device memory of
  * mx_layer_norm_backward_workspace() bytes, 4-byte aligned (NULL will do without dweight and dbias); two
  * calls that may run at the same time need one each. Alignment: that of the elements; dy, x and dx on 16

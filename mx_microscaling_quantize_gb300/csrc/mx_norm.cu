@@ -550,7 +550,10 @@ struct NormRing {
       bulk_copy(dy_at(stage), static_cast<const char*>(a.y) + row * dyb, dyb, bar);
     }
   }
-  __device__ __forceinline__ void read(int stage, int c, uint64_t* x, uint64_t* dy) const {
+  // A run of x and its dy. Of a checkpoint not its values but (code scale rstd) f + less in one operation, with f
+  // and less of the row: a value is rounded with what is done to it, not on its own.
+  __device__ __forceinline__ void read(int stage, int c, float rstd, float f, uint64_t less, uint64_t* x,
+                                       uint64_t* dy) const {
     if constexpr (XT == kTypeB128) {
       uint32_t lo, hi;
       float s;
@@ -558,9 +561,9 @@ struct NormRing {
       asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(scale_at(stage) + col / kB128 * 4 + c * 8));
       values4(lo, x[0], x[1]);
       values4(hi, x[2], x[3]);
-      // (not packed: ptxas joins a packed product and the sum after it, and with it two roundings)
+      const uint64_t by = pair(s * rstd * f);  // (rstd f, or rstd^2, may be beyond fp32 where this is not)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = pair(__fmul_rn(lo_of(x[j]), s), __fmul_rn(hi_of(x[j]), s));
+      for (int j = 0; j < 4; ++j) x[j] = fma_pair(x[j], by, less);
     } else {
       read8<XT == kTypeFp32>(x_at(stage) + (col + c * 256) * (kX / 8), x);
     }
@@ -669,8 +672,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   }
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
     const int stage = rows.stage;
-    const float rstd = rstd_next;
-    const uint64_t minus = pair(-mean_next), r2 = pair(rstd);
+    constexpr bool kFold = XT == kTypeB128;
+    const float rstd = rstd_next, mean = mean_next;
+    const uint64_t minus = pair(-mean), r2 = pair(rstd), less = pair(-mean * rstd);
     if (row + step < a.M) {
       rstd_next = load_f32(a.rstd + row + step);
       if (a.mean) mean_next = load_f32(a.mean + row + step);
@@ -681,11 +685,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     for (int c = 0; c < C; ++c) {
       if (!there(c)) continue;
       uint64_t x[4], y[4], w[4];
-      ring.read(stage, c, x, y);
+      ring.read(stage, c, rstd, 1.0f, less, x, y);
       Param::read(w_at, c, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[j] = mul_pair(add_pair(x[j], minus), r2);
+        if constexpr (!kFold) x[j] = mul_pair(add_pair(x[j], minus), r2);
         dw[c][j] = fma_pair(y[j], x[j], dw[c][j]);
         db[c][j] = add_pair(db[c][j], y[j]);
         y[j] = mul_pair(y[j], w[j]);
@@ -697,19 +701,20 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     row_sums(part, slot, group, W, s1, s2);
     // all of the group have read the row before this one for the last time
     if (S > 1) ring.request(a, rows, row + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);
-    // dx = rstd g - rstd s1 - (x - mean) rstd^2 s2
-    const uint64_t m1 = pair(a.mean ? -s1 * per_k * rstd : 0.0f), m2 = pair(-s2 * per_k * rstd * rstd);
+    // dx = rstd g - rstd s1 - xhat rstd s2
+    const float c0 = a.mean ? -s1 * per_k * rstd : 0.0f, cx = -s2 * per_k * rstd;
+    const uint64_t m1 = pair(c0), m2 = pair(cx), rest = pair(fmaf(lo_of(less), cx, c0));
     const int64_t at = row * K + col;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (!there(c)) continue;
       uint64_t x[4], y[4], w[4];
-      ring.read(stage, c, x, y);
+      ring.read(stage, c, rstd, cx, rest, x, y);
       Param::read(w_at, c, w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        x[j] = add_pair(x[j], minus);
-        y[j] = fma_pair(mul_pair(y[j], w[j]), r2, fma_pair(x[j], m2, m1));
+        if constexpr (!kFold) x[j] = fma_pair(mul_pair(add_pair(x[j], minus), r2), m2, m1);
+        y[j] = fma_pair(mul_pair(y[j], w[j]), r2, x[j]);
       }
       uint32_t o[8];
       if (dx_f32) {

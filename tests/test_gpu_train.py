@@ -138,7 +138,7 @@ def test_layer_norm_backward_from_checkpoint(M, K, dy_type, dx_type, center):
                                                                  checkpoint=True)
     dx, dw, db = mxq.mx_layer_norm_backward(dy, kept, mean, rstd, w, x_scales=kept_scales, out_dtype=dx_type)
     v = T.values(cpu(kept), cpu(kept_scales)).astype(np.float64)
-    want = T.norm_backward(T.f64(dy), v, either(mean), T.f64(rstd), T.f64(w), center)
+    want = T.norm_backward(T.f64(dy), v, either(mean), T.f64(rstd), T.f64(w), center, checkpoint=True)
     T.check_values(dx, want[0], want[3], dx_type, "dx")
     T.check_values(dw, want[1], want[4], FP32, "dw")
     T.check_values(db, want[2], want[5], FP32, "db")

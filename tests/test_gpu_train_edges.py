@@ -74,7 +74,7 @@ def test_norm_backward_of_bases_that_allow_no_wide_loads(M, K, which, checkpoint
         if which in (name, "all"):
             args[name] = off_base(args[name])
     dx, dw, db = mxq.mx_layer_norm_backward(args["dy"], args["x"], mean, rstd, args["w"], dx=args["dx"], **kw)
-    want = T.norm_backward(T.f64(dy), v, T.f64(mean), T.f64(rstd), T.f64(w), True)
+    want = T.norm_backward(T.f64(dy), v, T.f64(mean), T.f64(rstd), T.f64(w), True, checkpoint=checkpoint)
     T.check_values(dx, want[0], want[3], BF16, "dx")
     T.check_values(dw, want[1], want[4], FP32, "dw")
     T.check_values(db, want[2], want[5], FP32, "db")

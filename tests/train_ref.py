@@ -58,8 +58,13 @@ def norm(x, w, b, eps, center):
     return y + b, mean, rstd, tol
 
 
-def norm_backward(dy, x, mean, rstd, w, center):
-    """-> dx, dw, db and the bounds of each before rounding. mean, rstd: what the kernel was given."""
+def norm_backward(dy, x, mean, rstd, w, center, checkpoint=False):
+    """-> dx, dw, db and the bounds of each before rounding. mean, rstd: what the kernel was given.
+
+    checkpoint: x is of products code * scale, rounded here, that the kernel may fold into xhat =
+    fma(code, scale * rstd, -(mean * rstd)) and (code, scale * c, -mean c + ..) in dx, c = s2 rstd^2: beside the
+    rounding of x (U |x|) those of scale * rstd, of mean * rstd and of their sum, each at most U (|x| + |mean|)
+    rstd, so that xhat is off by at most 4 U (|x| + |mean|) rstd more."""
     M, K = x.shape
     w = np.ones(K) if w is None else w
     mean = np.zeros(M) if mean is None else mean
@@ -73,7 +78,12 @@ def norm_backward(dy, x, mean, rstd, w, center):
     a2 = np.abs(g * xh).mean(1, keepdims=True)
     tol = DEPTH * U * r * (np.abs(g) + a1 + np.abs(xh) * a2)
     rows = (M + DEPTH) * U
-    return dx, (dy * xh).sum(0), dy.sum(0), tol, rows * np.abs(dy * xh).sum(0), rows * np.abs(dy).sum(0)
+    tol_w = rows * np.abs(dy * xh).sum(0)
+    if checkpoint:  # what xhat is off by more, in its own place, in s2 and in the weight's gradient
+        off = 4 * U * (np.abs(x) + np.abs(mean)[:, None]) * r
+        tol = tol + r * (off * np.abs(s2) + np.abs(xh) * (np.abs(g) * off).mean(1, keepdims=True))
+        tol_w = tol_w + (np.abs(dy) * off).sum(0)
+    return dx, (dy * xh).sum(0), dy.sum(0), tol, tol_w, rows * np.abs(dy).sum(0)
 
 
 # ---------------------------------------------------------------------------------------------
