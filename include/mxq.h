@@ -450,7 +450,7 @@ mx_status mx_combine_backward_whole(const void* dout, const void* y, const int32
  *   rstd = 1 / sqrt(sum_i (x_i - mean)^2 / K + eps),  y_i = (x_i - mean) rstd weight_i + bias_i.
  * In fp32, the variance from the differences to the mean; y rounded once. weight, bias: [K] of w_type,
  * NULL for ones and zeros (w_type is then not used, but must be valid). mean, rstd: fp32 [M] or NULL,
- * what mx_layer_norm_backward takes. K <= 16384.
+ * what mx_layer_norm_backward takes (zeros when K == 0). K <= 16384.
  *
  * mx_layer_norm: y [M, K] of y_type. Alignment: that of the elements; all four on 32 bytes with
  *   K % 8 == 0 take wide loads.
@@ -473,8 +473,9 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
  *   dx_i = rstd (g_i - sum g / K - xhat_i sum(g xhat) / K), the second term only when centred,
  *   dweight_i = sum over the rows of dy_i xhat_i,  dbias_i = sum over the rows of dy_i,
  * dx of dx_type, dweight and dbias fp32 [K] or NULL (not wanted; zeros when M == 0). A checkpoint's value
- * may be rounded with what is done to it (code * (scale rstd) - mean rstd), not on its own first. Sums in fp32, in an
- * order that the sizes and the device alone decide. workspace: device memory of
+ * may be rounded with what is done to it (code * (scale rstd) - mean rstd), not on its own first; mean rstd
+ * must then be finite in fp32. Sums in fp32, in an order that the sizes, types, alignment and device alone
+ * decide. workspace: device memory of
  * mx_layer_norm_backward_workspace() bytes, 4-byte aligned (NULL will do without dweight and dbias); two
  * calls that may run at the same time need one each. Alignment: that of the elements; dy, x and dx on 16
  * bytes and weight on 32 with K % 8 == 0 take wide loads. dx must not overlap the inputs.

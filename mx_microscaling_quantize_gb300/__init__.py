@@ -911,8 +911,9 @@ def mx_layer_norm_backward(dy, x, mean, rstd, weight=None, *, x_scales=None, wei
         need = mx_layer_norm_backward_workspace(M, K)
         if workspace is None:
             workspace = _empty((need,), torch.uint8, dy, stream, scratch=True)
-        elif workspace.device != dy.device or workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"workspace must have {need} bytes on {dy.device}")
+        elif workspace.device != dy.device or not workspace.is_contiguous() or \
+                workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace must have {need} contiguous bytes on {dy.device}")
     _check(lib().mx_layer_norm_backward(_ptr(dy), _TYPES[dy.dtype], _ptr(x), x_type, _ptr(x_scales),
                                         _ptr(mean), _ptr(rstd), _ptr(weight), w_type, M, K, _ptr(dx),
                                         _TYPES[dtype], _ptr(dweight), _ptr(dbias), _ptr(workspace),

@@ -22,10 +22,11 @@ namespace {
 constexpr int kMaxParts = 304;  // of the weight's gradient: rows are split over at most so many CTAs
 constexpr int kNormThreads = 512, kMaxStages = 4;  // of a CTA
 constexpr int kNormSmem = 224 * 1024;  // of a CTA, dynamic
-constexpr int kMaxGroups = 15;         // of several warps: a barrier each, beside the CTA's
 constexpr unsigned long long kNormDrainNs = 2000000000ull;  // 2 s, whatever the limit of other waits
 
-// Barrier of one group of warps: of several warps barrier group + 1 (there are 16), of one warp the warp's.
+// Barrier of one group of warps: of several warps barrier group + 1 (there are 16, the CTA's among them), of one
+// warp the warp's.
+static_assert(kNormThreads / 64 <= 15, "groups of several warps have a barrier each");
 __device__ __forceinline__ void group_sync(int group, int threads) {
   if (threads == 32) {
     __syncwarp();
@@ -881,7 +882,6 @@ struct Groups {
 };
 Groups fit_groups(int most, int W, size_t fixed, size_t stage) {
   Groups g{most / 32 / W, 0, 0};
-  if (W > 1 && g.count > kMaxGroups) g.count = kMaxGroups;
   while (g.count > 1 && fixed + g.count * stage > kNormSmem) --g.count;
   if (fixed + g.count * stage > kNormSmem) return Groups{0, 0, 0};
   g.stages = stage ? (int)((kNormSmem - fixed) / (g.count * stage)) : 0;

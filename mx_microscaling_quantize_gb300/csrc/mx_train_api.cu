@@ -43,6 +43,15 @@ mx_status run_norm(cudaError_t (*launch)(const mxq::NormArgs&, cudaStream_t), mx
   });
 }
 
+// fp32 results of a call whose sums are empty: n zeros in each of a and b (or null)
+mx_status zeros(float* a, float* b, int64_t n, void* stream) {
+  cudaError_t err = cudaSuccess;
+  if (n == 0) return MX_OK;
+  if (a) err = cudaMemsetAsync(a, 0, (size_t)n * 4, as_stream(stream));
+  if (b && err == cudaSuccess) err = cudaMemsetAsync(b, 0, (size_t)n * 4, as_stream(stream));
+  return err == cudaSuccess ? MX_OK : MX_ERR_CUDA;
+}
+
 mx_status check_norm(int64_t M, int64_t K) {
   return sizes_ok(M, K) && K <= mxq::kNormMaxCols ? MX_OK : MX_ERR_SHAPE;
 }
@@ -53,10 +62,11 @@ mx_status layer_norm(const void* x, int x_type, const void* weight, const void* 
   const mx_status st = check_norm(M, K);
   if (st != MX_OK) return st;
   if (!float_type(x_type) || !float_type(w_type) || !float_type(y_type)) return MX_ERR_UNSUPPORTED;
-  if (M == 0 || K == 0) return MX_OK;
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return MX_ERR_ALIGN;
+  if (M == 0 || K == 0) return zeros(mean, rstd, M, stream);
   if (!x || !y) return MX_ERR_NULL;
   if (!aligned(x, size_of(x_type)) || !aligned(y, size_of(y_type)) || !aligned(weight, size_of(w_type)) ||
-      !aligned(bias, size_of(w_type)) || !aligned(mean, 4) || !aligned(rstd, 4)) {
+      !aligned(bias, size_of(w_type))) {
     return MX_ERR_ALIGN;
   }
   mxq::NormArgs a{};
@@ -89,12 +99,7 @@ mx_status layer_norm_backward(const void* dy, int dy_type, const void* x, int x_
   if (x_type == MX_TYPE_E4M3_B128 && K % 32 != 0) return MX_ERR_SHAPE;
   if (K == 0) return MX_OK;
   if (!aligned(dweight, 4) || !aligned(dbias, 4)) return MX_ERR_ALIGN;
-  if (M == 0) {  // sums over no rows
-    cudaError_t err = cudaSuccess;
-    if (dweight) err = cudaMemsetAsync(dweight, 0, (size_t)K * 4, as_stream(stream));
-    if (dbias && err == cudaSuccess) err = cudaMemsetAsync(dbias, 0, (size_t)K * 4, as_stream(stream));
-    return err == cudaSuccess ? MX_OK : MX_ERR_CUDA;
-  }
+  if (M == 0) return zeros(dweight, dbias, K, stream);
   if (!dy || !x || !rstd || !dx || (x_type == MX_TYPE_E4M3_B128 && !x_scales)) return MX_ERR_NULL;
   if ((dweight || dbias) && !workspace) return MX_ERR_NULL;
   if (!aligned(dy, size_of(dy_type)) || !aligned(x, size_of(x_type)) || !aligned(dx, size_of(dx_type)) ||
@@ -154,11 +159,11 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
   if (st != MX_OK) return st;
   if (K % 32 != 0) return MX_ERR_SHAPE;
   if (!float_type(x_type) || !float_type(w_type)) return MX_ERR_UNSUPPORTED;
-  if (M == 0 || K == 0) return MX_OK;
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return MX_ERR_ALIGN;
+  if (M == 0 || K == 0) return zeros(mean, rstd, M, stream);
   if (!x || !codes || !scales || (x_codes == nullptr) != (x_scales == nullptr)) return MX_ERR_NULL;
   if (!aligned(x, 32) || !aligned(codes, 32) || !aligned(scales, 4) || !aligned(x_codes, 32) ||
-      !aligned(x_scales, 4) || !aligned(weight, 32) || !aligned(bias, 32) || !aligned(mean, 4) ||
-      !aligned(rstd, 4)) {
+      !aligned(x_scales, 4) || !aligned(weight, 32) || !aligned(bias, 32)) {
     return MX_ERR_ALIGN;
   }
   mxq::NormArgs a{};

@@ -196,6 +196,27 @@ def test_norm_of_no_rows_and_no_columns():
     assert mxq.mx_layer_norm_backward(none, none, mean, rstd)[0].shape == (3, 0)
 
 
+def test_norm_statistics_of_rows_without_columns_are_zeros():
+    none = torch.empty(3, 0, device="cuda")
+    for norm in (mxq.mx_layer_norm, mxq.mx_layer_norm_b128):
+        mean, rstd = torch.full((3,), 7.0, device="cuda"), torch.full((3,), 7.0, device="cuda")
+        norm(none, mean=mean, rstd=rstd)
+        assert not mean.any() and not rstd.any()
+
+
+def test_norm_backward_refuses_a_workspace_that_is_shorter_than_it_looks():
+    x = torch.zeros(4, 64, dtype=BF16, device="cuda")
+    mean, rstd = torch.zeros(4, device="cuda"), torch.ones(4, device="cuda")
+    need = mxq.mx_layer_norm_backward_workspace(4, 64)
+    for bad in (torch.zeros(1, device="cuda").expand(need), torch.zeros(need // 4 - 1, device="cuda"),
+                torch.zeros(need, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            mxq.mx_layer_norm_backward(x, x, mean, rstd, workspace=bad)
+    with pytest.raises(mxq.MXError):
+        mxq.mx_layer_norm_backward(x, x, mean, rstd,
+                                   workspace=torch.zeros(need + 1, dtype=torch.uint8, device="cuda")[1:])
+
+
 def test_norm_writes_nothing_beside_its_outputs():
     M, K = 7, 1000
     x = rows(1, M, K, BF16)
