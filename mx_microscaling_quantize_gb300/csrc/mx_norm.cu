@@ -635,8 +635,10 @@ __device__ __forceinline__ void join_shares(const NormArgs& a, const float* sm, 
 // adds up. Groups of W warps walk rows, their sums of dw and db in registers, the next rows on their way into
 // the group's stages, the weights in shared memory. A row is read from its stage twice, for the sums over it
 // and for dx: dw and db leave no registers to keep it in. Two groups and more work beside each other up to
-// 8192 columns, one while the other waits for its sums. FULL: K is a multiple of a warp's 1024 columns.
-template <int XT, bool DYF32, bool FULL>
+// 8192 columns, one while the other waits for its sums. MODE: K is a multiple of a warp's 1024 columns or not, or
+// of any such K no more rows than CTAs, whose dw and db are their shares as they are.
+constexpr int kAnyCols = 0, kFullCols = 1, kSingleRows = 2;
+template <int XT, bool DYF32, int MODE>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs a, int W, int S) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
   using Ring = NormRing<XT, DYF32>;
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   __syncthreads();
   const bool dx_f32 = a.dx_type == kTypeFp32;
   const float per_k = __fdiv_rn(1.0f, (float)K);
-  auto there = [&](int c) { return FULL || col + c * 256 < K; };
+  auto there = [&](int c) { return MODE == kFullCols || col + c * 256 < K; };
 
   uint64_t dw[C][4], db[C][4];
 #pragma unroll
@@ -740,7 +742,33 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   }
   if (XT == kTypeB128) asm volatile("cp.async.wait_all;" ::: "memory");  // scales asked for after a give-up
   if (!a.dweight && !a.dbias) return;
-  // through shared memory in any case: a lane's runs of 8 columns would leave as many partial lines
+  if constexpr (MODE == kSingleRows) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float* to = share(a, k);
+      if (!to) continue;
+      const bool wide = (reinterpret_cast<uintptr_t>(to) & 31) == 0;
+      to += col;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (!there(c)) continue;
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o[2 * j] = __float_as_uint(lo_of(k ? db[c][j] : dw[c][j]));
+          o[2 * j + 1] = __float_as_uint(hi_of(k ? db[c][j] : dw[c][j]));
+        }
+        if (wide) {
+          store32B(to + c * 256, o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) to[c * 256 + j] = __uint_as_float(o[j]);
+        }
+      }
+    }
+    return;
+  }
+  // through shared memory, one group too: beside the loop's registers there is no room for another way
   const int groups = blockDim.x / T;
   __syncthreads();
 #pragma unroll
@@ -890,6 +918,13 @@ Groups fit_groups(int most, int W, size_t fixed, size_t stage) {
   return g;
 }
 
+// Few rows go to as many CTAs as there are: `count` groups of a CTA, or as many as M rows need at `slots` a round
+// (64 rows of 1024 into codes 4.7 -> 3.2 us, of 8192 5.1 -> 4.0; gradients 8.0 -> 5.0 and 9.7 -> 7.7).
+int spread(int count, int64_t M, int64_t slots) {
+  const int64_t need = (M + slots - 1) / slots;
+  return need < count ? (int)need : count;
+}
+
 template <bool XF32, int P, int R, bool QUANT>
 cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
   const int W = (int)((a.K + P * 256 - 1) / (P * 256));
@@ -902,12 +937,12 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
     if (!g.count) return run_norm<XF32, P, 1, QUANT>(a, stream);
   }
   if (!g.count) return cudaErrorInvalidConfiguration;
-  const int threads = 32 * W * g.count;
-  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, g.smem, 1);
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), 32 * W * g.count, g.smem, 1);
   if (slots <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t ctas = (a.M + g.count * R - 1) / (g.count * R);
-  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(threads), g.smem, stream, a, W,
-                    g.stages);
+  const int count = spread(g.count, a.M, R * slots);
+  const int64_t ctas = (a.M + count * R - 1) / (count * R);
+  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(32 * W * count), g.smem, stream, a,
+                    W, g.stages);
 }
 // Rows of up to 512 columns are one warp's with one or two runs per lane; longer ones a group's with four.
 template <bool XF32, bool QUANT>
@@ -934,21 +969,27 @@ cudaError_t pick_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
 }
 
 // `cols` columns of a row per warp; bytes of shared memory per thread of a group once, and per thread and stage.
-cudaError_t run_backward(void (*kernel)(NormArgs, int, int), int fixed, int stage, const NormArgs& a, int cols,
-                         cudaStream_t stream) {
+// single: the kernel for no more rows than CTAs, or null.
+using BackwardKernel = void (*)(NormArgs, int, int);
+cudaError_t run_backward(BackwardKernel kernel, BackwardKernel single, int fixed, int stage, const NormArgs& a,
+                         int cols, cudaStream_t stream) {
   const int W = (int)((a.K + cols - 1) / cols);
   Groups g = fit_groups(kNormThreads, W, (size_t)fixed * 32 * W, (size_t)stage * 32 * W);
   if (!g.count) return cudaErrorInvalidConfiguration;
-  const int threads = 32 * W * g.count;
   const bool params = a.dweight || a.dbias;
   if (params && g.smem < (size_t)g.count * a.K * 8) g.smem = (size_t)g.count * a.K * 8;  // the groups' shares
-  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), threads, g.smem, 1);
+  int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), 32 * W * g.count, g.smem, 1);
+  if (single && a.M <= slots) {
+    kernel = single;
+    slots = resident_ctas(reinterpret_cast<const void*>(kernel), 32 * W * g.count, g.smem, 1);
+  }
   if (slots <= 0) return cudaErrorInvalidConfiguration;
-  int64_t ctas = (a.M + g.count - 1) / g.count;
+  const int count = spread(g.count, a.M, slots);
+  int64_t ctas = (a.M + count - 1) / count;
   if (ctas > slots) ctas = slots;
   if (params && ctas > kMaxParts) ctas = kMaxParts;
   const cudaError_t err =
-      launch_pdl(kernel, dim3((unsigned)ctas), dim3(threads), g.smem, stream, a, W, g.stages);
+      launch_pdl(kernel, dim3((unsigned)ctas), dim3(32 * W * count), g.smem, stream, a, W, g.stages);
   if (err != cudaSuccess || !params || ctas == 1) return err;
   return launch_pdl(&norm_reduce_kernel, dim3((unsigned)((a.K + 31) / 32), 2), dim3(512), 0, stream, a,
                     (int)ctas);
@@ -957,8 +998,9 @@ cudaError_t run_backward(void (*kernel)(NormArgs, int, int), int fixed, int stag
 template <int XT, bool DYF32>
 cudaError_t run_ring(const NormArgs& a, cudaStream_t stream) {
   using Ring = NormRing<XT, DYF32>;
-  return run_backward(a.K % 1024 == 0 ? &norm_backward_kernel<XT, DYF32, true> : &norm_backward_kernel<XT, DYF32, false>,
-                      Ring::kWeights, Ring::kStage, a, 1024, stream);
+  return run_backward(a.K % 1024 == 0 ? &norm_backward_kernel<XT, DYF32, kFullCols>
+                                      : &norm_backward_kernel<XT, DYF32, kAnyCols>,
+                      &norm_backward_kernel<XT, DYF32, kSingleRows>, Ring::kWeights, Ring::kStage, a, 1024, stream);
 }
 
 cudaError_t pick_ring(const NormArgs& a, cudaStream_t stream) {
@@ -986,8 +1028,8 @@ cudaError_t launch_norm_backward(const NormArgs& a, cudaStream_t stream) {
   const bool vec = a.K % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) && aligned_to(a.dx, 16) &&
                    aligned_to(a.weight, 32);
   if (vec) return pick_ring(a, stream);
-  return a.K <= 8192 ? run_backward(&norm_backward_any_kernel<16>, 0, 0, a, 512, stream)
-                     : run_backward(&norm_backward_any_kernel<32>, 0, 0, a, 1024, stream);
+  return a.K <= 8192 ? run_backward(&norm_backward_any_kernel<16>, nullptr, 0, 0, a, 512, stream)
+                     : run_backward(&norm_backward_any_kernel<32>, nullptr, 0, 0, a, 1024, stream);
 }
 
 }  // namespace mxq

@@ -80,6 +80,28 @@ def test_norm_backward_of_bases_that_allow_no_wide_loads(M, K, which, checkpoint
     T.check_values(db, want[2], want[5], FP32, "db")
 
 
+@pytest.mark.parametrize("M", [1, 2, 152, 153, 160, 305])
+@pytest.mark.parametrize("K", [40, 1024, 2080, 9000])
+def test_norm_parameter_gradients_at_any_base(M, K):
+    """Few rows leave their shares of dw and db as they are, more of them go through the groups' sums."""
+    x, dy = rows(M + K, M, K, BF16), rows(M * 5 + K, M, K, BF16, 0.0)
+    w, _ = params(K, K, FP32)
+    _, mean, rstd = mxq.mx_layer_norm(x, w, None, stats=True)
+    want = T.norm_backward(T.f64(dy), T.f64(x), T.f64(mean), T.f64(rstd), T.f64(w), True)
+    need = mxq.mx_layer_norm_backward_workspace(M, K)
+    guarded = [torch.full((n + 16,), -3.0, device="cuda") for n in (K, K, need // 4)]
+    for at in (0, 1, 4, 8):
+        dw, db, ws = (g[at:at + n] for g, n in zip(guarded, (K, K, need // 4)))
+        mxq.mx_layer_norm_backward(dy, x, mean, rstd, w, dweight=dw, dbias=db, workspace=ws)
+        T.check_values(dw, want[1], want[4], FP32, "dw")
+        T.check_values(db, want[2], want[5], FP32, "db")
+        for g, n in zip(guarded, (K, K, need // 4)):
+            assert (g[:at] == -3).all() and (g[at + n:] == -3).all()
+            g.fill_(-3.0)
+        only = mxq.mx_layer_norm_backward(dy, x, mean, rstd, w, weight_grad=False)
+        assert only[1] is None and same(only[2], mxq.mx_layer_norm_backward(dy, x, mean, rstd, w)[2])
+
+
 @pytest.mark.parametrize("K", [96, 1024, 1111, 8192])
 @pytest.mark.parametrize("x_type", [BF16, FP32])
 def test_norm_of_large_means(K, x_type):
