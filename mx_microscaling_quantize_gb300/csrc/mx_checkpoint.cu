@@ -10,7 +10,8 @@ namespace mxq {
 
 namespace {
 
-// A lane's 16 codes of a row times their block's scale: 17 bytes read, 32 or 64 written. Bound by memory.
+// A lane's 16 codes of a row times their block's scale: 17 bytes read, 32 or 64 written. Bound by memory:
+// 8192 x 8192 into bf16 31.5 us (30.4 at the rate of a plain copy), into fp32 49.5.
 template <bool F32>
 __global__ void __launch_bounds__(256) b128_dequant_kernel(DequantB128Args a, int64_t chunks, int64_t items) {
   pdl_launch_dependents();
