@@ -120,23 +120,23 @@ __device__ __forceinline__ uint32_t absmax_pairs(const uint64_t* v) {
   return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
-// Maxima of N values of each lane over runs of 2^STEPS lanes, N of them, found by halves: the first steps
-// exchange half of the values that are left and keep the other half, so log2 N of them give each lane one
+// Maxima of N values of each lane over 2^STEPS lanes (those that differ in STEPS bits, the lowest of them bit
+// LOW), N of them, found by halves: the first steps exchange half of the values that are left and keep the other half, so log2 N of them give each lane one
 // value, index (its highest log2 N bits of STEPS). take gives a lane any of the N from the lane that has it.
-template <int N, int STEPS>
+template <int N, int STEPS, int LOW = 0>
 struct RunMax {
   static constexpr int kHalvings = N == 8 ? 3 : N == 4 ? 2 : N == 2 ? 1 : 0;
   static_assert(N == 1 || N == 2 || N == 4 || N == 8, "values of a lane");
   static_assert(kHalvings <= STEPS, "more values than lanes");
 
   int lane;
-  __device__ __forceinline__ int index() const { return (lane & ((1 << STEPS) - 1)) >> (STEPS - kHalvings); }
+  __device__ __forceinline__ int index() const { return (lane >> LOW & ((1 << STEPS) - 1)) >> (STEPS - kHalvings); }
   // whether this lane is the first that has its value
-  __device__ __forceinline__ bool first() const { return (lane & ((1 << (STEPS - kHalvings)) - 1)) == 0; }
+  __device__ __forceinline__ bool first() const { return (lane >> LOW & ((1 << (STEPS - kHalvings)) - 1)) == 0; }
   __device__ __forceinline__ uint32_t reduce(uint32_t (&m)[N]) const {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const int d = 1 << (STEPS - 1 - s), left = N >> (s + 1);
+      const int d = 1 << (LOW + STEPS - 1 - s), left = N >> (s + 1);
       if (s < kHalvings) {
         const bool high = lane & d;
 #pragma unroll
@@ -151,7 +151,7 @@ struct RunMax {
     return m[0];
   }
   __device__ __forceinline__ float take(float v, int j) const {
-    return __shfl_sync(0xFFFFFFFFu, v, (lane & ~((1 << STEPS) - 1)) | j << (STEPS - kHalvings));
+    return __shfl_sync(0xFFFFFFFFu, v, (lane & ~(((1 << STEPS) - 1) << LOW)) | j << (LOW + STEPS - kHalvings));
   }
 };
 

@@ -317,11 +317,15 @@ __global__ void __launch_bounds__(kTileThreads, 4) b128_cols_kernel(B128QuantArg
 // v = code * scale in fp32): a checkpoint's way into the weights' gradient, at half of the bytes that bf16
 // rows take. A tile is 128 rows of one block of their scales, copied to shared memory kRecolStages - 1 tiles
 // ahead (16-byte pieces, those of row r at places permuted by r / 8; missing rows are filled with zeros).
-// A warp makes 16 columns of it alone: lane (q, h) holds rows 8 q .. and columns 8 h .. of these as fp32, the
-// columns' abs-maxes are reduced over the 16 lanes q, and the codes leave through 2 KB of the warp's own. One barrier a
-// tile, for the copies of the other threads. 8192 x 8192 26.9 us (20.7 at the rate of a plain copy; from bf16
-// 31), 16384 rows gathered for 128 experts 23.7: 8.5 instructions for a value, issued in 60 % of the cycles by 16
-// warps of 108 registers. Three CTAs of 80 registers, lanes of 4 rows in two halves, took 31.8 and 26.7.
+// A warp makes 16 columns of it alone: lane (q, h) = (lane / 2, lane % 2) holds rows 8 q .. and columns 8 h .. of
+// these as fp32 (16 lanes of a read meet every bank once; with q in the low bits two rows shared theirs: 26.8 ->
+// 26.0 us), the columns' abs-maxes are reduced over the 16 lanes q, and the codes leave through 2 KB of the warp's
+// own (the 64-byte halves of columns 8 .. changed over, for the banks). One barrier a tile, for the copies of the
+// other threads.
+// 8192 x 8192 26.0 us (20.7 at the rate of a plain copy; from bf16 31), 16384 rows gathered for 128 experts 22.7:
+// 8.7 instructions for a value, issued in 60 % of the cycles by 16 warps of 108 registers. More warps of fewer
+// registers were slower: three CTAs an SM with lanes of 4 rows 31.8 and 26.7, with columns in two halves 28.6 and
+// 26.7, four CTAs of those 29.2 and 27.1.
 constexpr int kRecolThreads = 256, kRecolStages = 4;
 struct RecolsShared {
   uint4 in[kRecolStages][128 * 8];
@@ -336,8 +340,8 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
   RecolsShared& s = *reinterpret_cast<RecolsShared*>(recols_shared);
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane & 15, h = lane >> 4;
-  const RunMax<8, 4> max_of{lane};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q = lane >> 1, h = lane & 1;
+  const RunMax<8, 4, 1> max_of{lane};
   int64_t blocks = a.blocks;
   if (a.offsets) {
     for (int e = tid; e <= a.E; e += kRecolThreads) {
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
       uint64_t u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = mul_pair(v[i][j / 2], r);
-      uint8_t* to = out + (h * 8 + j) * 128 + q * 8;
+      uint8_t* to = out + (h * 8 + j) * 128 + (q * 8 ^ h * 64);
       *reinterpret_cast<uint2*>(to) = make_uint2(codes4(lo_of(u[0]), lo_of(u[1]), lo_of(u[2]), lo_of(u[3])),
                                                  codes4(lo_of(u[4]), lo_of(u[5]), lo_of(u[6]), lo_of(u[7])));
       *reinterpret_cast<uint2*>(to + 128) =
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(kRecolThreads, 2) b128_recols_kernel(B128Quant
     uint8_t* dst = a.codes + (c0 + (lane >> 3)) * pitch + b * kB128 + (lane & 7) * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 w = s.out[warp][i * 32 + lane];
+      const uint4 w = s.out[warp][i * 32 + (i < 2 ? lane : lane ^ 4)];
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
       if (c0 + i * 4 + (lane >> 3) < K) store16B(dst + i * 4 * pitch, u);
     }
