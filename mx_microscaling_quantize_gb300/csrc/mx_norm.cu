@@ -262,18 +262,20 @@ __device__ __forceinline__ void store_stats(const NormArgs& a, int64_t row, floa
 
 // R rows from `row` on, P runs of 8 columns per lane and row, 256 apart from col on, as codes with their
 // blocks' scales.
-template <int R, int P>
+template <int R, int P, bool FULL>
 __device__ __forceinline__ void store_codes(const uint64_t (&v)[R * P][4], int lane, uint8_t* codes, float* scales,
                                             int64_t M, int K, int64_t row, int col) {
+  const bool second = row + 1 < M;
+  uint8_t* to = codes + row * K + col;
   run_codes<R * P>(
       v, lane,
       [&](int n, uint32_t lo, uint32_t hi) {
         const int p = n % P, r = n / P;
-        if (col + p * 256 < K && row + r < M) store8B(codes + (row + r) * K + col + p * 256, lo, hi);
+        if ((FULL || col + p * 256 < K) && (r == 0 || second)) store8B(to + r * K + p * 256, lo, hi);
       },
       [&](int n, float scale) {
         const int p = n % P, r = n / P, kb = (col + p * 256) / kB128;
-        if (kb * kB128 < K && row + r < M) scales[kb * M + row + r] = scale;
+        if ((FULL || kb * kB128 < K) && (r == 0 || second)) scales[kb * M + row + r] = scale;
       });
 }
 
@@ -359,9 +361,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
     float mean[R], sq[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      uint64_t s[2] = {0u, 0u};
+      uint64_t s[2] = {x[r * P][0], x[r * P][1]};
 #pragma unroll
-      for (int i = 0; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[r * P + i / 4][i % 4]);
+      for (int i = 2; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[r * P + i / 4][i % 4]);
       s[0] = add_pair(s[0], s[1]);
       mean[r] = lo_of(s[0]) + hi_of(s[0]);
     }
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
     request(row + S * step, rows.stage);
     rows.next();
     if constexpr (QUANT) {
-      if (a.x_codes) store_codes<R, P>(x, lane, a.x_codes, a.x_scales_out, a.M, K, row, col);
+      if (a.x_codes) store_codes<R, P, FULL>(x, lane, a.x_codes, a.x_scales_out, a.M, K, row, col);
     }
     uint64_t minus[R], r2[R];
 #pragma unroll
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
         }
       }
     }
-    if constexpr (QUANT) store_codes<R, P>(x, lane, a.codes, a.scales, a.M, K, row, col);
+    if constexpr (QUANT) store_codes<R, P, FULL>(x, lane, a.codes, a.scales, a.M, K, row, col);
   }
 }
 
