@@ -727,7 +727,10 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     const float c0 = a.mean ? -s1 * per_k * rstd : 0.0f, cx = -s2 * per_k * rstd;
     const uint64_t m1 = pair(c0), m2 = pair(cx), rest = pair(fmaf(lo_of(less), cx, c0));
     const int64_t at = row * K + col;
-#pragma unroll
+    // (fp32 rows one run at a time: with the runs beside each other registers spill, 8192 x 8192 109 -> 112 us; bf16
+    // rows and checkpoints lose without, 4096 x 16384 97 -> 99 and 76 -> 83)
+    constexpr int kBeside = XT == kTypeFp32 ? 1 : C;
+#pragma unroll kBeside
     for (int c = 0; c < C; ++c) {
       if (!there(c)) continue;
       uint64_t x[4], y[4], w[4];
