@@ -11,8 +11,8 @@
 // costs no digits. All sums are in fp32 in a fixed order.
 //
 // x[8192, 8192] against its bytes at the rate of a plain copy (6.7 TB/s): bf16 into bf16 47 us (40), fp32 into
-// bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 53 (41); gradients bf16 69 (60; 62 without those of the
-// parameters), fp32 x 111 (100), from a checkpoint 70 (50). Rows of 2048, 4001 of them: into codes 9.5 us,
+// bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 52 (41), fp32 into codes 58 (50); gradients bf16 69 (60; 62 without those of the
+// parameters), fp32 x 109 (100), from a checkpoint 70 (50). Rows of 2048, 4001 of them: into codes 9.5 us,
 // gradients 18. One row of 8192: 3.7 and 4.3.
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
@@ -301,9 +301,10 @@ __device__ __forceinline__ void warp_sums(float (&v)[R], bool high) {
 // rows' own are as much of the shared memory's time as a row's bytes are of the memory's), the steps of the
 // sums and a block's quotients (8192 x 8192 into codes: one row 54 us, two 42). FULL: K is a multiple of a
 // warp's columns.
-// Codes are bound by their instructions, 12 for a value and 16 with a checkpoint, issued in 54 % of the cycles by 16
-// warps (an SM's registers hold no more). 32 warps of half as many values each share those steps
-// among fewer values: 42 -> 53 us.
+// Codes take 12 instructions for a value and 15 with a checkpoint, issued in 54 % of the cycles by 16 warps (an
+// SM's registers hold no more), which wait for shared memory, for results and for the arithmetic pipes in like
+// parts: dropping one in fifteen of them, or half of the exchanges over the warps, changed nothing for bf16. 32
+// warps of half as many values each share the steps of a row among fewer values: 42 -> 53 us.
 template <bool XF32, int P, int R, bool QUANT, bool FULL>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W, int S) {
   extern __shared__ __align__(16) uint8_t norm_shared[];
