@@ -11,9 +11,9 @@
 // costs no digits. All sums are in fp32 in a fixed order.
 //
 // x[8192, 8192] against its bytes at the rate of a plain copy (6.7 TB/s): bf16 into bf16 47 us (40), fp32 into
-// bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 52 (41), fp32 into codes 58 (50); gradients bf16 69 (60; 62 without those of the
-// parameters), fp32 x 109 (100), from a checkpoint 70 (50). Rows of 2048, 4001 of them: into codes 9.5 us,
-// gradients 18. One row of 8192: 3.7 and 4.3.
+// bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 52 (41), fp32 into codes 58 (50); gradients bf16 69 (60;
+// 62 without those of the parameters), fp32 x 109 (100), from a checkpoint 70 (50). Rows of 2048, 4001 of them:
+// into codes 9.5 us, gradients 18. One row of 8192: 3.7 and 4.3.
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"
