@@ -8,10 +8,12 @@
 // All in fp32, rounded once: to codes under the scale of the block of 128 that they form, or to bf16.
 //
 // Bound by memory: u is read once, h and (asked for) its checkpoint are written by the same pass. A warp
-// takes 512 columns of a row, a lane two runs of 8 in packed pairs; 16 lanes hold a block. 4096 x 28672 gated
-// against its bytes at the rate of a plain copy: silu 96 us (88), with a checkpoint 140 (122), backward from it
-// into bf16 and an operand 180 (178); gelu 116, 152 and 202, bound by its instructions, 25 for a value and
-// 40 backward, issued in 65 % of the cycles; ungated gelu 92 (53).
+// takes 512 columns of a row (1024 forward without a gate), a lane a run of 8 of each 256 in packed pairs; 16 lanes
+// hold a block. CTAs of four warps, whose places on an SM are taken again as soon as these four are done, as many
+// of them as their values' registers allow. 4096 x 28672 gated against its bytes at the rate of a plain copy: silu
+// 89 us (88), with a checkpoint 127 (122), backward from it into bf16 and an operand 179 (178); with eight warps a
+// CTA 96, 139 and 178, with two 115 (the rate at which CTAs start), 129 and 179. gelu 108, 142 and 190, bound by its
+// instructions, 25 for a value and 40 backward; ungated gelu 80 (53).
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"
@@ -22,9 +24,12 @@ namespace mxq {
 
 namespace {
 
-constexpr int kActThreads = 256;
-constexpr int kActRuns = 2;                 // runs of 8 columns per lane
-constexpr int kActCols = kActRuns * 32 * 8;  // columns of a warp's tile
+constexpr int kActThreads = 128;
+// Runs of 8 columns per lane; a warp's tile has 256 times as many columns. Without a gate the forward pass has
+// registers for twice as many (4096 x 28672 gelu 91 -> 80 us), the backward pass has not (bf16 102 -> 111).
+template <bool GATED>
+constexpr int kForwardRuns = GATED ? 2 : 4;
+constexpr int kBackwardRuns = 2;
 
 // The hardware's approximate exponential of two and reciprocal (relative 2^-22 and 2^-23; results below
 // 2^-126 are 0).
@@ -109,47 +114,48 @@ struct ActTile {
   __device__ __forceinline__ int column(int p) const { return col0 + p * 256; }
   __device__ __forceinline__ bool has(int p) const { return column(p) < H; }
 };
-__device__ __forceinline__ bool act_tile(const ActArgs& a, bool gated, int across, ActTile& t) {
+template <int RUNS, bool GATED>
+__device__ __forceinline__ bool act_tile(const ActArgs& a, int across, ActTile& t) {
   constexpr int kWarps = kActThreads / 32;
   const int warp = threadIdx.x >> 5;
   t.lane = threadIdx.x & 31;
   t.row = (int64_t)blockIdx.x * (kWarps >> across) + (warp >> across);
-  t.col0 = (((int)blockIdx.y << across) + (warp & ((1 << across) - 1))) * kActCols + t.lane * 8;
+  const int tile = ((int)(blockIdx.y + gridDim.y * blockIdx.z) << across) + (warp & ((1 << across) - 1));
+  t.col0 = tile * (RUNS * 256) + t.lane * 8;
   t.H = (int)a.H;
-  t.U = gated ? 2 * t.H : t.H;
+  t.U = GATED ? 2 * t.H : t.H;
   t.R = a.R;
   return t.row < t.R && t.col0 - t.lane * 8 < t.H;
 }
 
-// N runs (kActRuns of each of N / kActRuns parts of rows of `width` columns, a part H columns) as codes and
-// scales.
-template <int N>
+// N runs (RUNS of each of N / RUNS parts of rows of `width` columns, a part H columns) as codes and scales.
+template <int RUNS, int N>
 __device__ __forceinline__ void store_runs(const uint64_t (&v)[N][4], const ActTile& t, int width,
                                            uint8_t* codes, float* scales) {
   uint8_t* to = codes + t.row * width;
   run_codes<N>(
       v, t.lane,
       [&](int n, uint32_t lo, uint32_t hi) {
-        const int p = n % kActRuns;
-        if (t.has(p)) store8B(to + (n / kActRuns) * t.H + t.column(p), lo, hi);
+        const int p = n % RUNS;
+        if (t.has(p)) store8B(to + (n / RUNS) * t.H + t.column(p), lo, hi);
       },
       [&](int n, float s) {
-        const int p = n % kActRuns;
-        const int kb = ((n / kActRuns) * t.H + t.column(p)) / kB128;
+        const int p = n % RUNS;
+        const int kb = ((n / RUNS) * t.H + t.column(p)) / kB128;
         if ((t.column(p) & ~(kB128 - 1)) < t.H) scales[kb * t.R + t.row] = s;
       });
 }
 
 // A lane's runs of `part` (0: gate, 1: up) of its row of u, bf16 or codes, or of dh.
-template <bool CODES>
+template <bool CODES, int RUNS>
 struct ActRuns {
-  uint32_t raw[kActRuns][CODES ? 2 : 4];
-  float scale[kActRuns];
+  uint32_t raw[RUNS][CODES ? 2 : 4];
+  float scale[RUNS];
 
   __device__ __forceinline__ void load(const void* u, const float* scales, const ActTile& t, int width,
                                        int part) {
 #pragma unroll
-    for (int p = 0; p < kActRuns; ++p) {
+    for (int p = 0; p < RUNS; ++p) {
       scale[p] = 0.0f;
 #pragma unroll
       for (int j = 0; j < (CODES ? 2 : 4); ++j) raw[p][j] = 0u;
@@ -179,46 +185,46 @@ struct ActRuns {
 };
 
 template <int KIND, bool GATED>
-__global__ void __launch_bounds__(kActThreads) activation_kernel(ActArgs a, int across) {
+__global__ void __launch_bounds__(kActThreads, GATED ? 9 : 8) activation_kernel(ActArgs a, int across) {
+  constexpr int kParts = GATED ? 2 : 1, kRuns = kForwardRuns<GATED>;
   pdl_launch_dependents();
   pdl_wait();
   ActTile t;
-  if (!act_tile(a, GATED, across, t)) return;
-  constexpr int kParts = GATED ? 2 : 1;
-  ActRuns<false> in[kParts];
+  if (!act_tile<kRuns, GATED>(a, across, t)) return;
+  ActRuns<false, kRuns> in[kParts];
 #pragma unroll
   for (int k = 0; k < kParts; ++k) in[k].load(a.u, nullptr, t, t.U, k);
-  uint64_t u[kParts * kActRuns][4], h[kActRuns][4];
+  uint64_t u[kParts * kRuns][4], h[kRuns][4];
 #pragma unroll
-  for (int n = 0; n < kParts * kActRuns; ++n) in[n / kActRuns].values(n % kActRuns, u[n]);
-  if (a.u_codes) store_runs<kParts * kActRuns>(u, t, t.U, a.u_codes, a.u_scales_out);
+  for (int n = 0; n < kParts * kRuns; ++n) in[n / kRuns].values(n % kRuns, u[n]);
+  if (a.u_codes) store_runs<kRuns, kParts * kRuns>(u, t, t.U, a.u_codes, a.u_scales_out);
 #pragma unroll
-  for (int p = 0; p < kActRuns; ++p) {
+  for (int p = 0; p < kRuns; ++p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint64_t none;
       h[p][j] = act<KIND, false>(u[p][j], none);
-      if constexpr (GATED) h[p][j] = mul_pair(h[p][j], u[kActRuns + p][j]);
+      if constexpr (GATED) h[p][j] = mul_pair(h[p][j], u[kRuns + p][j]);
     }
   }
-  store_runs<kActRuns>(h, t, a.H, a.codes, a.scales);
+  store_runs<kRuns, kRuns>(h, t, a.H, a.codes, a.scales);
 }
 
 template <int KIND, bool GATED, bool CODES>
-__global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArgs a, int across) {
+__global__ void __launch_bounds__(kActThreads, GATED ? 8 : 9) activation_backward_kernel(ActArgs a, int across) {
+  constexpr int kParts = GATED ? 2 : 1, kRuns = kBackwardRuns;
   pdl_launch_dependents();
   pdl_wait();
   ActTile t;
-  if (!act_tile(a, GATED, across, t)) return;
-  constexpr int kParts = GATED ? 2 : 1;
-  ActRuns<CODES> in[kParts];
-  ActRuns<false> dh;
+  if (!act_tile<kRuns, GATED>(a, across, t)) return;
+  ActRuns<CODES, kRuns> in[kParts];
+  ActRuns<false, kRuns> dh;
 #pragma unroll
   for (int k = 0; k < kParts; ++k) in[k].load(a.u, a.u_scales, t, t.U, k);
   dh.load(a.dh, nullptr, t, a.H, 0);
-  uint64_t du[kParts * kActRuns][4];
+  uint64_t du[kParts * kRuns][4];
 #pragma unroll
-  for (int p = 0; p < kActRuns; ++p) {
+  for (int p = 0; p < kRuns; ++p) {
     uint64_t g[4], up[4], e[4];
     in[0].values(p, g);
     if constexpr (GATED) in[kParts - 1].values(p, up);
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArg
       uint64_t d;
       const uint64_t h = act<KIND, true>(g[j], d);
       if constexpr (GATED) {
-        du[kActRuns + p][j] = mul_pair(e[j], h);
+        du[kRuns + p][j] = mul_pair(e[j], h);
         du[p][j] = mul_pair(mul_pair(e[j], up[j]), d);
       } else {
         du[p][j] = mul_pair(e[j], d);
@@ -237,15 +243,15 @@ __global__ void __launch_bounds__(kActThreads) activation_backward_kernel(ActArg
   }
   if (a.du) {
 #pragma unroll
-    for (int n = 0; n < kParts * kActRuns; ++n) {
-      if (!t.has(n % kActRuns)) continue;
+    for (int n = 0; n < kParts * kRuns; ++n) {
+      if (!t.has(n % kRuns)) continue;
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = bf16_word(du[n][j]);
-      store16B(static_cast<uint16_t*>(a.du) + t.row * t.U + (n / kActRuns) * a.H + t.column(n % kActRuns), o);
+      store16B(static_cast<uint16_t*>(a.du) + t.row * t.U + (n / kRuns) * a.H + t.column(n % kRuns), o);
     }
   }
-  if (a.codes) store_runs<kParts * kActRuns>(du, t, t.U, a.codes, a.scales);
+  if (a.codes) store_runs<kRuns, kParts * kRuns>(du, t, t.U, a.codes, a.scales);
 }
 
 template <typename F>
@@ -255,13 +261,16 @@ cudaError_t by_kind(int kind, F&& f) {
   return f(std::integral_constant<int, MX_ACT_GELU_TANH>());
 }
 
-cudaError_t run(void (*kernel)(ActArgs, int), const ActArgs& a, cudaStream_t stream) {
-  const int64_t col_tiles = (a.H + kActCols - 1) / kActCols;
+cudaError_t run(void (*kernel)(ActArgs, int), int runs, const ActArgs& a, cudaStream_t stream) {
+  const int cols = runs * 256;
+  const int64_t col_tiles = (a.H + cols - 1) / cols;
   constexpr int kWarps = kActThreads / 32;
   int across = 0;
   while ((1 << across) < kWarps && (1 << across) < col_tiles) ++across;
   const int rows = kWarps >> across;
-  const dim3 grid((unsigned)((a.R + rows - 1) / rows), (unsigned)((col_tiles + (1 << across) - 1) >> across));
+  // columns over y and, where those are too many, z
+  const int64_t n = (col_tiles + (1 << across) - 1) >> across, z = (n + 65534) / 65535;
+  const dim3 grid((unsigned)((a.R + rows - 1) / rows), (unsigned)((n + z - 1) / z), (unsigned)z);
   return launch_pdl(kernel, grid, dim3(kActThreads), 0, stream, a, across);
 }
 
@@ -270,7 +279,8 @@ cudaError_t run(void (*kernel)(ActArgs, int), const ActArgs& a, cudaStream_t str
 cudaError_t launch_activation(const ActArgs& a, cudaStream_t stream) {
   return by_kind(a.kind, [&](auto kind) {
     constexpr int KIND = decltype(kind)::value;
-    return run(a.gated ? &activation_kernel<KIND, true> : &activation_kernel<KIND, false>, a, stream);
+    return a.gated ? run(&activation_kernel<KIND, true>, kForwardRuns<true>, a, stream)
+                   : run(&activation_kernel<KIND, false>, kForwardRuns<false>, a, stream);
   });
 }
 
@@ -279,10 +289,10 @@ cudaError_t launch_activation_backward(const ActArgs& a, cudaStream_t stream) {
     constexpr int KIND = decltype(kind)::value;
     if (a.u_scales) {
       return run(a.gated ? &activation_backward_kernel<KIND, true, true>
-                         : &activation_backward_kernel<KIND, false, true>, a, stream);
+                         : &activation_backward_kernel<KIND, false, true>, kBackwardRuns, a, stream);
     }
     return run(a.gated ? &activation_backward_kernel<KIND, true, false>
-                       : &activation_backward_kernel<KIND, false, false>, a, stream);
+                       : &activation_backward_kernel<KIND, false, false>, kBackwardRuns, a, stream);
   });
 }
 

@@ -151,7 +151,8 @@ struct RunMax {
     return m[0];
   }
   __device__ __forceinline__ float take(float v, int j) const {
-    return __shfl_sync(0xFFFFFFFFu, v, (lane & ~(((1 << STEPS) - 1) << LOW)) | j << (LOW + STEPS - kHalvings));
+    const int others = lane & ~(((1 << STEPS) - 1) << LOW);
+    return __shfl_sync(0xFFFFFFFFu, v, others | j << (LOW + STEPS - kHalvings));
   }
 };
 

@@ -691,6 +691,26 @@ def test_far_end_of_activations(gated):
         del du, dc, ds
 
 
+@pytest.mark.parametrize("H", [1 << 27, (1 << 27) - 32, 512 * 4 * 65535])
+def test_activation_of_the_longest_rows(H):
+    """More tiles of columns than one dimension of a grid may have."""
+    u = torch.zeros(1, H, device="cuda", dtype=BF16)
+    at = list(range(0, H // 128, H // 1280)) + [H // 128 - 1]  # blocks with values in them
+    for i in at:
+        u[0, i * 128:i * 128 + 128] = rows(i, 1, 128, BF16)[0]
+    dh = torch.ones_like(u)
+    codes, scales = mxq.mx_activation_b128(u, mxq.GELU, gated=False)
+    du, dc, ds = mxq.mx_activation_backward(dh, u, mxq.GELU, gated=False, operand=True)
+    for i in at:
+        one = slice(i * 128, i * 128 + 128)
+        want = mxq.mx_activation_b128(u[:, one].contiguous(), mxq.GELU, gated=False)
+        assert torch.equal(codes[:, one], want[0]) and torch.equal(scales[i], want[1][0])
+        ref = mxq.mx_activation_backward(dh[:, one].contiguous(), u[:, one].contiguous(), mxq.GELU, gated=False,
+                                         operand=True)
+        assert same(du[:, one], ref[0]) and torch.equal(dc[:, one], ref[1]) and torch.equal(ds[i], ref[2][0])
+    assert not codes.count_nonzero() - sum(codes[:, i * 128:i * 128 + 128].count_nonzero() for i in at)
+
+
 def test_far_end_of_checkpoints():
     x, near = far_rows(5)
     codes, scales = mxq.mx_quantize_b128_rows(x)
