@@ -301,7 +301,7 @@ __device__ __forceinline__ void warp_sums(float (&v)[R], bool high) {
 // rows' own are as much of the shared memory's time as a row's bytes are of the memory's), the steps of the
 // sums and a block's quotients (8192 x 8192 into codes: one row 54 us, two 42). FULL: K is a multiple of a
 // warp's columns.
-// Codes take 12 instructions for a value and 15 with a checkpoint, issued in 54 % of the cycles by 16 warps (an
+// Codes take 12 instructions for a value and 16 with a checkpoint, issued in 54 % of the cycles by 16 warps (an
 // SM's registers hold no more), which wait for shared memory, for results and for the arithmetic pipes in like
 // parts: dropping one in fifteen of them, or half of the exchanges over the warps, changed nothing for bf16. 32
 // warps of half as many values each share the steps of a row among fewer values: 42 -> 53 us.
