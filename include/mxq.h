@@ -437,8 +437,8 @@ mx_status mx_combine_backward_whole(const void* dout, const void* y, const int32
  * operand of the next product, activation checkpoints in 8 bits, and what the backward pass makes of
  * them. A checkpoint is E4M3 codes [M, K] with scales [ceil(K / 128), M] as mx_quantize_b128_rows
  * writes them; it stands for the values code * scale, one fp32 product each (a block with a NaN or an
- * infinity: NaN). The conventions at the top of this file hold; alignment is stated per call. These
- * have no counterpart on the pages.
+ * infinity: NaN). The conventions at the top of this file hold; alignment is stated per call; no output
+ * may overlap an input or another output. These have no counterpart on the pages.
  * ------------------------------------------------------------------------------------------ */
 
 /* a checkpoint, where a call takes one in place of bf16 or fp32 */
@@ -478,7 +478,7 @@ mx_status mx_layer_norm_b128(const void* x, int x_type, const void* weight, cons
  * decide. workspace: device memory of
  * mx_layer_norm_backward_workspace() bytes, 4-byte aligned (NULL will do without dweight and dbias); two
  * calls that may run at the same time need one each. Alignment: that of the elements; dy, x and dx on 16
- * bytes and weight on 32 with K % 8 == 0 take wide loads. dx must not overlap the inputs.
+ * bytes and weight on 32 with K % 8 == 0 take wide loads.
  */
 mx_status mx_layer_norm_backward_workspace(int64_t M, int64_t K, int64_t* bytes);
 
