@@ -54,11 +54,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ float load_as_f32(const void* p, bool f32, int64_t i) {
-  return f32 ? load_f32(static_cast<const float*>(p) + i)
-             : __uint_as_float(load_u16(static_cast<const uint16_t*>(p) + i) << 16);
-}
-
 // 8 consecutive values of a weight or a bias (aligned to 32 bytes), kept in L1 for the next rows.
 __device__ __forceinline__ void load_param(const void* p, bool f32, int i, uint64_t (&v)[4]) {
   if (f32) {
@@ -74,57 +69,53 @@ __device__ __forceinline__ void load_param(const void* p, bool f32, int i, uint6
   }
 }
 
-// N values of a weight or a bias (fallback where there is none), a group's width apart.
+// N values of a lane, 32 apart from its first on, of which `left` places from there on are in the row: all of most
+// warps, which then ask nothing value by value and address them all from one register. Of a weight or a bias
+// (fallback where there is none):
 template <int N, typename F>
-__device__ __forceinline__ void load_params(const void* p, bool f32, int K, F&& column, float fallback,
-                                            float (&v)[N]) {
+__device__ __forceinline__ void for_values(int left, F&& f) {
+  if (left > (N - 1) * 32) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i * 32 < left) f(i);
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_params(const void* p, bool f32, int col, int left, float fallback, float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = fallback;
   if (!p) return;
   if (f32) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) v[i] = load_f32(static_cast<const float*>(p) + column(i));
-    }
+    const float* at = static_cast<const float*>(p) + col;
+    for_values<N>(left, [&](int i) { v[i] = load_f32(at + i * 32); });
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) v[i] = load_as_f32(p, false, column(i));
-    }
+    const uint16_t* at = static_cast<const uint16_t*>(p) + col;
+    for_values<N>(left, [&](int i) { v[i] = __uint_as_float(load_u16(at + i * 32) << 16); });
   }
 }
-
-// N values of a row (0 where there is none) as they lie in memory, so that nothing waits for them before they are
-// used (value_of), and their way back.
-template <int N, typename F>
-__device__ __forceinline__ void load_values(const char* row, bool f32, int K, F&& column, uint32_t (&v)[N]) {
+// Of a row from `at` on (0 where there is none), as they lie in memory, so that nothing waits for them before they
+// are used (value_of), and their way back.
+template <int N>
+__device__ __forceinline__ void load_values(const char* at, bool f32, int left, uint32_t (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = 0u;
   if (f32) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) v[i] = __float_as_uint(load_f32(reinterpret_cast<const float*>(row) + column(i)));
-    }
+    for_values<N>(left, [&](int i) { v[i] = __float_as_uint(load_f32(reinterpret_cast<const float*>(at) + i * 32)); });
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) v[i] = load_u16(reinterpret_cast<const uint16_t*>(row) + column(i));
-    }
+    for_values<N>(left, [&](int i) { v[i] = load_u16(reinterpret_cast<const uint16_t*>(at) + i * 32); });
   }
 }
 __device__ __forceinline__ float value_of(uint32_t raw, bool f32) { return __uint_as_float(raw << (f32 ? 0 : 16)); }
-template <int N, typename F>
-__device__ __forceinline__ void store_values(char* row, bool f32, int K, F&& column, const float (&v)[N]) {
+template <int N>
+__device__ __forceinline__ void store_values(char* at, bool f32, int left, const float (&v)[N]) {
   if (f32) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) reinterpret_cast<float*>(row)[column(i)] = v[i];
-    }
+    for_values<N>(left, [&](int i) { reinterpret_cast<float*>(at)[i * 32] = v[i]; });
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) reinterpret_cast<uint16_t*>(row)[column(i)] = (uint16_t)pack_bf16(v[i], 0.0f);
-    }
+    for_values<N>(left, [&](int i) { reinterpret_cast<uint16_t*>(at)[i * 32] = (uint16_t)pack_bf16(v[i], 0.0f); });
   }
 }
 
@@ -456,7 +447,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   }
 }
 
-// The same for rows of any length and alignment: 16 columns per lane, a group's width apart, loaded and
+// The same for rows of any length and alignment: 512 columns a warp, 16 a lane, loaded and
 // stored one by one. Such loads and stores are what bounds it, so up to 8192 columns the parameters stay in
 // registers (they would be half of the loads) and the next row is on its way: 3000 x 7777 bf16 34 us (14 of
 // bytes), 56 without both.
@@ -470,24 +461,18 @@ __global__ void __launch_bounds__(THREADS, 1) norm_any_kernel(NormArgs a, int W)
   const int T = 32 * W, group = threadIdx.x / T, t = threadIdx.x - group * T, K = (int)a.K;
   const int64_t step = (int64_t)gridDim.x * (blockDim.x / T);
   int64_t row = (int64_t)blockIdx.x * (blockDim.x / T) + group;
-  auto column = [&](int i) { return i * T + t; };
-  auto count = [&](int w) {  // columns of the group's warp w
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) n += min(max(K - i * T - 32 * w, 0), 32);
-    return (float)n;
-  };
-  const int lane = threadIdx.x & 31;
+  auto count = [&](int w) { return (float)min(max(K - w * 512, 0), 512); };  // columns of the group's warp w
+  const int lane = threadIdx.x & 31, col = (t >> 5) * 512 + lane, left = K - col;
   const float mine = count(t >> 5), theirs = lane < W ? count(lane) : 0.0f;
   const bool w_f32 = a.w_type == kTypeFp32, y_f32 = a.y_type == kTypeFp32;
   float x[16], w[16], b[16];
   uint32_t raw[16];
   auto load = [&](int64_t at) {
-    load_values(static_cast<const char*>(a.x) + at * K * (XF32 ? 4 : 2), XF32, K, column, raw);
+    load_values(static_cast<const char*>(a.x) + (at * K + col) * (XF32 ? 4 : 2), XF32, left, raw);
   };
   auto params = [&] {
-    load_params(a.weight, w_f32, K, column, 1.0f, w);
-    load_params(a.bias, w_f32, K, column, 0.0f, b);
+    load_params(a.weight, w_f32, col, left, 1.0f, w);
+    load_params(a.bias, w_f32, col, left, 0.0f, b);
   };
   if constexpr (kKeep) {
     if (row < a.M) load(row);
@@ -506,11 +491,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_any_kernel(NormArgs a, int W)
       mean = mine > 0.0f ? __fdiv_rn(warp_sum(s[0] + s[1]), mine) : 0.0f;
     }
     float s[2] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float d = column(i) < K ? x[i] - mean : 0.0f;
-      s[i & 1] = fmaf(d, d, s[i & 1]);
-    }
+    for_values<16>(left, [&](int i) { s[i & 1] = fmaf(x[i] - mean, x[i] - mean, s[i & 1]); });
     float sq = warp_sum(s[0] + s[1]);
     if (W > 1) {  // the warps' sums about their own means, joined with the means' distances from the row's
       if (lane == 0) part[slot][threadIdx.x >> 5] = make_float2(mean, sq);
@@ -524,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1) norm_any_kernel(NormArgs a, int W)
     if constexpr (!kKeep) params();
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = fmaf((x[i] - mean) * rstd, w[i], b[i]);
-    store_values(static_cast<char*>(a.y) + row * K * (y_f32 ? 4 : 2), y_f32, K, column, x);
+    store_values(static_cast<char*>(a.y) + (row * K + col) * (y_f32 ? 4 : 2), y_f32, left, x);
   }
 }
 
@@ -810,7 +791,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   join_shares(a, reinterpret_cast<const float*>(ring_shared), groups);
 }
 
-// The same for rows of any length and alignment: N values of a lane, a group's width apart, loaded one by
+// The same for rows of any length and alignment: 32 N columns a warp, N a lane, loaded one by
 // one; up to 8192 columns (16 values) with the weights in registers and the next row on its way: 3000 x 7777
 // bf16 73 us (21 of bytes), 130 without both.
 template <int N>
@@ -826,36 +807,36 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(Norm
   const bool x_f32 = a.x_type == kTypeFp32, dy_f32 = a.y_type == kTypeFp32, dx_f32 = a.dx_type == kTypeFp32;
   const bool codes = a.x_type == kTypeB128, w_f32 = a.w_type == kTypeFp32;
   const float per_k = __fdiv_rn(1.0f, (float)K);
-  auto column = [&](int i) { return i * T + t; };
+  const int col = (t >> 5) * (32 * N) + (threadIdx.x & 31), left = K - col;
   float dw[N], db[N], w[N];
   uint32_t x[N], dy[N];
   auto load = [&](int64_t at) {
-    const char* from = static_cast<const char*>(a.x) + at * K * (codes ? 1 : x_f32 ? 4 : 2);
+    const char* from = static_cast<const char*>(a.x) + (at * K + col) * (codes ? 1 : x_f32 ? 4 : 2);
     if (codes) {
+      const float* scales = a.x_scales + (int64_t)(t >> 5) * (32 * N / kB128) * a.M + at;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        x[i] = 0u;
-        if (column(i) >= K) continue;
+      for (int i = 0; i < N; ++i) x[i] = 0u;
+      for_values<N>(left, [&](int i) {
         float lo, hi;
-        e4m3x2_to_f32(load_u8(from + column(i)), lo, hi);
-        x[i] = __float_as_uint(__fmul_rn(lo, load_f32(a.x_scales + column(i) / kB128 * a.M + at)));
-      }
+        e4m3x2_to_f32(load_u8(from + i * 32), lo, hi);
+        x[i] = __float_as_uint(__fmul_rn(lo, load_f32(scales + i / 4 * a.M)));
+      });
     } else {
-      load_values(from, x_f32, K, column, x);
+      load_values(from, x_f32, left, x);
     }
-    load_values(static_cast<const char*>(a.y) + at * K * (dy_f32 ? 4 : 2), dy_f32, K, column, dy);
+    load_values(static_cast<const char*>(a.y) + (at * K + col) * (dy_f32 ? 4 : 2), dy_f32, left, dy);
   };
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.0f;
   if constexpr (kKeep) {
     if (row < a.M) load(row);
-    load_params(a.weight, w_f32, K, column, 1.0f, w);
+    load_params(a.weight, w_f32, col, left, 1.0f, w);
   }
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
     const float rstd = load_f32(a.rstd + row), mean = a.mean ? load_f32(a.mean + row) : 0.0f;
     if constexpr (!kKeep) {
       load(row);
-      load_params(a.weight, w_f32, K, column, 1.0f, w);
+      load_params(a.weight, w_f32, col, left, 1.0f, w);
     }
     float xh[N], g[N], s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -876,17 +857,14 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(Norm
     s2 *= per_k;
 #pragma unroll
     for (int i = 0; i < N; ++i) g[i] = fmaf(-xh[i], s2, g[i] - s1) * rstd;
-    store_values(static_cast<char*>(a.dx) + row * K * (dx_f32 ? 4 : 2), dx_f32, K, column, g);
+    store_values(static_cast<char*>(a.dx) + (row * K + col) * (dx_f32 ? 4 : 2), dx_f32, left, g);
   }
   if (!a.dweight && !a.dbias) return;
   const int groups = blockDim.x / T;
   float* sm = reinterpret_cast<float*>(ring_shared);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (column(i) < K) sm[(k * groups + group) * K + column(i)] = k ? db[i] : dw[i];
-    }
+    for_values<N>(left, [&](int i) { sm[(k * groups + group) * K + col + i * 32] = k ? db[i] : dw[i]; });
   }
   join_shares(a, sm, groups);
 }
