@@ -448,9 +448,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
 }
 
 // The same for rows of any length and alignment: 512 columns a warp, 16 a lane, loaded and
-// stored one by one. Such loads and stores are what bounds it, so up to 8192 columns the parameters stay in
-// registers (they would be half of the loads) and the next row is on its way: 3000 x 7777 bf16 34 us (14 of
-// bytes), 56 without both.
+// stored one by one; up to 8192 columns the parameters stay in registers (they would be half of the loads) and the
+// next row is on its way. 3000 x 7777 bf16 31.5 us (14 of bytes), 56 without both; with the parameters in shared
+// memory and 32 warps 32.5.
 template <bool XF32, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_any_kernel(NormArgs a, int W) {
   constexpr int kWarps = THREADS / 32;
@@ -791,9 +791,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
   join_shares(a, reinterpret_cast<const float*>(ring_shared), groups);
 }
 
-// The same for rows of any length and alignment: 32 N columns a warp, N a lane, loaded one by
-// one; up to 8192 columns (16 values) with the weights in registers and the next row on its way: 3000 x 7777
-// bf16 73 us (21 of bytes), 130 without both.
+// The same for rows of any length and alignment: 32 N columns a warp, N a lane, loaded one by one; up to 8192
+// columns (16 values) with the weights in registers and the next row on its way: 3000 x 7777 bf16 55 us (21 of
+// bytes), 130 without both. A lane's columns a group's width apart, asked for one by one, took 73 us.
 template <int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(NormArgs a, int W, int) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
@@ -954,13 +954,13 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
   return a.K <= 512 ? run_norm<XF32, 2, 2, QUANT>(a, stream) : run_norm<XF32, 4, 2, QUANT>(a, stream);
 }
 
-// G rows of a CTA at once.
 cudaError_t run_any(void (*kernel)(NormArgs, int), const NormArgs& a, int W, cudaStream_t stream) {
-  const int G = W >= 16 ? 1 : 16 / W;
-  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), 32 * W * G, 0, 0);
+  const int most = W >= 16 ? 1 : 16 / W;
+  const int64_t slots = resident_ctas(reinterpret_cast<const void*>(kernel), 32 * W * most, 0, 0);
   if (slots <= 0) return cudaErrorInvalidConfiguration;
-  const int64_t ctas = (a.M + G - 1) / G;
-  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(32 * W * G), 0, stream, a, W);
+  const int count = spread(most, a.M, slots);
+  const int64_t ctas = (a.M + count - 1) / count;
+  return launch_pdl(kernel, dim3((unsigned)(ctas < slots ? ctas : slots)), dim3(32 * W * count), 0, stream, a, W);
 }
 
 template <bool XF32>
