@@ -13,7 +13,7 @@
 // x[8192, 8192] against its bytes at the rate of a plain copy (6.7 TB/s): bf16 into bf16 47 us (40), fp32 into
 // bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 52 (41), fp32 into codes 58 (50); gradients bf16 69 (60;
 // 62 without those of the parameters), fp32 x 109 (100), from a checkpoint 70 (50). Rows of 2048, 4001 of them:
-// into codes 9.5 us, gradients 18. One row of 8192: 3.7 and 4.3.
+// into codes 9.5 us, gradients 18. One row of 8192: 2.7 and 4.3.
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"
@@ -54,18 +54,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// 8 consecutive values of a weight or a bias (aligned to 32 bytes), kept in L1 for the next rows.
-__device__ __forceinline__ void load_param(const void* p, bool f32, int i, uint64_t (&v)[4]) {
+// 8 consecutive values (aligned to their size)
+__device__ __forceinline__ void load_run(const char* p, bool f32, uint64_t (&v)[4]) {
   if (f32) {
     asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
                  : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3])
-                 : "l"(static_cast<const float*>(p) + i));
+                 : "l"(p));
   } else {
-    const uint4 q = load_v4(static_cast<const uint16_t*>(p) + i);
+    const uint4 q = load_v4(p);
     v[0] = bf16_pair(q.x);
     v[1] = bf16_pair(q.y);
     v[2] = bf16_pair(q.z);
     v[3] = bf16_pair(q.w);
+  }
+}
+__device__ __forceinline__ void store_run(void* p, bool f32, int64_t at, const uint64_t (&y)[4]) {
+  uint32_t o[8];
+  if (f32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[2 * j] = __float_as_uint(lo_of(y[j]));
+      o[2 * j + 1] = __float_as_uint(hi_of(y[j]));
+    }
+    store32B(static_cast<float*>(p) + at, o);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = bf16_word(y[j]);
+    store16B(static_cast<uint16_t*>(p) + at, o);
   }
 }
 
@@ -217,7 +232,7 @@ struct ParamRuns {
     for (int c = 0; c < P; ++c) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[c][j] = pair(none);
-      if (p && col + c * 256 < K) load_param(p, f32, col + c * 256, v[c]);
+      if (p && col + c * 256 < K) load_run(static_cast<const char*>(p) + (col + c * 256) * (f32 ? 4 : 2), f32, v[c]);
     }
 #pragma unroll
     for (int c = 0; c < P; ++c) {
@@ -427,24 +442,86 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
         for (int j = 0; j < 4; ++j) y[j] = fma_pair(mul_pair(add_pair(y[j], minus[r]), r2[r]), w[j], b[j]);
         if constexpr (!QUANT) {
           if (row + r >= a.M) continue;
-          uint32_t o[8];
-          if (y_f32) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              o[2 * j] = __float_as_uint(lo_of(y[j]));
-              o[2 * j + 1] = __float_as_uint(hi_of(y[j]));
-            }
-            store32B(static_cast<float*>(a.y) + at + (int64_t)r * K + p * 256, o);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = bf16_word(y[j]);
-            store16B(static_cast<uint16_t*>(a.y) + at + (int64_t)r * K + p * 256, o);
-          }
+          store_run(a.y, y_f32, at + (int64_t)r * K + p * 256, y);
         }
       }
     }
     if constexpr (QUANT) store_codes<R, P, FULL>(x, lane, a.codes, a.scales, a.M, K, row, col);
   }
+}
+
+// The same, to the bit, for few rows: a CTA's one row and its parameters come straight to registers, all of them at
+// once. One row of 8192 into codes 2.7 us, 64 rows 3.1, most of it the wait for memory and two sums.
+template <bool XF32, int P, bool QUANT>
+__global__ void __launch_bounds__(kNormThreads) norm_row_kernel(NormArgs a) {
+  __shared__ float2 part[kNormThreads / 32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int W = blockDim.x / 32, K = (int)a.K, lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
+  const int col = wi * (P * 256) + lane * 8;
+  const int64_t row = blockIdx.x, at = row * K + col;
+  auto there = [&](int p) { return col + p * 256 < K; };
+  uint64_t x[P][4], w[P][4], b[P][4];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[p][j] = b[p][j] = 0u;
+      w[p][j] = pair(1.0f);
+    }
+    if (there(p)) load_run(static_cast<const char*>(a.x) + (at + p * 256) * (XF32 ? 4 : 2), XF32, x[p]);
+  }
+  const int w_size = a.w_type == kTypeFp32 ? 4 : 2;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (!there(p)) continue;
+    const int64_t from = (int64_t)(col + p * 256) * w_size;
+    if (a.weight) load_run(static_cast<const char*>(a.weight) + from, w_size == 4, w[p]);
+    if (a.bias) load_run(static_cast<const char*>(a.bias) + from, w_size == 4, b[p]);
+  }
+  auto count = [&](int k) { return (float)min(max(K - k * (P * 256), 0), P * 256); };  // columns of warp k
+  const float per_k = __fdiv_rn(1.0f, (float)K);
+  uint64_t s[2] = {x[0][0], x[0][1]};
+#pragma unroll
+  for (int i = 2; i < 4 * P; ++i) s[i & 1] = add_pair(s[i & 1], x[i / 4][i % 4]);
+  s[0] = add_pair(s[0], s[1]);
+  float mean = warp_sum(lo_of(s[0]) + hi_of(s[0]));
+  mean = a.center ? mean * __fdiv_rn(1.0f, count(wi)) : 0.0f;
+  uint64_t minus = pair(-mean);
+  s[0] = s[1] = 0u;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (!there(p)) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t d = add_pair(x[p][j], minus);
+      s[j & 1] = fma_pair(d, d, s[j & 1]);
+    }
+  }
+  s[0] = add_pair(s[0], s[1]);
+  float sq = warp_sum(lo_of(s[0]) + hi_of(s[0]));
+  if (W > 1) {
+    if (lane == 0) part[wi] = make_float2(mean, sq);
+    __syncthreads();
+    const float theirs = lane < W ? count(lane) : 0.0f;
+    const float2 q = lane < W ? part[lane] : make_float2(0.0f, 0.0f);
+    mean = warp_sum(q.x * theirs) * per_k;
+    sq = warp_sum(fmaf((q.x - mean) * theirs, q.x - mean, q.y));
+  }
+  const float rstd = __frsqrt_rn(fmaf(sq, per_k, a.eps));
+  if (threadIdx.x == 0) store_stats(a, row, mean, rstd);
+  if constexpr (QUANT) {
+    if (a.x_codes) store_codes<1, P, false>(x, lane, a.x_codes, a.x_scales_out, a.M, K, row, col);
+  }
+  minus = pair(-mean);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (!there(p)) continue;  // zeros
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[p][j] = fma_pair(mul_pair(add_pair(x[p][j], minus), pair(rstd)), w[p][j], b[p][j]);
+    if constexpr (!QUANT) store_run(a.y, a.y_type == kTypeFp32, at + p * 256, x[p]);
+  }
+  if constexpr (QUANT) store_codes<1, P, false>(x, lane, a.codes, a.scales, a.M, K, row, col);
 }
 
 // The same for rows of any length and alignment: 512 columns a warp, 16 a lane, loaded and
@@ -922,7 +999,7 @@ Groups fit_groups(int most, int W, size_t fixed, size_t stage) {
 }
 
 // Few rows go to as many CTAs as there are: `count` groups of a CTA, or as many as M rows need at `slots` a round
-// (64 rows of 1024 into codes 4.7 -> 3.2 us, of 8192 5.1 -> 4.0; gradients 8.0 -> 5.0 and 9.7 -> 7.7).
+// (gradients of 64 rows of 1024 8.0 -> 5.0 us, of 8192 9.7 -> 7.7).
 int spread(int count, int64_t M, int64_t slots) {
   const int64_t need = (M + slots - 1) / slots;
   return need < count ? (int)need : count;
@@ -933,6 +1010,13 @@ cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
   const int W = (int)((a.K + P * 256 - 1) / (P * 256));
   const auto kernel =
       a.K % (P * 256) == 0 ? &norm_kernel<XF32, P, R, QUANT, true> : &norm_kernel<XF32, P, R, QUANT, false>;
+  // Rows that are all resident at once, at most 8 an SM, go by the kernel without shared memory for rows and
+  // parameters (into bf16: 1 x 8192 3.5 -> 2.5 us, 300 x 8192 4.6 -> 4.2, but 600 x 8192 6.3 -> 7.6; 1200 x 1024 3.3 ->
+  // 2.9, 2400 x 1024 4.2 -> 4.5).
+  const auto row = &norm_row_kernel<XF32, P, QUANT>;
+  if (a.M <= resident_ctas(reinterpret_cast<const void*>(row), 32 * W, 0, 8)) {
+    return launch_pdl(row, dim3((unsigned)a.M), dim3(32 * W), 0, stream, a);
+  }
   const Groups g = fit_groups(kNormThreads, W, (size_t)64 * W * ParamRuns<P>::kBytes,
                               (size_t)32 * W * R * P * 8 * (XF32 ? 4 : 2));
   // two rows of more than 14336 columns of fp32 do not fit beside their parameters

@@ -202,6 +202,31 @@ def test_rows_do_not_depend_on_their_neighbours(M, K):
     T.check_values(db, want[2], want[5], FP32, "db")
 
 
+@pytest.mark.parametrize("M,K", [(4001, 2048), (1219, 1032), (2501, 520), (1217, 40), (701, 8200), (305, 16384),
+                                 (465, 5120), (3001, 96), (331, 14400), (2435, 256), (1233, 512), (613, 4096)])
+@pytest.mark.parametrize("x_type", [BF16, FP32])
+@pytest.mark.parametrize("center", [True, False])
+def test_norm_of_many_rows_is_that_of_few(M, K, x_type, center):
+    """Few rows go by a kernel of their own (a CTA each), many by groups that walk pairs of them: the same bits."""
+    x = rows(M + K, M, K, x_type)
+    w, b = params(K, K, FP32 if M % 2 else BF16)
+    kw = dict(center=center, stats=True)
+    parts = [x[i:i + 100].contiguous() for i in range(0, M, 100)]
+
+    def check(many, few, dims):
+        for i, dim in enumerate(dims):
+            got = many[i]
+            assert got is None and few[0][i] is None or same(got, torch.cat([f[i] for f in few], dim))
+    for y_type in (BF16, FP32):
+        check(mxq.mx_layer_norm(x, w, b, out_dtype=y_type, **kw),
+              [mxq.mx_layer_norm(p, w, b, out_dtype=y_type, **kw) for p in parts], (0, 0, 0))
+    if K % 32 == 0:
+        check(mxq.mx_layer_norm_b128(x, w, b, checkpoint=True, **kw),
+              [mxq.mx_layer_norm_b128(p, w, b, checkpoint=True, **kw) for p in parts], (0, 1, 0, 0, 0, 1))
+        check(mxq.mx_layer_norm_b128(x, w, None, **kw), [mxq.mx_layer_norm_b128(p, w, None, **kw) for p in parts],
+              (0, 1, 0, 0))
+
+
 def test_norm_of_no_rows_and_no_columns():
     empty = torch.empty(0, 64, dtype=BF16, device="cuda")
     w, b = params(1, 64, FP32)
