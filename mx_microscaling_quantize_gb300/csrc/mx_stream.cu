@@ -734,10 +734,12 @@ int resident_ctas(const void* kernel, int threads, size_t dyn_smem, int max_per_
   }
   cudaFuncAttributes fa{};
   if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return 0;
-  // raised only: a kernel may run with more shared memory in other calls
-  if (dyn_smem > 48 * 1024 && (size_t)fa.maxDynamicSharedSizeBytes < dyn_smem &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn_smem) !=
-          cudaSuccess) {
+  // Without being given more a kernel has 48 KB, for what is fixed and what the launch asks for together. Raised
+  // only: it may run with more in other calls.
+  const size_t limit = (size_t)fa.maxDynamicSharedSizeBytes;
+  if (fa.sharedSizeBytes + dyn_smem > 48 * 1024 && (limit < dyn_smem || limit <= 48 * 1024) &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)std::max(limit, dyn_smem)) != cudaSuccess) {
     return 0;
   }
   const int warps = (threads + 31) / 32;
