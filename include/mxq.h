@@ -603,9 +603,11 @@ mx_status mx_selftest_gemm_b128_grouped_give_up(const void* a_codes, const float
 /*
  * The same self-test of the layer norm's kernels, whose waits are for rows on their way to shared memory:
  * mx_layer_norm of bf16 rows into bf16, and mx_layer_norm_backward from bf16 dy and bf16 or checkpointed
- * rows (x_type) into a bf16 dx, every wait limited to limit_ns (K % 8 == 0 and rows on 32 bytes: others,
- * and up to some hundreds of rows of mx_layer_norm, run without such waits). y and dx then hold unspecified values. Errors as those calls, and MX_ERR_SHAPE
- * for a limit out of range, M == 0 and K == 0.
+ * rows (x_type) into a bf16 dx, every wait limited to limit_ns; what a wait that ran out had asked for is
+ * waited for once more, 2 s at most, before the kernel ends. Rows that allow no wide loads run without such
+ * waits, and as few rows of mx_layer_norm as are resident at once: 8 a multiprocessor up to 1024 columns, 2
+ * of 8192, 1 of 16384. y and dx then hold unspecified values. Errors as those calls, and MX_ERR_SHAPE for a
+ * limit out of range, M == 0 and K == 0.
  */
 mx_status mx_selftest_layer_norm_give_up(const void* x, int64_t M, int64_t K, void* y, int64_t limit_ns,
                                          void* stream);

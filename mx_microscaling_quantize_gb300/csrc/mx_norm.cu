@@ -164,9 +164,9 @@ __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_
       : "memory");
 }
 
-// The rows that a group asks for: S stages, each with a barrier, taken in turn. Thread 0 of the group asks;
-// where its wait runs out it waits for all that it has asked for and asks for
-// nothing more, so that no copy outlives the CTA.
+// The rows that a group asks for: S stages, each with a barrier, taken in turn. A thread whose wait runs out waits once
+// more, with one limit, for all that it has asked for, so that no copy outlives the CTA; after that it asks for nothing
+// and waits for nothing, but goes on arriving, so that the barriers go on for the threads that wait.
 struct RowStages {
   uint32_t bars;
   int S, ahead, stage = 0, parity = 0;  // ahead: rows asked for when one is waited for
@@ -191,7 +191,7 @@ struct RowStages {
         : "memory");
     return ok != 0;
   }
-  __device__ __forceinline__ void wait(const NormArgs& a, int64_t row, int64_t step, int t) {
+  __device__ __forceinline__ void wait(const NormArgs& a, int64_t row, int64_t step) {
     if (failed) return;
     const uint32_t ns = (uint32_t)min(a.wait_limit_ns, 1000000ull);
     if (landed(bar(stage), parity, ns)) return;
@@ -203,11 +203,16 @@ struct RowStages {
         break;
       }
     }
-    if (!failed || t != 0) return;
+    if (!failed) return;
+    const unsigned long long t1 = tc::global_ns();
     for (int k = 0; k < ahead && row + k * step < a.M; ++k) {
       const int s = stage + k < S ? stage + k : stage + k - S;
-      bool late = false;
-      tc::mbar_wait(bar(s), s == stage + k ? parity : parity ^ 1, &late, kNormDrainNs, a.err);
+      while (!landed(bar(s), s == stage + k ? parity : parity ^ 1, 1000000u)) {
+        if (tc::global_ns() - t1 > kNormDrainNs) {
+          atomicOr(a.err, 1u);
+          break;
+        }
+      }
     }
   }
   __device__ __forceinline__ void next() {
@@ -343,7 +348,11 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   int64_t row = ((int64_t)blockIdx.x * (blockDim.x / T) + group) * R;
   const uint32_t row_bytes = K * kSize;
   auto request = [&](int64_t at, int stage) {
-    if (t != 0 || at >= a.M || rows.failed) return;
+    if (t != 0 || at >= a.M) return;
+    if (rows.failed) {
+      tc::mbar_arrive(rows.bar(stage));
+      return;
+    }
     const uint32_t bytes = (uint32_t)(a.M - at < R ? a.M - at : R) * row_bytes;
     tc::mbar_arrive_expect_tx(rows.bar(stage), bytes);
     bulk_copy(rows_at + stage * T * kStage, static_cast<const char*>(a.x) + at * row_bytes, bytes,
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_kernel(NormArgs a, int W
   const int w_of = R == 1 ? lane : lane & 15;
   const float theirs = w_of < W ? count(w_of) : 0.0f;
   for (int slot = 0; row < a.M; row += step, slot ^= 1) {
-    rows.wait(a, row, step, t);
+    rows.wait(a, row, step);
     uint64_t x[R * P][4];
     const uint32_t from = rows_at + rows.stage * T * kStage + col * kSize;
 #pragma unroll
@@ -617,8 +626,13 @@ struct NormRing {
 
   // Asks for a row: called by all of the group, once the stage has been read by all of them.
   __device__ __forceinline__ void request(const NormArgs& a, const RowStages& rows, int64_t row, int stage) const {
-    if (row >= a.M || rows.failed) return;
+    if (row >= a.M) return;
     const uint32_t bar = rows.bar(stage);
+    if (rows.failed) {
+      if (XT == kTypeB128) tc::mbar_arrive(bar);
+      if (t == 0) tc::mbar_arrive(bar);
+      return;
+    }
     if constexpr (XT == kTypeB128) {
       if (t < (K + kB128 - 1) / kB128) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale_at(stage) + t * 4),
@@ -770,7 +784,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
       rstd_next = load_f32(a.rstd + row + step);
       if (a.mean) mean_next = load_f32(a.mean + row + step);
     }
-    rows.wait(a, row, step, t);
+    rows.wait(a, row, step);
     uint64_t c1 = 0u, c2 = 0u;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -831,7 +845,6 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
     }
     rows.next();
   }
-  if (XT == kTypeB128) asm volatile("cp.async.wait_all;" ::: "memory");  // scales asked for after a give-up
   if (!a.dweight && !a.dbias) return;
   if constexpr (MODE == kSingleRows) {
 #pragma unroll
