@@ -180,23 +180,34 @@ struct RowStages {
     tc::fence_proxy_async_smem();
   }
   __device__ __forceinline__ uint32_t bar(int s) const { return bars + s * 8; }
-  // One attempt, of at most `ns`.
-  static __device__ __forceinline__ bool landed(uint32_t bar, uint32_t parity, uint32_t ns) {
+  // One attempt. The hardware's own wait takes any time up to kAttemptNs and more (a limit given to it does not end it
+  // sooner), so shorter limits look without waiting.
+  static constexpr uint32_t kAttemptNs = 1000000;
+  static __device__ __forceinline__ bool landed(uint32_t bar, uint32_t parity, bool look) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, P;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(ns)
-        : "memory");
+    if (look) {
+      asm volatile(
+          "{\n\t.reg .pred P;\n\tmbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, P;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    } else {
+      asm volatile(
+          "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, P;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity), "r"(kAttemptNs)
+          : "memory");
+    }
     return ok != 0;
   }
   __device__ __forceinline__ void wait(const NormArgs& a, int64_t row, int64_t step) {
     if (failed) return;
-    const uint32_t ns = (uint32_t)min(a.wait_limit_ns, 1000000ull);
-    if (landed(bar(stage), parity, ns)) return;
+    const bool look = a.wait_limit_ns <= 100ull * kAttemptNs;
+    if (landed(bar(stage), parity, look)) return;
     const unsigned long long t0 = tc::global_ns();
-    while (!landed(bar(stage), parity, ns)) {
+    while (!landed(bar(stage), parity, look)) {
       if (tc::global_ns() - t0 > a.wait_limit_ns) {
         failed = true;
         atomicOr(a.err, 1u);
@@ -205,9 +216,10 @@ struct RowStages {
     }
     if (!failed) return;
     const unsigned long long t1 = tc::global_ns();
+#pragma unroll 1
     for (int k = 0; k < ahead && row + k * step < a.M; ++k) {
       const int s = stage + k < S ? stage + k : stage + k - S;
-      while (!landed(bar(s), s == stage + k ? parity : parity ^ 1, 1000000u)) {
+      while (!landed(bar(s), s == stage + k ? parity : parity ^ 1, false)) {
         if (tc::global_ns() - t1 > kNormDrainNs) {
           atomicOr(a.err, 1u);
           break;

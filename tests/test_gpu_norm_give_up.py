@@ -1,5 +1,5 @@
-"""Give-ups of the layer norm's kernels: a wait that runs out costs the call no time beyond what it had asked for,
-whichever threads it runs out for."""
+"""Give-ups of the layer norm's kernels: the limit reaches them, and a wait that runs out costs the call no time beyond
+what it had asked for, whichever threads it runs out for."""
 
 import time
 
@@ -37,6 +37,25 @@ def calls(M, K):
            (lambda ns: mxq.mx_selftest_layer_norm_backward_give_up(dy, kept, mean, rstd, ns, x_scales=kept_scales),
             lambda: mxq.mx_layer_norm_backward(dy, kept, mean, rstd, x_scales=kept_scales)[0])]
     return [(give_up, call, call()) for give_up, call in out]
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+def test_a_limit_of_1_ns_is_a_give_up(M, K):
+    """Rows from memory take hundreds of ns: with nothing of them in the caches some wait is too short. Not in every
+    call: a row that has landed before it is waited for is no give-up, and the GPU's clock, by which a limit is
+    measured, goes in steps that are longer than a wait of the shortest rows. One call of ten and more does at every
+    size here, so that 200 of them without are less likely than 1e-9."""
+    beside = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")  # twice the L2
+
+    def gives_up(call):
+        beside.fill_(1)
+        torch.cuda.synchronize()
+        assert mxq.mx_device_errors() == 0
+        call(1)
+        return mxq.mx_device_errors() == 1
+    for give_up, call, want in calls(M, K):
+        assert any(gives_up(give_up) for _ in range(200))
+        assert same(call(), want) and mxq.mx_device_errors() == 0
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
