@@ -13,8 +13,9 @@ measured HBM copy bandwidth, with the DRAM traffic per launch that an ncu captur
 profiles/mx_stream_qdq_traffic.json while the kernel's sources are unchanged), the CPU oracle timed
 on the host cores (cpu_baseline), an end-to-end figure through the same calls with the inputs
 copied in from, and the outputs back to, pinned host memory every step (e2e; copies in both
-directions pipelined over two buffer sets), SM clocks sampled during the timed region, and
-per-workload kernel figures for the other workloads, cold (a 256 MiB buffer is written before
+directions pipelined over two buffer sets), and SM clocks sampled during the timed region. A second
+JSON object, on stderr, has the kernel figures of the other workloads (a hundred of them, ten times
+the line's length, which a reader of the line's end would lose its beginning to), cold (a 256 MiB buffer is written before
 each timed launch; mean of the launches, since event timestamps advance in ~2 us steps) and
 steady (launches back to back over copies of the buffers that together exceed 3x L2).
 
@@ -1096,6 +1097,15 @@ def end_to_end(mxq, xw_b, xa_b, dev, steps):
             "pipeline": "2 buffer sets; H2D, QDQ and D2H on 3 streams"}
 
 
+def emit(line):
+    """One JSON line on stdout, the figures of the other workloads on stderr."""
+    line = dict(line)
+    workloads = line.pop("workloads", None)
+    if workloads is not None:
+        print(json.dumps({"workloads": workloads}), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
+
+
 def run_ours(args):
     import torch
     rank, world, local = dist_setup(args.gpus)
@@ -1207,7 +1217,7 @@ def run_ours(args):
             "sample": f"{one_passes} passes of the weight's first {one_rows} rows "
                       f"(E2M1 QDQ of x[{one_rows},8192]) in {one_s:.1f} s on one thread"}
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        emit(line)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
