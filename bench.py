@@ -14,10 +14,10 @@ profiles/mx_stream_qdq_traffic.json while the kernel's sources are unchanged), t
 on the host cores (cpu_baseline), an end-to-end figure through the same calls with the inputs
 copied in from, and the outputs back to, pinned host memory every step (e2e; copies in both
 directions pipelined over two buffer sets), and SM clocks sampled during the timed region. A second
-JSON object, on stderr, has the kernel figures of the other workloads (a hundred of them, ten times
-the line's length, which a reader of the line's end would lose its beginning to), cold (a 256 MiB buffer is written before
-each timed launch; mean of the launches, since event timestamps advance in ~2 us steps) and
-steady (launches back to back over copies of the buffers that together exceed 3x L2).
+JSON object, on stderr, has the kernel figures of the other workloads (a hundred of them, 30 KB,
+which would cost a reader of the output's end the line's beginning), cold (a 256 MiB buffer is
+written before each timed launch; mean of the launches, since event timestamps advance in ~2 us
+steps) and steady (launches back to back over copies of the buffers that together exceed 3x L2).
 
 --impl reference times the CPU oracle instead (bounded sample per step, all host cores).
 """

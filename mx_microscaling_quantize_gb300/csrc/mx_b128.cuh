@@ -121,8 +121,9 @@ __device__ __forceinline__ uint32_t absmax_pairs(const uint64_t* v) {
 }
 
 // Maxima of N values of each lane over 2^STEPS lanes (those that differ in STEPS bits, the lowest of them bit
-// LOW), N of them, found by halves: the first steps exchange half of the values that are left and keep the other half, so log2 N of them give each lane one
-// value, index (its highest log2 N bits of STEPS). take gives a lane any of the N from the lane that has it.
+// LOW), N of them, found by halves: the first steps exchange half of the values that are left and keep the other
+// half, so log2 N of them give each lane one value, index (its highest log2 N bits of STEPS). take gives a lane any
+// of the N from the lane that has it.
 template <int N, int STEPS, int LOW = 0>
 struct RunMax {
   static constexpr int kHalvings = N == 8 ? 3 : N == 4 ? 2 : N == 2 ? 1 : 0;

@@ -11,9 +11,10 @@
 // costs what its own sum in fp32 is off by, not the digits of its square. All sums are in fp32 in a fixed order.
 //
 // x[8192, 8192] against its bytes at the rate of a plain copy (6.7 TB/s): bf16 into bf16 47 us (40), fp32 into
-// bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 52 (41), fp32 into codes 58 (50); gradients bf16 69 (60;
-// 62 without those of the parameters), fp32 x 109 (100), from a checkpoint 70 (50). Rows of 2048, 4001 of them:
-// into codes 9.5 us, gradients 18. One row of 8192: 2.7 and 4.3.
+// bf16 64 (60), bf16 into codes 42 (30), with a checkpoint 52 (41), fp32 into codes 58 (50); gradients bf16 68 (60;
+// 61 without those of the parameters), fp32 x 109 (100), from a checkpoint 70 (50); of fp32 dy into bf16 101 (80),
+// 136 (100) and 93 (71), with 32 to 48 bytes of registers spilled. Rows of 2048, 4001 of them: into codes 9.5 us, gradients 18. One
+// row of 8192: 2.7 and 4.3.
 #include "mx_b128.cuh"
 #include "mx_device.cuh"
 #include "mx_launch.h"
@@ -558,7 +559,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_row_kernel(NormArgs a) {
 // The same for rows of any length and alignment: 512 columns a warp, 16 a lane, loaded and
 // stored one by one; up to 8192 columns the parameters stay in registers (they would be half of the loads) and the
 // next row is on its way. 3000 x 7777 bf16 31.5 us (14 of bytes), 56 without both; with the parameters in shared
-// memory and 32 warps 32.5.
+// memory and 32 warps 32.5. 23 instructions for a value (11 in packed pairs and wide loads), issued in 45 % of the
+// cycles by 16 warps. Longer rows, 32 warps of 64 registers that spill 8 bytes and load the parameters with every row:
+// 2000 x 9999 40 us (12 of bytes).
 template <bool XF32, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_any_kernel(NormArgs a, int W) {
   constexpr int kWarps = THREADS / 32;
@@ -745,8 +748,8 @@ __device__ __forceinline__ void join_shares(const NormArgs& a, const float* sm, 
 // stages, the weights in shared memory. A row is read from its stage twice, for the sums over it and for dx: dw
 // and db leave no registers to keep it in (8192 x 8192 from a checkpoint with xhat kept in shared memory in
 // between: 77 -> 87 us). Two groups and more work beside each other up to 8192 columns, one while the other waits
-// for its sums; one alone has 4096 x 16384 in 98 us for 60 of bytes. From a checkpoint bound by its instructions,
-// 23 for a value, issued in 59 % of the cycles; the parameters' gradients cost 6 us, for the groups' join, the
+// for its sums; one alone has 4096 x 16384 in 100 us for 60 of bytes. From a checkpoint bound by its instructions,
+// 22 for a value, issued in 58 % of the cycles; the parameters' gradients cost 6 us, for the groups' join, the
 // shares and the launch that adds them up.
 // MODE: K is a multiple of a warp's 1024 columns or not; or, of any such K, no more rows than CTAs: one group a
 // CTA, whose sums leave its registers as its share (one row of 8192 6.0 -> 4.3 us; as a branch of the others it
@@ -905,7 +908,9 @@ __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_kernel(NormArgs
 
 // The same for rows of any length and alignment: 32 N columns a warp, N a lane, loaded one by one; up to 8192
 // columns (16 values) with the weights in registers and the next row on its way: 3000 x 7777 bf16 55 us (21 of
-// bytes), 130 without both. A lane's columns a group's width apart, asked for one by one, took 73 us.
+// bytes), 130 without both. A lane's columns a group's width apart, asked for one by one, took 73 us. 32 instructions
+// for a value, issued in 38 % of the cycles; 164 bytes of registers are spilled. With 32 values (over 8192 columns, 708
+// bytes spilled) 2000 x 9999 take 90 us (18 of bytes).
 template <int N>
 __global__ void __launch_bounds__(kNormThreads, 1) norm_backward_any_kernel(NormArgs a, int W, int) {
   extern __shared__ __align__(16) uint8_t ring_shared[];
